@@ -401,6 +401,174 @@ NVFP4_API nvfp4_status_t nvfp4_harmonize_fused_scales(uint8_t* scales, const flo
                                             int64_t K, float* shared_gs, uint32_t* counters,
                                             void* stream);
 
+/*
+ * Serving the Gated DeltaNet mixer between its projections.  The calls below
+ * share these conventions:
+ *   - Packed sequences: `cu_seqlens` is a DEVICE array of n_seqs + 1
+ *     non-decreasing int32 row numbers; sequence i is rows cu_seqlens[i] ..
+ *     cu_seqlens[i + 1] - 1 of the row arrays (none when they are equal).
+ *     The host never reads it, so lengths may change under a captured graph.
+ *     Rows outside every sequence are neither read nor written; row numbers
+ *     outside 0 .. T are cut off there.
+ *   - State pools: what a request carries from call to call lives in slot
+ *     slots[i] (DEVICE int32, or NULL for slot i) of a pool of n_slots.  A
+ *     sequence or request whose slot is outside 0 .. n_slots - 1 is skipped:
+ *     its output rows are written as zeros and no state is touched (unused
+ *     rows of a padded batch carry -1).  Slots of one call must be distinct.
+ *   - Non-finite inputs of a request give unspecified values in that
+ *     request's outputs and state (of the value heads they reach), and
+ *     change no other request's.
+ */
+
+/*
+ * nvfp4_gdn_prefill -- the Gated DeltaNet recurrence of nvfp4_gdn_recurrence
+ * over packed prompts, bf16 in and out with fp32 states (picx.dev summary
+ * page, "Introduction and Theoretical Foundation" > "Gated DeltaNet
+ * Mechanics"): per value head and token
+ *     S_t = alpha_t S_{t-1} + beta_t khat_t (v_t - S_{t-1}^T khat_t)^T,
+ *     o_t = S_t^T qhat_t / sqrt(128),  alpha_t = exp(g_t),
+ * qhat, khat the head's q, k divided by max(|.|, 1e-6).
+ *
+ *   x           device bf16 [T x ldx], one row per token (read); 16-byte
+ *               aligned, ldx and the columns multiples of 8; ldx < 2^23
+ *   q_col, k_col   first column of q / k: n_qk_heads heads of 128 values
+ *   v_col       first column of v: n_v_heads heads of 128
+ *   gates       device [T x ldg] of `gates_dtype` (NVFP4_IN_F32 / _BF16):
+ *               the log-decay gates g at g_col and the write strengths beta
+ *               at beta_col, n_v_heads columns each (the layout
+ *               nvfp4_gemm_segmented_gates writes); ldg < 2^23
+ *   cu_seqlens, n_seqs   as above, 1 <= n_seqs <= 2^20
+ *   T           rows of x, gates and o, 0 <= T <= INT_MAX
+ *   n_qk_heads, n_v_heads   as for nvfp4_gdn_recurrence
+ *   state_in    device fp32 [n_slots x n_v_heads x 128 x 128] (d_k row
+ *               major), 16-byte aligned, or NULL: every sequence starts at
+ *               zero (read)
+ *   state_out   same layout, or NULL; the states after the last tokens
+ *               (written; of an empty sequence its start state).  May be
+ *               state_in itself
+ *   slots, n_slots   as above
+ *   o           device out, bf16 [T x ldo], head h at columns 128 h; 16-byte
+ *               aligned, ldo a multiple of 8, ldo >= 128 n_v_heads
+ *   workspace   device scratch, 256-byte aligned, of at least
+ *               nvfp4_gdn_prefill_workspace_size() bytes, overwritten
+ * Gates are expected non-positive and write strengths in [0, 1] (then the
+ * state cannot grow); other values follow the same formulas.
+ */
+NVFP4_API nvfp4_status_t nvfp4_gdn_prefill(const void* x, int64_t ldx, int64_t q_col, int64_t k_col, int64_t v_col,
+                                           const void* gates, int32_t gates_dtype, int64_t ldg, int64_t g_col,
+                                           int64_t beta_col, const int32_t* cu_seqlens, int32_t n_seqs, int64_t T,
+                                           int32_t n_qk_heads, int32_t n_v_heads, const float* state_in,
+                                           float* state_out, const int32_t* slots, int32_t n_slots, void* o,
+                                           int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace nvfp4_gdn_prefill needs for T rows in n_seqs sequences. */
+NVFP4_API size_t nvfp4_gdn_prefill_workspace_size(int64_t T, int32_t n_seqs, int32_t n_qk_heads,
+                                                  int32_t n_v_heads);
+
+/*
+ * nvfp4_gdn_decode -- the same recurrence for one new token of each of
+ * `batch` requests: row b of x and gates is the token of request b, whose
+ * state slot is read and updated in place.
+ *
+ *   x           device [batch x ldx] of `x_dtype` (NVFP4_IN_F32 / _BF16), as
+ *               for nvfp4_gdn_prefill (columns and ldx multiples of 8 bf16
+ *               or 4 fp32 values)
+ *   gates ...   as for nvfp4_gdn_prefill
+ *   batch       0 <= batch, batch * n_v_heads <= 2^20
+ *   states      device fp32 [n_slots x n_v_heads x 128 x 128], 16-byte
+ *               aligned (read and written)
+ *   o           device out [batch x ldo] of `o_dtype` (NVFP4_OUT_F32 /
+ *               _BF16); 16-byte aligned, ldo a multiple of 8 bf16 or 4 fp32
+ * All arithmetic is fp32.
+ */
+NVFP4_API nvfp4_status_t nvfp4_gdn_decode(const void* x, int32_t x_dtype, int64_t ldx, int64_t q_col, int64_t k_col,
+                                          int64_t v_col, const void* gates, int32_t gates_dtype, int64_t ldg,
+                                          int64_t g_col, int64_t beta_col, int64_t batch, int32_t n_qk_heads,
+                                          int32_t n_v_heads, float* states, const int32_t* slots, int32_t n_slots,
+                                          void* o, int32_t o_dtype, int64_t ldo, void* stream);
+
+/*
+ * nvfp4_conv_silu -- the mixer's short causal convolution per channel with
+ * SiLU, between the in-projection and the recurrence (the pages name the GDN
+ * convs among what stays in bf16: LIT-800, "Key takeaways", recipe bullet;
+ * width and activation are not on the pages and are this call's assumption):
+ *     y_t[c] = silu(sum_{i < width} w[c][i] x_{t - width + 1 + i}[c]),
+ * silu(v) = v / (1 + exp(-v)), in fp32 in this order.  The rows before a
+ * sequence's first are the last width - 1 inputs of its request, kept oldest
+ * first in its slot; without a pool they are zeros.
+ *
+ *   x           device [T x ldx] of `dtype` (NVFP4_IN_F32 / _BF16), `channels`
+ *               columns (read); must not overlap y (NVFP4_ERR_ALIAS)
+ *   w           device fp32 [channels x width]
+ *   width       2, 3 or 4
+ *   cu_seqlens, n_seqs   as above; NULL: every row is the one new token of
+ *               its own request (row i is request i, n_seqs is ignored)
+ *   T           rows, 0 <= T <= INT_MAX (2^22 without cu_seqlens)
+ *   channels    1 .. 2^20
+ *   state       device [n_slots x (width - 1) x channels] of `dtype`, or
+ *               NULL (read, and written with the last width - 1 inputs)
+ *   slots, n_slots   as above (not read without a state)
+ *   y           device out [T x ldy] of `dtype`
+ * Any alignment of whole elements works; 16-byte aligned pointers and
+ * strides and channels % 8 == 0 take 16-byte loads.
+ */
+NVFP4_API nvfp4_status_t nvfp4_conv_silu(const void* x, int32_t dtype, int64_t ldx, int64_t channels, const float* w,
+                                         int32_t width, const int32_t* cu_seqlens, int32_t n_seqs, int64_t T,
+                                         void* state, const int32_t* slots, int32_t n_slots, void* y, int64_t ldy,
+                                         void* stream);
+
+/*
+ * nvfp4_add_rmsnorm -- the norm in front of a block with the residual add
+ * before it, and the quantization behind it (norms stay in bf16 in the pages'
+ * recipe, LIT-800, "Key takeaways"; their inputs to every linear layer are
+ * quantized, picx.dev summary, "Background", item 1):
+ *     t = residual + scale x,   y = t / sqrt(mean_row(t^2) + eps) * w
+ * in fp32, t unrounded.
+ *
+ *   x           device [rows x ldx] of `x_dtype` (NVFP4_IN_F32 / _BF16)
+ *   residual    device [rows x ldr] of `r_dtype`, or NULL for zeros
+ *   scale       the residual scale, finite
+ *   w           device fp32 [cols];  eps > 0 and finite
+ *   rows, cols  0 <= rows <= 2^22, 1 <= cols <= 16384
+ *   residual_out  device out [rows x ldro] of `r_dtype`: t, or NULL.  May be
+ *               residual itself (same stride)
+ *   y           device out [rows x ldy] of `y_dtype` (NVFP4_OUT_F32 / _BF16),
+ *               or NULL when codes are asked for
+ *   y_gs, y_codes, y_scales   y as NVFP4 under the given tensor scale *y_gs
+ *               (device, read), the bytes nvfp4_quantize gives for the fp32
+ *               y: [rows x cols/2] (8-byte aligned) and [rows x cols/16]; or
+ *               all three NULL.  They need cols % 16 == 0 and every pointer
+ *               and row stride above 16-byte aligned
+ * Without codes, any alignment of whole elements works; aligned rows of
+ * cols % 16 == 0 take 16-byte loads.
+ */
+NVFP4_API nvfp4_status_t nvfp4_add_rmsnorm(const void* x, int32_t x_dtype, int64_t ldx, const void* residual,
+                                           int32_t r_dtype, int64_t ldr, float scale, const float* w, float eps,
+                                           int64_t rows, int64_t cols, void* residual_out, int64_t ldro, void* y,
+                                           int32_t y_dtype, int64_t ldy, const float* y_gs, uint8_t* y_codes,
+                                           uint8_t* y_scales, void* stream);
+
+/*
+ * nvfp4_rmsnorm_gated -- the norm between the recurrence and the
+ * out-projection, fused with the gate z and the quantization.  Per group of
+ * `group` columns (a value head):
+ *     y = o / sqrt(mean_group(o^2) + eps) * w * silu(z)
+ * in fp32, silu with the hardware exp2 of -z log2(e) and reciprocal.  The
+ * pages name the projection z but not its use, which is this call's
+ * assumption.
+ *
+ *   o, z        device [rows x ldo] / [rows x ldz] of o_dtype / z_dtype
+ *   w           device fp32 [group], the same for every group
+ *   rows, cols  rows >= 0, rows * cols < 2^35; cols % group == 0
+ *   group       16, 32, 64, ... or 1024
+ *   y, y_dtype, ldy, y_gs, y_codes, y_scales   as for nvfp4_add_rmsnorm
+ * All pointers and row strides 16-byte aligned (codes 8, scales 1).
+ */
+NVFP4_API nvfp4_status_t nvfp4_rmsnorm_gated(const void* o, int32_t o_dtype, int64_t ldo, const void* z,
+                                             int32_t z_dtype, int64_t ldz, const float* w, float eps, int64_t rows,
+                                             int64_t cols, int32_t group, void* y, int32_t y_dtype, int64_t ldy,
+                                             const float* y_gs, uint8_t* y_codes, uint8_t* y_scales, void* stream);
+
 /* Bytes of workspace nvfp4_gemm, nvfp4_gemm_segmented and
  * nvfp4_gemm_segmented_gates need for this
  * shape: the partial sums of the split tail tiles (256 KiB per tile and

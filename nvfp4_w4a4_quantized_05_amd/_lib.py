@@ -26,6 +26,8 @@ EXPORTS = ("nvfp4_quantize", "nvfp4_gemm", "nvfp4_gemm_segmented", "nvfp4_gemm_s
            "nvfp4_quantize_gemm", "nvfp4_gdn_recurrence", "nvfp4_gemm_swiglu_quantize",
            "nvfp4_quantize_gemm_workspace_size", "nvfp4_quantize_gemm_no_alloc",
            "nvfp4_quantize_gemm_no_alloc_max_bytes", "nvfp4_harmonize_fused_scales",
+           "nvfp4_gdn_prefill", "nvfp4_gdn_prefill_workspace_size", "nvfp4_gdn_decode", "nvfp4_conv_silu",
+           "nvfp4_add_rmsnorm", "nvfp4_rmsnorm_gated",
            "nvfp4_gemm_workspace_size", "nvfp4_status_string", "nvfp4_last_hip_error")
 
 _lib = None
@@ -73,6 +75,23 @@ def load() -> ctypes.CDLL:
     lib.nvfp4_quantize_gemm_no_alloc.restype = i32
     lib.nvfp4_quantize_gemm_no_alloc_max_bytes.argtypes = []
     lib.nvfp4_quantize_gemm_no_alloc_max_bytes.restype = sz
+    f32 = ctypes.c_float
+    lib.nvfp4_gdn_prefill.argtypes = [vp, i64, i64, i64, i64, vp, i32, i64, i64, i64, vp, i32, i64, i32, i32, vp, vp,
+                                      vp, i32, vp, i64, vp, sz, vp]
+    lib.nvfp4_gdn_prefill.restype = i32
+    lib.nvfp4_gdn_prefill_workspace_size.argtypes = [i64, i32, i32, i32]
+    lib.nvfp4_gdn_prefill_workspace_size.restype = sz
+    lib.nvfp4_gdn_decode.argtypes = [vp, i32, i64, i64, i64, i64, vp, i32, i64, i64, i64, i64, i32, i32, vp, vp, i32,
+                                     vp, i32, i64, vp]
+    lib.nvfp4_gdn_decode.restype = i32
+    lib.nvfp4_conv_silu.argtypes = [vp, i32, i64, i64, vp, i32, vp, i32, i64, vp, vp, i32, vp, i64, vp]
+    lib.nvfp4_conv_silu.restype = i32
+    lib.nvfp4_add_rmsnorm.argtypes = [vp, i32, i64, vp, i32, i64, f32, vp, f32, i64, i64, vp, i64, vp, i32, i64, vp,
+                                      vp, vp, vp]
+    lib.nvfp4_add_rmsnorm.restype = i32
+    lib.nvfp4_rmsnorm_gated.argtypes = [vp, i32, i64, vp, i32, i64, vp, f32, i64, i64, i32, vp, i32, i64, vp, vp, vp,
+                                        vp]
+    lib.nvfp4_rmsnorm_gated.restype = i32
     lib.nvfp4_harmonize_fused_scales.argtypes = [vp, vp, ctypes.POINTER(i64), i32, i64, vp, vp, vp]
     lib.nvfp4_harmonize_fused_scales.restype = i32
     lib.nvfp4_gemm_workspace_size.argtypes = [i64, i64, i64, i32]
@@ -324,6 +343,221 @@ def gdn_recurrence(x: torch.Tensor, *, q_col: int, k_col: int, v_col: int, g_col
                                      _ptr(snap_steps), n_snaps, _ptr(snaps), _stream(stream))
     _check(st, "nvfp4_gdn_recurrence")
     return state_out
+
+
+_DTYPE_CODE = {torch.float32: 0, torch.bfloat16: 1}  # NVFP4_IN_* and NVFP4_OUT_*
+
+
+def _rows2d(t, what):
+    """A 2-D bf16 or fp32 tensor with unit column stride; returns its dtype code."""
+    code = _DTYPE_CODE.get(t.dtype)
+    if code is None or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be 2-D bf16 or fp32 with unit column stride, got {t.dtype} {tuple(t.shape)}")
+    return code
+
+
+def _ld(t):
+    """Row stride of a 2-D tensor (of one row or fewer: its columns)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _i32_vector(t, n, what):
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 vector of {n} values")
+
+
+def _state_pool(t, shape, dtype, what):
+    """A contiguous [n_slots, *shape] pool; returns n_slots."""
+    if t.dtype != dtype or t.shape[1:] != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous {dtype} [n_slots, {', '.join(map(str, shape))}]")
+    return t.shape[0]
+
+
+def gdn_prefill(x: torch.Tensor, gates: torch.Tensor, cu_seqlens: torch.Tensor, *, q_col: int, k_col: int,
+                v_col: int, g_col: int, beta_col: int, n_qk_heads: int, n_v_heads: int,
+                state_in: torch.Tensor | None = None, state_out: torch.Tensor | None = None,
+                slots: torch.Tensor | None = None, o: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, stream=None):
+    """Gated DeltaNet recurrence over packed prompts: sequence i is rows
+    cu_seqlens[i] .. cu_seqlens[i + 1] - 1 (device int32) of x (bf16: q, k, v
+    at their columns) and of gates (bf16 or fp32: g and beta at theirs).  It
+    starts from slot slots[i] of state_in [n_slots, n_v_heads, 128, 128]
+    (zeros if None) and leaves its state in that slot of state_out (which may
+    be state_in).  Returns o, bf16 [T, n_v_heads * 128]; rows of no sequence
+    are not written."""
+    if _rows2d(x, "x") != 1:
+        raise ValueError("x must be bf16")
+    gates_dtype = _rows2d(gates, "gates")
+    T, n_seqs = x.shape[0], cu_seqlens.shape[0] - 1
+    _i32_vector(cu_seqlens, max(n_seqs, 1) + 1, "cu_seqlens")
+    if gates.shape[0] != T:
+        raise ValueError("x and gates must have the same rows")
+    n_slots = n_seqs
+    for t, what in ((state_in, "state_in"), (state_out, "state_out")):
+        if t is not None:
+            n_slots = _state_pool(t, (n_v_heads, 128, 128), torch.float32, what)
+    if state_in is not None and state_out is not None and state_in.shape != state_out.shape:
+        raise ValueError("state_in and state_out must have the same slots")
+    if slots is not None:
+        _i32_vector(slots, n_seqs, "slots")
+        if state_in is None and state_out is None:
+            raise ValueError("slots without a state pool")
+    if o is not None:
+        _out_matrix(o, T, n_v_heads * 128, torch.bfloat16)
+    _need_gpu(x, gates, cu_seqlens, state_in, state_out, slots, o, workspace)
+    if o is None:
+        o = torch.empty((T, n_v_heads * 128), dtype=torch.bfloat16, device=x.device)
+    lib = load()
+    need = lib.nvfp4_gdn_prefill_workspace_size(T, n_seqs, n_qk_heads, n_v_heads)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    have = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = lib.nvfp4_gdn_prefill(_ptr(x), _ld(x), q_col, k_col, v_col, _ptr(gates), gates_dtype, _ld(gates), g_col,
+                               beta_col, _ptr(cu_seqlens), n_seqs, T, n_qk_heads, n_v_heads, _ptr(state_in),
+                               _ptr(state_out), _ptr(slots), n_slots, _ptr(o), _ld(o), _ptr(workspace), have,
+                               _stream(stream))
+    _check(st, "nvfp4_gdn_prefill")
+    return o
+
+
+def gdn_decode(x: torch.Tensor, gates: torch.Tensor, states: torch.Tensor, *, q_col: int, k_col: int, v_col: int,
+               g_col: int, beta_col: int, n_qk_heads: int, n_v_heads: int, slots: torch.Tensor | None = None,
+               o: torch.Tensor | None = None, stream=None):
+    """The same recurrence for one new token of each request: row b of x and
+    gates (bf16 or fp32) is request b's, slot slots[b] (b if None) of states
+    [n_slots, n_v_heads, 128, 128] fp32 is updated in place.  Returns o
+    [batch, n_v_heads * 128] (bf16 or fp32 as given, else x's type); requests
+    whose slot is negative get a row of zeros."""
+    x_dtype, gates_dtype = _rows2d(x, "x"), _rows2d(gates, "gates")
+    B = x.shape[0]
+    if gates.shape[0] != B:
+        raise ValueError("x and gates must have the same rows")
+    n_slots = _state_pool(states, (n_v_heads, 128, 128), torch.float32, "states")
+    if slots is not None:
+        _i32_vector(slots, B, "slots")
+    if o is None:
+        o = torch.empty((B, n_v_heads * 128), dtype=x.dtype, device=x.device)
+    o_dtype = _rows2d(o, "o")
+    _out_matrix(o, B, n_v_heads * 128, o.dtype)
+    _need_gpu(x, gates, states, slots, o)
+    st = load().nvfp4_gdn_decode(_ptr(x), x_dtype, _ld(x), q_col, k_col, v_col, _ptr(gates), gates_dtype, _ld(gates),
+                                 g_col, beta_col, B, n_qk_heads, n_v_heads, _ptr(states), _ptr(slots), n_slots,
+                                 _ptr(o), o_dtype, _ld(o), _stream(stream))
+    _check(st, "nvfp4_gdn_decode")
+    return o
+
+
+def conv_silu(x: torch.Tensor, weight: torch.Tensor, *, cu_seqlens: torch.Tensor | None = None,
+              state: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+              out: torch.Tensor | None = None, stream=None):
+    """silu of the causal convolution of each column of x [T, channels] (bf16
+    or fp32) with weight [channels, width] fp32, per packed sequence of
+    cu_seqlens (device int32), or, without cu_seqlens, for one new row of each
+    request.  state [n_slots, width - 1, channels] (x's type) holds the last
+    inputs of each request, read and updated in slot slots[i].  Returns out
+    [T, channels] of x's type."""
+    dtype = _rows2d(x, "x")
+    T, channels = x.shape
+    if weight.dtype != torch.float32 or weight.dim() != 2 or weight.shape[0] != channels \
+            or not weight.is_contiguous():
+        raise ValueError("weight must be contiguous float32 [channels, width]")
+    width = weight.shape[1]
+    n_seqs = T
+    if cu_seqlens is not None:
+        n_seqs = cu_seqlens.shape[0] - 1
+        _i32_vector(cu_seqlens, max(n_seqs, 1) + 1, "cu_seqlens")
+    n_slots = 0
+    if state is not None:
+        n_slots = _state_pool(state, (width - 1, channels), x.dtype, "state")
+    if slots is not None:
+        _i32_vector(slots, n_seqs, "slots")
+        if state is None:
+            raise ValueError("slots without a state pool")
+    if out is not None:
+        _out_matrix(out, T, channels, x.dtype)
+    _need_gpu(x, weight, cu_seqlens, state, slots, out)
+    if out is None:
+        out = torch.empty((T, channels), dtype=x.dtype, device=x.device)
+    st = load().nvfp4_conv_silu(_ptr(x), dtype, _ld(x), channels, _ptr(weight), width, _ptr(cu_seqlens),
+                                n_seqs if cu_seqlens is not None else 0, T, _ptr(state), _ptr(slots), n_slots,
+                                _ptr(out), _ld(out), _stream(stream))
+    _check(st, "nvfp4_conv_silu")
+    return out
+
+
+def _norm_out(rows, cols, out, out_dtype, y_gs, codes, scales, device):
+    """Destinations of a norm's y: (out, codes, scales), made where they are not given."""
+    if y_gs is not None:
+        _f32_scalars(y_gs, 1, "y_gs")
+        if cols % 16:
+            raise ValueError("columns must be a multiple of 16 to be quantized")
+        if codes is None:
+            codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=device)
+        if scales is None:
+            scales = torch.empty((rows, cols // 16), dtype=torch.uint8, device=device)
+        _u8_matrix(codes, (rows, cols // 2), "codes")
+        _u8_matrix(scales, (rows, cols // 16), "scales")
+    elif codes is not None or scales is not None:
+        raise ValueError("codes and scales need y_gs, the tensor scale")
+    if out is None and (y_gs is None or out_dtype is not None):
+        out = torch.empty((rows, cols), dtype=out_dtype or torch.bfloat16, device=device)
+    if out is not None:
+        _rows2d(out, "out")
+        _out_matrix(out, rows, cols, out_dtype or out.dtype)
+    return out, codes, scales
+
+
+def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor | None = None, scale: float = 1.0,
+                eps: float = 1e-6, residual_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                out_dtype=None, y_gs: torch.Tensor | None = None, codes: torch.Tensor | None = None,
+                scales: torch.Tensor | None = None, stream=None):
+    """t = residual + scale * x (written to residual_out if given, which may be
+    residual) and y = RMSNorm(t) * weight (float32 [cols]).  y goes to out
+    (bf16 or fp32; made in bf16 if neither out nor y_gs is given) and, with
+    y_gs, as NVFP4 codes and scales under that tensor scale.  Returns out, or
+    with y_gs (out or None, codes, scales)."""
+    x_dtype = _rows2d(x, "x")
+    rows, cols = x.shape
+    if weight.dtype != torch.float32 or weight.shape != (cols,) or not weight.is_contiguous():
+        raise ValueError("weight must be contiguous float32 [cols]")
+    r_dtype = x_dtype
+    for t, what in ((residual, "residual"), (residual_out, "residual_out")):
+        if t is not None:
+            r_dtype = _rows2d(t, what)
+            if t.shape != x.shape:
+                raise ValueError(f"{what} must have the shape of x")
+    if residual is not None and residual_out is not None and residual.dtype != residual_out.dtype:
+        raise ValueError("residual and residual_out must have the same dtype")
+    out, codes, scales = _norm_out(rows, cols, out, out_dtype, y_gs, codes, scales, x.device)
+    _need_gpu(x, weight, residual, residual_out, out, y_gs, codes, scales)
+    st = load().nvfp4_add_rmsnorm(
+        _ptr(x), x_dtype, _ld(x), _ptr(residual), r_dtype, _ld(residual) if residual is not None else 0, scale,
+        _ptr(weight), eps, rows, cols, _ptr(residual_out), _ld(residual_out) if residual_out is not None else 0,
+        _ptr(out), _DTYPE_CODE[out.dtype] if out is not None else 0, _ld(out) if out is not None else 0, _ptr(y_gs),
+        _ptr(codes), _ptr(scales), _stream(stream))
+    _check(st, "nvfp4_add_rmsnorm")
+    return out if y_gs is None else (out, codes, scales)
+
+
+def rmsnorm_gated(o: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6,
+                  out: torch.Tensor | None = None, out_dtype=None, y_gs: torch.Tensor | None = None,
+                  codes: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
+    """y = RMSNorm of each group of weight.numel() columns of o, times weight,
+    times silu(z); destinations and return value as for add_rmsnorm."""
+    o_dtype, z_dtype = _rows2d(o, "o"), _rows2d(z, "z")
+    rows, cols = o.shape
+    if weight.dtype != torch.float32 or weight.dim() != 1 or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous float32 vector")
+    if z.shape != o.shape:
+        raise ValueError("z must have the shape of o")
+    out, codes, scales = _norm_out(rows, cols, out, out_dtype, y_gs, codes, scales, o.device)
+    _need_gpu(o, z, weight, out, y_gs, codes, scales)
+    st = load().nvfp4_rmsnorm_gated(
+        _ptr(o), o_dtype, _ld(o), _ptr(z), z_dtype, _ld(z), _ptr(weight), eps, rows, cols, weight.shape[0], _ptr(out),
+        _DTYPE_CODE[out.dtype] if out is not None else 0, _ld(out) if out is not None else 0, _ptr(y_gs),
+        _ptr(codes), _ptr(scales), _stream(stream))
+    _check(st, "nvfp4_rmsnorm_gated")
+    return out if y_gs is None else (out, codes, scales)
 
 
 def quantize_gemm(x: torch.Tensor, a_gs: torch.Tensor, w_codes, w_scales, w_gs, *, out_dtype=torch.float32,

@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <climits>
+#include <cmath>
 
 #include "nvfp4_internal.h"
 
@@ -91,6 +92,46 @@ nvfp4_status_t quantize_gemm_launch(const void* x, int32_t in_dtype, int64_t ldx
   if (st != NVFP4_OK) return st;
   return hip_status(nvfp4::launch_gemm(codes, scales, a_gs, w_codes, w_scales, cs, M, N, K, y, out_bf16, ldy,
                                        (hipStream_t)stream));
+}
+
+bool in_dtype_ok(int32_t d) { return d == NVFP4_IN_F32 || d == NVFP4_IN_BF16; }
+int64_t in_size(int32_t d) { return d == NVFP4_IN_BF16 ? 2 : 4; }
+// rows of ld values of 4 bytes can be addressed with 64-bit offsets
+bool extent_ok(int64_t rows, int64_t ld) { return ld > 0 && rows <= INT64_MAX / ld / 4; }
+bool row_aligned(const void* p, int64_t ld, int64_t esize) { return aligned(p, 16) && ld * esize % 16 == 0; }
+
+// Shapes of the rows of nvfp4_gdn_prefill and nvfp4_gdn_decode.
+nvfp4_status_t gdn_rows_shape(const nvfp4::GdnRows& in, int32_t gates_dtype) {
+  constexpr int64_t kD = 128, kMaxLd = (int64_t)1 << 23;
+  if (!in_dtype_ok(gates_dtype)) return NVFP4_ERR_DTYPE;
+  if (in.ldx <= 0 || in.ldx >= kMaxLd || in.ldg <= 0 || in.ldg >= kMaxLd) return NVFP4_ERR_SHAPE;
+  if (in.n_qk < 1 || in.n_v < 1 || in.n_v > 65535 || in.n_v % in.n_qk != 0) return NVFP4_ERR_SHAPE;
+  const auto inside = [](int64_t col, int64_t width, int64_t ld) { return col >= 0 && col <= ld - width; };
+  if (!inside(in.q_col, in.n_qk * kD, in.ldx) || !inside(in.k_col, in.n_qk * kD, in.ldx) ||
+      !inside(in.v_col, in.n_v * kD, in.ldx) || !inside(in.g_col, in.n_v, in.ldg) ||
+      !inside(in.beta_col, in.n_v, in.ldg))
+    return NVFP4_ERR_SHAPE;
+  return NVFP4_OK;
+}
+
+// x, its columns and gates aligned for the kernels' loads.
+bool gdn_rows_aligned(const nvfp4::GdnRows& in, int64_t xsize) {
+  const int64_t per = 16 / xsize;
+  return row_aligned(in.x, in.ldx, xsize) && in.q_col % per == 0 && in.k_col % per == 0 && in.v_col % per == 0 &&
+         aligned(in.gates, in.gates_bf16 ? 2 : 4);
+}
+
+// Checks of a norm's destinations that nvfp4_add_rmsnorm and
+// nvfp4_rmsnorm_gated share; `quant`: codes are asked for.
+nvfp4_status_t norm_out_checks(const nvfp4::NormOut& out, int64_t rows, int64_t cols, bool& quant) {
+  quant = out.gs || out.codes || out.scales;
+  if (quant && (!out.gs || !out.codes || !out.scales)) return NVFP4_ERR_NULL;
+  if (!quant && !out.y) return NVFP4_ERR_NULL;
+  if (out.y && (out.ldy < cols || !extent_ok(rows, out.ldy))) return NVFP4_ERR_SHAPE;
+  if (quant && cols % 16 != 0) return NVFP4_ERR_SHAPE;
+  if (quant && (!aligned(out.codes, 8) || !aligned(out.gs, 4))) return NVFP4_ERR_ALIGN;
+  if (out.y && !aligned(out.y, out.y_bf16 ? 2 : 4)) return NVFP4_ERR_ALIGN;
+  return NVFP4_OK;
 }
 
 }  // namespace
@@ -340,6 +381,156 @@ nvfp4_status_t nvfp4_harmonize_fused_scales(uint8_t* scales, const float* module
     if (s0 + 4 > g0 && s0 < g1) return NVFP4_ERR_ALIAS;
     return hip_status(nvfp4::launch_harmonize(scales, module_gs, module_rows, n_modules, K, shared_gs,
                                               counters, (hipStream_t)stream));
+  } catch (...) {
+    return NVFP4_ERR_HIP;
+  }
+}
+
+nvfp4_status_t nvfp4_gdn_prefill(const void* x, int64_t ldx, int64_t q_col, int64_t k_col, int64_t v_col,
+                                 const void* gates, int32_t gates_dtype, int64_t ldg, int64_t g_col,
+                                 int64_t beta_col, const int32_t* cu_seqlens, int32_t n_seqs, int64_t T,
+                                 int32_t n_qk_heads, int32_t n_v_heads, const float* state_in, float* state_out,
+                                 const int32_t* slots, int32_t n_slots, void* o, int64_t ldo, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  try {
+    const nvfp4::GdnRows in{x,   ldx,   q_col,    k_col,      v_col,    gates, gates_dtype == NVFP4_IN_BF16,
+                            ldg, g_col, beta_col, n_qk_heads, n_v_heads};
+    const nvfp4_status_t st = gdn_rows_shape(in, gates_dtype);
+    if (st != NVFP4_OK) return st;
+    if (T < 0 || T > INT_MAX || n_seqs < 1 || n_seqs > (1 << 20) || n_slots < 0) return NVFP4_ERR_SHAPE;
+    if (ldo < (int64_t)n_v_heads * 128 || !extent_ok(T, ldo)) return NVFP4_ERR_SHAPE;
+    if ((int64_t)n_seqs * n_v_heads > (1 << 20)) return NVFP4_ERR_SHAPE;  // grid size
+    if (!cu_seqlens || (T > 0 && (!x || !gates || !o))) return NVFP4_ERR_NULL;
+    if ((T > 0 && !gdn_rows_aligned(in, 2)) || !row_aligned(o, ldo, 2) || !aligned(cu_seqlens, 4) ||
+        !aligned(state_in, 16) || !aligned(state_out, 16) || !aligned(slots, 4))
+      return NVFP4_ERR_ALIGN;
+    const size_t need = nvfp4::gdn_prefill_workspace_bytes(T, n_seqs, n_qk_heads, n_v_heads);
+    if (workspace_bytes < need) return NVFP4_ERR_WORKSPACE;
+    if (need > 0 && !workspace) return NVFP4_ERR_NULL;
+    if (need > 0 && !aligned(workspace, 256)) return NVFP4_ERR_ALIGN;
+    return hip_status(nvfp4::launch_gdn_prefill(in, cu_seqlens, n_seqs, T, state_in, state_out, slots, n_slots, o,
+                                                ldo, workspace, (hipStream_t)stream));
+  } catch (...) {
+    return NVFP4_ERR_HIP;
+  }
+}
+
+size_t nvfp4_gdn_prefill_workspace_size(int64_t T, int32_t n_seqs, int32_t n_qk_heads, int32_t n_v_heads) {
+  if (T < 0 || T > INT_MAX || n_seqs < 1 || n_seqs > (1 << 20) || n_qk_heads < 1 || n_v_heads < 1 ||
+      n_v_heads > 65535 || n_v_heads % n_qk_heads != 0)
+    return 0;
+  return nvfp4::gdn_prefill_workspace_bytes(T, n_seqs, n_qk_heads, n_v_heads);
+}
+
+nvfp4_status_t nvfp4_gdn_decode(const void* x, int32_t x_dtype, int64_t ldx, int64_t q_col, int64_t k_col,
+                                int64_t v_col, const void* gates, int32_t gates_dtype, int64_t ldg, int64_t g_col,
+                                int64_t beta_col, int64_t batch, int32_t n_qk_heads, int32_t n_v_heads,
+                                float* states, const int32_t* slots, int32_t n_slots, void* o, int32_t o_dtype,
+                                int64_t ldo, void* stream) {
+  try {
+    if (!in_dtype_ok(x_dtype) || (o_dtype != NVFP4_OUT_F32 && o_dtype != NVFP4_OUT_BF16)) return NVFP4_ERR_DTYPE;
+    const nvfp4::GdnRows in{x,   ldx,   q_col,    k_col,      v_col,    gates, gates_dtype == NVFP4_IN_BF16,
+                            ldg, g_col, beta_col, n_qk_heads, n_v_heads};
+    const nvfp4_status_t st = gdn_rows_shape(in, gates_dtype);
+    if (st != NVFP4_OK) return st;
+    if (batch < 0 || batch > (1 << 20) || batch * n_v_heads > (1 << 20) || n_slots < 0) return NVFP4_ERR_SHAPE;
+    if (ldo < (int64_t)n_v_heads * 128 || !extent_ok(batch, ldo)) return NVFP4_ERR_SHAPE;
+    if (batch == 0) return NVFP4_OK;
+    if (!x || !gates || !states || !o) return NVFP4_ERR_NULL;
+    if (!gdn_rows_aligned(in, in_size(x_dtype)) || !row_aligned(o, ldo, o_dtype == NVFP4_OUT_BF16 ? 2 : 4) ||
+        !aligned(states, 16) || !aligned(slots, 4))
+      return NVFP4_ERR_ALIGN;
+    return hip_status(nvfp4::launch_gdn_decode(in, x_dtype == NVFP4_IN_BF16, batch, states, slots, n_slots, o,
+                                               o_dtype == NVFP4_OUT_BF16, ldo, (hipStream_t)stream));
+  } catch (...) {
+    return NVFP4_ERR_HIP;
+  }
+}
+
+nvfp4_status_t nvfp4_conv_silu(const void* x, int32_t dtype, int64_t ldx, int64_t channels, const float* w,
+                               int32_t width, const int32_t* cu_seqlens, int32_t n_seqs, int64_t T, void* state,
+                               const int32_t* slots, int32_t n_slots, void* y, int64_t ldy, void* stream) {
+  try {
+    if (!in_dtype_ok(dtype)) return NVFP4_ERR_DTYPE;
+    if (width < 2 || width > 4 || channels < 1 || channels > (1 << 20) || n_slots < 0) return NVFP4_ERR_SHAPE;
+    if (T < 0 || T > (cu_seqlens ? (int64_t)INT_MAX : (int64_t)1 << 22)) return NVFP4_ERR_SHAPE;
+    if (cu_seqlens && (n_seqs < 1 || n_seqs > (1 << 20))) return NVFP4_ERR_SHAPE;
+    if (ldx < channels || ldy < channels || !extent_ok(T, ldx) || !extent_ok(T, ldy)) return NVFP4_ERR_SHAPE;
+    if (T == 0) return NVFP4_OK;
+    if (!x || !w || !y) return NVFP4_ERR_NULL;
+    const int64_t e = in_size(dtype);
+    if (!aligned(x, e) || !aligned(y, e) || !aligned(state, e) || !aligned(w, 4) || !aligned(cu_seqlens, 4) ||
+        !aligned(slots, 4))
+      return NVFP4_ERR_ALIGN;
+    // neighbouring rows are read by other threads than the ones that write them
+    const uintptr_t x0 = (uintptr_t)x, x1 = x0 + (uintptr_t)(((T - 1) * ldx + channels) * e);
+    const uintptr_t y0 = (uintptr_t)y, y1 = y0 + (uintptr_t)(((T - 1) * ldy + channels) * e);
+    if (x0 < y1 && y0 < x1) return NVFP4_ERR_ALIAS;
+    // without a pool every sequence starts at zeros and none is skipped
+    return hip_status(nvfp4::launch_conv_silu(x, dtype == NVFP4_IN_BF16, ldx, channels, w, width, cu_seqlens,
+                                              n_seqs, T, state, state ? slots : nullptr, state ? n_slots : 1, y, ldy,
+                                              (hipStream_t)stream));
+  } catch (...) {
+    return NVFP4_ERR_HIP;
+  }
+}
+
+nvfp4_status_t nvfp4_add_rmsnorm(const void* x, int32_t x_dtype, int64_t ldx, const void* residual, int32_t r_dtype,
+                                 int64_t ldr, float scale, const float* w, float eps, int64_t rows, int64_t cols,
+                                 void* residual_out, int64_t ldro, void* y, int32_t y_dtype, int64_t ldy,
+                                 const float* y_gs, uint8_t* y_codes, uint8_t* y_scales, void* stream) {
+  try {
+    if (!in_dtype_ok(x_dtype) || !in_dtype_ok(r_dtype)) return NVFP4_ERR_DTYPE;
+    if (y_dtype != NVFP4_OUT_F32 && y_dtype != NVFP4_OUT_BF16) return NVFP4_ERR_DTYPE;
+    if (rows < 0 || rows > (1 << 22) || cols < 1 || cols > nvfp4::kMaxNormCols) return NVFP4_ERR_SHAPE;
+    if (!(eps > 0.0f) || !std::isfinite(eps) || !std::isfinite(scale)) return NVFP4_ERR_SHAPE;
+    if (ldx < cols || !extent_ok(rows, ldx)) return NVFP4_ERR_SHAPE;
+    if (residual && (ldr < cols || !extent_ok(rows, ldr))) return NVFP4_ERR_SHAPE;
+    if (residual_out && (ldro < cols || !extent_ok(rows, ldro))) return NVFP4_ERR_SHAPE;
+    if (rows == 0) return NVFP4_OK;
+    if (!x || !w) return NVFP4_ERR_NULL;
+    const nvfp4::NormOut out{y, y_dtype == NVFP4_OUT_BF16, ldy, y_gs, y_codes, y_scales};
+    bool quant = false;
+    const nvfp4_status_t st = norm_out_checks(out, rows, cols, quant);
+    if (st != NVFP4_OK) return st;
+    const int64_t xe = in_size(x_dtype), re = in_size(r_dtype);
+    if (!aligned(x, xe) || !aligned(residual, re) || !aligned(residual_out, re) || !aligned(w, 4))
+      return NVFP4_ERR_ALIGN;
+    if (quant && (!row_aligned(x, ldx, xe) || (residual && !row_aligned(residual, ldr, re)) ||
+                  (residual_out && !row_aligned(residual_out, ldro, re)) ||
+                  (y && !row_aligned(y, ldy, out.y_bf16 ? 2 : 4)) || !aligned(w, 16)))
+      return NVFP4_ERR_ALIGN;
+    return hip_status(nvfp4::launch_add_rmsnorm(x, x_dtype == NVFP4_IN_BF16, ldx, residual,
+                                                r_dtype == NVFP4_IN_BF16, ldr, scale, w, eps, rows, cols,
+                                                residual_out, ldro, out, (hipStream_t)stream));
+  } catch (...) {
+    return NVFP4_ERR_HIP;
+  }
+}
+
+nvfp4_status_t nvfp4_rmsnorm_gated(const void* o, int32_t o_dtype, int64_t ldo, const void* z, int32_t z_dtype,
+                                   int64_t ldz, const float* w, float eps, int64_t rows, int64_t cols, int32_t group,
+                                   void* y, int32_t y_dtype, int64_t ldy, const float* y_gs, uint8_t* y_codes,
+                                   uint8_t* y_scales, void* stream) {
+  try {
+    if (!in_dtype_ok(o_dtype) || !in_dtype_ok(z_dtype)) return NVFP4_ERR_DTYPE;
+    if (y_dtype != NVFP4_OUT_F32 && y_dtype != NVFP4_OUT_BF16) return NVFP4_ERR_DTYPE;
+    if (group < 16 || group > 1024 || (group & (group - 1)) != 0) return NVFP4_ERR_SHAPE;
+    if (rows < 0 || cols < 1 || cols % group != 0 || cols > INT_MAX || ldo < cols || ldz < cols)
+      return NVFP4_ERR_SHAPE;
+    if (rows >= ((int64_t)1 << 35) / cols || !extent_ok(rows, ldo) || !extent_ok(rows, ldz)) return NVFP4_ERR_SHAPE;
+    if (!(eps > 0.0f) || !std::isfinite(eps)) return NVFP4_ERR_SHAPE;
+    if (rows == 0) return NVFP4_OK;
+    if (!o || !z || !w) return NVFP4_ERR_NULL;
+    const nvfp4::NormOut out{y, y_dtype == NVFP4_OUT_BF16, ldy, y_gs, y_codes, y_scales};
+    bool quant = false;
+    const nvfp4_status_t st = norm_out_checks(out, rows, cols, quant);
+    if (st != NVFP4_OK) return st;
+    if (!row_aligned(o, ldo, in_size(o_dtype)) || !row_aligned(z, ldz, in_size(z_dtype)) || !aligned(w, 16) ||
+        (y && !row_aligned(y, ldy, out.y_bf16 ? 2 : 4)))
+      return NVFP4_ERR_ALIGN;
+    return hip_status(nvfp4::launch_rmsnorm_gated(o, o_dtype == NVFP4_IN_BF16, ldo, z, z_dtype == NVFP4_IN_BF16, ldz,
+                                                  w, eps, rows, cols, group, out, (hipStream_t)stream));
   } catch (...) {
     return NVFP4_ERR_HIP;
   }

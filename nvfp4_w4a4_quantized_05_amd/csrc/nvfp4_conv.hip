@@ -1,0 +1,244 @@
+// Short causal convolution per channel, with SiLU, over packed sequences or
+// one row for each of many requests:
+//
+//   y_t = silu(sum_{i < W} w[c][i] x_{t - W + 1 + i}),  silu(v) = v / (1 + exp(-v))
+//
+// where the rows before a sequence's first are the last W - 1 inputs of its
+// request, kept oldest first in a slot of the state pool (zeros without a
+// pool), and the slot gets the sequence's own last W - 1 inputs.  Sums are
+// fp32 in tap order; x, y and the pool are bf16 or fp32.
+//
+// HBM-bound (2 values moved for 2 W + 4 flops).  Packed form: a lane owns
+// kVec neighbouring channels and walks kRows rows with the last W - 1 inputs
+// in registers, so a row is read once but for the W - 1 rows above a tile.
+// The tile that holds a sequence's first row also takes every row whose
+// window reaches into the pool's slot (W - 1 rows, also past the tile's end)
+// and updates the slot: one thread reads and writes each value of it.
+#include "nvfp4_device.h"
+#include "nvfp4_internal.h"
+
+namespace nvfp4 {
+namespace {
+
+template <bool kBf16, int kVec>
+struct Row {
+  float v[kVec];
+  __device__ __forceinline__ void load(const void* base, int64_t at) {
+    if constexpr (kVec == 1) {
+      if constexpr (kBf16)
+        v[0] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(base)[at] << 16);
+      else
+        v[0] = reinterpret_cast<const float*>(base)[at];
+    } else if constexpr (kBf16) {
+      const u32x4_t a = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint16_t*>(base) + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(a[i] << 16);
+        v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const floatx4_t a = *reinterpret_cast<const floatx4_t*>(reinterpret_cast<const float*>(base) + at + 4 * i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * i + e] = a[e];
+      }
+    }
+  }
+  __device__ __forceinline__ void store(void* base, int64_t at) const {
+    if constexpr (kVec == 1) {
+      if constexpr (kBf16)
+        reinterpret_cast<uint16_t*>(base)[at] = (uint16_t)pack_bf16(v[0], 0.0f);
+      else
+        reinterpret_cast<float*>(base)[at] = v[0];
+    } else if constexpr (kBf16) {
+      u32x4_t a;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+      __builtin_nontemporal_store(a, reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(base) + at));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        floatx4_t a;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] = v[4 * i + e];
+        __builtin_nontemporal_store(a, reinterpret_cast<floatx4_t*>(reinterpret_cast<float*>(base) + at + 4 * i));
+      }
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) v[e] = 0.0f;
+  }
+};
+
+// y of one row from its window (win[W - 1] is the row itself).
+template <bool kBf16, int kVec, int kW>
+__device__ __forceinline__ Row<kBf16, kVec> conv_row(const Row<kBf16, kVec> (&win)[kW], const float (&w)[kVec][kW]) {
+  Row<kBf16, kVec> y;
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kW; ++i) s = fmaf(w[e][i], win[i].v[e], s);
+    y.v[e] = silu(s);
+  }
+  return y;
+}
+
+template <int kVec, int kW>
+__device__ __forceinline__ void load_weights(const float* w, int64_t c, float (&out)[kVec][kW]) {
+#pragma unroll
+  for (int e = 0; e < kVec; ++e)
+#pragma unroll
+    for (int i = 0; i < kW; ++i) out[e][i] = w[(c + e) * kW + i];
+}
+
+constexpr int kConvThreads = 256;
+
+// Packed sequences: grid (row tiles of `rows`, channel blocks).
+template <bool kBf16, int kVec, int kW>
+__global__ __launch_bounds__(kConvThreads) void conv_silu_kernel(
+    const void* __restrict__ x, int64_t ldx, int64_t channels, const float* __restrict__ w, const int32_t* __restrict__ cu,
+    int n_seqs, int64_t T, void* state, const int32_t* __restrict__ slots, int n_slots, void* __restrict__ y,
+    int64_t ldy, int rows) {
+  using R = Row<kBf16, kVec>;
+  const int64_t c = ((int64_t)blockIdx.y * kConvThreads + threadIdx.x) * kVec;
+  if (c >= channels) return;
+  const int64_t t0 = (int64_t)blockIdx.x * rows;
+  const int64_t t1 = min(t0 + rows, T);
+  float wt[kVec][kW];
+  load_weights<kVec, kW>(w, c, wt);
+
+  // the sequences that have a row in [t0, t1): from the last one that starts at or before t0
+  int lo = 0, hi = n_seqs;
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (cu[mid + 1] > t0) hi = mid; else lo = mid + 1;
+  }
+  for (int s = lo; s < n_seqs; ++s) {
+    const int64_t start = cu[s], end = min((int64_t)cu[s + 1], T);
+    if (start >= t1) break;
+    if (end <= start || start < 0) continue;
+    const bool mine = start >= t0;  // this tile holds the first row
+    int64_t t = mine ? start : max(t0, min(start + kW - 1, end));
+    const int64_t stop = mine ? min(end, max(t1, start + kW - 1)) : min(end, t1);
+    if (t >= stop) continue;
+    const int slot = state ? (slots ? slots[s] : s) : 0;
+    if (slot < 0 || slot >= n_slots) {  // a skipped sequence: zeros
+      R z;
+      z.zero();
+      for (; t < stop; ++t) z.store(y, t * ldy + c);
+      continue;
+    }
+    R win[kW];
+    if (mine) {
+      R old[kW - 1];
+#pragma unroll
+      for (int i = 0; i < kW - 1; ++i) {
+        if (state) old[i].load(state, ((int64_t)slot * (kW - 1) + i) * channels + c); else old[i].zero();
+        win[i] = old[i];
+      }
+      if (state) {  // the last W - 1 inputs of [old; this sequence]
+        const int64_t len = end - start;
+#pragma unroll
+        for (int i = 0; i < kW - 1; ++i) {
+          const int64_t r = len - (kW - 1) + i;
+          R nw;
+          if (r >= 0) {
+            nw.load(x, (start + r) * ldx + c);
+          } else {
+            nw = old[0];
+#pragma unroll
+            for (int j = 1; j < kW - 1; ++j)
+              if (j == len + i) nw = old[j];
+          }
+          nw.store(state, ((int64_t)slot * (kW - 1) + i) * channels + c);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kW - 1; ++i) win[i].load(x, (t - (kW - 1) + i) * ldx + c);
+    }
+    for (; t < stop; ++t) {
+      win[kW - 1].load(x, t * ldx + c);
+      conv_row<kBf16, kVec, kW>(win, wt).store(y, t * ldy + c);
+#pragma unroll
+      for (int i = 0; i < kW - 1; ++i) win[i] = win[i + 1];
+    }
+  }
+}
+
+// One row for each request: grid (requests, channel blocks).
+template <bool kBf16, int kVec, int kW>
+__global__ __launch_bounds__(kConvThreads) void conv_silu_step_kernel(
+    const void* __restrict__ x, int64_t ldx, int64_t channels, const float* __restrict__ w, void* state,
+    const int32_t* __restrict__ slots, int n_slots, void* __restrict__ y, int64_t ldy) {
+  using R = Row<kBf16, kVec>;
+  const int64_t c = ((int64_t)blockIdx.y * kConvThreads + threadIdx.x) * kVec;
+  if (c >= channels) return;
+  const int64_t b = blockIdx.x;
+  const int slot = state ? (slots ? slots[b] : (int)b) : 0;
+  if (slot < 0 || slot >= n_slots) {
+    R z;
+    z.zero();
+    z.store(y, b * ldy + c);
+    return;
+  }
+  float wt[kVec][kW];
+  load_weights<kVec, kW>(w, c, wt);
+  R win[kW];
+  win[kW - 1].load(x, b * ldx + c);
+#pragma unroll
+  for (int i = 0; i < kW - 1; ++i) {
+    if (state) win[i].load(state, ((int64_t)slot * (kW - 1) + i) * channels + c); else win[i].zero();
+  }
+  conv_row<kBf16, kVec, kW>(win, wt).store(y, b * ldy + c);
+  if (state) {
+#pragma unroll
+    for (int i = 0; i < kW - 1; ++i) win[i + 1].store(state, ((int64_t)slot * (kW - 1) + i) * channels + c);
+  }
+}
+
+template <bool kBf16, int kVec, int kW>
+hipError_t launch_conv_typed(const void* x, int64_t ldx, int64_t channels, const float* w, const int32_t* cu,
+                             int n_seqs, int64_t T, void* state, const int32_t* slots, int n_slots, void* y,
+                             int64_t ldy, hipStream_t stream) {
+  const unsigned blocks = (unsigned)((channels + kConvThreads * kVec - 1) / (kConvThreads * kVec));
+  if (cu) {
+    const int rows = 64;
+    const dim3 grid((unsigned)((T + rows - 1) / rows), blocks);
+    conv_silu_kernel<kBf16, kVec, kW><<<grid, kConvThreads, 0, stream>>>(x, ldx, channels, w, cu, n_seqs, T, state,
+                                                                         slots, n_slots, y, ldy, rows);
+  } else {
+    const dim3 grid((unsigned)T, blocks);
+    conv_silu_step_kernel<kBf16, kVec, kW><<<grid, kConvThreads, 0, stream>>>(x, ldx, channels, w, state, slots,
+                                                                              n_slots, y, ldy);
+  }
+  return hipGetLastError();
+}
+
+template <bool kBf16, int kVec>
+hipError_t launch_conv_width(int width, const void* x, int64_t ldx, int64_t channels, const float* w,
+                             const int32_t* cu, int n_seqs, int64_t T, void* state, const int32_t* slots,
+                             int n_slots, void* y, int64_t ldy, hipStream_t stream) {
+  const auto f = width == 2   ? launch_conv_typed<kBf16, kVec, 2>
+                 : width == 3 ? launch_conv_typed<kBf16, kVec, 3>
+                              : launch_conv_typed<kBf16, kVec, 4>;
+  return f(x, ldx, channels, w, cu, n_seqs, T, state, slots, n_slots, y, ldy, stream);
+}
+
+}  // namespace
+
+hipError_t launch_conv_silu(const void* x, bool bf16, int64_t ldx, int64_t channels, const float* w, int width,
+                            const int32_t* cu, int n_seqs, int64_t T, void* state, const int32_t* slots, int n_slots,
+                            void* y, int64_t ldy, hipStream_t stream) {
+  const int64_t e = bf16 ? 2 : 4;
+  const bool vec = channels % 8 == 0 && (uintptr_t)x % 16 == 0 && ldx * e % 16 == 0 && (uintptr_t)y % 16 == 0 &&
+                   ldy * e % 16 == 0 && (uintptr_t)state % 16 == 0;
+  const auto f = bf16 ? (vec ? launch_conv_width<true, 8> : launch_conv_width<true, 1>)
+                      : (vec ? launch_conv_width<false, 8> : launch_conv_width<false, 1>);
+  return f(width, x, ldx, channels, w, cu, n_seqs, T, state, slots, n_slots, y, ldy, stream);
+}
+
+}  // namespace nvfp4

@@ -41,4 +41,31 @@ __device__ __forceinline__ float tensor_scale_from_amax(float amax) {
   return g == 0.0f ? 1.0f : g;
 }
 
+// Two fp32 values as bf16, round-to-nearest-even, a in the low half (NaN stays NaN).
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float float2v_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  float2v_t f;
+  f[0] = a;
+  f[1] = b;
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2_t));
+}
+
+// silu(z) = z / (1 + exp(-z)) with the hardware exp2 and reciprocal.  Both
+// terms of the denominator carry a factor 2^-24, and so does z: with it the
+// reciprocal stays a normal number down to results of 2^-126 (the hardware
+// flushes subnormal reciprocals), at no more than one multiply.
+__device__ __forceinline__ float silu(float z) {
+  const float e = __builtin_amdgcn_exp2f(fmaf(-1.44269504088896340736f, z, -24.0f));
+  return (z * 0x1p-24f) * __builtin_amdgcn_rcpf(e + 0x1p-24f);
+}
+
+// Sum over the wave's 64 lanes, the same bits in every lane: each step adds
+// the same two values in either order.
+__device__ __forceinline__ float wave_sum64(float v) {
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
+  return v;
+}
+
 }  // namespace nvfp4

@@ -109,4 +109,55 @@ hipError_t launch_gdn_recurrence(const float* x, int64_t ldx, int64_t q_col, int
 // NULL ([n_v x 128 x 128] fp32; s_in may equal s_out).
 hipError_t launch_gdn_start_state(const float* s_in, float* s_out, int n_v, hipStream_t stream);
 
+// Where the rows of a Gated DeltaNet call lie: q, k (n_qk heads) and v (n_v
+// heads of 128) at columns of x, log-decay gates and write strengths (n_v
+// each) at columns of gates, one row per token.
+struct GdnRows {
+  const void* x;
+  int64_t ldx, q_col, k_col, v_col;
+  const void* gates;
+  bool gates_bf16;
+  int64_t ldg, g_col, beta_col;
+  int n_qk, n_v;
+};
+
+// One token for each of `batch` requests; the request's state slot is
+// updated in place.  Arguments as nvfp4_gdn_decode, already checked.
+hipError_t launch_gdn_decode(const GdnRows& in, bool x_bf16, int64_t batch, float* states, const int32_t* slots,
+                             int n_slots, void* o, bool o_bf16, int64_t ldo, hipStream_t stream);
+
+// Packed prompts (bf16 rows); arguments as nvfp4_gdn_prefill, already
+// checked; workspace of gdn_prefill_workspace_bytes().
+size_t gdn_prefill_workspace_bytes(int64_t T, int64_t n_seqs, int n_qk, int n_v);
+hipError_t launch_gdn_prefill(const GdnRows& in, const int32_t* cu, int n_seqs, int64_t T, const float* s_in,
+                              float* s_out, const int32_t* slots, int n_slots, void* o, int64_t ldo, void* workspace,
+                              hipStream_t stream);
+
+// Causal convolution + SiLU; cu NULL: one row per request.  Arguments as
+// nvfp4_conv_silu, already checked.
+hipError_t launch_conv_silu(const void* x, bool bf16, int64_t ldx, int64_t channels, const float* w, int width,
+                            const int32_t* cu, int n_seqs, int64_t T, void* state, const int32_t* slots, int n_slots,
+                            void* y, int64_t ldy, hipStream_t stream);
+
+// Where a norm's y goes: values (bf16 or fp32) if y, NVFP4 codes and block
+// scales under tensor scale *gs if codes.
+struct NormOut {
+  void* y;
+  bool y_bf16;
+  int64_t ldy;
+  const float* gs;
+  uint8_t* codes;
+  uint8_t* scales;
+};
+
+// Columns of an add_rmsnorm row: one workgroup holds it, 16 values per lane.
+constexpr int64_t kMaxNormCols = 16384;
+
+hipError_t launch_add_rmsnorm(const void* x, bool x_bf16, int64_t ldx, const void* residual, bool r_bf16,
+                              int64_t ldr, float scale, const float* w, float eps, int64_t rows, int64_t cols,
+                              void* sum, int64_t lds, const NormOut& out, hipStream_t stream);
+hipError_t launch_rmsnorm_gated(const void* o, bool o_bf16, int64_t ldo, const void* z, bool z_bf16, int64_t ldz,
+                                const float* w, float eps, int64_t rows, int64_t cols, int group,
+                                const NormOut& out, hipStream_t stream);
+
 }  // namespace nvfp4

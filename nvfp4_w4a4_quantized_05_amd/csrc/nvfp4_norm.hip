@@ -1,0 +1,258 @@
+// The norms around a block, fused with what stands next to them.
+//
+//   add_rmsnorm    t = residual + scale x;  y = t / sqrt(mean(t^2) + eps) w
+//   rmsnorm_gated  per group of a row: y = o / sqrt(mean(o^2) + eps) w silu(z),
+//                  silu(z) = z / (1 + exp(-z))
+//
+// t goes out in the residual's type; y goes out in bf16 or fp32, or as NVFP4
+// codes and block scales under a given tensor scale (what the projection that
+// follows reads), or as both.  Everything between the loads and those stores
+// is fp32: t is not rounded before its norm, y not before it is quantized.
+//
+// Both are HBM-bound: one pass, every value held in registers between its
+// load and its stores.  A lane owns chunks of 16 consecutive values (one
+// NVFP4 block, so quantize_block needs no exchange between lanes).
+#include "nvfp4_device.h"
+#include "nvfp4_internal.h"
+#include "nvfp4_quant_block.h"
+
+namespace nvfp4 {
+namespace {
+
+// 16 values from p (16-byte aligned), bf16 or fp32.
+template <bool kBf16>
+__device__ __forceinline__ void load16(const void* base, int64_t at, float v[16]) {
+  if constexpr (kBf16) {
+    const u32x4_t* p = reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint16_t*>(base) + at);
+    const u32x4_t a = __builtin_nontemporal_load(p), b = __builtin_nontemporal_load(p + 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(a[i] << 16);
+      v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+      v[8 + 2 * i] = __uint_as_float(b[i] << 16);
+      v[9 + 2 * i] = __uint_as_float(b[i] & 0xFFFF0000u);
+    }
+  } else {
+    const floatx4_t* p = reinterpret_cast<const floatx4_t*>(reinterpret_cast<const float*>(base) + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const floatx4_t t = __builtin_nontemporal_load(p + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * i + e] = t[e];
+    }
+  }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void store16(void* base, int64_t at, const float v[16]) {
+  if constexpr (kBf16) {
+    u32x4_t a, b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+      b[i] = pack_bf16(v[8 + 2 * i], v[9 + 2 * i]);
+    }
+    u32x4_t* p = reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(base) + at);
+    __builtin_nontemporal_store(a, p);
+    __builtin_nontemporal_store(b, p + 1);
+  } else {
+    floatx4_t* p = reinterpret_cast<floatx4_t*>(reinterpret_cast<float*>(base) + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      floatx4_t t;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[e] = v[4 * i + e];
+      __builtin_nontemporal_store(t, p + i);
+    }
+  }
+}
+
+__device__ __forceinline__ void load_weight16(const float* w, int64_t at, float v[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const floatx4_t t = *reinterpret_cast<const floatx4_t*>(w + at + 4 * i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[4 * i + e] = t[e];
+  }
+}
+
+// y's destinations: values (or NULL) and NVFP4 codes with block scales (or NULL).
+__device__ __forceinline__ void store_y(const NormOut& out, int64_t row, int64_t col, int64_t cols,
+                                        const float y[16], float g, float r6) {
+  if (out.y) {
+    if (out.y_bf16)
+      store16<true>(out.y, row * out.ldy + col, y);
+    else
+      store16<false>(out.y, row * out.ldy + col, y);
+  }
+  if (out.codes) {
+    uint32_t w0, w1;
+    const uint32_t s = quantize_block(y, g, r6, w0, w1);
+    const int64_t b = (row * cols + col) / kBlock;
+    u32x2_t c;
+    c[0] = w0;
+    c[1] = w1;
+    __builtin_nontemporal_store(c, reinterpret_cast<u32x2_t*>(out.codes) + b);
+    __builtin_nontemporal_store((uint8_t)s, out.scales + b);
+  }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ float load_one(const void* p, int64_t at) {
+  if constexpr (kBf16) return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[at] << 16);
+  return reinterpret_cast<const float*>(p)[at];
+}
+__device__ __forceinline__ void store_one(void* p, bool bf16, int64_t at, float v) {
+  if (bf16)
+    reinterpret_cast<uint16_t*>(p)[at] = (uint16_t)pack_bf16(v, 0.0f);
+  else
+    reinterpret_cast<float*>(p)[at] = v;
+}
+
+// One workgroup (blockDim.x threads, whole waves) per row, kChunks x 16 values per lane.
+// kVec: lane l's chunk c is the 16 consecutive values from (c * threads + l) * 16.  Otherwise
+// (columns, strides or pointers that 16-byte loads cannot take) its value e is column
+// (16 c + e) * threads + l, so that a wave's loads still cover consecutive addresses.
+template <bool kXBf16, bool kRBf16, bool kVec, int kChunks>
+__global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const void* x, int64_t ldx, const void* residual,
+                                                           int64_t ldr, float scale, const float* __restrict__ w,
+                                                           float eps, int64_t cols, void* sum, int64_t lds,
+                                                           NormOut out) {
+  const int64_t row = blockIdx.x;
+  const int threads = blockDim.x, tid = threadIdx.x;
+  const int64_t chunks = cols / 16;
+  float t[kChunks][16];
+  float ss = 0.0f;
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    if constexpr (kVec) {
+      const int64_t at = (int64_t)c * threads + tid;
+      if (at < chunks) {
+        load16<kXBf16>(x, row * ldx + at * 16, t[c]);
+        if (residual) {
+          float r[16];
+          load16<kRBf16>(residual, row * ldr + at * 16, r);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) t[c][e] = fmaf(scale, t[c][e], r[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) t[c][e] *= scale;
+        }
+        if (sum) store16<kRBf16>(sum, row * lds + at * 16, t[c]);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) ss = fmaf(t[c][e], t[c][e], ss);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int64_t col = (int64_t)(16 * c + e) * threads + tid;
+        if (col < cols) {
+          const float r = residual ? load_one<kRBf16>(residual, row * ldr + col) : 0.0f;
+          t[c][e] = fmaf(scale, load_one<kXBf16>(x, row * ldx + col), r);
+          if (sum) store_one(sum, kRBf16, row * lds + col, t[c][e]);
+          ss = fmaf(t[c][e], t[c][e], ss);
+        }
+      }
+    }
+  }
+  __shared__ float part[16];
+  ss = wave_sum64(ss);
+  if (threads > 64) {
+    if ((tid & 63) == 0) part[tid >> 6] = ss;
+    __syncthreads();
+    ss = 0.0f;
+    for (int i = 0; i < threads / 64; ++i) ss += part[i];
+  }
+  const float rms = 1.0f / sqrtf(ss / (float)cols + eps);
+  const float g = out.codes ? *out.gs : 1.0f, r6 = __builtin_amdgcn_rcpf(6.0f * g);
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    if constexpr (kVec) {
+      const int64_t at = (int64_t)c * threads + tid;
+      if (at < chunks) {
+        float wv[16];
+        load_weight16(w, at * 16, wv);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) t[c][e] = t[c][e] * rms * wv[e];
+        store_y(out, row, at * 16, cols, t[c], g, r6);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int64_t col = (int64_t)(16 * c + e) * threads + tid;
+        if (col < cols) store_one(out.y, out.y_bf16, row * out.ldy + col, t[c][e] * rms * w[col]);
+      }
+    }
+  }
+}
+
+// One lane per 16 values; the group's lanes (group / 16, a power of two up to 64) are consecutive
+// and add their squares with lane exchanges.
+template <bool kOBf16, bool kZBf16>
+__global__ __launch_bounds__(256) void rmsnorm_gated_kernel(const void* __restrict__ o, int64_t ldo,
+                                                            const void* __restrict__ z, int64_t ldz,
+                                                            const float* __restrict__ w, float eps, int64_t rows,
+                                                            int64_t cols, int group, NormOut out) {
+  const int64_t chunks = cols / 16;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = i / chunks, col = (i - row * chunks) * 16;
+  // whole groups are past the end together: chunks is a multiple of the group's lanes
+  const bool live = row < rows;
+  float ov[16], zv[16], ss = 0.0f;
+  if (live) {
+    load16<kOBf16>(o, row * ldo + col, ov);
+    load16<kZBf16>(z, row * ldz + col, zv);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) ss = fmaf(ov[e], ov[e], ss);
+  }
+  for (int m = 1; m < group / 16; m <<= 1) ss += __shfl_xor(ss, m, 64);
+  if (!live) return;
+  const float rms = 1.0f / sqrtf(ss / (float)group + eps);
+  float wv[16];
+  load_weight16(w, col & (group - 1), wv);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) ov[e] = ov[e] * rms * wv[e] * silu(zv[e]);
+  const float g = out.codes ? *out.gs : 1.0f;
+  store_y(out, row, col, cols, ov, g, __builtin_amdgcn_rcpf(6.0f * g));
+}
+
+template <bool kXBf16, bool kRBf16>
+hipError_t launch_add_typed(bool vec, const void* x, int64_t ldx, const void* residual, int64_t ldr, float scale,
+                            const float* w, float eps, int64_t rows, int64_t cols, void* sum, int64_t lds,
+                            const NormOut& out, hipStream_t stream) {
+  const unsigned threads = (unsigned)((cols + 16 * 64 - 1) / (16 * 64) * 64);
+#define NVFP4_ADD_NORM(V, C)                                                                                   \
+  add_rmsnorm_kernel<kXBf16, kRBf16, V, C><<<(unsigned)rows, threads, 0, stream>>>(x, ldx, residual, ldr, scale, w, \
+                                                                                   eps, cols, sum, lds, out)
+  if (vec) NVFP4_ADD_NORM(true, 1);
+  else NVFP4_ADD_NORM(false, 1);
+#undef NVFP4_ADD_NORM
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_add_rmsnorm(const void* x, bool x_bf16, int64_t ldx, const void* residual, bool r_bf16,
+                              int64_t ldr, float scale, const float* w, float eps, int64_t rows, int64_t cols,
+                              void* sum, int64_t lds, const NormOut& out, hipStream_t stream) {
+  const auto fits = [](const void* p, int64_t ld, bool bf16) {
+    return !p || ((uintptr_t)p % 16 == 0 && ld * (bf16 ? 2 : 4) % 16 == 0);
+  };
+  const bool vec = cols % 16 == 0 && fits(x, ldx, x_bf16) && fits(residual, ldr, r_bf16) && fits(sum, lds, r_bf16) &&
+                   fits(out.y, out.ldy, out.y_bf16) && (uintptr_t)w % 16 == 0;
+  const auto f = x_bf16 ? (r_bf16 ? launch_add_typed<true, true> : launch_add_typed<true, false>)
+                        : (r_bf16 ? launch_add_typed<false, true> : launch_add_typed<false, false>);
+  return f(vec, x, ldx, residual, ldr, scale, w, eps, rows, cols, sum, lds, out, stream);
+}
+
+hipError_t launch_rmsnorm_gated(const void* o, bool o_bf16, int64_t ldo, const void* z, bool z_bf16, int64_t ldz,
+                                const float* w, float eps, int64_t rows, int64_t cols, int group,
+                                const NormOut& out, hipStream_t stream) {
+  const unsigned grid = (unsigned)((rows * (cols / 16) + 255) / 256);
+  const auto f = o_bf16 ? (z_bf16 ? rmsnorm_gated_kernel<true, true> : rmsnorm_gated_kernel<true, false>)
+                        : (z_bf16 ? rmsnorm_gated_kernel<false, true> : rmsnorm_gated_kernel<false, false>);
+  f<<<grid, 256, 0, stream>>>(o, ldo, z, ldz, w, eps, rows, cols, group, out);
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4
