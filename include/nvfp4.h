@@ -437,8 +437,9 @@ NVFP4_API nvfp4_status_t nvfp4_harmonize_fused_scales(uint8_t* scales, const flo
  *               the log-decay gates g at g_col and the write strengths beta
  *               at beta_col, n_v_heads columns each (the layout
  *               nvfp4_gemm_segmented_gates writes); ldg < 2^23
- *   cu_seqlens, n_seqs   as above, 1 <= n_seqs <= 2^20
- *   T           rows of x, gates and o, 0 <= T <= INT_MAX
+ *   cu_seqlens, n_seqs   as above, n_seqs >= 1, n_seqs * n_v_heads <= 2^20
+ *   T           rows of x, gates and o, 0 <= T <= INT_MAX and
+ *               (T / 64 + n_seqs + 1) * n_qk_heads < 2^24
  *   n_qk_heads, n_v_heads   as for nvfp4_gdn_recurrence
  *   state_in    device fp32 [n_slots x n_v_heads x 128 x 128] (d_k row
  *               major), 16-byte aligned, or NULL: every sequence starts at
@@ -448,7 +449,7 @@ NVFP4_API nvfp4_status_t nvfp4_harmonize_fused_scales(uint8_t* scales, const flo
  *               state_in itself
  *   slots, n_slots   as above
  *   o           device out, bf16 [T x ldo], head h at columns 128 h; 16-byte
- *               aligned, ldo a multiple of 8, ldo >= 128 n_v_heads
+ *               aligned, ldo a multiple of 8, 128 n_v_heads <= ldo < 2^23
  *   workspace   device scratch, 256-byte aligned, of at least
  *               nvfp4_gdn_prefill_workspace_size() bytes, overwritten
  * Gates are expected non-positive and write strengths in [0, 1] (then the

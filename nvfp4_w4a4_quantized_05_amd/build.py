@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libnvfp4.so")
 SOURCES = ["nvfp4_quantize.hip", "nvfp4_gemm.hip", "nvfp4_harmonize.hip", "nvfp4_gdn.hip", "nvfp4_noalloc.hip",
-           "nvfp4_gdn_serve.hip", "nvfp4_conv.hip", "nvfp4_norm.hip", "nvfp4_api.cpp"]
+           "nvfp4_gdn_serve.hip", "nvfp4_gdn_chunk.hip", "nvfp4_conv.hip", "nvfp4_norm.hip", "nvfp4_api.cpp"]
 ARCH = "gfx950"
 
 # Packed fp32 ops are disabled on purpose: the compiler must not form

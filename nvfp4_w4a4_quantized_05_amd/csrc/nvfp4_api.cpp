@@ -398,8 +398,10 @@ nvfp4_status_t nvfp4_gdn_prefill(const void* x, int64_t ldx, int64_t q_col, int6
     const nvfp4_status_t st = gdn_rows_shape(in, gates_dtype);
     if (st != NVFP4_OK) return st;
     if (T < 0 || T > INT_MAX || n_seqs < 1 || n_seqs > (1 << 20) || n_slots < 0) return NVFP4_ERR_SHAPE;
-    if (ldo < (int64_t)n_v_heads * 128 || !extent_ok(T, ldo)) return NVFP4_ERR_SHAPE;
-    if ((int64_t)n_seqs * n_v_heads > (1 << 20)) return NVFP4_ERR_SHAPE;  // grid size
+    if (ldo < (int64_t)n_v_heads * 128 || ldo >= ((int64_t)1 << 23)) return NVFP4_ERR_SHAPE;
+    // grid sizes (threads below 2^32)
+    if ((int64_t)n_seqs * n_v_heads > (1 << 20) || (T / 64 + n_seqs + 1) * n_qk_heads >= (1 << 24))
+      return NVFP4_ERR_SHAPE;
     if (!cu_seqlens || (T > 0 && (!x || !gates || !o))) return NVFP4_ERR_NULL;
     if ((T > 0 && !gdn_rows_aligned(in, 2)) || !row_aligned(o, ldo, 2) || !aligned(cu_seqlens, 4) ||
         !aligned(state_in, 16) || !aligned(state_out, 16) || !aligned(slots, 4))

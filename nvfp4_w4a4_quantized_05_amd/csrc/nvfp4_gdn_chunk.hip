@@ -1,0 +1,613 @@
+// Gated DeltaNet over packed prompts, 64 tokens at a time on the matrix cores.
+//
+// The recurrence (per value head, S [d_k x d_v] = [128 x 128], |q| = |k| = 1)
+//     w_t = beta_t (v_t - S_{t-1}^T k_t),  S_t = alpha_t S_{t-1} + k_t w_t^T,
+//     o_t = S_t^T q_t / sqrt(128),         alpha_t = exp(g_t)
+// is linear in S, so a chunk of C = 64 tokens can be written out.  With G_i the
+// sum of the chunk's g up to token i, B_i = G_i - g_i the sum before it, and S
+// the state at its start, S_{i-1} = e^{B_i} S + sum_{j<i} e^{B_i - G_j} k_j w_j^T, so
+//     w_i + beta_i sum_{j<i} e^{B_i - G_j} (k_i . k_j) w_j = beta_i (v_i - e^{B_i} S^T k_i).
+// With A_ij = beta_i e^{B_i - G_j} (k_i . k_j) for j < i and T = (I + A)^-1 diag(beta):
+//     W  = T (V - diag(e^B) K S)                                    (64 x 128)
+//     O  = (diag(e^G) Q S + P W) / sqrt(128),  P_ij = e^{G_i - G_j} (q_i . k_j), j <= i
+//     S' = e^{G_C} S + K^T diag(e^{G_C - G_j}) W
+// T and P do not depend on S.  One kernel makes them for every chunk at once;
+// a second one walks the chunks of each sequence with S in registers.
+//
+// Precision.  q, k and v are bf16, so every product of two of them is exact in
+// the matrix cores.  S, T, V - ... and W are fp32 and enter as the sum of three
+// bf16 numbers (8 + 8 + 8 bits: exact), with the six largest of the nine
+// products where both sides are split: the state is as exact as an fp32 sum.
+// For O alone, whose result is bf16, S, P and W are rounded to bf16 once.
+// Decays inside a chunk are exponentials of differences of G, which is summed
+// in fp64 and kept as two floats, so that a strong decay before both tokens
+// does not cost the difference its digits.
+#include "nvfp4_device.h"
+#include "nvfp4_internal.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kD = 128;        // head dimension
+constexpr int kC = 64;         // tokens per chunk
+constexpr float kNormEps = 1e-6f;
+constexpr float kRsqrtD = 0.08838834764831845f;  // 1 / sqrt(128)
+// exp of less is 0 in fp32; keeps differences of G finite for alpha = 0
+constexpr float kMinGate = -200.0f;
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef short shortx4_t __attribute__((ext_vector_type(4)));
+
+// What the first kernel leaves for a chunk and value head, in the order the
+// second one's lanes read it.  A 64 x 64 lower triangular matrix is kept as
+// matrix-core A operands of 16 rows x 32 columns: rows 16 w .. + 15, columns
+// 32 s .. + 31, s <= w / 2, a lane's eight columns being 32 s + 4 g + {0..3}
+// and 32 s + 16 + 4 g + {0..3} (g = lane / 16): the order in which two
+// 16 x 16 results lie in the lanes, so that results are operands as they are.
+constexpr int kOperand = 1024;                     // bytes: 64 lanes x 8 bf16
+constexpr int kBlocks = 6;                         // (w, s) with s <= w / 2
+constexpr int kOffP = 3 * kBlocks * kOperand;      // after T's three terms
+constexpr int kOffVec = kOffP + kBlocks * kOperand;  // a, b, c [64] and e^{G_C}, fp32
+constexpr int kUnitBytes = kOffVec + 1024;
+// And for a chunk and q/k head: K, then Q, as operands of 16 tokens x 32
+// columns, [32 columns][16 tokens], so that a load is 1 KiB in a row.
+constexpr int kHeadBytes = 2 * 16 * kOperand;
+constexpr int kOffQ = 16 * kOperand;
+__device__ __forceinline__ constexpr int block_of(int w, int s) { return w < 2 ? w : 2 * w - 2 + s; }
+
+constexpr int kBufferFlags = 0x00020000;    // raw buffer, 32-bit data format
+constexpr uint32_t kOutside = 0x80000000u;  // an offset past every resource used here
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, kBufferFlags);
+}
+__device__ __forceinline__ u32x4_t load16b(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
+__device__ __forceinline__ floatx4_t mfma_bf16(u32x4_t a, u32x4_t b, floatx4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                 0, 0, 0);
+}
+
+// a = hi + mid + lo exactly, each a bf16 (hi rounded to nearest); two values packed.
+__device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  hi = pack_bf16(a, b);
+  const float ra = a - __uint_as_float(hi << 16), rb = b - __uint_as_float(hi & 0xFFFF0000u);
+  const uint32_t ma = __float_as_uint(ra) & 0xFFFF0000u, mb = __float_as_uint(rb) & 0xFFFF0000u;
+  mid = __builtin_amdgcn_perm(mb, ma, 0x07060302u);
+  lo = __builtin_amdgcn_perm(__float_as_uint(rb - __uint_as_float(mb)), __float_as_uint(ra - __uint_as_float(ma)),
+                             0x07060302u);
+}
+
+__device__ __forceinline__ u32x4_t join(u32x2_t a, u32x2_t b) {
+  u32x4_t r;
+  r[0] = a[0], r[1] = a[1], r[2] = b[0], r[3] = b[1];
+  return r;
+}
+
+// Row numbers a call may use: cut off at 0 and T.
+__device__ __forceinline__ int64_t row_clip(int32_t r, int64_t T) { return min(max((int64_t)r, (int64_t)0), T); }
+// Workspace place of a sequence's first chunk.  cu / 64 + s leaves room for
+// one partial chunk per sequence, so places need no sum over sequences.
+__device__ __forceinline__ int64_t first_place(int64_t start, int s) { return start / kC + s; }
+
+// LDS writes made visible to the workgroup without waiting for loads from
+// memory in flight (the next chunk's).
+__device__ __forceinline__ void lds_barrier() {
+  __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// ---------------------------------------------------------------- chunk by chunk, independent of the state
+//
+// One workgroup per chunk and q/k head; it makes T, P and the row factors of
+// each value head of the group.  Wave w owns token rows 16 w .. + 15.  The
+// products k . k and q . k are formed transposed (rows j in the accumulators,
+// columns i in the lanes), which is P's and T's operand order.  The inverse
+// of I + A goes by blocks, in fp32: each wave substitutes forward through its
+// 16 x 16 diagonal block, then blocks of 32 and of 64 are joined by
+// -X_22 A_21 X_11 with fp32 matrix products.  (Summing powers of A instead
+// would overflow for equal keys, whose inverse is harmless.)
+constexpr int kKStride = kD + 8;   // bf16 per LDS row of K
+constexpr int kXStride = kC + 4;   // floats per LDS row of A, T
+
+__global__ __launch_bounds__(256) void gdn_chunk_prepare_kernel(GdnRows in, const int32_t* __restrict__ cu, int n_seqs,
+                                                                int64_t T, uint8_t* __restrict__ ws, uint8_t* __restrict__ wsh) {
+  __shared__ uint16_t kl[kC * kKStride];
+  __shared__ float X[kC * kXStride];
+  __shared__ floatx4_t yb[4][64];
+  __shared__ float rk_l[kC], ghi_l[kC], glo_l[kC], beta_l[kC];
+
+  const int hk = blockIdx.x % in.n_qk;
+  const int64_t place = blockIdx.x / in.n_qk;
+  // the last sequence whose first place is not past this one
+  int s = 0, hi = n_seqs - 1;
+  while (s < hi) {
+    const int mid = (s + hi + 1) / 2;
+    if (first_place(row_clip(cu[mid], T), mid) <= place) s = mid; else hi = mid - 1;
+  }
+  const int64_t start = row_clip(cu[s], T), end = row_clip(cu[s + 1], T);
+  const int64_t t0 = start + (place - first_place(start, s)) * kC;
+  if (place < first_place(start, s) || t0 >= end) return;
+  const int rows = (int)min((int64_t)kC, end - t0);
+
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int m = lane & 15, g = lane >> 4;
+  const uint32_t ld = (uint32_t)in.ldx * 2;
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(reinterpret_cast<const uint16_t*>(in.x) + t0 * in.ldx, (int64_t)rows * ld);
+  u32x4_t kf[4], qf[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t at = (uint32_t)(16 * w + m) * ld + (uint32_t)(hk * kD + 32 * i + 8 * g) * 2;
+    const bool live = 16 * w + m < rows;
+    kf[i] = load16b(rx, live ? at + (uint32_t)in.k_col * 2 : kOutside);
+    qf[i] = load16b(rx, live ? at + (uint32_t)in.q_col * 2 : kOutside);
+  }
+  float k2 = 0.0f, q2 = 0.0f;
+  uint8_t* head = wsh + (place * in.n_qk + hk) * kHeadBytes;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    *reinterpret_cast<u32x4_t*>(head + (4 * i + w) * kOperand + lane * 16) = kf[i];
+    *reinterpret_cast<u32x4_t*>(head + kOffQ + (4 * i + w) * kOperand + lane * 16) = qf[i];
+    *reinterpret_cast<u32x4_t*>(&kl[(16 * w + m) * kKStride + 32 * i + 8 * g]) = kf[i];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float k0 = __uint_as_float(kf[i][e] << 16), k1 = __uint_as_float(kf[i][e] & 0xFFFF0000u);
+      const float q0 = __uint_as_float(qf[i][e] << 16), q1 = __uint_as_float(qf[i][e] & 0xFFFF0000u);
+      k2 = fmaf(k0, k0, fmaf(k1, k1, k2));
+      q2 = fmaf(q0, q0, fmaf(q1, q1, q2));
+    }
+  }
+  k2 += __shfl_xor(k2, 16, 64);
+  q2 += __shfl_xor(q2, 16, 64);
+  k2 += __shfl_xor(k2, 32, 64);
+  q2 += __shfl_xor(q2, 32, 64);
+  const float rk_i = 1.0f / fmaxf(sqrtf(k2), kNormEps);             // token i = 16 w + m
+  const float rq_i = kRsqrtD / fmaxf(sqrtf(q2), kNormEps);
+  if (g == 0) rk_l[16 * w + m] = rk_i;
+  __syncthreads();
+
+  floatx4_t kk[4], qk[4];  // [j tile]: rows j = 16 tile + 4 g + e, column i
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    kk[j] = qk[j] = floatx4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    if (j > w) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const u32x4_t a = *reinterpret_cast<const u32x4_t*>(&kl[(16 * j + m) * kKStride + 32 * i + 8 * g]);
+      kk[j] = mfma_bf16(a, kf[i], kk[j]);
+      qk[j] = mfma_bf16(a, qf[i], qk[j]);
+    }
+  }
+
+  const int group = in.n_v / in.n_qk;
+  for (int hv = 0; hv < group; ++hv) {
+    const int h = hk * group + hv;
+    uint8_t* unit = ws + (place * in.n_v + h) * kUnitBytes;
+    // lane = token here (every wave the same): gates and their running sums
+    float gate = 0.0f, beta = 0.0f;
+    if (lane < rows) {
+      const int64_t at = (t0 + lane) * in.ldg + h;
+      if (in.gates_bf16) {
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(in.gates) + at;
+        gate = __uint_as_float((uint32_t)p[in.g_col] << 16);
+        beta = __uint_as_float((uint32_t)p[in.beta_col] << 16);
+      } else {
+        const float* p = reinterpret_cast<const float*>(in.gates) + at;
+        gate = p[in.g_col];
+        beta = p[in.beta_col];
+      }
+    }
+    gate = gate < kMinGate ? kMinGate : gate;  // a NaN stays one
+    double sum = gate;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const double up = __shfl_up(sum, o, 64);
+      if (lane >= o) sum += up;
+    }
+    const double before = sum - (double)gate;
+    const float ghi = (float)sum, glo = (float)(sum - (double)ghi);
+    const float total = __shfl((float)sum, 63, 64);
+    const float to_end = (float)(__shfl(sum, 63, 64) - sum);
+    if (w == 0) {
+      ghi_l[lane] = ghi;
+      glo_l[lane] = glo;
+      beta_l[lane] = beta;
+    }
+    // row factors, token 16 w + m: lanes g = 0 write a (K S), b (Q S), c (writes to the chunk's end)
+    const double before_i = __shfl(before, 16 * w + m, 64), sum_i = __shfl(sum, 16 * w + m, 64);
+    const float bhi_i = (float)before_i, blo_i = (float)(before_i - (double)bhi_i);
+    const float ghi_i = (float)sum_i, glo_i = (float)(sum_i - (double)ghi_i);
+    const float beta_i = __shfl(beta, 16 * w + m, 64), to_end_i = __shfl(to_end, 16 * w + m, 64);
+    if (g == 0) {
+      float* vec = reinterpret_cast<float*>(unit + kOffVec);
+      vec[16 * w + m] = expf(bhi_i) * rk_i;
+      vec[kC + 16 * w + m] = expf(ghi_i) * rq_i;
+      vec[2 * kC + 16 * w + m] = expf(to_end_i) * rk_i;
+      if (w == 0 && m == 0) vec[3 * kC] = expf(total);
+    }
+    __syncthreads();
+
+    // A (fp32, to LDS) and P (bf16, out)
+    const int i = 16 * w + m;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j > (w | 1)) continue;
+      floatx4_t a = {0.0f, 0.0f, 0.0f, 0.0f}, p = a;
+      if (j <= w) {
+        const floatx4_t gh = *reinterpret_cast<const floatx4_t*>(&ghi_l[16 * j + 4 * g]);
+        const floatx4_t gl = *reinterpret_cast<const floatx4_t*>(&glo_l[16 * j + 4 * g]);
+        const floatx4_t rk = *reinterpret_cast<const floatx4_t*>(&rk_l[16 * j + 4 * g]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int jj = 16 * j + 4 * g + e;
+          if (jj < i) a[e] = beta_i * rk_i * rk[e] * kk[j][e] * expf((bhi_i - gh[e]) + (blo_i - gl[e]));
+          if (jj <= i) p[e] = rq_i * rk[e] * qk[j][e] * expf((ghi_i - gh[e]) + (glo_i - gl[e]));
+        }
+        *reinterpret_cast<floatx4_t*>(&X[i * kXStride + 16 * j + 4 * g]) = a;
+      }
+      u32x2_t pp;
+      pp[0] = pack_bf16(p[0], p[1]);
+      pp[1] = pack_bf16(p[2], p[3]);
+      *reinterpret_cast<u32x2_t*>(unit + kOffP + block_of(w, j / 2) * kOperand + lane * 16 + (j & 1) * 8) = pp;
+    }
+    __syncthreads();
+
+    // diagonal block w: lane m solves column m, x_r = [r = m] - sum_{k<r} A_rk x_k
+    {
+      float x[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        float v = r == m ? 1.0f : 0.0f;
+#pragma unroll
+        for (int k4 = 0; k4 < r; k4 += 4) {
+          const floatx4_t a = *reinterpret_cast<const floatx4_t*>(&X[(16 * w + r) * kXStride + 16 * w + k4]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (k4 + e < r) v = fmaf(-a[e], x[k4 + e], v);
+        }
+        x[r] = v;
+      }
+      __builtin_amdgcn_wave_barrier();  // all reads of the block before its inverse overwrites it
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (g == 0) X[(16 * w + r) * kXStride + 16 * w + m] = x[r];
+    }
+    __syncthreads();
+
+    // blocks as matrix-core operands: A operand rows are read along, B operands down the columns
+    auto a_op = [&](int r, int c) { return *reinterpret_cast<const floatx4_t*>(&X[(16 * r + m) * kXStride + 16 * c + 4 * g]); };
+    auto b_op = [&](int r, int c) {
+      floatx4_t b;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e] = X[(16 * r + 4 * g + e) * kXStride + 16 * c + m];
+      return b;
+    };
+    auto product = [&](floatx4_t a, floatx4_t b, floatx4_t acc) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], acc, 0, 0, 0);
+      return acc;
+    };
+    auto put = [&](int r, int c, floatx4_t v) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) X[(16 * r + 4 * g + e) * kXStride + 16 * c + m] = -v[e];
+    };
+    const floatx4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (w < 2) {  // blocks (1, 0) and (3, 2)
+      const int c = 2 * w, r = c + 1;
+      put(r, c, product(a_op(r, r), product(a_op(r, c), b_op(c, c), zero), zero));
+    }
+    __syncthreads();
+    {  // blocks (2..3, 0..1): wave w has row 2 + w / 2, column w % 2
+      const int r = 2 + w / 2, c = w & 1;
+      floatx4_t y = zero;
+      if (c == 0) y = product(a_op(r, 0), b_op(0, 0), y);
+      y = product(a_op(r, 1), b_op(1, c), y);
+      yb[w][lane] = y;
+      __syncthreads();
+      floatx4_t x = product(a_op(r, 2), yb[c][lane], zero);
+      if (r == 3) x = product(a_op(3, 3), y, x);
+      put(r, c, x);
+    }
+    __syncthreads();
+
+    // T = (I + A)^-1 diag(beta), split in three, in operand order
+#pragma unroll
+    for (int sb = 0; sb < 2; ++sb) {
+      if (sb > w / 2) continue;
+      u32x4_t t[3];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int j = 2 * sb + half;
+        floatx4_t v = zero;
+        if (j <= w) {
+          v = a_op(w, j);
+          const floatx4_t b = *reinterpret_cast<const floatx4_t*>(&beta_l[16 * j + 4 * g]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] *= b[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t hi3, mid3, lo3;
+          split3(v[2 * e], v[2 * e + 1], hi3, mid3, lo3);
+          t[0][2 * half + e] = hi3;
+          t[1][2 * half + e] = mid3;
+          t[2][2 * half + e] = lo3;
+        }
+      }
+#pragma unroll
+      for (int term = 0; term < 3; ++term)
+        *reinterpret_cast<u32x4_t*>(unit + (term * kBlocks + block_of(w, sb)) * kOperand + lane * 16) = t[term];
+    }
+    __syncthreads();  // X, the sums and beta are free again
+  }
+}
+
+// ---------------------------------------------------------------- the walk over a sequence's chunks
+//
+// One workgroup per sequence, value head and 16 state columns (columns do not
+// meet).  Wave w holds state rows 32 w .. + 31 as two accumulators and multiplies
+// them with its own 32 columns of K and Q for all 64 tokens; the four waves'
+// partial sums meet in LDS.  From there on wave w has token rows 16 w .. + 15:
+// V - diag(a) K S, then (after an exchange) T times that, then (after another)
+// its state rows' update and its output rows.  Three barriers a chunk.
+// Accumulator row 4 c + e of state tile t is row 32 w + 8 c + 4 t + e of S, so
+// that a lane's rows of both tiles are eight neighbours: K's operand is one
+// 16-byte load.
+constexpr int kCols = 16;
+constexpr int kParts = kD / kCols;
+constexpr int kTStride = 40;  // bf16 per LDS row of a wave's K columns
+
+struct ChunkOperands {
+  u32x4_t k[4], q[4];      // [t]: token tile (w + t) % 4
+  u32x4_t t[3][2], p[2];   // [term][32 columns], [32 columns]
+  uint16_t v[4];           // token rows 16 w + 4 g + e
+  floatx4_t a, b, c;
+  float decay;
+};
+
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void gdn_chunk_scan_kernel(
+    GdnRows in, const int32_t* __restrict__ cu, int n_seqs, int64_t T, const uint8_t* __restrict__ ws, const uint8_t* __restrict__ wsh, const float* s_in,
+    float* s_out, const int32_t* __restrict__ slots, int n_slots, uint16_t* __restrict__ o, int64_t ldo) {
+  __shared__ floatx4_t part_ks[4][3][64], part_qs[4][3][64];  // [token tile][its other waves][lane]
+  __shared__ u32x2_t rest[3][4][64];                          // V - ..: [term][token tile][lane]
+  __shared__ u32x2_t wr[4][4][64];                            // writes: three terms to the state, one to O
+  __shared__ uint16_t kt[4][kC * kTStride];                   // [wave]: its 32 columns of K
+
+  // the eight column parts of a unit run on one XCD and share its L2
+  const int unit = (int)(blockIdx.x / (8 * kParts)) * 8 + blockIdx.x % 8;
+  const int part = blockIdx.x / 8 % kParts;
+  if (unit >= n_seqs * in.n_v) return;
+  const int s = unit / in.n_v, h = unit % in.n_v, hk = h / (in.n_v / in.n_qk);
+  const int64_t start = row_clip(cu[s], T), end = row_clip(cu[s + 1], T);
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int m = lane & 15, g = lane >> 4;
+  const int col = part * kCols + m;
+  const int slot = slots ? slots[s] : s;
+  if (slot < 0 || slot >= n_slots) {
+    for (int64_t t = start + tid / kCols; t < end; t += 256 / kCols)
+      o[t * ldo + h * kD + part * kCols + tid % kCols] = 0;
+    return;
+  }
+
+  const int64_t state_at = ((int64_t)slot * in.n_v + h) * kD * kD + (32 * w + 8 * g) * kD + col;
+  floatx4_t S[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) S[t][e] = s_in ? s_in[state_at + (4 * t + e) * kD] : 0.0f;
+
+  const uint32_t ld = (uint32_t)in.ldx * 2;
+  const int n_chunks = (int)((end - start + kC - 1) / kC);
+  const int64_t place0 = first_place(start, s);
+  auto fetch = [&](int c, ChunkOperands& f) {
+    // chunks past the end have empty resources: their loads read nothing
+    const bool live = c < n_chunks;
+    const int64_t t0 = start + (int64_t)(live ? c : 0) * kC;
+    const int64_t rows = live ? min((int64_t)kC, end - t0) : 0;
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(reinterpret_cast<const uint16_t*>(in.x) + t0 * in.ldx, rows * ld);
+    const __amdgpu_buffer_rsrc_t rh =
+        make_rsrc(wsh + ((place0 + (live ? c : 0)) * in.n_qk + hk) * kHeadBytes, live ? kHeadBytes : 0);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const uint32_t at = (uint32_t)((4 * w + (w + t) % 4) * kOperand + lane * 16);
+      f.k[t] = load16b(rh, at);
+      f.q[t] = load16b(rh, at + kOffQ);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      f.v[e] = __builtin_amdgcn_raw_buffer_load_b16(
+          rx, (uint32_t)(16 * w + 4 * g + e) * ld + (uint32_t)(in.v_col + h * kD + col) * 2, 0, 0);
+    const __amdgpu_buffer_rsrc_t ru =
+        make_rsrc(ws + ((place0 + (live ? c : 0)) * in.n_v + h) * kUnitBytes, live ? kUnitBytes : 0);
+#pragma unroll
+    for (int sb = 0; sb < 2; ++sb) {
+      const uint32_t at = sb <= w / 2 ? (uint32_t)(block_of(w, sb) * kOperand + lane * 16) : kOutside;
+#pragma unroll
+      for (int term = 0; term < 3; ++term) f.t[term][sb] = load16b(ru, at + term * kBlocks * kOperand);
+      f.p[sb] = load16b(ru, at + kOffP);
+    }
+    const uint32_t row = kOffVec + (16 * w + 4 * g) * 4;
+    f.a = __builtin_bit_cast(floatx4_t, load16b(ru, row));
+    f.b = __builtin_bit_cast(floatx4_t, load16b(ru, row + kC * 4));
+    f.c = __builtin_bit_cast(floatx4_t, load16b(ru, row + 2 * kC * 4));
+    f.decay = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(ru, kOffVec + 3 * kC * 4, 0, 0));
+  };
+
+  auto chunk = [&](int c, const ChunkOperands& f) {
+    const floatx4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    // K's columns for the update, read back transposed below (this wave's own)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) *reinterpret_cast<u32x4_t*>(&kt[w][(16 * ((w + t) % 4) + m) * kTStride + 8 * g]) = f.k[t];
+
+    u32x4_t sp[3];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t hi3, mid3, lo3;
+        split3(S[t][2 * e], S[t][2 * e + 1], hi3, mid3, lo3);
+        sp[0][2 * t + e] = hi3;
+        sp[1][2 * t + e] = mid3;
+        sp[2][2 * t + e] = lo3;
+      }
+    floatx4_t ks[4], qs[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) ks[t] = mfma_bf16(f.k[t], sp[2], zero);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) ks[t] = mfma_bf16(f.k[t], sp[1], ks[t]);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) ks[t] = mfma_bf16(f.k[t], sp[0], ks[t]);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) qs[t] = mfma_bf16(f.q[t], sp[1], zero);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) qs[t] = mfma_bf16(f.q[t], sp[0], qs[t]);
+    // tile (w + t) % 4 goes to its wave; this wave's own is t = 0
+#pragma unroll
+    for (int t = 1; t < 4; ++t) {
+      part_ks[(w + t) % 4][t - 1][lane] = ks[t];
+      part_qs[(w + t) % 4][t - 1][lane] = qs[t];
+    }
+    lds_barrier();
+
+    floatx4_t kst = ks[0], qst = qs[0];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const floatx4_t x = part_ks[w][i][lane], y = part_qs[w][i][lane];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) kst[e] += x[e], qst[e] += y[e];
+    }
+    float r[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = fmaf(-f.a[e], kst[e], __uint_as_float((uint32_t)f.v[e] << 16));
+    u32x2_t r3[3];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint32_t hi3, mid3, lo3;
+      split3(r[2 * e], r[2 * e + 1], hi3, mid3, lo3);
+      r3[0][e] = hi3;
+      r3[1][e] = mid3;
+      r3[2][e] = lo3;
+    }
+#pragma unroll
+    for (int term = 0; term < 3; ++term) rest[term][w][lane] = r3[term];
+    lds_barrier();
+
+    // W = T (V - ..): the six products of terms i, j with i + j <= 2
+    floatx4_t wt = zero;
+    {
+      u32x4_t rv[3][2];
+#pragma unroll
+      for (int term = 0; term < 3; ++term)
+#pragma unroll
+        for (int sb = 0; sb < 2; ++sb) rv[term][sb] = join(rest[term][2 * sb][lane], rest[term][2 * sb + 1][lane]);
+      floatx4_t w1 = zero;
+#pragma unroll
+      for (int order = 2; order >= 0; --order)
+#pragma unroll
+        for (int i = 0; i <= order; ++i) {
+          wt = mfma_bf16(f.t[i][0], rv[order - i][0], wt);
+          w1 = mfma_bf16(f.t[i][1], rv[order - i][1], w1);
+        }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) wt[e] += w1[e];
+    }
+    u32x2_t w4[4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint32_t hi3, mid3, lo3;
+      split3(wt[2 * e] * f.c[2 * e], wt[2 * e + 1] * f.c[2 * e + 1], hi3, mid3, lo3);
+      w4[0][e] = hi3;
+      w4[1][e] = mid3;
+      w4[2][e] = lo3;
+      w4[3][e] = pack_bf16(wt[2 * e], wt[2 * e + 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wr[i][w][lane] = w4[i];
+    lds_barrier();
+
+    u32x4_t wv[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int sb = 0; sb < 2; ++sb) wv[i][sb] = join(wr[i][2 * sb][lane], wr[i][2 * sb + 1][lane]);
+    // S' = e^{G_C} S + K^T (c W)
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[t][e] *= f.decay;
+      u32x4_t kT[2];
+#pragma unroll
+      for (int sb = 0; sb < 2; ++sb)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          // lane 4 j + c of a group of 16 reads token row j's columns 8 c + 4 t .. + 3; the lanes get them back by
+          // column: lane 4 c + e holds column 8 c + 4 t + e of token rows 0 .. 3
+          typedef __attribute__((address_space(3))) shortx4_t lds_shortx4_t;
+          const uint16_t* at = &kt[w][(32 * sb + 16 * half + 4 * g + m / 4) * kTStride + 8 * (m % 4) + 4 * t];
+          const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4_t*)at));
+          kT[sb][2 * half] = v[0];
+          kT[sb][2 * half + 1] = v[1];
+        }
+#pragma unroll
+      for (int term = 2; term >= 0; --term)
+#pragma unroll
+        for (int sb = 0; sb < 2; ++sb) S[t] = mfma_bf16(kT[sb], wv[term][sb], S[t]);
+    }
+    // O = b Q S + P W
+    floatx4_t ov;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ov[e] = f.b[e] * qst[e];
+#pragma unroll
+    for (int sb = 0; sb < 2; ++sb) ov = mfma_bf16(f.p[sb], wv[3][sb], ov);
+    const int64_t t0 = start + (int64_t)c * kC;
+    const __amdgpu_buffer_rsrc_t ro = make_rsrc(o + t0 * ldo, min((int64_t)kC, end - t0) * ldo * 2);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack_bf16(ov[e], 0.0f), ro,
+                                            (uint32_t)((16 * w + 4 * g + e) * ldo + h * kD + col) * 2, 0, 0);
+  };
+
+  ChunkOperands f0, f1;
+  fetch(0, f0);
+  for (int c = 0; c < n_chunks; c += 2) {
+    fetch(c + 1, f1);
+    __builtin_amdgcn_sched_barrier(0);
+    chunk(c, f0);
+    if (c + 1 == n_chunks) break;
+    fetch(c + 2, f0);
+    __builtin_amdgcn_sched_barrier(0);
+    chunk(c + 1, f1);
+  }
+  if (s_out) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s_out[state_at + (4 * t + e) * kD] = S[t][e];
+  }
+}
+
+// Places in the workspace: first_place() of the last sequence plus its chunks is at most this.
+int64_t chunk_places(int64_t T, int64_t n_seqs) { return T / kC + n_seqs + 1; }
+
+}  // namespace
+
+size_t gdn_prefill_workspace_bytes(int64_t T, int64_t n_seqs, int n_qk, int n_v) {
+  return (size_t)(chunk_places(T, n_seqs) * ((int64_t)n_v * kUnitBytes + (int64_t)n_qk * kHeadBytes));
+}
+
+hipError_t launch_gdn_prefill(const GdnRows& in, const int32_t* cu, int n_seqs, int64_t T, const float* s_in,
+                              float* s_out, const int32_t* slots, int n_slots, void* o, int64_t ldo, void* workspace,
+                              hipStream_t stream) {
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* wsh = ws + chunk_places(T, n_seqs) * in.n_v * kUnitBytes;
+  gdn_chunk_prepare_kernel<<<(unsigned)(chunk_places(T, n_seqs) * in.n_qk), 256, 0, stream>>>(in, cu, n_seqs, T, ws,
+                                                                                                       wsh);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t units = (int64_t)n_seqs * in.n_v;
+  gdn_chunk_scan_kernel<<<(unsigned)((units + 7) / 8 * 8 * kParts), 256, 0, stream>>>(
+      in, cu, n_seqs, T, ws, wsh, s_in, s_out, slots, n_slots, static_cast<uint16_t*>(o), ldo);
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

@@ -156,23 +156,6 @@ __global__ __launch_bounds__(256) void gdn_decode_kernel(GdnRows in, float* stat
   gdn_tokens<kXBf16, kCols>(in, b, b + 1, h, part, s, s, o, o_bf16, ldo);
 }
 
-// grid: sequences x value heads x column parts
-template <int kCols>
-__global__ __launch_bounds__(256) void gdn_prefill_tokens_kernel(GdnRows in, const int32_t* cu, int64_t T,
-                                                                 const float* s_in, float* s_out,
-                                                                 const int32_t* slots, int n_slots, void* o,
-                                                                 int64_t ldo) {
-  constexpr int kParts = kD / kCols;
-  const int part = blockIdx.x % kParts, h = blockIdx.x / kParts % in.n_v;
-  const int s = blockIdx.x / kParts / in.n_v;
-  const int64_t t0 = max(cu[s], 0), t1 = min((int64_t)cu[s + 1], T);
-  const int slot = slots ? slots[s] : s;
-  if (slot < 0 || slot >= n_slots) return zero_rows<kCols>(t0, t1, h, part, o, true, ldo);
-  const int64_t at = ((int64_t)slot * in.n_v + h) * kD * kD;
-  gdn_tokens<true, kCols>(in, t0, t1, h, part, s_in ? s_in + at : nullptr, s_out ? s_out + at : nullptr, o, true,
-                          ldo);
-}
-
 }  // namespace
 
 hipError_t launch_gdn_decode(const GdnRows& in, bool x_bf16, int64_t batch, float* states, const int32_t* slots,
@@ -181,18 +164,6 @@ hipError_t launch_gdn_decode(const GdnRows& in, bool x_bf16, int64_t batch, floa
   const unsigned grid = (unsigned)(batch * in.n_v * (kD / kCols));
   const auto f = x_bf16 ? gdn_decode_kernel<true, kCols> : gdn_decode_kernel<false, kCols>;
   f<<<grid, 256, 0, stream>>>(in, states, slots, n_slots, o, o_bf16, ldo);
-  return hipGetLastError();
-}
-
-size_t gdn_prefill_workspace_bytes(int64_t T, int64_t n_seqs, int n_qk, int n_v) { return 0; }
-
-hipError_t launch_gdn_prefill(const GdnRows& in, const int32_t* cu, int n_seqs, int64_t T, const float* s_in,
-                              float* s_out, const int32_t* slots, int n_slots, void* o, int64_t ldo, void* workspace,
-                              hipStream_t stream) {
-  (void)workspace;
-  constexpr int kCols = 32;
-  gdn_prefill_tokens_kernel<kCols><<<(unsigned)((int64_t)n_seqs * in.n_v * (kD / kCols)), 256, 0, stream>>>(
-      in, cu, T, s_in, s_out, slots, n_slots, o, ldo);
   return hipGetLastError();
 }
 
