@@ -110,12 +110,13 @@ __device__ __forceinline__ void lds_barrier() {
 constexpr int kKStride = kD + 8;   // bf16 per LDS row of K
 constexpr int kXStride = kC + 4;   // floats per LDS row of A, T
 
-__global__ __launch_bounds__(256) void gdn_chunk_prepare_kernel(GdnRows in, const int32_t* __restrict__ cu, int n_seqs,
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void gdn_chunk_prepare_kernel(GdnRows in, const int32_t* __restrict__ cu, int n_seqs,
                                                                 int64_t T, uint8_t* __restrict__ ws, uint8_t* __restrict__ wsh) {
-  __shared__ uint16_t kl[kC * kKStride];
-  __shared__ float X[kC * kXStride];
-  __shared__ floatx4_t yb[4][64];
-  __shared__ float rk_l[kC], ghi_l[kC], glo_l[kC], beta_l[kC];
+  __shared__ __attribute__((aligned(16))) uint16_t kl[kC * kKStride];
+  __shared__ __attribute__((aligned(16))) float X[kC * kXStride];
+  // K is read only before the first head's gates; then its place takes four blocks of 16 x 16
+  floatx4_t(&yb)[4][64] = *reinterpret_cast<floatx4_t(*)[4][64]>(kl);
+  __shared__ float rk_l[kC], rq_l[kC], ghi_l[4][kC], glo_l[4][kC], alpha_l[4][kC], beta_l[4][kC];
 
   const int hk = blockIdx.x % in.n_qk;
   const int64_t place = blockIdx.x / in.n_qk;
@@ -163,10 +164,11 @@ __global__ __launch_bounds__(256) void gdn_chunk_prepare_kernel(GdnRows in, cons
   q2 += __shfl_xor(q2, 32, 64);
   const float rk_i = 1.0f / fmaxf(sqrtf(k2), kNormEps);             // token i = 16 w + m
   const float rq_i = kRsqrtD / fmaxf(sqrtf(q2), kNormEps);
-  if (g == 0) rk_l[16 * w + m] = rk_i;
+  if (g == 0) rk_l[16 * w + m] = rk_i, rq_l[16 * w + m] = rq_i;
   __syncthreads();
 
-  floatx4_t kk[4], qk[4];  // [j tile]: rows j = 16 tile + 4 g + e, column i
+  // rows j = 16 tile + 4 g + e, column i, of the unit vectors' products (q's with 1 / sqrt(128))
+  floatx4_t kk[4], qk[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     kk[j] = qk[j] = floatx4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -177,80 +179,97 @@ __global__ __launch_bounds__(256) void gdn_chunk_prepare_kernel(GdnRows in, cons
       kk[j] = mfma_bf16(a, kf[i], kk[j]);
       qk[j] = mfma_bf16(a, qf[i], qk[j]);
     }
+    const floatx4_t rk = *reinterpret_cast<const floatx4_t*>(&rk_l[16 * j + 4 * g]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      kk[j][e] *= rk[e] * rk_i;
+      qk[j][e] *= rk[e] * rq_i;
+    }
+    __builtin_amdgcn_sched_barrier(0);  // one tile's operands at a time
   }
 
   const int group = in.n_v / in.n_qk;
   for (int hv = 0; hv < group; ++hv) {
     const int h = hk * group + hv;
-    uint8_t* unit = ws + (place * in.n_v + h) * kUnitBytes;
-    // lane = token here (every wave the same): gates and their running sums
-    float gate = 0.0f, beta = 0.0f;
-    if (lane < rows) {
-      const int64_t at = (t0 + lane) * in.ldg + h;
-      if (in.gates_bf16) {
-        const uint16_t* p = reinterpret_cast<const uint16_t*>(in.gates) + at;
-        gate = __uint_as_float((uint32_t)p[in.g_col] << 16);
-        beta = __uint_as_float((uint32_t)p[in.beta_col] << 16);
-      } else {
-        const float* p = reinterpret_cast<const float*>(in.gates) + at;
-        gate = p[in.g_col];
-        beta = p[in.beta_col];
+    const __amdgpu_buffer_rsrc_t unit = make_rsrc(ws + (place * in.n_v + h) * kUnitBytes, kUnitBytes);
+    // the lane's number, unknown to the compiler anew for each head: else it
+    // computes every LDS address before the loop and holds them (over 100 registers)
+    int lane = tid & 63;
+    __asm__ volatile("" : "+v"(lane));
+    const int m = lane & 15, g = lane >> 4;
+    if (hv % 4 == 0) {  // the next four heads' gates, one per wave, lane = token: running sums in fp64, base 2
+      if (hv > 0) __syncthreads();
+      float gate = 0.0f, beta = 0.0f;
+      if (hv + w < group && lane < rows) {
+        const int64_t at = (t0 + lane) * in.ldg + h + w;
+        if (in.gates_bf16) {
+          const uint16_t* p = reinterpret_cast<const uint16_t*>(in.gates) + at;
+          gate = __uint_as_float((uint32_t)p[in.g_col] << 16);
+          beta = __uint_as_float((uint32_t)p[in.beta_col] << 16);
+        } else {
+          const float* p = reinterpret_cast<const float*>(in.gates) + at;
+          gate = p[in.g_col];
+          beta = p[in.beta_col];
+        }
       }
-    }
-    gate = gate < kMinGate ? kMinGate : gate;  // a NaN stays one
-    double sum = gate;
+      gate = gate < kMinGate ? kMinGate : gate;  // a NaN stays one
+      const double step = (double)gate * 1.4426950408889634;
+      double sum = step;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const double up = __shfl_up(sum, o, 64);
-      if (lane >= o) sum += up;
+      for (int o = 1; o < 64; o <<= 1) {
+        const double up = __shfl_up(sum, o, 64);
+        if (lane >= o) sum += up;
+      }
+      const float ghi = (float)sum;
+      const float total = __shfl(ghi, 63, 64);
+      ghi_l[w][lane] = ghi;
+      glo_l[w][lane] = (float)(sum - (double)ghi);
+      alpha_l[w][lane] = __builtin_amdgcn_exp2f((float)step);
+      beta_l[w][lane] = beta;
+      if (hv + w < group) {
+        // row factors: of K S, of Q S, and of the writes to the chunk's end
+        float* vec = reinterpret_cast<float*>(ws + (place * in.n_v + h + w) * kUnitBytes + kOffVec);
+        vec[lane] = __builtin_amdgcn_exp2f((float)(sum - step)) * rk_l[lane];
+        vec[kC + lane] = __builtin_amdgcn_exp2f(ghi) * rq_l[lane];
+        vec[2 * kC + lane] = __builtin_amdgcn_exp2f((float)(__shfl(sum, 63, 64) - sum)) * rk_l[lane];
+        if (lane == 0) vec[3 * kC] = __builtin_amdgcn_exp2f(total);
+      }
+      __syncthreads();
     }
-    const double before = sum - (double)gate;
-    const float ghi = (float)sum, glo = (float)(sum - (double)ghi);
-    const float total = __shfl((float)sum, 63, 64);
-    const float to_end = (float)(__shfl(sum, 63, 64) - sum);
-    if (w == 0) {
-      ghi_l[lane] = ghi;
-      glo_l[lane] = glo;
-      beta_l[lane] = beta;
-    }
-    // row factors, token 16 w + m: lanes g = 0 write a (K S), b (Q S), c (writes to the chunk's end)
-    const double before_i = __shfl(before, 16 * w + m, 64), sum_i = __shfl(sum, 16 * w + m, 64);
-    const float bhi_i = (float)before_i, blo_i = (float)(before_i - (double)bhi_i);
-    const float ghi_i = (float)sum_i, glo_i = (float)(sum_i - (double)ghi_i);
-    const float beta_i = __shfl(beta, 16 * w + m, 64), to_end_i = __shfl(to_end, 16 * w + m, 64);
-    if (g == 0) {
-      float* vec = reinterpret_cast<float*>(unit + kOffVec);
-      vec[16 * w + m] = expf(bhi_i) * rk_i;
-      vec[kC + 16 * w + m] = expf(ghi_i) * rq_i;
-      vec[2 * kC + 16 * w + m] = expf(to_end_i) * rk_i;
-      if (w == 0 && m == 0) vec[3 * kC] = expf(total);
-    }
-    __syncthreads();
+    const int hw = hv % 4;
 
     // A (fp32, to LDS) and P (bf16, out)
     const int i = 16 * w + m;
+    const float alpha_i = alpha_l[hw][i], beta_i = beta_l[hw][i];
+    const float bhi = i ? ghi_l[hw][max(i - 1, 0)] : 0.0f, blo = i ? glo_l[hw][max(i - 1, 0)] : 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (j > (w | 1)) continue;
-      floatx4_t a = {0.0f, 0.0f, 0.0f, 0.0f}, p = a;
+      floatx4_t p = {0.0f, 0.0f, 0.0f, 0.0f};
       if (j <= w) {
-        const floatx4_t gh = *reinterpret_cast<const floatx4_t*>(&ghi_l[16 * j + 4 * g]);
-        const floatx4_t gl = *reinterpret_cast<const floatx4_t*>(&glo_l[16 * j + 4 * g]);
-        const floatx4_t rk = *reinterpret_cast<const floatx4_t*>(&rk_l[16 * j + 4 * g]);
+        const floatx4_t gh = *reinterpret_cast<const floatx4_t*>(&ghi_l[hw][16 * j + 4 * g]);
+        const floatx4_t gl = *reinterpret_cast<const floatx4_t*>(&glo_l[hw][16 * j + 4 * g]);
+        floatx4_t a;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int jj = 16 * j + 4 * g + e;
-          if (jj < i) a[e] = beta_i * rk_i * rk[e] * kk[j][e] * expf((bhi_i - gh[e]) + (blo_i - gl[e]));
-          if (jj <= i) p[e] = rq_i * rk[e] * qk[j][e] * expf((ghi_i - gh[e]) + (glo_i - gl[e]));
+          const float d = __builtin_amdgcn_exp2f((bhi - gh[e]) + (blo - gl[e]));  // e^{G_{i-1} - G_j}
+          a[e] = beta_i * d * kk[j][e];
+          p[e] = alpha_i * d * qk[j][e];
+          if (j == w) {
+            const int jj = 4 * g + e;  // j - 16 w; above the diagonal d may be infinite
+            a[e] = jj < m ? a[e] : 0.0f;
+            p[e] = jj < m ? p[e] : jj == m ? qk[j][e] : 0.0f;
+          }
         }
         *reinterpret_cast<floatx4_t*>(&X[i * kXStride + 16 * j + 4 * g]) = a;
       }
       u32x2_t pp;
       pp[0] = pack_bf16(p[0], p[1]);
       pp[1] = pack_bf16(p[2], p[3]);
-      *reinterpret_cast<u32x2_t*>(unit + kOffP + block_of(w, j / 2) * kOperand + lane * 16 + (j & 1) * 8) = pp;
+      __builtin_amdgcn_raw_buffer_store_b64(pp, unit, (uint32_t)(lane * 16 + (j & 1) * 8),
+                                            kOffP + block_of(w, j / 2) * kOperand, 0);
     }
-    __syncthreads();
+    __builtin_amdgcn_wave_barrier();  // the diagonal block is this wave's own
 
     // diagonal block w: lane m solves column m, x_r = [r = m] - sum_{k<r} A_rk x_k
     {
@@ -266,6 +285,7 @@ __global__ __launch_bounds__(256) void gdn_chunk_prepare_kernel(GdnRows in, cons
             if (k4 + e < r) v = fmaf(-a[e], x[k4 + e], v);
         }
         x[r] = v;
+        if (r % 2) __asm__ volatile("" ::"v"(x[r]) : "memory");  // rows read a few ahead, not all 16 (160 registers)
       }
       __builtin_amdgcn_wave_barrier();  // all reads of the block before its inverse overwrites it
 #pragma unroll
@@ -321,7 +341,7 @@ __global__ __launch_bounds__(256) void gdn_chunk_prepare_kernel(GdnRows in, cons
         floatx4_t v = zero;
         if (j <= w) {
           v = a_op(w, j);
-          const floatx4_t b = *reinterpret_cast<const floatx4_t*>(&beta_l[16 * j + 4 * g]);
+          const floatx4_t b = *reinterpret_cast<const floatx4_t*>(&beta_l[hw][16 * j + 4 * g]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] *= b[e];
         }
@@ -336,9 +356,10 @@ __global__ __launch_bounds__(256) void gdn_chunk_prepare_kernel(GdnRows in, cons
       }
 #pragma unroll
       for (int term = 0; term < 3; ++term)
-        *reinterpret_cast<u32x4_t*>(unit + (term * kBlocks + block_of(w, sb)) * kOperand + lane * 16) = t[term];
+        __builtin_amdgcn_raw_buffer_store_b128(t[term], unit, (uint32_t)(lane * 16),
+                                               (term * kBlocks + block_of(w, sb)) * kOperand, 0);
     }
-    __syncthreads();  // X, the sums and beta are free again
+    __syncthreads();  // X is free again
   }
 }
 
