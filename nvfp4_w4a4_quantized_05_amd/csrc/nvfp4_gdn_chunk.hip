@@ -366,162 +366,160 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
 // ---------------------------------------------------------------- the walk over a sequence's chunks
 //
 // One workgroup per sequence, value head and 16 state columns (columns do not
-// meet).  Wave w holds state rows 32 w .. + 31 as two accumulators and multiplies
-// them with its own 32 columns of K and Q for all 64 tokens; the four waves'
-// partial sums meet in LDS.  From there on wave w has token rows 16 w .. + 15:
-// V - diag(a) K S, then (after an exchange) T times that, then (after another)
-// its state rows' update and its output rows.  Three barriers a chunk.
+// meet); eight waves, two per SIMD.  Waves 0-3 carry the state from chunk to
+// chunk, waves 4-7 make the outputs beside them.
+//   State wave w holds state rows 32 w .. + 31 as two accumulators and
+// multiplies them with its own 32 columns of K for all 64 tokens; the four
+// waves' partial sums meet in LDS.  From there on it has token rows 16 w .. +
+// 15: V - diag(a) K S, then (after an exchange) T times that, which is W, then
+// (after another) the update of its state rows.  Three barriers a chunk.
+//   Output wave w has token rows 16 w .. + 15: Q S from the state's terms that
+// the state waves share, then P W.  It forms both transposed (rows = state
+// columns, lanes = tokens), so that a lane holds four neighbours of a row of o.
 // Accumulator row 4 c + e of state tile t is row 32 w + 8 c + 4 t + e of S, so
-// that a lane's rows of both tiles are eight neighbours: K's operand is one
-// 16-byte load.
+// that a lane's rows of both tiles are eight neighbours.
 constexpr int kCols = 16;
 constexpr int kParts = kD / kCols;
+constexpr int kScanThreads = 512;
 constexpr int kTStride = 40;  // bf16 per LDS row of a wave's K columns
 
-struct ChunkOperands {
-  u32x4_t k[4], q[4];      // [t]: token tile (w + t) % 4
-  u32x4_t t[3][2], p[2];   // [term][32 columns], [32 columns]
-  uint16_t v[4];           // token rows 16 w + 4 g + e
-  floatx4_t a, b, c;
+struct ScanShared {
+  floatx4_t part[4][3][64];    // K S: [token tile][its other waves][lane]
+  u32x2_t rest[3][4][64];      // V - diag(a) K S: [term][token tile][lane]
+  u32x2_t wr[4][4][64];        // W: three terms (scaled) for the state, one for o
+  u32x4_t state[4][2][64];     // S's first two terms: [32 rows][term][lane]
+  uint16_t kt[4][kC * kTStride];  // [wave]: its 32 columns of K
+  uint16_t v[4][512];             // [wave]: its 16 rows of V (and as much that is not read)
+};
+
+// One unit's rows and workspace, chunk by chunk; chunks past the end have
+// empty resources, whose loads read nothing.
+struct ChunkSource {
+  const uint8_t* unit;   // of chunk 0
+  const uint8_t* head;
+  const uint16_t* v;     // first row's part of V
+  uint16_t* o;
+  int64_t unit_step, head_step, v_step, o_step;  // bytes, bytes, values, values per chunk
+  int n_chunks, last_rows;
+  __device__ __forceinline__ int rows(int c) const { return c < n_chunks - 1 ? kC : c < n_chunks ? last_rows : 0; }
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t units(int c) const {
+    return make_rsrc(unit + (c < n_chunks ? c : 0) * unit_step, c < n_chunks ? kUnitBytes : 0);
+  }
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t heads(int c) const {
+    return make_rsrc(head + (c < n_chunks ? c : 0) * head_step, c < n_chunks ? kHeadBytes : 0);
+  }
+};
+
+struct StateOperands {
+  u32x4_t k[4];      // [t]: token tile (w + t) % 4
+  u32x4_t t[3][2];   // [term][32 columns]
+  u32x4_t v;         // lanes 0-31: half a row of V, row lane / 2
+  floatx4_t a, c;    // token rows 16 w + 4 g + e
   float decay;
 };
 
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void gdn_chunk_scan_kernel(
-    GdnRows in, const int32_t* __restrict__ cu, int n_seqs, int64_t T, const uint8_t* __restrict__ ws, const uint8_t* __restrict__ wsh, const float* s_in,
-    float* s_out, const int32_t* __restrict__ slots, int n_slots, uint16_t* __restrict__ o, int64_t ldo) {
-  __shared__ floatx4_t part_ks[4][3][64], part_qs[4][3][64];  // [token tile][its other waves][lane]
-  __shared__ u32x2_t rest[3][4][64];                          // V - ..: [term][token tile][lane]
-  __shared__ u32x2_t wr[4][4][64];                            // writes: three terms to the state, one to O
-  __shared__ uint16_t kt[4][kC * kTStride];                   // [wave]: its 32 columns of K
+struct OutputOperands {
+  u32x4_t q[4], p[2];
+  float b;           // token row 16 w + m
+};
 
-  // the eight column parts of a unit run on one XCD and share its L2
-  const int unit = (int)(blockIdx.x / (8 * kParts)) * 8 + blockIdx.x % 8;
-  const int part = blockIdx.x / 8 % kParts;
-  if (unit >= n_seqs * in.n_v) return;
-  const int s = unit / in.n_v, h = unit % in.n_v, hk = h / (in.n_v / in.n_qk);
-  const int64_t start = row_clip(cu[s], T), end = row_clip(cu[s + 1], T);
-  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+__device__ __forceinline__ void scan_state(const ChunkSource& src, uint32_t v_ld, ScanShared& sh, int w, int lane,
+                                           floatx4_t (&S)[2]) {
   const int m = lane & 15, g = lane >> 4;
-  const int col = part * kCols + m;
-  const int slot = slots ? slots[s] : s;
-  if (slot < 0 || slot >= n_slots) {
-    for (int64_t t = start + tid / kCols; t < end; t += 256 / kCols)
-      o[t * ldo + h * kD + part * kCols + tid % kCols] = 0;
-    return;
-  }
+  const floatx4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  typedef __attribute__((address_space(3))) shortx4_t lds_shortx4_t;
 
-  const int64_t state_at = ((int64_t)slot * in.n_v + h) * kD * kD + (32 * w + 8 * g) * kD + col;
-  floatx4_t S[2];
+  auto fetch_k = [&](int c, StateOperands& f) {
+    const __amdgpu_buffer_rsrc_t r = src.heads(c);
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) S[t][e] = s_in ? s_in[state_at + (4 * t + e) * kD] : 0.0f;
-
-  const uint32_t ld = (uint32_t)in.ldx * 2;
-  const int n_chunks = (int)((end - start + kC - 1) / kC);
-  const int64_t place0 = first_place(start, s);
-  auto fetch = [&](int c, ChunkOperands& f) {
-    // chunks past the end have empty resources: their loads read nothing
-    const bool live = c < n_chunks;
-    const int64_t t0 = start + (int64_t)(live ? c : 0) * kC;
-    const int64_t rows = live ? min((int64_t)kC, end - t0) : 0;
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(reinterpret_cast<const uint16_t*>(in.x) + t0 * in.ldx, rows * ld);
-    const __amdgpu_buffer_rsrc_t rh =
-        make_rsrc(wsh + ((place0 + (live ? c : 0)) * in.n_qk + hk) * kHeadBytes, live ? kHeadBytes : 0);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const uint32_t at = (uint32_t)((4 * w + (w + t) % 4) * kOperand + lane * 16);
-      f.k[t] = load16b(rh, at);
-      f.q[t] = load16b(rh, at + kOffQ);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      f.v[e] = __builtin_amdgcn_raw_buffer_load_b16(
-          rx, (uint32_t)(16 * w + 4 * g + e) * ld + (uint32_t)(in.v_col + h * kD + col) * 2, 0, 0);
-    const __amdgpu_buffer_rsrc_t ru =
-        make_rsrc(ws + ((place0 + (live ? c : 0)) * in.n_v + h) * kUnitBytes, live ? kUnitBytes : 0);
+    for (int t = 0; t < 4; ++t) f.k[t] = load16b(r, (uint32_t)((4 * w + (w + t) % 4) * kOperand + lane * 16));
+  };
+  auto fetch_t = [&](int c, StateOperands& f) {
+    const __amdgpu_buffer_rsrc_t r = src.units(c);
 #pragma unroll
     for (int sb = 0; sb < 2; ++sb) {
       const uint32_t at = sb <= w / 2 ? (uint32_t)(block_of(w, sb) * kOperand + lane * 16) : kOutside;
 #pragma unroll
-      for (int term = 0; term < 3; ++term) f.t[term][sb] = load16b(ru, at + term * kBlocks * kOperand);
-      f.p[sb] = load16b(ru, at + kOffP);
+      for (int term = 0; term < 3; ++term) f.t[term][sb] = load16b(r, at + term * kBlocks * kOperand);
     }
+  };
+  auto fetch_v = [&](int c, StateOperands& f) {
+    const __amdgpu_buffer_rsrc_t rv = make_rsrc(src.v + (c < src.n_chunks ? c : 0) * src.v_step, (int64_t)src.rows(c) * v_ld);
+    f.v = load16b(rv, lane < 32 ? (uint32_t)(16 * w + lane / 2) * v_ld + (lane & 1) * 16 : kOutside);
+    const __amdgpu_buffer_rsrc_t r = src.units(c);
     const uint32_t row = kOffVec + (16 * w + 4 * g) * 4;
-    f.a = __builtin_bit_cast(floatx4_t, load16b(ru, row));
-    f.b = __builtin_bit_cast(floatx4_t, load16b(ru, row + kC * 4));
-    f.c = __builtin_bit_cast(floatx4_t, load16b(ru, row + 2 * kC * 4));
-    f.decay = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(ru, kOffVec + 3 * kC * 4, 0, 0));
+    f.a = __builtin_bit_cast(floatx4_t, load16b(r, row));
+    f.c = __builtin_bit_cast(floatx4_t, load16b(r, row + 2 * kC * 4));
+    f.decay = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, kOffVec + 3 * kC * 4, 0, 0));
   };
 
-  auto chunk = [&](int c, const ChunkOperands& f) {
-    const floatx4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    // K's columns for the update, read back transposed below (this wave's own)
+  // One chunk with its operands in f; those of chunk `next` are asked for in
+  // pieces between the steps, so that the loads do not queue in front of one.
+  auto chunk = [&](const StateOperands& f, int next, StateOperands& fn) {
+    // K's columns and V's rows, read back transposed below (this wave's own)
 #pragma unroll
-    for (int t = 0; t < 4; ++t) *reinterpret_cast<u32x4_t*>(&kt[w][(16 * ((w + t) % 4) + m) * kTStride + 8 * g]) = f.k[t];
+    for (int t = 0; t < 4; ++t) *reinterpret_cast<u32x4_t*>(&sh.kt[w][(16 * ((w + t) % 4) + m) * kTStride + 8 * g]) = f.k[t];
+    *reinterpret_cast<u32x4_t*>(&sh.v[w][lane * 8]) = f.v;
 
     u32x4_t sp[3];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        uint32_t hi3, mid3, lo3;
-        split3(S[t][2 * e], S[t][2 * e + 1], hi3, mid3, lo3);
-        sp[0][2 * t + e] = hi3;
-        sp[1][2 * t + e] = mid3;
-        sp[2][2 * t + e] = lo3;
+        uint32_t hi, mid, lo;
+        split3(S[t][2 * e], S[t][2 * e + 1], hi, mid, lo);
+        sp[0][2 * t + e] = hi;
+        sp[1][2 * t + e] = mid;
+        sp[2][2 * t + e] = lo;
       }
-    floatx4_t ks[4], qs[4];
+    floatx4_t ks[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) ks[t] = mfma_bf16(f.k[t], sp[2], zero);
+    sh.state[w][0][lane] = sp[0];
+    sh.state[w][1][lane] = sp[1];
 #pragma unroll
     for (int t = 0; t < 4; ++t) ks[t] = mfma_bf16(f.k[t], sp[1], ks[t]);
 #pragma unroll
     for (int t = 0; t < 4; ++t) ks[t] = mfma_bf16(f.k[t], sp[0], ks[t]);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) qs[t] = mfma_bf16(f.q[t], sp[1], zero);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) qs[t] = mfma_bf16(f.q[t], sp[0], qs[t]);
+    fetch_v(next, fn);
     // tile (w + t) % 4 goes to its wave; this wave's own is t = 0
 #pragma unroll
-    for (int t = 1; t < 4; ++t) {
-      part_ks[(w + t) % 4][t - 1][lane] = ks[t];
-      part_qs[(w + t) % 4][t - 1][lane] = qs[t];
-    }
+    for (int t = 1; t < 4; ++t) sh.part[(w + t) % 4][t - 1][lane] = ks[t];
     lds_barrier();
 
-    floatx4_t kst = ks[0], qst = qs[0];
+    floatx4_t kst = ks[0];
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-      const floatx4_t x = part_ks[w][i][lane], y = part_qs[w][i][lane];
+      const floatx4_t x = sh.part[w][i][lane];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) kst[e] += x[e], qst[e] += y[e];
+      for (int e = 0; e < 4; ++e) kst[e] += x[e];
     }
+    // lane 4 j + c of a group of 16 reads columns 4 c .. + 3 of row 4 g + j; the lanes get them back by column
+    const u32x2_t vt = __builtin_bit_cast(
+        u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4_t*)&sh.v[w][(4 * g + m / 4) * kCols + 4 * (m % 4)]));
     float r[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = fmaf(-f.a[e], kst[e], __uint_as_float((uint32_t)f.v[e] << 16));
-    u32x2_t r3[3];
+    for (int e = 0; e < 4; ++e)
+      r[e] = fmaf(-f.a[e], kst[e], __uint_as_float(e & 1 ? vt[e / 2] & 0xFFFF0000u : vt[e / 2] << 16));
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      uint32_t hi3, mid3, lo3;
-      split3(r[2 * e], r[2 * e + 1], hi3, mid3, lo3);
-      r3[0][e] = hi3;
-      r3[1][e] = mid3;
-      r3[2][e] = lo3;
+      uint32_t hi, mid, lo;
+      split3(r[2 * e], r[2 * e + 1], hi, mid, lo);
+      sh.rest[0][w][lane][e] = hi;
+      sh.rest[1][w][lane][e] = mid;
+      sh.rest[2][w][lane][e] = lo;
     }
-#pragma unroll
-    for (int term = 0; term < 3; ++term) rest[term][w][lane] = r3[term];
+    fetch_k(next, fn);
     lds_barrier();
 
     // W = T (V - ..): the six products of terms i, j with i + j <= 2
-    floatx4_t wt = zero;
+    floatx4_t wt = zero, w1 = zero;
     {
       u32x4_t rv[3][2];
 #pragma unroll
       for (int term = 0; term < 3; ++term)
 #pragma unroll
-        for (int sb = 0; sb < 2; ++sb) rv[term][sb] = join(rest[term][2 * sb][lane], rest[term][2 * sb + 1][lane]);
-      floatx4_t w1 = zero;
+        for (int sb = 0; sb < 2; ++sb) rv[term][sb] = join(sh.rest[term][2 * sb][lane], sh.rest[term][2 * sb + 1][lane]);
 #pragma unroll
       for (int order = 2; order >= 0; --order)
 #pragma unroll
@@ -529,28 +527,26 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void g
           wt = mfma_bf16(f.t[i][0], rv[order - i][0], wt);
           w1 = mfma_bf16(f.t[i][1], rv[order - i][1], w1);
         }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) wt[e] += w1[e];
     }
-    u32x2_t w4[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) wt[e] += w1[e];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      uint32_t hi3, mid3, lo3;
-      split3(wt[2 * e] * f.c[2 * e], wt[2 * e + 1] * f.c[2 * e + 1], hi3, mid3, lo3);
-      w4[0][e] = hi3;
-      w4[1][e] = mid3;
-      w4[2][e] = lo3;
-      w4[3][e] = pack_bf16(wt[2 * e], wt[2 * e + 1]);
+      uint32_t hi, mid, lo;
+      split3(wt[2 * e] * f.c[2 * e], wt[2 * e + 1] * f.c[2 * e + 1], hi, mid, lo);
+      sh.wr[0][w][lane][e] = hi;
+      sh.wr[1][w][lane][e] = mid;
+      sh.wr[2][w][lane][e] = lo;
+      sh.wr[3][w][lane][e] = pack_bf16(wt[2 * e], wt[2 * e + 1]);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) wr[i][w][lane] = w4[i];
+    fetch_t(next, fn);
     lds_barrier();
 
-    u32x4_t wv[4][2];
+    u32x4_t wv[3][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 3; ++i)
 #pragma unroll
-      for (int sb = 0; sb < 2; ++sb) wv[i][sb] = join(wr[i][2 * sb][lane], wr[i][2 * sb + 1][lane]);
+      for (int sb = 0; sb < 2; ++sb) wv[i][sb] = join(sh.wr[i][2 * sb][lane], sh.wr[i][2 * sb + 1][lane]);
     // S' = e^{G_C} S + K^T (c W)
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -561,10 +557,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void g
       for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          // lane 4 j + c of a group of 16 reads token row j's columns 8 c + 4 t .. + 3; the lanes get them back by
-          // column: lane 4 c + e holds column 8 c + 4 t + e of token rows 0 .. 3
-          typedef __attribute__((address_space(3))) shortx4_t lds_shortx4_t;
-          const uint16_t* at = &kt[w][(32 * sb + 16 * half + 4 * g + m / 4) * kTStride + 8 * (m % 4) + 4 * t];
+          // as above: lane 4 c + e gets column 8 c + 4 t + e of four token rows
+          const uint16_t* at = &sh.kt[w][(32 * sb + 16 * half + 4 * g + m / 4) * kTStride + 8 * (m % 4) + 4 * t];
           const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4_t*)at));
           kT[sb][2 * half] = v[0];
           kT[sb][2 * half + 1] = v[1];
@@ -574,36 +568,106 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void g
 #pragma unroll
         for (int sb = 0; sb < 2; ++sb) S[t] = mfma_bf16(kT[sb], wv[term][sb], S[t]);
     }
-    // O = b Q S + P W
-    floatx4_t ov;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) ov[e] = f.b[e] * qst[e];
-#pragma unroll
-    for (int sb = 0; sb < 2; ++sb) ov = mfma_bf16(f.p[sb], wv[3][sb], ov);
-    const int64_t t0 = start + (int64_t)c * kC;
-    const __amdgpu_buffer_rsrc_t ro = make_rsrc(o + t0 * ldo, min((int64_t)kC, end - t0) * ldo * 2);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack_bf16(ov[e], 0.0f), ro,
-                                            (uint32_t)((16 * w + 4 * g + e) * ldo + h * kD + col) * 2, 0, 0);
   };
 
-  ChunkOperands f0, f1;
-  fetch(0, f0);
-  for (int c = 0; c < n_chunks; c += 2) {
-    fetch(c + 1, f1);
-    __builtin_amdgcn_sched_barrier(0);
-    chunk(c, f0);
-    if (c + 1 == n_chunks) break;
-    fetch(c + 2, f0);
-    __builtin_amdgcn_sched_barrier(0);
-    chunk(c + 1, f1);
+  StateOperands f0, f1;
+  fetch_k(0, f0);
+  fetch_v(0, f0);
+  fetch_t(0, f0);
+  int c = 0;
+  for (; c + 1 < src.n_chunks; c += 2) {
+    chunk(f0, c + 1, f1);
+    chunk(f1, c + 2, f0);
   }
+  if (c < src.n_chunks) chunk(f0, c + 1, f1);
+}
+
+__device__ __forceinline__ void scan_output(const ChunkSource& src, uint32_t o_ld, ScanShared& sh, int w, int lane) {
+  const int m = lane & 15, g = lane >> 4;
+  auto fetch = [&](int c, OutputOperands& f) {
+    const __amdgpu_buffer_rsrc_t rh = src.heads(c), r = src.units(c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f.q[i] = load16b(rh, (uint32_t)(kOffQ + (4 * i + w) * kOperand + lane * 16));
+#pragma unroll
+    for (int sb = 0; sb < 2; ++sb)
+      f.p[sb] = load16b(r, sb <= w / 2 ? (uint32_t)(kOffP + block_of(w, sb) * kOperand + lane * 16) : kOutside);
+    f.b = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, kOffVec + (kC + 16 * w + m) * 4, 0, 0));
+  };
+  auto chunk = [&](int c, const OutputOperands& f, OutputOperands& fn) {
+    fetch(c + 1, fn);
+    lds_barrier();
+    floatx4_t ov = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int term = 1; term >= 0; --term)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ov = mfma_bf16(sh.state[i][term][lane], f.q[i], ov);
+    lds_barrier();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ov[e] *= f.b;
+    lds_barrier();
+#pragma unroll
+    for (int sb = 0; sb < 2; ++sb) ov = mfma_bf16(join(sh.wr[3][2 * sb][lane], sh.wr[3][2 * sb + 1][lane]), f.p[sb], ov);
+    const __amdgpu_buffer_rsrc_t ro = make_rsrc(src.o + c * src.o_step, (int64_t)src.rows(c) * o_ld);
+    u32x2_t out;
+    out[0] = pack_bf16(ov[0], ov[1]);
+    out[1] = pack_bf16(ov[2], ov[3]);
+    __builtin_amdgcn_raw_buffer_store_b64(out, ro, (uint32_t)(16 * w + m) * o_ld + 8 * g, 0, 0);
+  };
+  OutputOperands f0, f1;
+  fetch(0, f0);
+  int c = 0;
+  for (; c + 1 < src.n_chunks; c += 2) {
+    chunk(c, f0, f1);
+    chunk(c + 1, f1, f0);
+  }
+  if (c < src.n_chunks) chunk(c, f0, f1);
+}
+
+__global__ __launch_bounds__(kScanThreads) void gdn_chunk_scan_kernel(
+    GdnRows in, const int32_t* __restrict__ cu, int n_seqs, int64_t T, const uint8_t* ws, const uint8_t* wsh,
+    const float* s_in, float* s_out, const int32_t* __restrict__ slots, int n_slots,
+    uint16_t* o, int64_t ldo) {
+  __shared__ ScanShared sh;
+  // the eight column parts of a unit run on one XCD and share its L2
+  const int unit = (int)(blockIdx.x / (8 * kParts)) * 8 + blockIdx.x % 8;
+  const int part = blockIdx.x / 8 % kParts;
+  if (unit >= n_seqs * in.n_v) return;
+  const int s = unit / in.n_v, h = unit % in.n_v, hk = h / (in.n_v / in.n_qk);
+  const int64_t start = row_clip(cu[s], T), end = max(row_clip(cu[s + 1], T), start);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = part * kCols;
+  const int slot = slots ? slots[s] : s;
+  if (slot < 0 || slot >= n_slots) {
+    for (int64_t t = start + tid / kCols; t < end; t += kScanThreads / kCols)
+      o[t * ldo + h * kD + col + tid % kCols] = 0;
+    return;
+  }
+  ChunkSource src;
+  const int64_t place = first_place(start, s);
+  src.unit_step = (int64_t)in.n_v * kUnitBytes;
+  src.unit = ws + place * src.unit_step + (int64_t)h * kUnitBytes;
+  src.head_step = (int64_t)in.n_qk * kHeadBytes;
+  src.head = wsh + place * src.head_step + (int64_t)hk * kHeadBytes;
+  src.v_step = kC * in.ldx;
+  src.v = reinterpret_cast<const uint16_t*>(in.x) + start * in.ldx + in.v_col + h * kD + col;
+  src.o_step = kC * ldo;
+  src.o = o + start * ldo + h * kD + col;
+  src.n_chunks = (int)((end - start + kC - 1) / kC);
+  src.last_rows = (int)(end - start - (int64_t)(src.n_chunks - 1) * kC);
+  if (wave >= 4) return scan_output(src, (uint32_t)ldo * 2, sh, wave - 4, lane);
+
+  const int64_t at = ((int64_t)slot * in.n_v + h) * kD * kD + (32 * wave + 8 * (lane >> 4)) * kD + col + (lane & 15);
+  floatx4_t S[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) S[t][e] = s_in ? s_in[at + (4 * t + e) * kD] : 0.0f;
+  scan_state(src, (uint32_t)in.ldx * 2, sh, wave, lane, S);
   if (s_out) {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s_out[state_at + (4 * t + e) * kD] = S[t][e];
+      for (int e = 0; e < 4; ++e) s_out[at + (4 * t + e) * kD] = S[t][e];
   }
 }
 
@@ -626,7 +690,7 @@ hipError_t launch_gdn_prefill(const GdnRows& in, const int32_t* cu, int n_seqs, 
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t units = (int64_t)n_seqs * in.n_v;
-  gdn_chunk_scan_kernel<<<(unsigned)((units + 7) / 8 * 8 * kParts), 256, 0, stream>>>(
+  gdn_chunk_scan_kernel<<<(unsigned)((units + 7) / 8 * 8 * kParts), kScanThreads, 0, stream>>>(
       in, cu, n_seqs, T, ws, wsh, s_in, s_out, slots, n_slots, static_cast<uint16_t*>(o), ldo);
   return hipGetLastError();
 }
