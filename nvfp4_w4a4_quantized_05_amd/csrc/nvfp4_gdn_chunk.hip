@@ -376,6 +376,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
 //   Output wave w has token rows 16 w .. + 15: Q S from the state's terms that
 // the state waves share, then P W.  It forms both transposed (rows = state
 // columns, lanes = tokens), so that a lane holds four neighbours of a row of o.
+// The output waves also bring V and the row factors to LDS.
+//   Issuing loads bounds the walk as much as the chain of steps does (about 20
+// cycles each on the path to the cache): a chunk takes 63.
 // Accumulator row 4 c + e of state tile t is row 32 w + 8 c + 4 t + e of S, so
 // that a lane's rows of both tiles are eight neighbours.
 constexpr int kCols = 16;
@@ -386,10 +389,11 @@ constexpr int kTStride = 40;  // bf16 per LDS row of a wave's K columns
 struct ScanShared {
   floatx4_t part[4][3][64];    // K S: [token tile][its other waves][lane]
   u32x2_t rest[3][4][64];      // V - diag(a) K S: [term][token tile][lane]
-  u32x2_t wr[4][4][64];        // W: three terms (scaled) for the state, one for o
+  u32x2_t wr[5][4][64];        // W: three terms (scaled) for the state, one for o
   u32x4_t state[4][2][64];     // S's first two terms: [32 rows][term][lane]
   uint16_t kt[4][kC * kTStride];  // [wave]: its 32 columns of K
-  uint16_t v[4][512];             // [wave]: its 16 rows of V (and as much that is not read)
+  uint16_t v[kC * kCols];         // V
+  float vec[2][256];              // row factors a, b, c [64] and e^{G_C} (and as much that is not read)
 };
 
 // One unit's rows and workspace, chunk by chunk; chunks past the end have
@@ -400,6 +404,7 @@ struct ChunkSource {
   const uint16_t* v;     // first row's part of V
   uint16_t* o;
   int64_t unit_step, head_step, v_step, o_step;  // bytes, bytes, values, values per chunk
+  uint32_t v_ld, o_ld;   // bytes per row
   int n_chunks, last_rows;
   __device__ __forceinline__ int rows(int c) const { return c < n_chunks - 1 ? kC : c < n_chunks ? last_rows : 0; }
   __device__ __forceinline__ __amdgpu_buffer_rsrc_t units(int c) const {
@@ -410,56 +415,47 @@ struct ChunkSource {
   }
 };
 
+// kB: blocks of 32 columns that a wave's 16 rows of T and P have left of the
+// diagonal: 1 for waves 0 and 1, 2 for waves 2 and 3.
+template <int kB>
 struct StateOperands {
   u32x4_t k[4];      // [t]: token tile (w + t) % 4
-  u32x4_t t[3][2];   // [term][32 columns]
-  u32x4_t v;         // lanes 0-31: half a row of V, row lane / 2
-  floatx4_t a, c;    // token rows 16 w + 4 g + e
-  float decay;
+  u32x4_t t[3][kB];  // [term][32 columns]
 };
 
+template <int kB>
 struct OutputOperands {
-  u32x4_t q[4], p[2];
-  float b;           // token row 16 w + m
+  u32x4_t q[4], p[kB];
+  u32x4_t shared;    // waves 0, 1: half a row of V, row 32 w + lane / 2; wave 2: row factors
 };
 
-__device__ __forceinline__ void scan_state(const ChunkSource& src, uint32_t v_ld, ScanShared& sh, int w, int lane,
+template <int kB>
+__device__ __forceinline__ void scan_state(const ChunkSource& src, ScanShared& sh, int w, int lane,
                                            floatx4_t (&S)[2]) {
   const int m = lane & 15, g = lane >> 4;
   const floatx4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
   typedef __attribute__((address_space(3))) shortx4_t lds_shortx4_t;
 
-  auto fetch_k = [&](int c, StateOperands& f) {
+  auto fetch_k = [&](int c, StateOperands<kB>& f) {
     const __amdgpu_buffer_rsrc_t r = src.heads(c);
 #pragma unroll
     for (int t = 0; t < 4; ++t) f.k[t] = load16b(r, (uint32_t)((4 * w + (w + t) % 4) * kOperand + lane * 16));
   };
-  auto fetch_t = [&](int c, StateOperands& f) {
+  auto fetch_t = [&](int c, StateOperands<kB>& f) {
     const __amdgpu_buffer_rsrc_t r = src.units(c);
 #pragma unroll
-    for (int sb = 0; sb < 2; ++sb) {
-      const uint32_t at = sb <= w / 2 ? (uint32_t)(block_of(w, sb) * kOperand + lane * 16) : kOutside;
+    for (int sb = 0; sb < kB; ++sb)
 #pragma unroll
-      for (int term = 0; term < 3; ++term) f.t[term][sb] = load16b(r, at + term * kBlocks * kOperand);
-    }
-  };
-  auto fetch_v = [&](int c, StateOperands& f) {
-    const __amdgpu_buffer_rsrc_t rv = make_rsrc(src.v + (c < src.n_chunks ? c : 0) * src.v_step, (int64_t)src.rows(c) * v_ld);
-    f.v = load16b(rv, lane < 32 ? (uint32_t)(16 * w + lane / 2) * v_ld + (lane & 1) * 16 : kOutside);
-    const __amdgpu_buffer_rsrc_t r = src.units(c);
-    const uint32_t row = kOffVec + (16 * w + 4 * g) * 4;
-    f.a = __builtin_bit_cast(floatx4_t, load16b(r, row));
-    f.c = __builtin_bit_cast(floatx4_t, load16b(r, row + 2 * kC * 4));
-    f.decay = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, kOffVec + 3 * kC * 4, 0, 0));
+      for (int term = 0; term < 3; ++term)
+        f.t[term][sb] = load16b(r, (uint32_t)((term * kBlocks + block_of(w, sb)) * kOperand + lane * 16));
   };
 
   // One chunk with its operands in f; those of chunk `next` are asked for in
   // pieces between the steps, so that the loads do not queue in front of one.
-  auto chunk = [&](const StateOperands& f, int next, StateOperands& fn) {
-    // K's columns and V's rows, read back transposed below (this wave's own)
+  auto chunk = [&](const StateOperands<kB>& f, int next, StateOperands<kB>& fn) {
+    // K's columns, read back transposed below (this wave's own)
 #pragma unroll
     for (int t = 0; t < 4; ++t) *reinterpret_cast<u32x4_t*>(&sh.kt[w][(16 * ((w + t) % 4) + m) * kTStride + 8 * g]) = f.k[t];
-    *reinterpret_cast<u32x4_t*>(&sh.v[w][lane * 8]) = f.v;
 
     u32x4_t sp[3];
 #pragma unroll
@@ -481,7 +477,6 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, uint32_t v_ld
     for (int t = 0; t < 4; ++t) ks[t] = mfma_bf16(f.k[t], sp[1], ks[t]);
 #pragma unroll
     for (int t = 0; t < 4; ++t) ks[t] = mfma_bf16(f.k[t], sp[0], ks[t]);
-    fetch_v(next, fn);
     // tile (w + t) % 4 goes to its wave; this wave's own is t = 0
 #pragma unroll
     for (int t = 1; t < 4; ++t) sh.part[(w + t) % 4][t - 1][lane] = ks[t];
@@ -496,11 +491,14 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, uint32_t v_ld
     }
     // lane 4 j + c of a group of 16 reads columns 4 c .. + 3 of row 4 g + j; the lanes get them back by column
     const u32x2_t vt = __builtin_bit_cast(
-        u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4_t*)&sh.v[w][(4 * g + m / 4) * kCols + 4 * (m % 4)]));
+        u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4_t*)&sh.v[(16 * w + 4 * g + m / 4) * kCols + 4 * (m % 4)]));
+    const floatx4_t fa = *reinterpret_cast<const floatx4_t*>(&sh.vec[0][16 * w + 4 * g]);
+    const floatx4_t fc = *reinterpret_cast<const floatx4_t*>(&sh.vec[0][2 * kC + 16 * w + 4 * g]);
+    const float decay = sh.vec[0][3 * kC];
     float r[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      r[e] = fmaf(-f.a[e], kst[e], __uint_as_float(e & 1 ? vt[e / 2] & 0xFFFF0000u : vt[e / 2] << 16));
+      r[e] = fmaf(-fa[e], kst[e], __uint_as_float(e & 1 ? vt[e / 2] & 0xFFFF0000u : vt[e / 2] << 16));
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       uint32_t hi, mid, lo;
@@ -515,29 +513,47 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, uint32_t v_ld
     // W = T (V - ..): the six products of terms i, j with i + j <= 2
     floatx4_t wt = zero, w1 = zero;
     {
-      u32x4_t rv[3][2];
+      u32x4_t rv[3][kB];
 #pragma unroll
       for (int term = 0; term < 3; ++term)
 #pragma unroll
-        for (int sb = 0; sb < 2; ++sb) rv[term][sb] = join(sh.rest[term][2 * sb][lane], sh.rest[term][2 * sb + 1][lane]);
+        for (int sb = 0; sb < kB; ++sb) rv[term][sb] = join(sh.rest[term][2 * sb][lane], sh.rest[term][2 * sb + 1][lane]);
+      int n = 0;
 #pragma unroll
       for (int order = 2; order >= 0; --order)
 #pragma unroll
-        for (int i = 0; i <= order; ++i) {
-          wt = mfma_bf16(f.t[i][0], rv[order - i][0], wt);
-          w1 = mfma_bf16(f.t[i][1], rv[order - i][1], w1);
-        }
+        for (int i = 0; i <= order; ++i)
+#pragma unroll
+          for (int sb = 0; sb < kB; ++sb) {  // two sums in turn: a product waits for the one before it
+            floatx4_t& acc = n++ % 2 ? w1 : wt;
+            acc = mfma_bf16(f.t[i][sb], rv[order - i][sb], acc);
+          }
     }
+    u32x4_t kT[2][2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int sb = 0; sb < 2; ++sb)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          // as above: lane 4 c + e gets column 8 c + 4 t + e of four token rows
+          const uint16_t* at = &sh.kt[w][(32 * sb + 16 * half + 4 * g + m / 4) * kTStride + 8 * (m % 4) + 4 * t];
+          const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4_t*)at));
+          kT[t][sb][2 * half] = v[0];
+          kT[t][sb][2 * half + 1] = v[1];
+        }
 #pragma unroll
     for (int e = 0; e < 4; ++e) wt[e] += w1[e];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       uint32_t hi, mid, lo;
-      split3(wt[2 * e] * f.c[2 * e], wt[2 * e + 1] * f.c[2 * e + 1], hi, mid, lo);
+      split3(wt[2 * e] * fc[2 * e], wt[2 * e + 1] * fc[2 * e + 1], hi, mid, lo);
       sh.wr[0][w][lane][e] = hi;
       sh.wr[1][w][lane][e] = mid;
       sh.wr[2][w][lane][e] = lo;
-      sh.wr[3][w][lane][e] = pack_bf16(wt[2 * e], wt[2 * e + 1]);
+      const uint32_t p = pack_bf16(wt[2 * e], wt[2 * e + 1]);
+      sh.wr[3][w][lane][e] = p;
+      sh.wr[4][w][lane][e] = pack_bf16(wt[2 * e] - __uint_as_float(p << 16), wt[2 * e + 1] - __uint_as_float(p & 0xFFFF0000u));
     }
     fetch_t(next, fn);
     lds_barrier();
@@ -551,28 +567,16 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, uint32_t v_ld
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) S[t][e] *= f.decay;
-      u32x4_t kT[2];
-#pragma unroll
-      for (int sb = 0; sb < 2; ++sb)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          // as above: lane 4 c + e gets column 8 c + 4 t + e of four token rows
-          const uint16_t* at = &sh.kt[w][(32 * sb + 16 * half + 4 * g + m / 4) * kTStride + 8 * (m % 4) + 4 * t];
-          const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4_t*)at));
-          kT[sb][2 * half] = v[0];
-          kT[sb][2 * half + 1] = v[1];
-        }
+      for (int e = 0; e < 4; ++e) S[t][e] *= decay;
 #pragma unroll
       for (int term = 2; term >= 0; --term)
 #pragma unroll
-        for (int sb = 0; sb < 2; ++sb) S[t] = mfma_bf16(kT[sb], wv[term][sb], S[t]);
+        for (int sb = 0; sb < 2; ++sb) S[t] = mfma_bf16(kT[t][sb], wv[term][sb], S[t]);
     }
   };
 
-  StateOperands f0, f1;
+  StateOperands<kB> f0, f1;
   fetch_k(0, f0);
-  fetch_v(0, f0);
   fetch_t(0, f0);
   int c = 0;
   for (; c + 1 < src.n_chunks; c += 2) {
@@ -582,20 +586,34 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, uint32_t v_ld
   if (c < src.n_chunks) chunk(f0, c + 1, f1);
 }
 
-__device__ __forceinline__ void scan_output(const ChunkSource& src, uint32_t o_ld, ScanShared& sh, int w, int lane) {
+template <int kB>
+__device__ __forceinline__ void scan_output(const ChunkSource& src, ScanShared& sh, int w, int lane) {
   const int m = lane & 15, g = lane >> 4;
-  auto fetch = [&](int c, OutputOperands& f) {
+  auto fetch = [&](int c, OutputOperands<kB>& f) {
     const __amdgpu_buffer_rsrc_t rh = src.heads(c), r = src.units(c);
 #pragma unroll
     for (int i = 0; i < 4; ++i) f.q[i] = load16b(rh, (uint32_t)(kOffQ + (4 * i + w) * kOperand + lane * 16));
 #pragma unroll
-    for (int sb = 0; sb < 2; ++sb)
-      f.p[sb] = load16b(r, sb <= w / 2 ? (uint32_t)(kOffP + block_of(w, sb) * kOperand + lane * 16) : kOutside);
-    f.b = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, kOffVec + (kC + 16 * w + m) * 4, 0, 0));
+    for (int sb = 0; sb < kB; ++sb) f.p[sb] = load16b(r, (uint32_t)(kOffP + block_of(w, sb) * kOperand + lane * 16));
+    if constexpr (kB == 1) {
+      const __amdgpu_buffer_rsrc_t rv =
+          make_rsrc(src.v + (c < src.n_chunks ? c : 0) * src.v_step, (int64_t)src.rows(c) * src.v_ld);
+      f.shared = load16b(rv, (uint32_t)(32 * w + lane / 2) * src.v_ld + (lane & 1) * 16);
+    } else {
+      f.shared = load16b(r, w == 2 ? (uint32_t)(kOffVec + lane * 16) : kOutside);
+    }
   };
-  auto chunk = [&](int c, const OutputOperands& f, OutputOperands& fn) {
+  // what all waves need of a chunk, between the third barrier of the one before and its own first
+  auto share = [&](const OutputOperands<kB>& f) {
+    if constexpr (kB == 1)
+      *reinterpret_cast<u32x4_t*>(&sh.v[512 * w + 8 * lane]) = f.shared;
+    else
+      *reinterpret_cast<u32x4_t*>(&sh.vec[w - 2][4 * lane]) = f.shared;
+  };
+  auto chunk = [&](int c, const OutputOperands<kB>& f, OutputOperands<kB>& fn) {
     fetch(c + 1, fn);
     lds_barrier();
+    const float b = sh.vec[0][kC + 16 * w + m];
     floatx4_t ov = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int term = 1; term >= 0; --term)
@@ -603,18 +621,22 @@ __device__ __forceinline__ void scan_output(const ChunkSource& src, uint32_t o_l
       for (int i = 0; i < 4; ++i) ov = mfma_bf16(sh.state[i][term][lane], f.q[i], ov);
     lds_barrier();
 #pragma unroll
-    for (int e = 0; e < 4; ++e) ov[e] *= f.b;
+    for (int e = 0; e < 4; ++e) ov[e] *= b;
     lds_barrier();
 #pragma unroll
-    for (int sb = 0; sb < 2; ++sb) ov = mfma_bf16(join(sh.wr[3][2 * sb][lane], sh.wr[3][2 * sb + 1][lane]), f.p[sb], ov);
-    const __amdgpu_buffer_rsrc_t ro = make_rsrc(src.o + c * src.o_step, (int64_t)src.rows(c) * o_ld);
+    for (int i = 4; i > 2; --i)
+#pragma unroll
+      for (int sb = 0; sb < kB; ++sb) ov = mfma_bf16(join(sh.wr[i][2 * sb][lane], sh.wr[i][2 * sb + 1][lane]), f.p[sb], ov);
+    const __amdgpu_buffer_rsrc_t ro = make_rsrc(src.o + c * src.o_step, (int64_t)src.rows(c) * src.o_ld);
     u32x2_t out;
     out[0] = pack_bf16(ov[0], ov[1]);
     out[1] = pack_bf16(ov[2], ov[3]);
-    __builtin_amdgcn_raw_buffer_store_b64(out, ro, (uint32_t)(16 * w + m) * o_ld + 8 * g, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b64(out, ro, (uint32_t)(16 * w + m) * src.o_ld + 8 * g, 0, 0);
+    share(fn);
   };
-  OutputOperands f0, f1;
+  OutputOperands<kB> f0, f1;
   fetch(0, f0);
+  share(f0);
   int c = 0;
   for (; c + 1 < src.n_chunks; c += 2) {
     chunk(c, f0, f1);
@@ -654,7 +676,10 @@ __global__ __launch_bounds__(kScanThreads) void gdn_chunk_scan_kernel(
   src.o = o + start * ldo + h * kD + col;
   src.n_chunks = (int)((end - start + kC - 1) / kC);
   src.last_rows = (int)(end - start - (int64_t)(src.n_chunks - 1) * kC);
-  if (wave >= 4) return scan_output(src, (uint32_t)ldo * 2, sh, wave - 4, lane);
+  src.v_ld = (uint32_t)in.ldx * 2;
+  src.o_ld = (uint32_t)ldo * 2;
+  if (wave >= 6) return scan_output<2>(src, sh, wave - 4, lane);
+  if (wave >= 4) return scan_output<1>(src, sh, wave - 4, lane);
 
   const int64_t at = ((int64_t)slot * in.n_v + h) * kD * kD + (32 * wave + 8 * (lane >> 4)) * kD + col + (lane & 15);
   floatx4_t S[2];
@@ -662,7 +687,10 @@ __global__ __launch_bounds__(kScanThreads) void gdn_chunk_scan_kernel(
   for (int t = 0; t < 2; ++t)
 #pragma unroll
     for (int e = 0; e < 4; ++e) S[t][e] = s_in ? s_in[at + (4 * t + e) * kD] : 0.0f;
-  scan_state(src, (uint32_t)in.ldx * 2, sh, wave, lane, S);
+  if (wave < 2)
+    scan_state<1>(src, sh, wave, lane, S);
+  else
+    scan_state<2>(src, sh, wave, lane, S);
   if (s_out) {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
