@@ -453,10 +453,10 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, ScanShared& s
   // One chunk with its operands in f; those of chunk `next` are asked for in
   // pieces between the steps, so that the loads do not queue in front of one.
   auto chunk = [&](const StateOperands<kB>& f, int next, StateOperands<kB>& fn) {
+    __builtin_amdgcn_sched_barrier(0);
     // K's columns, read back transposed below (this wave's own)
 #pragma unroll
     for (int t = 0; t < 4; ++t) *reinterpret_cast<u32x4_t*>(&sh.kt[w][(16 * ((w + t) % 4) + m) * kTStride + 8 * g]) = f.k[t];
-
     u32x4_t sp[3];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -470,13 +470,14 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, ScanShared& s
       }
     floatx4_t ks[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) ks[t] = mfma_bf16(f.k[t], sp[2], zero);
+    for (int t = 0; t < 4; ++t) ks[t] = mfma_bf16(f.k[t], sp[0], zero);
+#pragma unroll
+    for (int term = 1; term < 3; ++term)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) ks[t] = mfma_bf16(f.k[t], sp[term], ks[t]);
     sh.state[w][0][lane] = sp[0];
     sh.state[w][1][lane] = sp[1];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) ks[t] = mfma_bf16(f.k[t], sp[1], ks[t]);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) ks[t] = mfma_bf16(f.k[t], sp[0], ks[t]);
+    __builtin_amdgcn_sched_barrier(0);
     // tile (w + t) % 4 goes to its wave; this wave's own is t = 0
 #pragma unroll
     for (int t = 1; t < 4; ++t) sh.part[(w + t) % 4][t - 1][lane] = ks[t];
