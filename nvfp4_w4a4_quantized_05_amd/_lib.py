@@ -347,30 +347,62 @@ def gdn_recurrence(x: torch.Tensor, *, q_col: int, k_col: int, v_col: int, g_col
 
 _DTYPE_CODE = {torch.float32: 0, torch.bfloat16: 1}  # NVFP4_IN_* and NVFP4_OUT_*
 
+# The calls of a decode step take 2-5 us on the GPU, so what these do per call
+# is kept short: one look at each tensor, addresses passed as plain integers.
 
-def _rows2d(t, what):
-    """A 2-D bf16 or fp32 tensor with unit column stride; returns its dtype code."""
+
+def _rows(t, what):
+    """(address, dtype code, rows, columns, row stride) of a 2-D bf16 or fp32
+    GPU tensor with unit column stride; the stride of one row or fewer is its
+    width."""
     code = _DTYPE_CODE.get(t.dtype)
-    if code is None or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what} must be 2-D bf16 or fp32 with unit column stride, got {t.dtype} {tuple(t.shape)}")
-    return code
+    if code is None or t.dim() != 2:
+        raise ValueError(f"{what} must be 2-D bf16 or fp32, got {t.dtype} {tuple(t.shape)}")
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError(f"{what} must have unit column stride")
+    if not t.is_cuda:
+        raise ValueError("nvfp4 calls take GPU tensors only")
+    return t.data_ptr(), code, rows, cols, ld if rows > 1 else (cols or 1)
 
 
-def _ld(t):
-    """Row stride of a 2-D tensor (of one row or fewer: its columns)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+def _vector(t, dtype, n, what):
+    """Address of a contiguous GPU vector of n values."""
+    if t.dtype != dtype or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} vector of {n} values, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError("nvfp4 calls take GPU tensors only")
+    return t.data_ptr()
 
 
-def _i32_vector(t, n, what):
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous int32 vector of {n} values")
+def _seqlens(t):
+    """(address, sequences) of cu_seqlens."""
+    n = t.shape[0] - 1 if t.dim() == 1 else 0
+    if n < 1:
+        raise ValueError("cu_seqlens must be a vector of n_seqs + 1 >= 2 row numbers")
+    return _vector(t, torch.int32, n + 1, "cu_seqlens"), n
 
 
-def _state_pool(t, shape, dtype, what):
-    """A contiguous [n_slots, *shape] pool; returns n_slots."""
+def _pool(t, dtype, shape, what):
+    """(address, slots) of a contiguous [n_slots, *shape] state pool."""
     if t.dtype != dtype or t.shape[1:] != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous {dtype} [n_slots, {', '.join(map(str, shape))}]")
-    return t.shape[0]
+    if not t.is_cuda:
+        raise ValueError("nvfp4 calls take GPU tensors only")
+    return t.data_ptr(), t.shape[0]
+
+
+def _out_rows(t, rows, cols, what):
+    """_rows of an output of `rows` rows and at least `cols` columns: (address, dtype code, row stride)."""
+    ptr, code, r, c, ld = _rows(t, what)
+    if r != rows or c < cols:
+        raise ValueError(f"{what} must be [{rows}, >= {cols}], got {tuple(t.shape)}")
+    return ptr, code, ld
+
+
+def _raw_stream(stream):
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
 def gdn_prefill(x: torch.Tensor, gates: torch.Tensor, cu_seqlens: torch.Tensor, *, q_col: int, k_col: int,
@@ -383,40 +415,44 @@ def gdn_prefill(x: torch.Tensor, gates: torch.Tensor, cu_seqlens: torch.Tensor, 
     at their columns) and of gates (bf16 or fp32: g and beta at theirs).  It
     starts from slot slots[i] of state_in [n_slots, n_v_heads, 128, 128]
     (zeros if None) and leaves its state in that slot of state_out (which may
-    be state_in).  Returns o, bf16 [T, n_v_heads * 128]; rows of no sequence
-    are not written."""
-    if _rows2d(x, "x") != 1:
+    be state_in).  Returns o, bf16 [T, >= n_v_heads * 128]; rows of no
+    sequence are not written."""
+    if x.dtype != torch.bfloat16:
         raise ValueError("x must be bf16")
-    gates_dtype = _rows2d(gates, "gates")
-    T, n_seqs = x.shape[0], cu_seqlens.shape[0] - 1
-    _i32_vector(cu_seqlens, max(n_seqs, 1) + 1, "cu_seqlens")
-    if gates.shape[0] != T:
+    xp, _, T, _, ldx = _rows(x, "x")
+    gp, gates_dtype, g_rows, _, ldg = _rows(gates, "gates")
+    if g_rows != T:
         raise ValueError("x and gates must have the same rows")
+    cp, n_seqs = _seqlens(cu_seqlens)
+    ip = op = sp = None
     n_slots = n_seqs
-    for t, what in ((state_in, "state_in"), (state_out, "state_out")):
-        if t is not None:
-            n_slots = _state_pool(t, (n_v_heads, 128, 128), torch.float32, what)
-    if state_in is not None and state_out is not None and state_in.shape != state_out.shape:
-        raise ValueError("state_in and state_out must have the same slots")
+    if state_in is not None:
+        ip, n_slots = _pool(state_in, torch.float32, (n_v_heads, 128, 128), "state_in")
+    if state_out is not None:
+        op, n_out = _pool(state_out, torch.float32, (n_v_heads, 128, 128), "state_out")
+        if ip is not None and n_out != n_slots:
+            raise ValueError("state_in and state_out must have the same slots")
+        n_slots = n_out
     if slots is not None:
-        _i32_vector(slots, n_seqs, "slots")
-        if state_in is None and state_out is None:
+        if ip is None and op is None:
             raise ValueError("slots without a state pool")
-    if o is not None:
-        _out_matrix(o, T, n_v_heads * 128, torch.bfloat16)
-    _need_gpu(x, gates, cu_seqlens, state_in, state_out, slots, o, workspace)
+        sp = _vector(slots, torch.int32, n_seqs, "slots")
     if o is None:
         o = torch.empty((T, n_v_heads * 128), dtype=torch.bfloat16, device=x.device)
+    o_ptr, o_dtype, ldo = _out_rows(o, T, n_v_heads * 128, "o")
+    if o_dtype != OUT_BF16:
+        raise ValueError("o must be bf16")
     lib = load()
     need = lib.nvfp4_gdn_prefill_workspace_size(T, n_seqs, n_qk_heads, n_v_heads)
-    if workspace is None and need:
+    if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    have = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    st = lib.nvfp4_gdn_prefill(_ptr(x), _ld(x), q_col, k_col, v_col, _ptr(gates), gates_dtype, _ld(gates), g_col,
-                               beta_col, _ptr(cu_seqlens), n_seqs, T, n_qk_heads, n_v_heads, _ptr(state_in),
-                               _ptr(state_out), _ptr(slots), n_slots, _ptr(o), _ld(o), _ptr(workspace), have,
-                               _stream(stream))
-    _check(st, "nvfp4_gdn_prefill")
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous GPU tensor")
+    st = lib.nvfp4_gdn_prefill(xp, ldx, q_col, k_col, v_col, gp, gates_dtype, ldg, g_col, beta_col, cp, n_seqs, T,
+                               n_qk_heads, n_v_heads, ip, op, sp, n_slots, o_ptr, ldo, workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), _raw_stream(stream))
+    if st:
+        raise Nvfp4Error(st, "nvfp4_gdn_prefill")
     return o
 
 
@@ -426,24 +462,21 @@ def gdn_decode(x: torch.Tensor, gates: torch.Tensor, states: torch.Tensor, *, q_
     """The same recurrence for one new token of each request: row b of x and
     gates (bf16 or fp32) is request b's, slot slots[b] (b if None) of states
     [n_slots, n_v_heads, 128, 128] fp32 is updated in place.  Returns o
-    [batch, n_v_heads * 128] (bf16 or fp32 as given, else x's type); requests
-    whose slot is negative get a row of zeros."""
-    x_dtype, gates_dtype = _rows2d(x, "x"), _rows2d(gates, "gates")
-    B = x.shape[0]
-    if gates.shape[0] != B:
+    [batch, >= n_v_heads * 128] (bf16 or fp32 as given, else x's type);
+    requests whose slot is negative get a row of zeros."""
+    xp, x_dtype, B, _, ldx = _rows(x, "x")
+    gp, gates_dtype, g_rows, _, ldg = _rows(gates, "gates")
+    if g_rows != B:
         raise ValueError("x and gates must have the same rows")
-    n_slots = _state_pool(states, (n_v_heads, 128, 128), torch.float32, "states")
-    if slots is not None:
-        _i32_vector(slots, B, "slots")
+    pp, n_slots = _pool(states, torch.float32, (n_v_heads, 128, 128), "states")
+    sp = _vector(slots, torch.int32, B, "slots") if slots is not None else None
     if o is None:
         o = torch.empty((B, n_v_heads * 128), dtype=x.dtype, device=x.device)
-    o_dtype = _rows2d(o, "o")
-    _out_matrix(o, B, n_v_heads * 128, o.dtype)
-    _need_gpu(x, gates, states, slots, o)
-    st = load().nvfp4_gdn_decode(_ptr(x), x_dtype, _ld(x), q_col, k_col, v_col, _ptr(gates), gates_dtype, _ld(gates),
-                                 g_col, beta_col, B, n_qk_heads, n_v_heads, _ptr(states), _ptr(slots), n_slots,
-                                 _ptr(o), o_dtype, _ld(o), _stream(stream))
-    _check(st, "nvfp4_gdn_decode")
+    op, o_dtype, ldo = _out_rows(o, B, n_v_heads * 128, "o")
+    st = load().nvfp4_gdn_decode(xp, x_dtype, ldx, q_col, k_col, v_col, gp, gates_dtype, ldg, g_col, beta_col, B,
+                                 n_qk_heads, n_v_heads, pp, sp, n_slots, op, o_dtype, ldo, _raw_stream(stream))
+    if st:
+        raise Nvfp4Error(st, "nvfp4_gdn_decode")
     return o
 
 
@@ -455,38 +488,34 @@ def conv_silu(x: torch.Tensor, weight: torch.Tensor, *, cu_seqlens: torch.Tensor
     cu_seqlens (device int32), or, without cu_seqlens, for one new row of each
     request.  state [n_slots, width - 1, channels] (x's type) holds the last
     inputs of each request, read and updated in slot slots[i].  Returns out
-    [T, channels] of x's type."""
-    dtype = _rows2d(x, "x")
-    T, channels = x.shape
+    [T, >= channels] of x's type."""
+    xp, dtype, T, channels, ldx = _rows(x, "x")
     if weight.dtype != torch.float32 or weight.dim() != 2 or weight.shape[0] != channels \
-            or not weight.is_contiguous():
-        raise ValueError("weight must be contiguous float32 [channels, width]")
+            or not weight.is_contiguous() or not weight.is_cuda:
+        raise ValueError("weight must be contiguous float32 [channels, width] on the GPU")
     width = weight.shape[1]
-    n_seqs = T
-    if cu_seqlens is not None:
-        n_seqs = cu_seqlens.shape[0] - 1
-        _i32_vector(cu_seqlens, max(n_seqs, 1) + 1, "cu_seqlens")
-    n_slots = 0
-    if state is not None:
-        n_slots = _state_pool(state, (width - 1, channels), x.dtype, "state")
+    cp, n_seqs = _seqlens(cu_seqlens) if cu_seqlens is not None else (None, T)
+    pp, n_slots = _pool(state, x.dtype, (width - 1, channels), "state") if state is not None else (None, 0)
+    sp = None
     if slots is not None:
-        _i32_vector(slots, n_seqs, "slots")
         if state is None:
             raise ValueError("slots without a state pool")
-    if out is not None:
-        _out_matrix(out, T, channels, x.dtype)
-    _need_gpu(x, weight, cu_seqlens, state, slots, out)
+        sp = _vector(slots, torch.int32, n_seqs, "slots")
     if out is None:
         out = torch.empty((T, channels), dtype=x.dtype, device=x.device)
-    st = load().nvfp4_conv_silu(_ptr(x), dtype, _ld(x), channels, _ptr(weight), width, _ptr(cu_seqlens),
-                                n_seqs if cu_seqlens is not None else 0, T, _ptr(state), _ptr(slots), n_slots,
-                                _ptr(out), _ld(out), _stream(stream))
-    _check(st, "nvfp4_conv_silu")
+    yp, y_dtype, ldy = _out_rows(out, T, channels, "out")
+    if y_dtype != dtype:
+        raise ValueError("out must have the dtype of x")
+    st = load().nvfp4_conv_silu(xp, dtype, ldx, channels, weight.data_ptr(), width, cp, n_seqs if cp else 0, T, pp, sp,
+                                n_slots, yp, ldy, _raw_stream(stream))
+    if st:
+        raise Nvfp4Error(st, "nvfp4_conv_silu")
     return out
 
 
 def _norm_out(rows, cols, out, out_dtype, y_gs, codes, scales, device):
-    """Destinations of a norm's y: (out, codes, scales), made where they are not given."""
+    """Destinations of a norm's y, made where they are not given: (out, its
+    address, dtype code and row stride, codes, scales)."""
     if y_gs is not None:
         _f32_scalars(y_gs, 1, "y_gs")
         if cols % 16:
@@ -497,14 +526,17 @@ def _norm_out(rows, cols, out, out_dtype, y_gs, codes, scales, device):
             scales = torch.empty((rows, cols // 16), dtype=torch.uint8, device=device)
         _u8_matrix(codes, (rows, cols // 2), "codes")
         _u8_matrix(scales, (rows, cols // 16), "scales")
+        _need_gpu(y_gs, codes, scales)
     elif codes is not None or scales is not None:
         raise ValueError("codes and scales need y_gs, the tensor scale")
     if out is None and (y_gs is None or out_dtype is not None):
         out = torch.empty((rows, cols), dtype=out_dtype or torch.bfloat16, device=device)
-    if out is not None:
-        _rows2d(out, "out")
-        _out_matrix(out, rows, cols, out_dtype or out.dtype)
-    return out, codes, scales
+    if out is None:
+        return None, None, 0, 0, codes, scales
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out must have dtype out_dtype")
+    yp, y_dtype, ldy = _out_rows(out, rows, cols, "out")
+    return out, yp, y_dtype, ldy, codes, scales
 
 
 def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor | None = None, scale: float = 1.0,
@@ -516,26 +548,24 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor
     (bf16 or fp32; made in bf16 if neither out nor y_gs is given) and, with
     y_gs, as NVFP4 codes and scales under that tensor scale.  Returns out, or
     with y_gs (out or None, codes, scales)."""
-    x_dtype = _rows2d(x, "x")
-    rows, cols = x.shape
-    if weight.dtype != torch.float32 or weight.shape != (cols,) or not weight.is_contiguous():
-        raise ValueError("weight must be contiguous float32 [cols]")
-    r_dtype = x_dtype
-    for t, what in ((residual, "residual"), (residual_out, "residual_out")):
-        if t is not None:
-            r_dtype = _rows2d(t, what)
-            if t.shape != x.shape:
-                raise ValueError(f"{what} must have the shape of x")
-    if residual is not None and residual_out is not None and residual.dtype != residual_out.dtype:
-        raise ValueError("residual and residual_out must have the same dtype")
-    out, codes, scales = _norm_out(rows, cols, out, out_dtype, y_gs, codes, scales, x.device)
-    _need_gpu(x, weight, residual, residual_out, out, y_gs, codes, scales)
-    st = load().nvfp4_add_rmsnorm(
-        _ptr(x), x_dtype, _ld(x), _ptr(residual), r_dtype, _ld(residual) if residual is not None else 0, scale,
-        _ptr(weight), eps, rows, cols, _ptr(residual_out), _ld(residual_out) if residual_out is not None else 0,
-        _ptr(out), _DTYPE_CODE[out.dtype] if out is not None else 0, _ld(out) if out is not None else 0, _ptr(y_gs),
-        _ptr(codes), _ptr(scales), _stream(stream))
-    _check(st, "nvfp4_add_rmsnorm")
+    xp, x_dtype, rows, cols, ldx = _rows(x, "x")
+    wp = _vector(weight, torch.float32, cols, "weight")
+    rp = tp = None
+    r_dtype, ldr, ldt = x_dtype, 0, 0
+    if residual is not None:
+        rp, r_dtype, r, c, ldr = _rows(residual, "residual")
+        if r != rows or c != cols:
+            raise ValueError("residual must have the shape of x")
+    if residual_out is not None:
+        tp, t_dtype, r, c, ldt = _rows(residual_out, "residual_out")
+        if r != rows or c != cols or (rp is not None and t_dtype != r_dtype):
+            raise ValueError("residual_out must have the shape of x and the dtype of residual")
+        r_dtype = t_dtype
+    out, yp, y_dtype, ldy, codes, scales = _norm_out(rows, cols, out, out_dtype, y_gs, codes, scales, x.device)
+    st = load().nvfp4_add_rmsnorm(xp, x_dtype, ldx, rp, r_dtype, ldr, scale, wp, eps, rows, cols, tp, ldt, yp,
+                                  y_dtype, ldy, _ptr(y_gs), _ptr(codes), _ptr(scales), _raw_stream(stream))
+    if st:
+        raise Nvfp4Error(st, "nvfp4_add_rmsnorm")
     return out if y_gs is None else (out, codes, scales)
 
 
@@ -544,19 +574,17 @@ def rmsnorm_gated(o: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *, eps
                   codes: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
     """y = RMSNorm of each group of weight.numel() columns of o, times weight,
     times silu(z); destinations and return value as for add_rmsnorm."""
-    o_dtype, z_dtype = _rows2d(o, "o"), _rows2d(z, "z")
-    rows, cols = o.shape
-    if weight.dtype != torch.float32 or weight.dim() != 1 or not weight.is_contiguous():
-        raise ValueError("weight must be a contiguous float32 vector")
-    if z.shape != o.shape:
+    op, o_dtype, rows, cols, ldo = _rows(o, "o")
+    zp, z_dtype, z_rows, z_cols, ldz = _rows(z, "z")
+    if z_rows != rows or z_cols != cols:
         raise ValueError("z must have the shape of o")
-    out, codes, scales = _norm_out(rows, cols, out, out_dtype, y_gs, codes, scales, o.device)
-    _need_gpu(o, z, weight, out, y_gs, codes, scales)
-    st = load().nvfp4_rmsnorm_gated(
-        _ptr(o), o_dtype, _ld(o), _ptr(z), z_dtype, _ld(z), _ptr(weight), eps, rows, cols, weight.shape[0], _ptr(out),
-        _DTYPE_CODE[out.dtype] if out is not None else 0, _ld(out) if out is not None else 0, _ptr(y_gs),
-        _ptr(codes), _ptr(scales), _stream(stream))
-    _check(st, "nvfp4_rmsnorm_gated")
+    group = weight.numel()
+    wp = _vector(weight, torch.float32, group, "weight")
+    out, yp, y_dtype, ldy, codes, scales = _norm_out(rows, cols, out, out_dtype, y_gs, codes, scales, o.device)
+    st = load().nvfp4_rmsnorm_gated(op, o_dtype, ldo, zp, z_dtype, ldz, wp, eps, rows, cols, group, yp, y_dtype, ldy,
+                                    _ptr(y_gs), _ptr(codes), _ptr(scales), _raw_stream(stream))
+    if st:
+        raise Nvfp4Error(st, "nvfp4_rmsnorm_gated")
     return out if y_gs is None else (out, codes, scales)
 
 
