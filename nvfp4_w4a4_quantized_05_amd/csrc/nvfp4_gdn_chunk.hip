@@ -50,9 +50,14 @@ constexpr int kOffP = 3 * kBlocks * kOperand;      // after T's three terms
 constexpr int kOffVec = kOffP + kBlocks * kOperand;  // a, b, c [64] and e^{G_C}, fp32
 constexpr int kUnitBytes = kOffVec + 1024;
 // And for a chunk and q/k head: K, then Q, as operands of 16 tokens x 32
-// columns, [32 columns][16 tokens], so that a load is 1 KiB in a row.
+// columns, [32 columns][16 tokens], so that a load is 1 KiB in a row.  K's
+// lanes are turned within each 16 (below) for reading it by columns.
 constexpr int kHeadBytes = 2 * 16 * kOperand;
 constexpr int kOffQ = 16 * kOperand;
+// Place in a K operand of the lane that holds token m's columns 8 g .. + 7:
+// the places of four neighbouring tokens' columns then lie in different LDS
+// banks when they are read column by column.
+__device__ __forceinline__ constexpr int k_place(int m, int g) { return 16 * g + ((m + 4 * g) & 15); }
 __device__ __forceinline__ constexpr int block_of(int w, int s) { return w < 2 ? w : 2 * w - 2 + s; }
 
 constexpr int kBufferFlags = 0x00020000;    // raw buffer, 32-bit data format
@@ -91,6 +96,22 @@ __device__ __forceinline__ int64_t row_clip(int32_t r, int64_t T) { return min(m
 // one partial chunk per sequence, so places need no sum over sequences.
 __device__ __forceinline__ int64_t first_place(int64_t start, int s) { return start / kC + s; }
 
+// The last sequence whose first place is not past `place`: the lanes of a
+// wave look at 64 sequences at once (every place number of the workspace has
+// one; the caller checks that the place is one of its chunks).
+__device__ __forceinline__ int sequence_of(const int32_t* cu, int n_seqs, int64_t T, int64_t place) {
+  const int lane = threadIdx.x & 63;
+  int first = 0, n = n_seqs;
+  while (n > 1) {
+    const int step = (n + 63) / 64, at = first + lane * step;
+    const bool before = lane * step < n && first_place(row_clip(cu[min(at, n_seqs - 1)], T), at) <= place;
+    const int hits = max(__builtin_popcountll(__builtin_amdgcn_ballot_w64(before)), 1);
+    first += (hits - 1) * step;
+    n = min(step, n - (hits - 1) * step);
+  }
+  return first;
+}
+
 // LDS writes made visible to the workgroup without waiting for loads from
 // memory in flight (the next chunk's).
 __device__ __forceinline__ void lds_barrier() {
@@ -111,21 +132,19 @@ constexpr int kKStride = kD + 8;   // bf16 per LDS row of K
 constexpr int kXStride = kC + 4;   // floats per LDS row of A, T
 
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void gdn_chunk_prepare_kernel(GdnRows in, const int32_t* __restrict__ cu, int n_seqs,
-                                                                int64_t T, uint8_t* __restrict__ ws, uint8_t* __restrict__ wsh) {
+                                                                int64_t T, uint8_t* __restrict__ ws, uint8_t* __restrict__ wsh,
+                                                                int split) {
   __shared__ __attribute__((aligned(16))) uint16_t kl[kC * kKStride];
   __shared__ __attribute__((aligned(16))) float X[kC * kXStride];
   // K is read only before the first head's gates; then its place takes four blocks of 16 x 16
   floatx4_t(&yb)[4][64] = *reinterpret_cast<floatx4_t(*)[4][64]>(kl);
   __shared__ float rk_l[kC], rq_l[kC], ghi_l[4][kC], glo_l[4][kC], alpha_l[4][kC], beta_l[4][kC];
 
-  const int hk = blockIdx.x % in.n_qk;
-  const int64_t place = blockIdx.x / in.n_qk;
-  // the last sequence whose first place is not past this one
-  int s = 0, hi = n_seqs - 1;
-  while (s < hi) {
-    const int mid = (s + hi + 1) / 2;
-    if (first_place(row_clip(cu[mid], T), mid) <= place) s = mid; else hi = mid - 1;
-  }
+  // `split` workgroups per chunk and q/k head share its value heads
+  const int group = in.n_v / in.n_qk, heads = group / split;
+  const int hk = blockIdx.x / split % in.n_qk, hv0 = blockIdx.x % split * heads;
+  const int64_t place = blockIdx.x / split / in.n_qk;
+  const int s = __builtin_amdgcn_readfirstlane(sequence_of(cu, n_seqs, T, place));
   const int64_t start = row_clip(cu[s], T), end = row_clip(cu[s + 1], T);
   const int64_t t0 = start + (place - first_place(start, s)) * kC;
   if (place < first_place(start, s) || t0 >= end) return;
@@ -147,8 +166,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
   uint8_t* head = wsh + (place * in.n_qk + hk) * kHeadBytes;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    *reinterpret_cast<u32x4_t*>(head + (4 * i + w) * kOperand + lane * 16) = kf[i];
-    *reinterpret_cast<u32x4_t*>(head + kOffQ + (4 * i + w) * kOperand + lane * 16) = qf[i];
+    if (hv0 == 0) {
+      *reinterpret_cast<u32x4_t*>(head + (4 * i + w) * kOperand + k_place(m, g) * 16) = kf[i];
+      *reinterpret_cast<u32x4_t*>(head + kOffQ + (4 * i + w) * kOperand + lane * 16) = qf[i];
+    }
     *reinterpret_cast<u32x4_t*>(&kl[(16 * w + m) * kKStride + 32 * i + 8 * g]) = kf[i];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -188,9 +209,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
     __builtin_amdgcn_sched_barrier(0);  // one tile's operands at a time
   }
 
-  const int group = in.n_v / in.n_qk;
-  for (int hv = 0; hv < group; ++hv) {
-    const int h = hk * group + hv;
+  for (int hv = 0; hv < heads; ++hv) {
+    const int h = hk * group + hv0 + hv;
     const __amdgpu_buffer_rsrc_t unit = make_rsrc(ws + (place * in.n_v + h) * kUnitBytes, kUnitBytes);
     // the lane's number, unknown to the compiler anew for each head: else it
     // computes every LDS address before the loop and holds them (over 100 registers)
@@ -200,7 +220,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
     if (hv % 4 == 0) {  // the next four heads' gates, one per wave, lane = token: running sums in fp64, base 2
       if (hv > 0) __syncthreads();
       float gate = 0.0f, beta = 0.0f;
-      if (hv + w < group && lane < rows) {
+      if (hv + w < heads && lane < rows) {
         const int64_t at = (t0 + lane) * in.ldg + h + w;
         if (in.gates_bf16) {
           const uint16_t* p = reinterpret_cast<const uint16_t*>(in.gates) + at;
@@ -226,7 +246,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
       glo_l[w][lane] = (float)(sum - (double)ghi);
       alpha_l[w][lane] = __builtin_amdgcn_exp2f((float)step);
       beta_l[w][lane] = beta;
-      if (hv + w < group) {
+      if (hv + w < heads) {
         // row factors: of K S, of Q S, and of the writes to the chunk's end
         float* vec = reinterpret_cast<float*>(ws + (place * in.n_v + h + w) * kUnitBytes + kOffVec);
         vec[lane] = __builtin_amdgcn_exp2f((float)(sum - step)) * rk_l[lane];
@@ -439,7 +459,7 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, ScanShared& s
   auto fetch_k = [&](int c, StateOperands<kB>& f) {
     const __amdgpu_buffer_rsrc_t r = src.heads(c);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) f.k[t] = load16b(r, (uint32_t)((4 * w + (w + t) % 4) * kOperand + lane * 16));
+    for (int t = 0; t < 4; ++t) f.k[t] = load16b(r, (uint32_t)((4 * w + (w + t) % 4) * kOperand + k_place(m, g) * 16));
   };
   auto fetch_t = [&](int c, StateOperands<kB>& f) {
     const __amdgpu_buffer_rsrc_t r = src.units(c);
@@ -700,8 +720,291 @@ __global__ __launch_bounds__(kScanThreads) void gdn_chunk_scan_kernel(
   }
 }
 
+// ---------------------------------------------------------------- the same walk, one wave per 16 columns
+//
+// With many sequences the walk need not be split over waves: here a wave
+// keeps all 128 rows of its 16 columns in registers (eight accumulators) and
+// goes through a chunk alone.  What it multiplies comes out of one product in
+// the lane order that the next one takes, so nothing is exchanged; the eight
+// waves of a workgroup (the 128 columns of one unit) share the chunk's K, Q, T
+// and P in LDS, two buffers deep, with one barrier a chunk.
+constexpr int kWideWaves = 8;
+constexpr int kWideThreads = 64 * kWideWaves;
+
+// The sequence at place n by length, longest first (workgroups start in the
+// order of their numbers, so the long ones are not left for the end); the
+// n-th itself with more sequences than lanes, which level out anyway.
+__device__ __forceinline__ int nth_longest(const int32_t* cu, int n_seqs, int64_t T, int n) {
+  if (n_seqs > 64) return n;
+  const int lane = threadIdx.x & 63;
+  int len = -1, rank = 0;
+  if (lane < n_seqs) len = (int)max(row_clip(cu[lane + 1], T) - row_clip(cu[lane], T), (int64_t)0);
+  for (int j = 0; j < n_seqs; ++j) {
+    const int other = __builtin_amdgcn_readlane(len, j);
+    rank += other > len || (other == len && j < lane);
+  }
+  return __builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < n_seqs && rank == n));
+}
+
+struct WideShared {
+  uint8_t head[2][kHeadBytes];                // [chunk parity]: K and Q
+  uint8_t unit[2][4 * kBlocks * kOperand];    // T and P
+  float vec[2][256];                          // row factors a, b, c [64] and e^{G_C} (and as much that is not read)
+  uint16_t v[kWideWaves][kC * kCols];         // [wave]: V's columns
+};
+
+__global__ __launch_bounds__(kWideThreads) void gdn_chunk_wide_kernel(
+    GdnRows in, const int32_t* __restrict__ cu, int n_seqs, int64_t T, const uint8_t* ws, const uint8_t* wsh,
+    const float* s_in, float* s_out, const int32_t* __restrict__ slots, int n_slots, uint16_t* o, int64_t ldo) {
+  __shared__ __attribute__((aligned(16))) WideShared sh;
+  typedef __attribute__((address_space(3))) shortx4_t lds_shortx4_t;
+  const int h = blockIdx.x % in.n_v, hk = h / (in.n_v / in.n_qk);
+  const int s = nth_longest(cu, n_seqs, T, blockIdx.x / in.n_v);
+  const int64_t start = row_clip(cu[s], T), end = max(row_clip(cu[s + 1], T), start);
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int m = lane & 15, g = lane >> 4;
+  const int col = kCols * w;
+  const int slot = slots ? slots[s] : s;
+  if (slot < 0 || slot >= n_slots) {
+    for (int64_t t = start + tid / kD; t < end; t += kWideThreads / kD) o[t * ldo + h * kD + tid % kD] = 0;
+    return;
+  }
+  const int n_chunks = (int)((end - start + kC - 1) / kC);
+  const int64_t place = first_place(start, s);
+  const uint32_t v_ld = (uint32_t)in.ldx * 2, o_ld = (uint32_t)ldo * 2;
+  auto rows = [&](int c) { return max((int64_t)0, min((int64_t)kC, end - start - (int64_t)c * kC)); };
+  auto units = [&](int c) {
+    return make_rsrc(ws + ((place + (c < n_chunks ? c : 0)) * in.n_v + h) * kUnitBytes, c < n_chunks ? kUnitBytes : 0);
+  };
+  auto heads = [&](int c) {
+    return make_rsrc(wsh + ((place + (c < n_chunks ? c : 0)) * in.n_qk + hk) * kHeadBytes, c < n_chunks ? kHeadBytes : 0);
+  };
+
+  // This wave's share of what goes to LDS: an eighth of K, Q, T and P, its columns of V; the row factors come from
+  // every wave alike.  No branches: a load in one makes its use wait for every load in flight.
+  constexpr int kHeadShare = kHeadBytes / kOperand / kWideWaves, kUnitShare = 4 * kBlocks / kWideWaves;
+  u32x4_t sk[kHeadShare], st[kUnitShare], sv[2], sf;
+  auto stage = [&](int c) {
+    const __amdgpu_buffer_rsrc_t rh = heads(c), ru = units(c);
+#pragma unroll
+    for (int i = 0; i < kHeadShare; ++i) sk[i] = load16b(rh, (uint32_t)((kHeadShare * w + i) * kOperand + lane * 16));
+#pragma unroll
+    for (int i = 0; i < kUnitShare; ++i) st[i] = load16b(ru, (uint32_t)((kUnitShare * w + i) * kOperand + lane * 16));
+    sf = load16b(ru, (uint32_t)(kOffVec + lane * 16));
+    const __amdgpu_buffer_rsrc_t rv =
+        make_rsrc(reinterpret_cast<const uint16_t*>(in.x) + (start + (c < n_chunks ? (int64_t)c * kC : 0)) * in.ldx + in.v_col + h * kD + col,
+                  rows(c) * v_ld);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) sv[i] = load16b(rv, (uint32_t)(32 * i + lane / 2) * v_ld + (lane & 1) * 16);
+  };
+  auto put = [&](int c) {
+    const int p = c & 1;
+#pragma unroll
+    for (int i = 0; i < kHeadShare; ++i)
+      *reinterpret_cast<u32x4_t*>(&sh.head[p][(kHeadShare * w + i) * kOperand + lane * 16]) = sk[i];
+#pragma unroll
+    for (int i = 0; i < kUnitShare; ++i)
+      *reinterpret_cast<u32x4_t*>(&sh.unit[p][(kUnitShare * w + i) * kOperand + lane * 16]) = st[i];
+    *reinterpret_cast<u32x4_t*>(&sh.vec[p][4 * lane]) = sf;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4_t*>(&sh.v[w][512 * i + 8 * lane]) = sv[i];
+  };
+
+  // row 4 c + e of accumulator S[i][t] is row 32 i + 8 c + 4 t + e of S
+  const int64_t at = ((int64_t)slot * in.n_v + h) * kD * kD + 8 * g * kD + col + m;
+  floatx4_t S[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[i][t][e] = s_in ? s_in[at + (32 * i + 4 * t + e) * kD] : 0.0f;
+
+  const floatx4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  stage(0);
+  put(0);
+  for (int c = 0; c < n_chunks; ++c) {
+    lds_barrier();
+    stage(c + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    const uint8_t* k_lds = sh.head[c & 1];
+    const uint8_t* q_lds = k_lds + kOffQ + lane * 16;
+    const uint8_t* t_lds = sh.unit[c & 1] + lane * 16;
+    const uint8_t* p_lds = t_lds + kOffP;
+    const float* vec = sh.vec[c & 1];
+
+    // K S and Q S (the latter transposed: rows = state columns, lanes = tokens)
+    floatx4_t ks[4] = {zero, zero, zero, zero}, qs[4] = {zero, zero, zero, zero};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      u32x4_t sp[3];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t hi, mid, lo;
+          split3(S[i][t][2 * e], S[i][t][2 * e + 1], hi, mid, lo);
+          sp[0][2 * t + e] = hi;
+          sp[1][2 * t + e] = mid;
+          sp[2][2 * t + e] = lo;
+        }
+      u32x4_t k[4], q[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        k[t] = *reinterpret_cast<const u32x4_t*>(k_lds + (4 * i + t) * kOperand + k_place(m, g) * 16);
+        q[t] = *reinterpret_cast<const u32x4_t*>(q_lds + (4 * i + t) * kOperand);
+      }
+      // a product into an accumulator waits for the one before it: eight accumulators in turn
+#pragma unroll
+      for (int term = 0; term < 3; ++term) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) ks[t] = mfma_bf16(k[t], sp[term], ks[t]);
+        if (term < 2)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) qs[t] = mfma_bf16(sp[term], q[t], qs[t]);
+      }
+    }
+
+    // V - diag(a) K S, split in three: [term][32 tokens]
+    u32x4_t rv[3][2];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const u32x2_t vt = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                         (lds_shortx4_t*)&sh.v[w][(16 * t + 4 * g + m / 4) * kCols + 4 * (m % 4)]));
+      const floatx4_t fa = *reinterpret_cast<const floatx4_t*>(&vec[16 * t + 4 * g]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t hi, mid, lo;
+        split3(fmaf(-fa[2 * e], ks[t][2 * e], __uint_as_float(vt[e] << 16)),
+               fmaf(-fa[2 * e + 1], ks[t][2 * e + 1], __uint_as_float(vt[e] & 0xFFFF0000u)), hi, mid, lo);
+        rv[0][t / 2][2 * (t % 2) + e] = hi;
+        rv[1][t / 2][2 * (t % 2) + e] = mid;
+        rv[2][t / 2][2 * (t % 2) + e] = lo;
+      }
+    }
+    // W = T (V - ..), six products; then diag(c) W in three terms and W in two.  Two row tiles at a time, two sums each.
+    u32x4_t wv[3][2], wo[2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      floatx4_t acc[2][2] = {{zero, zero}, {zero, zero}};  // [tile][parity]
+#pragma unroll
+      for (int sb = 0; sb <= u; ++sb) {
+        u32x4_t tf[2][3];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int term = 0; term < 3; ++term)
+            tf[t][term] = *reinterpret_cast<const u32x4_t*>(t_lds + (term * kBlocks + block_of(2 * u + t, sb)) * kOperand);
+        int n = 0;
+#pragma unroll
+        for (int order = 0; order < 3; ++order)
+#pragma unroll
+          for (int i = 0; i <= order; ++i, ++n)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) acc[t][n % 2] = mfma_bf16(tf[t][i], rv[order - i][sb], acc[t][n % 2]);
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const floatx4_t fc = *reinterpret_cast<const floatx4_t*>(&vec[2 * kC + 32 * u + 16 * t + 4 * g]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x = acc[t][0][2 * e] + acc[t][1][2 * e], y = acc[t][0][2 * e + 1] + acc[t][1][2 * e + 1];
+          uint32_t hi, mid, lo;
+          split3(x * fc[2 * e], y * fc[2 * e + 1], hi, mid, lo);
+          wv[0][u][2 * t + e] = hi;
+          wv[1][u][2 * t + e] = mid;
+          wv[2][u][2 * t + e] = lo;
+          const uint32_t b = pack_bf16(x, y);
+          wo[0][u][2 * t + e] = b;
+          wo[1][u][2 * t + e] = pack_bf16(x - __uint_as_float(b << 16), y - __uint_as_float(b & 0xFFFF0000u));
+        }
+      }
+    }
+    // O = b Q S + P W, transposed like Q S
+    const __amdgpu_buffer_rsrc_t ro = make_rsrc(o + (start + (int64_t)c * kC) * ldo + h * kD + col, rows(c) * o_ld);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const float b = vec[kC + 16 * t + m];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) qs[t][e] *= b;
+    }
+#pragma unroll
+    for (int sb = 0; sb < 2; ++sb) {
+      u32x4_t p[4];
+#pragma unroll
+      for (int t = 2 * sb; t < 4; ++t) p[t] = *reinterpret_cast<const u32x4_t*>(p_lds + block_of(t, sb) * kOperand);
+#pragma unroll
+      for (int term = 0; term < 2; ++term)
+#pragma unroll
+        for (int t = 2 * sb; t < 4; ++t) qs[t] = mfma_bf16(wo[term][sb], p[t], qs[t]);
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      u32x2_t out;
+      out[0] = pack_bf16(qs[t][0], qs[t][1]);
+      out[1] = pack_bf16(qs[t][2], qs[t][3]);
+      __builtin_amdgcn_raw_buffer_store_b64(out, ro, (uint32_t)(16 * t + m) * o_ld + 8 * g, 0, 0);
+    }
+
+    // S' = e^{G_C} S + K^T (c W)
+    const float decay = vec[3 * kC];
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {  // four accumulators in turn
+#pragma unroll
+      for (int i = j; i < j + 2; ++i)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[i][t][e] *= decay;
+#pragma unroll
+      for (int sb = 0; sb < 2; ++sb) {
+        u32x4_t kT[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              // lane 4 c + e of a group of 16 gets column 8 c + 4 t + e of token rows 4 g .. + 3
+              const uint8_t* from =
+                  k_lds + (4 * (j + i) + 2 * sb + half) * kOperand + k_place(4 * g + m / 4, m % 4) * 16 + 8 * t;
+              const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4_t*)from));
+              kT[i][t][2 * half] = v[0];
+              kT[i][t][2 * half + 1] = v[1];
+            }
+#pragma unroll
+        for (int term = 0; term < 3; ++term)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) S[j + i][t] = mfma_bf16(kT[i][t], wv[term][sb], S[j + i][t]);
+      }
+    }
+    put(c + 1);
+  }
+  if (s_out) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s_out[at + (32 * i + 4 * t + e) * kD] = S[i][t][e];
+  }
+}
+
 // Places in the workspace: first_place() of the last sequence plus its chunks is at most this.
 int64_t chunk_places(int64_t T, int64_t n_seqs) { return T / kC + n_seqs + 1; }
+
+// From this many sequences x value heads on, one workgroup walks a whole unit.
+// It needs about half the CU time per chunk, but leaves a CU to each unit and
+// takes 5.2 us a chunk instead of 1.3, so a few long units would be left over.
+// Measured, split / whole, 32 value heads: 32,768 tokens in 48 sequences 983 /
+// 654 us, in 16 (512 units) 885 / 795 us; 16,384 in 8 (256 units) 470 / 639 us.
+constexpr int64_t kWideUnits = 512;
+// Below this many chunks x q/k heads, the preparation takes one workgroup per
+// value head instead of one per q/k head (which makes the group's K and Q
+// products once): 300 tokens x 4 heads 11 -> 9 us.
+constexpr int64_t kFewChunkHeads = 256;
 
 }  // namespace
 
@@ -714,13 +1017,18 @@ hipError_t launch_gdn_prefill(const GdnRows& in, const int32_t* cu, int n_seqs, 
                               hipStream_t stream) {
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint8_t* wsh = ws + chunk_places(T, n_seqs) * in.n_v * kUnitBytes;
-  gdn_chunk_prepare_kernel<<<(unsigned)(chunk_places(T, n_seqs) * in.n_qk), 256, 0, stream>>>(in, cu, n_seqs, T, ws,
-                                                                                                       wsh);
+  const int64_t chunk_heads = chunk_places(T, n_seqs) * in.n_qk;
+  const int split = chunk_heads < kFewChunkHeads ? in.n_v / in.n_qk : 1;
+  gdn_chunk_prepare_kernel<<<(unsigned)(chunk_heads * split), 256, 0, stream>>>(in, cu, n_seqs, T, ws, wsh, split);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t units = (int64_t)n_seqs * in.n_v;
-  gdn_chunk_scan_kernel<<<(unsigned)((units + 7) / 8 * 8 * kParts), kScanThreads, 0, stream>>>(
-      in, cu, n_seqs, T, ws, wsh, s_in, s_out, slots, n_slots, static_cast<uint16_t*>(o), ldo);
+  if (units >= kWideUnits)
+    gdn_chunk_wide_kernel<<<(unsigned)units, kWideThreads, 0, stream>>>(
+        in, cu, n_seqs, T, ws, wsh, s_in, s_out, slots, n_slots, static_cast<uint16_t*>(o), ldo);
+  else
+    gdn_chunk_scan_kernel<<<(unsigned)((units + 7) / 8 * 8 * kParts), kScanThreads, 0, stream>>>(
+        in, cu, n_seqs, T, ws, wsh, s_in, s_out, slots, n_slots, static_cast<uint16_t*>(o), ldo);
   return hipGetLastError();
 }
 

@@ -160,6 +160,32 @@ def test_prefill_hard_values(kind):
     _prefill([200, 64, 1, 77], 2, 4, kind=kind, seed=5)
 
 
+@pytest.mark.parametrize("lens,n_qk,n_v,gates", [
+    ([1, 70, 0, 64, 130, 3, 63, 65] * 8, 2, 8, BF),              # 64 sequences x 8 heads
+    ([2, 66, 0, 1, 129] * 14, 1, 8, F32)])                       # 70 sequences x 8 heads
+def test_prefill_many_sequences(lens, n_qk, n_v, gates):
+    _prefill(lens, n_qk, n_v, gates=gates, seed=len(lens), pad=1, tail=3, skip=(4, 7, 23), separate=True)
+
+
+def test_prefill_many_sequences_hard_values():
+    _prefill([64, 20, 70] * 22, 1, 8, kind="reset", seed=21)
+    _prefill([30, 129] * 32, 2, 8, kind="scales", seed=22)
+    _prefill([200] + [5] * 63, 1, 8, kind="hold", seed=23)
+
+
+def test_prefill_of_a_sequence_does_not_depend_on_how_many_there_are():
+    """Both walks over the chunks (few sequences, many) against each other: o within the rounding of its products."""
+    x, gates, lay = _tensors(64 * 40, 2, 8, 24)
+    one = torch.zeros((1, 8, D, D), device=x.device)
+    many = torch.zeros((64, 8, D, D), device=x.device)
+    o = nv.gdn_prefill(x, gates, torch.arange(0, 65 * 40, 40, dtype=torch.int32, device=x.device), **lay, state_out=many)
+    for i in (0, 17, 63):
+        r = slice(40 * i, 40 * i + 40)
+        a = nv.gdn_prefill(x[r].contiguous(), gates[r].contiguous(), _cu(0, 40), **lay, state_out=one)
+        assert torch.allclose(a.float(), o[r].float(), rtol=2.0 ** -6, atol=2.0 ** -8 * float(a.float().abs().max()))
+        assert float((one[0] - many[i]).norm()) <= 40 * 400 * U * float(many[i].norm())
+
+
 def test_prefill_long():
     _prefill([2500], 1, 2, seed=9)
     _prefill([1500], 1, 1, kind="hold", seed=10)
