@@ -402,7 +402,7 @@ def _out_rows(t, rows, cols, what):
 
 
 def _raw_stream(stream):
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
 
 
 def gdn_prefill(x: torch.Tensor, gates: torch.Tensor, cu_seqlens: torch.Tensor, *, q_col: int, k_col: int,

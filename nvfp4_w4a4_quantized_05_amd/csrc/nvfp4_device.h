@@ -60,6 +60,23 @@ __device__ __forceinline__ float silu(float z) {
   return (z * 0x1p-24f) * __builtin_amdgcn_rcpf(e + 0x1p-24f);
 }
 
+// The largest i in 0 .. n - 1 for which before(i) holds, before(0) taken as
+// true and before true up to some i only: the wave's lanes ask about 64
+// places at a time.  All lanes of the wave must be active.
+template <class F>
+__device__ __forceinline__ int last_before(int n, F before) {
+  const int lane = threadIdx.x & 63;
+  int first = 0;
+  while (n > 1) {
+    const int step = (n + 63) / 64;
+    const bool yes = lane * step < n && before(first + lane * step);
+    const int hits = max(__builtin_popcountll(__builtin_amdgcn_ballot_w64(yes)), 1);
+    first += (hits - 1) * step;
+    n = min(step, n - (hits - 1) * step);
+  }
+  return __builtin_amdgcn_readfirstlane(first);
+}
+
 // Sum over the wave's 64 lanes, the same bits in every lane: each step adds
 // the same two values in either order.
 __device__ __forceinline__ float wave_sum64(float v) {

@@ -96,22 +96,6 @@ __device__ __forceinline__ int64_t row_clip(int32_t r, int64_t T) { return min(m
 // one partial chunk per sequence, so places need no sum over sequences.
 __device__ __forceinline__ int64_t first_place(int64_t start, int s) { return start / kC + s; }
 
-// The last sequence whose first place is not past `place`: the lanes of a
-// wave look at 64 sequences at once (every place number of the workspace has
-// one; the caller checks that the place is one of its chunks).
-__device__ __forceinline__ int sequence_of(const int32_t* cu, int n_seqs, int64_t T, int64_t place) {
-  const int lane = threadIdx.x & 63;
-  int first = 0, n = n_seqs;
-  while (n > 1) {
-    const int step = (n + 63) / 64, at = first + lane * step;
-    const bool before = lane * step < n && first_place(row_clip(cu[min(at, n_seqs - 1)], T), at) <= place;
-    const int hits = max(__builtin_popcountll(__builtin_amdgcn_ballot_w64(before)), 1);
-    first += (hits - 1) * step;
-    n = min(step, n - (hits - 1) * step);
-  }
-  return first;
-}
-
 // LDS writes made visible to the workgroup without waiting for loads from
 // memory in flight (the next chunk's).
 __device__ __forceinline__ void lds_barrier() {
@@ -144,7 +128,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
   const int group = in.n_v / in.n_qk, heads = group / split;
   const int hk = blockIdx.x / split % in.n_qk, hv0 = blockIdx.x % split * heads;
   const int64_t place = blockIdx.x / split / in.n_qk;
-  const int s = __builtin_amdgcn_readfirstlane(sequence_of(cu, n_seqs, T, place));
+  // the last sequence whose first place is not past this one
+  const int s = last_before(n_seqs, [&](int i) { return first_place(row_clip(cu[i], T), i) <= place; });
   const int64_t start = row_clip(cu[s], T), end = row_clip(cu[s + 1], T);
   const int64_t t0 = start + (place - first_place(start, s)) * kC;
   if (place < first_place(start, s) || t0 >= end) return;
