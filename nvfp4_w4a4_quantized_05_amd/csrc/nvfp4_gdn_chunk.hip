@@ -74,6 +74,26 @@ __device__ __forceinline__ floatx4_t mfma_bf16(u32x4_t a, u32x4_t b, floatx4_t c
                                                  0, 0, 0);
 }
 
+// Behind the last matrix instructions of a step, with their A and B operands:
+// keeps those registers taken for four more cycles of issue.  A vector
+// instruction that wrote such a register right behind the matrix instruction
+// was seen to change its operand on gfx950, and the compiler puts no wait
+// states there.  A CPU test looks for closer ones in the compiled code.
+__device__ __forceinline__ void hold(const u32x4_t& x) { __asm__ volatile("" ::"v"(x)); }
+__device__ __forceinline__ void hold(const floatx4_t& x) { __asm__ volatile("" ::"v"(x)); }
+template <class X, int N>
+__device__ __forceinline__ void hold(const X (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) hold(x[i]);
+}
+template <class... X>
+__device__ __forceinline__ void mfma_settle(const X&... x) {
+  __builtin_amdgcn_sched_barrier(0);
+  __asm__ volatile("s_nop 3");
+  (hold(x), ...);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // a = hi + mid + lo exactly, each a bf16 (hi rounded to nearest); two values packed.
 __device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
   hi = pack_bf16(a, b);
@@ -179,12 +199,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
   for (int j = 0; j < 4; ++j) {
     kk[j] = qk[j] = floatx4_t{0.0f, 0.0f, 0.0f, 0.0f};
     if (j > w) continue;
+    u32x4_t a[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const u32x4_t a = *reinterpret_cast<const u32x4_t*>(&kl[(16 * j + m) * kKStride + 32 * i + 8 * g]);
-      kk[j] = mfma_bf16(a, kf[i], kk[j]);
-      qk[j] = mfma_bf16(a, qf[i], qk[j]);
+      a[i] = *reinterpret_cast<const u32x4_t*>(&kl[(16 * j + m) * kKStride + 32 * i + 8 * g]);
+      kk[j] = mfma_bf16(a[i], kf[i], kk[j]);
+      qk[j] = mfma_bf16(a[i], qf[i], qk[j]);
     }
+    mfma_settle(a, kf, qf);
     const floatx4_t rk = *reinterpret_cast<const floatx4_t*>(&rk_l[16 * j + 4 * g]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -310,6 +332,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
     auto product = [&](floatx4_t a, floatx4_t b, floatx4_t acc) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], acc, 0, 0, 0);
+      mfma_settle(a, b);
       return acc;
     };
     auto put = [&](int r, int c, floatx4_t v) {
@@ -480,6 +503,7 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, ScanShared& s
     for (int term = 1; term < 3; ++term)
 #pragma unroll
       for (int t = 0; t < 4; ++t) ks[t] = mfma_bf16(f.k[t], sp[term], ks[t]);
+    mfma_settle(f.k, sp);
     sh.state[w][0][lane] = sp[0];
     sh.state[w][1][lane] = sp[1];
     __builtin_amdgcn_sched_barrier(0);
@@ -534,6 +558,7 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, ScanShared& s
             floatx4_t& acc = n++ % 2 ? w1 : wt;
             acc = mfma_bf16(f.t[i][sb], rv[order - i][sb], acc);
           }
+      mfma_settle(f.t, rv);
     }
     u32x4_t kT[2][2];
 #pragma unroll
@@ -579,6 +604,7 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, ScanShared& s
 #pragma unroll
         for (int sb = 0; sb < 2; ++sb) S[t] = mfma_bf16(kT[t][sb], wv[term][sb], S[t]);
     }
+    mfma_settle(kT, wv);
   };
 
   StateOperands<kB> f0, f1;
@@ -621,18 +647,28 @@ __device__ __forceinline__ void scan_output(const ChunkSource& src, ScanShared& 
     lds_barrier();
     const float b = sh.vec[0][kC + 16 * w + m];
     floatx4_t ov = {0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4_t st[2][4];
 #pragma unroll
     for (int term = 1; term >= 0; --term)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ov = mfma_bf16(sh.state[i][term][lane], f.q[i], ov);
+      for (int i = 0; i < 4; ++i) {
+        st[term][i] = sh.state[i][term][lane];
+        ov = mfma_bf16(st[term][i], f.q[i], ov);
+      }
+    mfma_settle(st, f.q);
     lds_barrier();
 #pragma unroll
     for (int e = 0; e < 4; ++e) ov[e] *= b;
     lds_barrier();
+    u32x4_t wo[2][kB];
 #pragma unroll
-    for (int i = 4; i > 2; --i)
+    for (int i = 1; i >= 0; --i)
 #pragma unroll
-      for (int sb = 0; sb < kB; ++sb) ov = mfma_bf16(join(sh.wr[i][2 * sb][lane], sh.wr[i][2 * sb + 1][lane]), f.p[sb], ov);
+      for (int sb = 0; sb < kB; ++sb) {
+        wo[i][sb] = join(sh.wr[3 + i][2 * sb][lane], sh.wr[3 + i][2 * sb + 1][lane]);
+        ov = mfma_bf16(wo[i][sb], f.p[sb], ov);
+      }
+    mfma_settle(wo, f.p);
     const __amdgpu_buffer_rsrc_t ro = make_rsrc(src.o + c * src.o_step, (int64_t)src.rows(c) * src.o_ld);
     u32x2_t out;
     out[0] = pack_bf16(ov[0], ov[1]);
@@ -848,6 +884,7 @@ __global__ __launch_bounds__(kWideThreads) void gdn_chunk_wide_kernel(
 #pragma unroll
           for (int t = 0; t < 4; ++t) qs[t] = mfma_bf16(sp[term], q[t], qs[t]);
       }
+      mfma_settle(sp, k, q);
     }
 
     // V - diag(a) K S, split in three: [term][32 tokens]
@@ -887,6 +924,7 @@ __global__ __launch_bounds__(kWideThreads) void gdn_chunk_wide_kernel(
           for (int i = 0; i <= order; ++i, ++n)
 #pragma unroll
             for (int t = 0; t < 2; ++t) acc[t][n % 2] = mfma_bf16(tf[t][i], rv[order - i][sb], acc[t][n % 2]);
+        mfma_settle(tf, rv);
       }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -922,6 +960,7 @@ __global__ __launch_bounds__(kWideThreads) void gdn_chunk_wide_kernel(
       for (int term = 0; term < 2; ++term)
 #pragma unroll
         for (int t = 2 * sb; t < 4; ++t) qs[t] = mfma_bf16(wo[term][sb], p[t], qs[t]);
+      mfma_settle(p[2], p[3], wo);
     }
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -963,6 +1002,7 @@ __global__ __launch_bounds__(kWideThreads) void gdn_chunk_wide_kernel(
           for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int t = 0; t < 2; ++t) S[j + i][t] = mfma_bf16(kT[i][t], wv[term][sb], S[j + i][t]);
+        mfma_settle(kT, wv);
       }
     }
     put(c + 1);
