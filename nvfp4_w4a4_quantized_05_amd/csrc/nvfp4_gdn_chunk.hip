@@ -18,7 +18,9 @@
 // the matrix cores.  S, T, V - ... and W are fp32 and enter as the sum of three
 // bf16 numbers (8 + 8 + 8 bits: exact), with the six largest of the nine
 // products where both sides are split: the state is as exact as an fp32 sum.
-// For O alone, whose result is bf16, S, P and W are rounded to bf16 once.
+// For O alone, whose result is bf16, S and W enter as their first two terms
+// and P is rounded to bf16 once: o is 0.0021 (2-norm, relative) off the 64-bit
+// result where rounding that to bf16 costs 0.0017.
 // Decays inside a chunk are exponentials of differences of G, which is summed
 // in fp64 and kept as two floats, so that a strong decay before both tokens
 // does not cost the difference its digits.
@@ -65,8 +67,8 @@ constexpr uint32_t kOutside = 0x80000000u;  // an offset past every resource use
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, kBufferFlags);
 }
-__device__ __forceinline__ u32x4_t load16b(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+__device__ __forceinline__ u32x4_t load16b(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t wave_off = 0) {
+  return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, wave_off, 0));
 }
 
 __device__ __forceinline__ floatx4_t mfma_bf16(u32x4_t a, u32x4_t b, floatx4_t c) {
@@ -406,7 +408,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
 // columns, lanes = tokens), so that a lane holds four neighbours of a row of o.
 // The output waves also bring V and the row factors to LDS.
 //   Issuing loads bounds the walk as much as the chain of steps does (about 20
-// cycles each on the path to the cache): a chunk takes 63.
+// cycles each on the path to the cache): a chunk takes 63.  Up to 128 registers
+// two workgroups share a CU, which takes 16,384 tokens in 8 sequences (32 value
+// heads) from 483 to 433 us; hence offsets that a wave has in common are kept in
+// scalar registers.
 // Accumulator row 4 c + e of state tile t is row 32 w + 8 c + 4 t + e of S, so
 // that a lane's rows of both tiles are eight neighbours.
 constexpr int kCols = 16;
@@ -425,7 +430,7 @@ struct ScanShared {
 };
 
 // One unit's rows and workspace, chunk by chunk; chunks past the end have
-// empty resources, whose loads read nothing.
+// empty resources (at chunk 0's address), and nothing uses what they load.
 struct ChunkSource {
   const uint8_t* unit;   // of chunk 0
   const uint8_t* head;
@@ -467,7 +472,7 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, ScanShared& s
   auto fetch_k = [&](int c, StateOperands<kB>& f) {
     const __amdgpu_buffer_rsrc_t r = src.heads(c);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) f.k[t] = load16b(r, (uint32_t)((4 * w + (w + t) % 4) * kOperand + k_place(m, g) * 16));
+    for (int t = 0; t < 4; ++t) f.k[t] = load16b(r, (uint32_t)(k_place(m, g) * 16), (uint32_t)((4 * w + (w + t) % 4) * kOperand));
   };
   auto fetch_t = [&](int c, StateOperands<kB>& f) {
     const __amdgpu_buffer_rsrc_t r = src.units(c);
@@ -475,7 +480,7 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, ScanShared& s
     for (int sb = 0; sb < kB; ++sb)
 #pragma unroll
       for (int term = 0; term < 3; ++term)
-        f.t[term][sb] = load16b(r, (uint32_t)((term * kBlocks + block_of(w, sb)) * kOperand + lane * 16));
+        f.t[term][sb] = load16b(r, (uint32_t)(lane * 16), (uint32_t)((term * kBlocks + block_of(w, sb)) * kOperand));
   };
 
   // One chunk with its operands in f; those of chunk `next` are asked for in
@@ -687,6 +692,21 @@ __device__ __forceinline__ void scan_output(const ChunkSource& src, ScanShared& 
   if (c < src.n_chunks) chunk(c, f0, f1);
 }
 
+// The sequence at place n by length, longest first (workgroups start in the
+// order of their numbers, so the long ones are not left for the end); the
+// n-th itself with more sequences than lanes, which level out anyway.
+__device__ __forceinline__ int nth_longest(const int32_t* cu, int n_seqs, int64_t T, int n) {
+  if (n_seqs < 2 || n_seqs > 64) return n;
+  const int lane = threadIdx.x & 63;
+  int len = -1, rank = 0;
+  if (lane < n_seqs) len = (int)max(row_clip(cu[lane + 1], T) - row_clip(cu[lane], T), (int64_t)0);
+  for (int j = 0; j < n_seqs; ++j) {
+    const int other = __builtin_amdgcn_readlane(len, j);
+    rank += other > len || (other == len && j < lane);
+  }
+  return __builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < n_seqs && rank == n));
+}
+
 __global__ __launch_bounds__(kScanThreads) void gdn_chunk_scan_kernel(
     GdnRows in, const int32_t* __restrict__ cu, int n_seqs, int64_t T, const uint8_t* ws, const uint8_t* wsh,
     const float* s_in, float* s_out, const int32_t* __restrict__ slots, int n_slots,
@@ -696,7 +716,7 @@ __global__ __launch_bounds__(kScanThreads) void gdn_chunk_scan_kernel(
   const int unit = (int)(blockIdx.x / (8 * kParts)) * 8 + blockIdx.x % 8;
   const int part = blockIdx.x / 8 % kParts;
   if (unit >= n_seqs * in.n_v) return;
-  const int s = unit / in.n_v, h = unit % in.n_v, hk = h / (in.n_v / in.n_qk);
+  const int s = nth_longest(cu, n_seqs, T, unit / in.n_v), h = unit % in.n_v, hk = h / (in.n_v / in.n_qk);
   const int64_t start = row_clip(cu[s], T), end = max(row_clip(cu[s + 1], T), start);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = part * kCols;
@@ -751,21 +771,6 @@ __global__ __launch_bounds__(kScanThreads) void gdn_chunk_scan_kernel(
 // and P in LDS, two buffers deep, with one barrier a chunk.
 constexpr int kWideWaves = 8;
 constexpr int kWideThreads = 64 * kWideWaves;
-
-// The sequence at place n by length, longest first (workgroups start in the
-// order of their numbers, so the long ones are not left for the end); the
-// n-th itself with more sequences than lanes, which level out anyway.
-__device__ __forceinline__ int nth_longest(const int32_t* cu, int n_seqs, int64_t T, int n) {
-  if (n_seqs > 64) return n;
-  const int lane = threadIdx.x & 63;
-  int len = -1, rank = 0;
-  if (lane < n_seqs) len = (int)max(row_clip(cu[lane + 1], T) - row_clip(cu[lane], T), (int64_t)0);
-  for (int j = 0; j < n_seqs; ++j) {
-    const int other = __builtin_amdgcn_readlane(len, j);
-    rank += other > len || (other == len && j < lane);
-  }
-  return __builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < n_seqs && rank == n));
-}
 
 struct WideShared {
   uint8_t head[2][kHeadBytes];                // [chunk parity]: K and Q
@@ -1023,8 +1028,8 @@ int64_t chunk_places(int64_t T, int64_t n_seqs) { return T / kC + n_seqs + 1; }
 // From this many sequences x value heads on, one workgroup walks a whole unit.
 // It needs about half the CU time per chunk, but leaves a CU to each unit and
 // takes 5.2 us a chunk instead of 1.3, so a few long units would be left over.
-// Measured, split / whole, 32 value heads: 32,768 tokens in 48 sequences 983 /
-// 654 us, in 16 (512 units) 885 / 795 us; 16,384 in 8 (256 units) 470 / 639 us.
+// Measured, split / whole, 32 value heads: 32,768 tokens in 48 sequences 883 /
+// 631 us, in 16 (512 units) 823 / 781 us; 16,384 in 8 (256 units) 433 / 632 us.
 constexpr int64_t kWideUnits = 512;
 // Below this many chunks x q/k heads, the preparation takes one workgroup per
 // value head instead of one per q/k head (which makes the group's K and Q
