@@ -453,7 +453,10 @@ NVFP4_API nvfp4_status_t nvfp4_harmonize_fused_scales(uint8_t* scales, const flo
  *   workspace   device scratch, 256-byte aligned, of at least
  *               nvfp4_gdn_prefill_workspace_size() bytes, overwritten
  * Gates are expected non-positive and write strengths in [0, 1] (then the
- * state cannot grow); other values follow the same formulas.
+ * state cannot grow); other values follow the same formulas.  What is not
+ * finite reaches what it reaches token by token: in q_t the outputs of that
+ * token and head, in k_t or a gate the outputs from t on and the state, in v_t
+ * the same of its column; nothing before t and no other sequence.
  */
 NVFP4_API nvfp4_status_t nvfp4_gdn_prefill(const void* x, int64_t ldx, int64_t q_col, int64_t k_col, int64_t v_col,
                                            const void* gates, int32_t gates_dtype, int64_t ldg, int64_t g_col,

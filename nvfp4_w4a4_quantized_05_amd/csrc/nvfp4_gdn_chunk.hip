@@ -24,6 +24,16 @@
 // Decays inside a chunk are exponentials of differences of G, which is summed
 // in fp64 and kept as two floats, so that a strong decay before both tokens
 // does not cost the difference its digits.
+//
+// Infinities and NaN.  Token by token, one in q_t reaches o_t alone, one in k_t
+// or a gate every output from t on, one in column c of v_t that column's; an
+// earlier token's output is never touched.  In a product over a chunk it would
+// be, by the zeros above the diagonals of T and P.  So a k, gate or v that is
+// not finite is replaced by zero, and NaN put in where it belongs: in the row
+// factor of Q S and the chunk's decay for k and gates, in the column's outputs
+// and state for v.
+#include <climits>
+
 #include "nvfp4_device.h"
 #include "nvfp4_internal.h"
 
@@ -145,6 +155,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
   // K is read only before the first head's gates; then its place takes four blocks of 16 x 16
   floatx4_t(&yb)[4][64] = *reinterpret_cast<floatx4_t(*)[4][64]>(kl);
   __shared__ float rk_l[kC], rq_l[kC], ghi_l[4][kC], glo_l[4][kC], alpha_l[4][kC], beta_l[4][kC];
+  __shared__ int k_bad_l[kC];
 
   // `split` workgroups per chunk and q/k head share its value heads
   const int group = in.n_v / in.n_qk, heads = group / split;
@@ -170,14 +181,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
     qf[i] = load16b(rx, live ? at + (uint32_t)in.q_col * 2 : kOutside);
   }
   float k2 = 0.0f, q2 = 0.0f;
-  uint8_t* head = wsh + (place * in.n_qk + hk) * kHeadBytes;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (hv0 == 0) {
-      *reinterpret_cast<u32x4_t*>(head + (4 * i + w) * kOperand + k_place(m, g) * 16) = kf[i];
-      *reinterpret_cast<u32x4_t*>(head + kOffQ + (4 * i + w) * kOperand + lane * 16) = qf[i];
-    }
-    *reinterpret_cast<u32x4_t*>(&kl[(16 * w + m) * kKStride + 32 * i + 8 * g]) = kf[i];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float k0 = __uint_as_float(kf[i][e] << 16), k1 = __uint_as_float(kf[i][e] & 0xFFFF0000u);
@@ -190,9 +195,21 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
   q2 += __shfl_xor(q2, 16, 64);
   k2 += __shfl_xor(k2, 32, 64);
   q2 += __shfl_xor(q2, 32, 64);
+  const bool k_bad = !(k2 <= __FLT_MAX__);
+  uint8_t* head = wsh + (place * in.n_qk + hk) * kHeadBytes;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) kf[i][e] = k_bad ? 0u : kf[i][e];
+    if (hv0 == 0) {
+      *reinterpret_cast<u32x4_t*>(head + (4 * i + w) * kOperand + k_place(m, g) * 16) = kf[i];
+      *reinterpret_cast<u32x4_t*>(head + kOffQ + (4 * i + w) * kOperand + lane * 16) = qf[i];
+    }
+    *reinterpret_cast<u32x4_t*>(&kl[(16 * w + m) * kKStride + 32 * i + 8 * g]) = kf[i];
+  }
   const float rk_i = 1.0f / fmaxf(sqrtf(k2), kNormEps);             // token i = 16 w + m
   const float rq_i = kRsqrtD / fmaxf(sqrtf(q2), kNormEps);
-  if (g == 0) rk_l[16 * w + m] = rk_i, rq_l[16 * w + m] = rq_i;
+  if (g == 0) rk_l[16 * w + m] = rk_i, rq_l[16 * w + m] = rq_i, k_bad_l[16 * w + m] = k_bad;
   __syncthreads();
 
   // rows j = 16 tile + 4 g + e, column i, of the unit vectors' products (q's with 1 / sqrt(128))
@@ -241,7 +258,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
           beta = p[in.beta_col];
         }
       }
-      gate = gate < kMinGate ? kMinGate : gate;  // a NaN stays one
+      gate = gate < kMinGate ? kMinGate : gate;
+      // the first token with a k or gate that is not finite: it and those behind it write nothing
+      const uint64_t bad = __builtin_amdgcn_ballot_w64(k_bad_l[lane] || !(fabsf(gate) <= __FLT_MAX__) ||
+                                                       !(fabsf(beta) <= __FLT_MAX__));
+      const bool lost = bad && lane >= __builtin_ctzll(bad);
+      if (lost) gate = beta = 0.0f;
       const double step = (double)gate * 1.4426950408889634;
       double sum = step;
 #pragma unroll
@@ -259,9 +281,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
         // row factors: of K S, of Q S, and of the writes to the chunk's end
         float* vec = reinterpret_cast<float*>(ws + (place * in.n_v + h + w) * kUnitBytes + kOffVec);
         vec[lane] = __builtin_amdgcn_exp2f((float)(sum - step)) * rk_l[lane];
-        vec[kC + lane] = __builtin_amdgcn_exp2f(ghi) * rq_l[lane];
+        vec[kC + lane] = lost ? __builtin_nanf("") : __builtin_amdgcn_exp2f(ghi) * rq_l[lane];
         vec[2 * kC + lane] = __builtin_amdgcn_exp2f((float)(__shfl(sum, 63, 64) - sum)) * rk_l[lane];
-        if (lane == 0) vec[3 * kC] = __builtin_amdgcn_exp2f(total);
+        if (lane == 0) vec[3 * kC] = bad ? __builtin_nanf("") : __builtin_amdgcn_exp2f(total);
       }
       __syncthreads();
     }
@@ -427,6 +449,8 @@ struct ScanShared {
   uint16_t kt[4][kC * kTStride];  // [wave]: its 32 columns of K
   uint16_t v[kC * kCols];         // V
   float vec[2][256];              // row factors a, b, c [64] and e^{G_C} (and as much that is not read)
+  int lost[kCols];                // a column's first token whose value is not finite
+  float decay[64][2];             // [lane][0]: e^{G_C}, NaN where the lane's column is lost
 };
 
 // One unit's rows and workspace, chunk by chunk; chunks past the end have
@@ -529,7 +553,6 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, ScanShared& s
         u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4_t*)&sh.v[(16 * w + 4 * g + m / 4) * kCols + 4 * (m % 4)]));
     const floatx4_t fa = *reinterpret_cast<const floatx4_t*>(&sh.vec[0][16 * w + 4 * g]);
     const floatx4_t fc = *reinterpret_cast<const floatx4_t*>(&sh.vec[0][2 * kC + 16 * w + 4 * g]);
-    const float decay = sh.vec[0][3 * kC];
     float r[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -600,6 +623,7 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, ScanShared& s
 #pragma unroll
       for (int sb = 0; sb < 2; ++sb) wv[i][sb] = join(sh.wr[i][2 * sb][lane], sh.wr[i][2 * sb + 1][lane]);
     // S' = e^{G_C} S + K^T (c W)
+    const float decay = sh.decay[lane][0];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
@@ -641,10 +665,22 @@ __device__ __forceinline__ void scan_output(const ChunkSource& src, ScanShared& 
     }
   };
   // what all waves need of a chunk, between the third barrier of the one before and its own first
-  auto share = [&](const OutputOperands<kB>& f) {
-    if constexpr (kB == 1)
+  auto share = [&](int c, OutputOperands<kB>& f) {
+    if constexpr (kB == 1) {
+      uint32_t full = 0;  // the carry of an exponent of all ones
+#pragma unroll
+      for (int e = 0; e < 4; ++e) full |= (f.shared[e] & 0x7F807F80u) + 0x00800080u;
+      if (full & 0x80008000u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t exponent = 0x7F80u << 16 * (e % 2);
+          if ((f.shared[e / 2] & exponent) == exponent) {
+            f.shared[e / 2] &= 0xFFFFu << 16 * (1 - e % 2);
+            atomicMin(&sh.lost[8 * (lane & 1) + e], c * kC + 32 * w + lane / 2);
+          }
+        }
       *reinterpret_cast<u32x4_t*>(&sh.v[512 * w + 8 * lane]) = f.shared;
-    else
+    } else
       *reinterpret_cast<u32x4_t*>(&sh.vec[w - 2][4 * lane]) = f.shared;
   };
   auto chunk = [&](int c, const OutputOperands<kB>& f, OutputOperands<kB>& fn) {
@@ -661,6 +697,7 @@ __device__ __forceinline__ void scan_output(const ChunkSource& src, ScanShared& 
         ov = mfma_bf16(st[term][i], f.q[i], ov);
       }
     mfma_settle(st, f.q);
+    if (kB == 2 && w == 2) sh.decay[lane][0] = sh.lost[m] < (c + 1) * kC ? __builtin_nanf("") : sh.vec[0][3 * kC];
     lds_barrier();
 #pragma unroll
     for (int e = 0; e < 4; ++e) ov[e] *= b;
@@ -675,15 +712,18 @@ __device__ __forceinline__ void scan_output(const ChunkSource& src, ScanShared& 
       }
     mfma_settle(wo, f.p);
     const __amdgpu_buffer_rsrc_t ro = make_rsrc(src.o + c * src.o_step, (int64_t)src.rows(c) * src.o_ld);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c * kC + 16 * w + m >= sh.lost[4 * g + e]) ov[e] = __builtin_nanf("");
     u32x2_t out;
     out[0] = pack_bf16(ov[0], ov[1]);
     out[1] = pack_bf16(ov[2], ov[3]);
     __builtin_amdgcn_raw_buffer_store_b64(out, ro, (uint32_t)(16 * w + m) * src.o_ld + 8 * g, 0, 0);
-    share(fn);
+    share(c + 1, fn);
   };
   OutputOperands<kB> f0, f1;
   fetch(0, f0);
-  share(f0);
+  share(0, f0);
   int c = 0;
   for (; c + 1 < src.n_chunks; c += 2) {
     chunk(c, f0, f1);
@@ -740,6 +780,8 @@ __global__ __launch_bounds__(kScanThreads) void gdn_chunk_scan_kernel(
   src.last_rows = (int)(end - start - (int64_t)(src.n_chunks - 1) * kC);
   src.v_ld = (uint32_t)in.ldx * 2;
   src.o_ld = (uint32_t)ldo * 2;
+  if (tid < kCols) sh.lost[tid] = INT_MAX;
+  __syncthreads();
   if (wave >= 6) return scan_output<2>(src, sh, wave - 4, lane);
   if (wave >= 4) return scan_output<1>(src, sh, wave - 4, lane);
 
@@ -847,6 +889,7 @@ __global__ __launch_bounds__(kWideThreads) void gdn_chunk_wide_kernel(
       for (int e = 0; e < 4; ++e) S[i][t][e] = s_in ? s_in[at + (32 * i + 4 * t + e) * kD] : 0.0f;
 
   const floatx4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  int lost = INT_MAX;  // the lane's column's first token whose V - diag(a) K S is not finite
   stage(0);
   put(0);
   for (int c = 0; c < n_chunks; ++c) {
@@ -893,22 +936,41 @@ __global__ __launch_bounds__(kWideThreads) void gdn_chunk_wide_kernel(
     }
 
     // V - diag(a) K S, split in three: [term][32 tokens]
-    u32x4_t rv[3][2];
+    float nan = 0.0f;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const u32x2_t vt = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                                                          (lds_shortx4_t*)&sh.v[w][(16 * t + 4 * g + m / 4) * kCols + 4 * (m % 4)]));
       const floatx4_t fa = *reinterpret_cast<const floatx4_t*>(&vec[16 * t + 4 * g]);
 #pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        ks[t][e] = fmaf(-fa[e], ks[t][e], __uint_as_float(e & 1 ? vt[e / 2] & 0xFFFF0000u : vt[e / 2] << 16));
+        nan = fmaf(ks[t][e], 0.0f, nan);
+      }
+    }
+    if (__builtin_amdgcn_ballot_w64(nan != nan)) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!(fabsf(ks[t][e]) <= __FLT_MAX__)) {
+            lost = min(lost, c * kC + 16 * t + 4 * g + e);
+            ks[t][e] = 0.0f;
+          }
+      lost = min(lost, __shfl_xor(lost, 16, 64));
+      lost = min(lost, __shfl_xor(lost, 32, 64));
+    }
+    u32x4_t rv[3][2];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
       for (int e = 0; e < 2; ++e) {
         uint32_t hi, mid, lo;
-        split3(fmaf(-fa[2 * e], ks[t][2 * e], __uint_as_float(vt[e] << 16)),
-               fmaf(-fa[2 * e + 1], ks[t][2 * e + 1], __uint_as_float(vt[e] & 0xFFFF0000u)), hi, mid, lo);
+        split3(ks[t][2 * e], ks[t][2 * e + 1], hi, mid, lo);
         rv[0][t / 2][2 * (t % 2) + e] = hi;
         rv[1][t / 2][2 * (t % 2) + e] = mid;
         rv[2][t / 2][2 * (t % 2) + e] = lo;
       }
-    }
     // W = T (V - ..), six products; then diag(c) W in three terms and W in two.  Two row tiles at a time, two sums each.
     u32x4_t wv[3][2], wo[2][2];
 #pragma unroll
@@ -965,8 +1027,20 @@ __global__ __launch_bounds__(kWideThreads) void gdn_chunk_wide_kernel(
       for (int term = 0; term < 2; ++term)
 #pragma unroll
         for (int t = 2 * sb; t < 4; ++t) qs[t] = mfma_bf16(wo[term][sb], p[t], qs[t]);
-      mfma_settle(p[2], p[3], wo);
+      if (sb == 0)
+        mfma_settle(p, wo);
+      else
+        mfma_settle(p[2], p[3], wo);
     }
+    const bool any_lost = __builtin_amdgcn_ballot_w64(lost != INT_MAX) != 0;
+    if (any_lost)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int from = __shfl(lost, 4 * g + e, 64);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          if (c * kC + 16 * t + m >= from) qs[t][e] = __builtin_nanf("");
+      }
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       u32x2_t out;
@@ -976,7 +1050,7 @@ __global__ __launch_bounds__(kWideThreads) void gdn_chunk_wide_kernel(
     }
 
     // S' = e^{G_C} S + K^T (c W)
-    const float decay = vec[3 * kC];
+    const float decay = lost != INT_MAX ? __builtin_nanf("") : vec[3 * kC];
 #pragma unroll
     for (int j = 0; j < 4; j += 2) {  // four accumulators in turn
 #pragma unroll

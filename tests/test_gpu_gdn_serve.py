@@ -398,3 +398,45 @@ def test_refusals():
         with pytest.raises(nv.Nvfp4Error):
             bad()
     assert nv.gdn_decode(x[:0], gates[:0], st8, **lay).shape == (0, 2 * D)
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("part,value", [("q", np.nan), ("k", np.nan), ("k", -np.inf), ("v", np.nan), ("v", np.inf),
+                                        ("g", np.nan), ("beta", np.inf)])
+def test_prefill_what_is_not_finite_stays_where_it_belongs(many, part, value):
+    """Bit for bit: a product with a zero of the inverse or the scores adds nothing, so what an infinity or NaN in
+    one token cannot reach token by token (earlier tokens, other heads, columns, sequences) is as without it."""
+    dev = need_gpu()
+    lens = [7, 150, 3] + ([1, 2] * 90 if many else [])
+    n, n_qk, n_v, T = len(lens), 2, 4, sum(lens)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device=dev)
+    x, g, beta = _inputs(T, n_qk, n_v, 31)
+    head, col = 1, 37                     # of q and k: value heads 2 and 3; of v and the gates: value head 1
+    for at in (0, 5, 38, 63, 64, 100, 127, 149):
+        print(f"[not finite] {part} {value} many {many} token {at}", flush=True)
+        res = []
+        for planted in (False, True):
+            xt, gt = torch.from_numpy(x).to(dev).to(BF), torch.from_numpy(np.concatenate([g, beta], 1)).to(dev)
+            row = 7 + at
+            if planted and part in "qkv":
+                xt[row, {"q": head * D, "k": (n_qk + head) * D, "v": (2 * n_qk + head) * D}[part] + col] = value
+            elif planted:
+                gt[row, head + (n_v if part == "beta" else 0)] = value
+            states = torch.ones((n, n_v, D, D), device=dev)
+            o = nv.gdn_prefill(xt, gt, cu, q_col=0, k_col=n_qk * D, v_col=2 * n_qk * D, g_col=0, beta_col=n_v,
+                               n_qk_heads=n_qk, n_v_heads=n_v, state_in=states, state_out=states)
+            torch.cuda.synchronize()
+            res.append((o.view(T, n_v, D).float(), states))
+        (o0, s0), (o1, s1) = res
+        hit_o, hit_s = torch.zeros_like(o0, dtype=torch.bool), torch.zeros_like(s0, dtype=torch.bool)
+        if part == "q":
+            hit_o[row, 2:] = True
+        else:
+            heads, cols = (slice(2, 4), slice(None)) if part == "k" else (slice(1, 2), slice(None))
+            if part == "v":
+                cols = slice(col, col + 1)
+            hit_o[row:157, heads, cols] = True
+            hit_s[1, heads, :, cols] = True
+        assert torch.all(torch.isfinite(o0)) and torch.all(torch.isfinite(s0))
+        assert not torch.any(torch.isfinite(o1[hit_o])) and not torch.any(torch.isfinite(s1[hit_s]))
+        assert torch.equal(o1[~hit_o], o0[~hit_o]) and torch.equal(s1[~hit_s], s0[~hit_s])
