@@ -351,6 +351,16 @@ _DTYPE_CODE = {torch.float32: 0, torch.bfloat16: 1}  # NVFP4_IN_* and NVFP4_OUT_
 # is kept short: one look at each tensor, addresses passed as plain integers.
 
 
+def _new(shape, dtype, device, stream):
+    """Memory that a call on `stream` makes itself, from that stream's pool: the
+    current stream's may still be in use there, and what is freed when the
+    call returns would be handed out to it while the kernels run."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _rows(t, what):
     """(address, dtype code, rows, columns, row stride) of a 2-D bf16 or fp32
     GPU tensor with unit column stride; the stride of one row or fewer is its
@@ -438,14 +448,14 @@ def gdn_prefill(x: torch.Tensor, gates: torch.Tensor, cu_seqlens: torch.Tensor, 
             raise ValueError("slots without a state pool")
         sp = _vector(slots, torch.int32, n_seqs, "slots")
     if o is None:
-        o = torch.empty((T, n_v_heads * 128), dtype=torch.bfloat16, device=x.device)
+        o = _new((T, n_v_heads * 128), torch.bfloat16, x.device, stream)
     o_ptr, o_dtype, ldo = _out_rows(o, T, n_v_heads * 128, "o")
     if o_dtype != OUT_BF16:
         raise ValueError("o must be bf16")
     lib = load()
     need = lib.nvfp4_gdn_prefill_workspace_size(T, n_seqs, n_qk_heads, n_v_heads)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _new(need, torch.uint8, x.device, stream)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous GPU tensor")
     st = lib.nvfp4_gdn_prefill(xp, ldx, q_col, k_col, v_col, gp, gates_dtype, ldg, g_col, beta_col, cp, n_seqs, T,
@@ -471,7 +481,7 @@ def gdn_decode(x: torch.Tensor, gates: torch.Tensor, states: torch.Tensor, *, q_
     pp, n_slots = _pool(states, torch.float32, (n_v_heads, 128, 128), "states")
     sp = _vector(slots, torch.int32, B, "slots") if slots is not None else None
     if o is None:
-        o = torch.empty((B, n_v_heads * 128), dtype=x.dtype, device=x.device)
+        o = _new((B, n_v_heads * 128), x.dtype, x.device, stream)
     op, o_dtype, ldo = _out_rows(o, B, n_v_heads * 128, "o")
     st = load().nvfp4_gdn_decode(xp, x_dtype, ldx, q_col, k_col, v_col, gp, gates_dtype, ldg, g_col, beta_col, B,
                                  n_qk_heads, n_v_heads, pp, sp, n_slots, op, o_dtype, ldo, _raw_stream(stream))
@@ -502,7 +512,7 @@ def conv_silu(x: torch.Tensor, weight: torch.Tensor, *, cu_seqlens: torch.Tensor
             raise ValueError("slots without a state pool")
         sp = _vector(slots, torch.int32, n_seqs, "slots")
     if out is None:
-        out = torch.empty((T, channels), dtype=x.dtype, device=x.device)
+        out = _new((T, channels), x.dtype, x.device, stream)
     yp, y_dtype, ldy = _out_rows(out, T, channels, "out")
     if y_dtype != dtype:
         raise ValueError("out must have the dtype of x")
@@ -513,7 +523,7 @@ def conv_silu(x: torch.Tensor, weight: torch.Tensor, *, cu_seqlens: torch.Tensor
     return out
 
 
-def _norm_out(rows, cols, out, out_dtype, y_gs, codes, scales, device):
+def _norm_out(rows, cols, out, out_dtype, y_gs, codes, scales, device, stream):
     """Destinations of a norm's y, made where they are not given: (out, its
     address, dtype code and row stride, codes, scales)."""
     if y_gs is not None:
@@ -521,16 +531,16 @@ def _norm_out(rows, cols, out, out_dtype, y_gs, codes, scales, device):
         if cols % 16:
             raise ValueError("columns must be a multiple of 16 to be quantized")
         if codes is None:
-            codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=device)
+            codes = _new((rows, cols // 2), torch.uint8, device, stream)
         if scales is None:
-            scales = torch.empty((rows, cols // 16), dtype=torch.uint8, device=device)
+            scales = _new((rows, cols // 16), torch.uint8, device, stream)
         _u8_matrix(codes, (rows, cols // 2), "codes")
         _u8_matrix(scales, (rows, cols // 16), "scales")
         _need_gpu(y_gs, codes, scales)
     elif codes is not None or scales is not None:
         raise ValueError("codes and scales need y_gs, the tensor scale")
     if out is None and (y_gs is None or out_dtype is not None):
-        out = torch.empty((rows, cols), dtype=out_dtype or torch.bfloat16, device=device)
+        out = _new((rows, cols), out_dtype or torch.bfloat16, device, stream)
     if out is None:
         return None, None, 0, 0, codes, scales
     if out_dtype is not None and out.dtype != out_dtype:
@@ -561,7 +571,7 @@ def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor
         if r != rows or c != cols or (rp is not None and t_dtype != r_dtype):
             raise ValueError("residual_out must have the shape of x and the dtype of residual")
         r_dtype = t_dtype
-    out, yp, y_dtype, ldy, codes, scales = _norm_out(rows, cols, out, out_dtype, y_gs, codes, scales, x.device)
+    out, yp, y_dtype, ldy, codes, scales = _norm_out(rows, cols, out, out_dtype, y_gs, codes, scales, x.device, stream)
     st = load().nvfp4_add_rmsnorm(xp, x_dtype, ldx, rp, r_dtype, ldr, scale, wp, eps, rows, cols, tp, ldt, yp,
                                   y_dtype, ldy, _ptr(y_gs), _ptr(codes), _ptr(scales), _raw_stream(stream))
     if st:
@@ -580,7 +590,7 @@ def rmsnorm_gated(o: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *, eps
         raise ValueError("z must have the shape of o")
     group = weight.numel()
     wp = _vector(weight, torch.float32, group, "weight")
-    out, yp, y_dtype, ldy, codes, scales = _norm_out(rows, cols, out, out_dtype, y_gs, codes, scales, o.device)
+    out, yp, y_dtype, ldy, codes, scales = _norm_out(rows, cols, out, out_dtype, y_gs, codes, scales, o.device, stream)
     st = load().nvfp4_rmsnorm_gated(op, o_dtype, ldo, zp, z_dtype, ldz, wp, eps, rows, cols, group, yp, y_dtype, ldy,
                                     _ptr(y_gs), _ptr(codes), _ptr(scales), _raw_stream(stream))
     if st:

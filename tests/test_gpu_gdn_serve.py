@@ -440,3 +440,25 @@ def test_prefill_what_is_not_finite_stays_where_it_belongs(many, part, value):
         assert torch.all(torch.isfinite(o0)) and torch.all(torch.isfinite(s0))
         assert not torch.any(torch.isfinite(o1[hit_o])) and not torch.any(torch.isfinite(s1[hit_s]))
         assert torch.equal(o1[~hit_o], o0[~hit_o]) and torch.equal(s1[~hit_s], s0[~hit_s])
+
+
+def test_memory_a_call_makes_belongs_to_its_stream():
+    """A call on a stream that is behind the current one: what the current stream takes and fills right after the call
+    returns must not be the call's workspace, nor may the call's output be memory that the current stream still uses."""
+    x, gates, lay = _tensors(600, 2, 4, 21)
+    cu = _cu(0, 600)
+    need = nv.load().nvfp4_gdn_prefill_workspace_size(600, 1, 2, 4)
+    want, want_d = nv.gdn_prefill(x, gates, cu, **lay), nv.gdn_decode(x, gates, torch.zeros((600, 4, D, D), device=x.device), **lay)
+    states = torch.zeros((600, 4, D, D), device=x.device)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(2_000_000)     # cycles: about a millisecond, then it ends
+    o = nv.gdn_prefill(x, gates, cu, **lay, stream=side)
+    od = nv.gdn_decode(x, gates, states, **lay, stream=side)
+    taken = [torch.full((need,), 255, dtype=torch.uint8, device=x.device) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(od, want_d)
+    pools = {b["address"] + sum(c["size"] for c in b["blocks"][:i]): b["stream"] for b in torch.cuda.memory_snapshot()
+             for i in range(len(b["blocks"]))}
+    assert pools[o.data_ptr()] == pools[od.data_ptr()] == side.cuda_stream != pools[taken[0].data_ptr()]
