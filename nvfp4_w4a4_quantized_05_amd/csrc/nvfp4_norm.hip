@@ -14,8 +14,9 @@
 // quantize_block needs no exchange between lanes).  A lane's two 16-byte loads
 // share cache lines with its neighbours' second ones, so they go through the
 // caches: 32768 x 5120 bf16 takes 242 us (5.5 TB/s) against 277 with
-// non-temporal loads and stores, the gated norm of 32768 x 4096 144 us (5.6
-// TB/s) against 150; four or five times the values per lane took 295 us.
+// non-temporal loads and stores (fp32, where a lane has four: 467 against 842),
+// the gated norm of 32768 x 4096 144 us (5.6 TB/s) against 150 (fp32: 236
+// against 337); four or five times the values per lane took 295 us.
 #include "nvfp4_device.h"
 #include "nvfp4_internal.h"
 #include "nvfp4_quant_block.h"
@@ -23,11 +24,15 @@
 namespace nvfp4 {
 namespace {
 
-// 16 values from p (16-byte aligned), bf16 or fp32.
+// Vectors at any element's address: the memory path takes them.
+typedef u32x4_t u32x4_at2 __attribute__((aligned(2)));
+typedef floatx4_t floatx4_at4 __attribute__((aligned(4)));
+
+// 16 values, bf16 or fp32.
 template <bool kBf16>
 __device__ __forceinline__ void load16(const void* base, int64_t at, float v[16]) {
   if constexpr (kBf16) {
-    const u32x4_t* p = reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint16_t*>(base) + at);
+    const u32x4_at2* p = reinterpret_cast<const u32x4_at2*>(reinterpret_cast<const uint16_t*>(base) + at);
     const u32x4_t a = p[0], b = p[1];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -37,10 +42,10 @@ __device__ __forceinline__ void load16(const void* base, int64_t at, float v[16]
       v[9 + 2 * i] = __uint_as_float(b[i] & 0xFFFF0000u);
     }
   } else {
-    const floatx4_t* p = reinterpret_cast<const floatx4_t*>(reinterpret_cast<const float*>(base) + at);
+    const floatx4_at4* p = reinterpret_cast<const floatx4_at4*>(reinterpret_cast<const float*>(base) + at);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const floatx4_t t = __builtin_nontemporal_load(p + i);
+      const floatx4_t t = p[i];
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[4 * i + e] = t[e];
     }
@@ -56,47 +61,18 @@ __device__ __forceinline__ void store16(void* base, int64_t at, const float v[16
       a[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
       b[i] = pack_bf16(v[8 + 2 * i], v[9 + 2 * i]);
     }
-    u32x4_t* p = reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(base) + at);
-    p[0]=a; p[1]=b;
+    u32x4_at2* p = reinterpret_cast<u32x4_at2*>(reinterpret_cast<uint16_t*>(base) + at);
+    p[0] = a;
+    p[1] = b;
   } else {
-    floatx4_t* p = reinterpret_cast<floatx4_t*>(reinterpret_cast<float*>(base) + at);
+    floatx4_at4* p = reinterpret_cast<floatx4_at4*>(reinterpret_cast<float*>(base) + at);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       floatx4_t t;
 #pragma unroll
       for (int e = 0; e < 4; ++e) t[e] = v[4 * i + e];
-      __builtin_nontemporal_store(t, p + i);
+      p[i] = t;
     }
-  }
-}
-
-__device__ __forceinline__ void load_weight16(const float* w, int64_t at, float v[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const floatx4_t t = *reinterpret_cast<const floatx4_t*>(w + at + 4 * i);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[4 * i + e] = t[e];
-  }
-}
-
-// y's destinations: values (or NULL) and NVFP4 codes with block scales (or NULL).
-__device__ __forceinline__ void store_y(const NormOut& out, int64_t row, int64_t col, int64_t cols,
-                                        const float y[16], float g, float r6) {
-  if (out.y) {
-    if (out.y_bf16)
-      store16<true>(out.y, row * out.ldy + col, y);
-    else
-      store16<false>(out.y, row * out.ldy + col, y);
-  }
-  if (out.codes) {
-    uint32_t w0, w1;
-    const uint32_t s = quantize_block(y, g, r6, w0, w1);
-    const int64_t b = (row * cols + col) / kBlock;
-    u32x2_t c;
-    c[0] = w0;
-    c[1] = w1;
-    __builtin_nontemporal_store(c, reinterpret_cast<u32x2_t*>(out.codes) + b);
-    __builtin_nontemporal_store((uint8_t)s, out.scales + b);
   }
 }
 
@@ -112,10 +88,51 @@ __device__ __forceinline__ void store_one(void* p, bool bf16, int64_t at, float 
     reinterpret_cast<float*>(p)[at] = v;
 }
 
+// The 16 values but for the first `before`.
+template <bool kBf16>
+__device__ __forceinline__ void store16_from(void* base, int64_t at, const float v[16], int before) {
+  if (before == 0) return store16<kBf16>(base, at, v);
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    if (e >= before) store_one(base, kBf16, at + e, v[e]);
+}
+
+__device__ __forceinline__ void load_weight16(const float* w, int64_t at, float v[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const floatx4_t t = *reinterpret_cast<const floatx4_at4*>(w + at + 4 * i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[4 * i + e] = t[e];
+  }
+}
+
+// y's destinations: values (or NULL) and NVFP4 codes with block scales (or NULL).
+__device__ __forceinline__ void store_y(const NormOut& out, int64_t row, int64_t col, int64_t cols,
+                                        const float y[16], float g, float r6, int before) {
+  if (out.y) {
+    if (out.y_bf16)
+      store16_from<true>(out.y, row * out.ldy + col, y, before);
+    else
+      store16_from<false>(out.y, row * out.ldy + col, y, before);
+  }
+  if (out.codes) {
+    uint32_t w0, w1;
+    const uint32_t s = quantize_block(y, g, r6, w0, w1);
+    const int64_t b = (row * cols + col) / kBlock;
+    u32x2_t c;
+    c[0] = w0;
+    c[1] = w1;
+    __builtin_nontemporal_store(c, reinterpret_cast<u32x2_t*>(out.codes) + b);
+    __builtin_nontemporal_store((uint8_t)s, out.scales + b);
+  }
+}
+
 // One workgroup (blockDim.x threads, whole waves) per row, 16 values per lane.
-// kVec: lane l has the 16 consecutive values from 16 l.  Otherwise (columns,
-// strides or pointers that 16-byte loads cannot take) its value e is column
-// e * threads + l, so that a wave's loads still cover consecutive addresses.
+// kVec: lane l has the 16 consecutive values from 16 l; where less than 16 are
+// left, the last 16 of the row, of which it leaves the first `before` to the
+// lane before it.  Rows of less than 16: value e is column e * threads + l.
+// Odd widths at full width of the loads: 8,000 rows of 1,033 bf16 take 17 us,
+// 22 with loads of single values.
 template <bool kXBf16, bool kRBf16, bool kVec>
 __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const void* x, int64_t ldx, const void* residual,
                                                            int64_t ldr, float scale, const float* __restrict__ w,
@@ -123,23 +140,24 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const void* x, int64_
                                                            NormOut out) {
   const int64_t row = blockIdx.x;
   const int threads = blockDim.x, tid = threadIdx.x;
-  const bool live = 16 * tid < cols;  // kVec: whole lanes
+  const bool live = 16 * tid < cols;
+  const int col0 = min(16 * tid, (int)cols - 16), before = 16 * tid - col0;
   float t[16], ss = 0.0f;
   if constexpr (kVec) {
     if (live) {
-      load16<kXBf16>(x, row * ldx + 16 * tid, t);
+      load16<kXBf16>(x, row * ldx + col0, t);
       if (residual) {
         float r[16];
-        load16<kRBf16>(residual, row * ldr + 16 * tid, r);
+        load16<kRBf16>(residual, row * ldr + col0, r);
 #pragma unroll
         for (int e = 0; e < 16; ++e) t[e] = fmaf(scale, t[e], r[e]);
       } else {
 #pragma unroll
         for (int e = 0; e < 16; ++e) t[e] *= scale;
       }
-      if (sum) store16<kRBf16>(sum, row * lds + 16 * tid, t);
+      if (sum) store16_from<kRBf16>(sum, row * lds + col0, t, before);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) ss = fmaf(t[e], t[e], ss);
+      for (int e = 0; e < 16; ++e) ss = e < before ? ss : fmaf(t[e], t[e], ss);
     }
   } else {
 #pragma unroll
@@ -165,11 +183,11 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const void* x, int64_
   if constexpr (kVec) {
     if (live) {
       float wv[16];
-      load_weight16(w, 16 * tid, wv);
+      load_weight16(w, col0, wv);
 #pragma unroll
       for (int e = 0; e < 16; ++e) t[e] = t[e] * rms * wv[e];
       const float g = out.codes ? *out.gs : 1.0f;
-      store_y(out, row, 16 * tid, cols, t, g, __builtin_amdgcn_rcpf(6.0f * g));
+      store_y(out, row, col0, cols, t, g, __builtin_amdgcn_rcpf(6.0f * g), before);
     }
   } else {
 #pragma unroll
@@ -207,7 +225,7 @@ __global__ __launch_bounds__(256) void rmsnorm_gated_kernel(const void* __restri
 #pragma unroll
   for (int e = 0; e < 16; ++e) ov[e] = ov[e] * rms * wv[e] * silu(zv[e]);
   const float g = out.codes ? *out.gs : 1.0f;
-  store_y(out, row, col, cols, ov, g, __builtin_amdgcn_rcpf(6.0f * g));
+  store_y(out, row, col, cols, ov, g, __builtin_amdgcn_rcpf(6.0f * g), 0);
 }
 
 template <bool kXBf16, bool kRBf16>
@@ -225,11 +243,7 @@ hipError_t launch_add_typed(bool vec, const void* x, int64_t ldx, const void* re
 hipError_t launch_add_rmsnorm(const void* x, bool x_bf16, int64_t ldx, const void* residual, bool r_bf16,
                               int64_t ldr, float scale, const float* w, float eps, int64_t rows, int64_t cols,
                               void* sum, int64_t lds, const NormOut& out, hipStream_t stream) {
-  const auto fits = [](const void* p, int64_t ld, bool bf16) {
-    return !p || ((uintptr_t)p % 16 == 0 && ld * (bf16 ? 2 : 4) % 16 == 0);
-  };
-  const bool vec = cols % 16 == 0 && fits(x, ldx, x_bf16) && fits(residual, ldr, r_bf16) && fits(sum, lds, r_bf16) &&
-                   fits(out.y, out.ldy, out.y_bf16) && (uintptr_t)w % 16 == 0;
+  const bool vec = cols >= 16;
   const auto f = x_bf16 ? (r_bf16 ? launch_add_typed<true, true> : launch_add_typed<true, false>)
                         : (r_bf16 ? launch_add_typed<false, true> : launch_add_typed<false, false>);
   return f(vec, x, ldx, residual, ldr, scale, w, eps, rows, cols, sum, lds, out, stream);

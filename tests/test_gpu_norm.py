@@ -193,3 +193,11 @@ def test_refusals():
                 lambda: nv.rmsnorm_gated(x[:, 8:136], x[:, 1:129], w[:128].contiguous())):
         with pytest.raises(nv.Nvfp4Error):
             bad()
+
+
+@pytest.mark.parametrize("cols", [15, 18, 31, 1009, 1025, 1039, 5119])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_add_rmsnorm_rows_that_end_inside_a_lane(cols, dtype):
+    """The last lane takes values that the lane before it has too, of which it may already have written the sum."""
+    _check_add(5, cols, dtype, dtype, dtype, 0.5, cols, pad=1)
+    _check_add(70, cols, dtype, dtype, BF, 1.0, cols + 1, in_place=True)
