@@ -20,6 +20,11 @@
 namespace nvfp4 {
 namespace {
 
+// Vectors at any element's address: the memory path takes them.
+typedef u32x4_t u32x4_at2 __attribute__((aligned(2)));
+typedef floatx4_t floatx4_at4 __attribute__((aligned(4)));
+
+// kVec neighbouring channels of a row: one, or 16 bytes (8 bf16, 4 fp32).
 template <bool kBf16, int kVec>
 struct Row {
   float v[kVec];
@@ -30,40 +35,42 @@ struct Row {
       else
         v[0] = reinterpret_cast<const float*>(base)[at];
     } else if constexpr (kBf16) {
-      const u32x4_t a = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint16_t*>(base) + at);
+      const u32x4_t a = *reinterpret_cast<const u32x4_at2*>(reinterpret_cast<const uint16_t*>(base) + at);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[2 * i] = __uint_as_float(a[i] << 16);
         v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
       }
     } else {
+      const floatx4_t a = *reinterpret_cast<const floatx4_at4*>(reinterpret_cast<const float*>(base) + at);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const floatx4_t a = *reinterpret_cast<const floatx4_t*>(reinterpret_cast<const float*>(base) + at + 4 * i);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * i + e] = a[e];
-      }
+      for (int e = 0; e < 4; ++e) v[e] = a[e];
     }
   }
-  __device__ __forceinline__ void store(void* base, int64_t at) const {
+  static __device__ __forceinline__ void store_one(void* base, int64_t at, float x) {
+    if constexpr (kBf16)
+      reinterpret_cast<uint16_t*>(base)[at] = (uint16_t)pack_bf16(x, 0.0f);
+    else
+      reinterpret_cast<float*>(base)[at] = x;
+  }
+  // all but the first `before`
+  __device__ __forceinline__ void store(void* base, int64_t at, int before) const {
     if constexpr (kVec == 1) {
-      if constexpr (kBf16)
-        reinterpret_cast<uint16_t*>(base)[at] = (uint16_t)pack_bf16(v[0], 0.0f);
-      else
-        reinterpret_cast<float*>(base)[at] = v[0];
+      store_one(base, at, v[0]);
+    } else if (before) {
+#pragma unroll
+      for (int e = 1; e < kVec; ++e)
+        if (e >= before) store_one(base, at + e, v[e]);
     } else if constexpr (kBf16) {
       u32x4_t a;
 #pragma unroll
       for (int i = 0; i < 4; ++i) a[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-      __builtin_nontemporal_store(a, reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(base) + at));
+      __builtin_nontemporal_store(a, reinterpret_cast<u32x4_at2*>(reinterpret_cast<uint16_t*>(base) + at));
     } else {
+      floatx4_t a;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        floatx4_t a;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) a[e] = v[4 * i + e];
-        __builtin_nontemporal_store(a, reinterpret_cast<floatx4_t*>(reinterpret_cast<float*>(base) + at + 4 * i));
-      }
+      for (int e = 0; e < 4; ++e) a[e] = v[e];
+      __builtin_nontemporal_store(a, reinterpret_cast<floatx4_at4*>(reinterpret_cast<float*>(base) + at));
     }
   }
   __device__ __forceinline__ void zero() {
@@ -95,9 +102,14 @@ __device__ __forceinline__ void load_weights(const float* w, int64_t c, float (&
 }
 
 constexpr int kConvThreads = 256;
-// Rows per tile and rows loaded at once.  On 32768 x 8192 bf16: 215 us (5.0
+// Where less than kVec channels are left, a lane takes the last kVec of the
+// row and leaves the first `before` to the lane before it (it loads them, also
+// from a slot that that lane is writing, and stores nothing of them): 9,000
+// rows of 4,895 bf16 take 39 us, 55 with a channel per lane.
+// Rows per tile and rows loaded at once.  On 32768 x 8192 bf16: 209 us (5.1
 // TB/s, a plain copy of that size reads and writes 4.9-5.0), against 222-227
-// with 64 rows, 232 with 8, and 298 / 219 with 128 / 512 threads.
+// with 64 rows, 232 with 8, and 298 / 219 with 128 / 512 threads.  fp32: 407 us
+// (5.3 TB/s) with 16 bytes a lane, 505-765 with 32.
 constexpr int kRows = 16, kAhead = 8;
 
 // Packed sequences: grid (tiles of kRows rows, channel blocks).
@@ -111,8 +123,10 @@ __global__ __launch_bounds__(kConvThreads) void conv_silu_kernel(
   const int64_t t1 = min(t0 + kRows, T);
   // the last sequence that starts at or before t0: no earlier one has a row in the tile
   const int first = last_before(n_seqs, [&](int i) { return cu[i] <= t0; });
-  const int64_t c = ((int64_t)blockIdx.y * kConvThreads + threadIdx.x) * kVec;
-  if (c >= channels) return;
+  const int64_t mine0 = ((int64_t)blockIdx.y * kConvThreads + threadIdx.x) * kVec;
+  if (mine0 >= channels) return;
+  const int64_t c = min(mine0, channels - kVec);
+  const int before = (int)(mine0 - c);
   float wt[kVec][kW];
   load_weights<kVec, kW>(w, c, wt);
 
@@ -128,7 +142,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_silu_kernel(
     if (slot < 0 || slot >= n_slots) {  // a skipped sequence: zeros
       R z;
       z.zero();
-      for (; t < stop; ++t) z.store(y, t * ldy + c);
+      for (; t < stop; ++t) z.store(y, t * ldy + c, before);
       continue;
     }
     R win[kW];
@@ -153,7 +167,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_silu_kernel(
             for (int j = 1; j < kW - 1; ++j)
               if (j == len + i) nw = old[j];
           }
-          nw.store(state, ((int64_t)slot * (kW - 1) + i) * channels + c);
+          nw.store(state, ((int64_t)slot * (kW - 1) + i) * channels + c, before);
         }
       }
     } else {
@@ -162,7 +176,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_silu_kernel(
     }
     auto row = [&](const R& next, int64_t at) {
       win[kW - 1] = next;
-      conv_row<kBf16, kVec, kW>(win, wt).store(y, at * ldy + c);
+      conv_row<kBf16, kVec, kW>(win, wt).store(y, at * ldy + c, before);
 #pragma unroll
       for (int i = 0; i < kW - 1; ++i) win[i] = win[i + 1];
     };
@@ -187,14 +201,16 @@ __global__ __launch_bounds__(kConvThreads) void conv_silu_step_kernel(
     const void* __restrict__ x, int64_t ldx, int64_t channels, const float* __restrict__ w, void* state,
     const int32_t* __restrict__ slots, int n_slots, void* __restrict__ y, int64_t ldy) {
   using R = Row<kBf16, kVec>;
-  const int64_t c = ((int64_t)blockIdx.y * kConvThreads + threadIdx.x) * kVec;
-  if (c >= channels) return;
+  const int64_t mine0 = ((int64_t)blockIdx.y * kConvThreads + threadIdx.x) * kVec;
+  if (mine0 >= channels) return;
+  const int64_t c = min(mine0, channels - kVec);
+  const int before = (int)(mine0 - c);
   const int64_t b = blockIdx.x;
   const int slot = state ? (slots ? slots[b] : (int)b) : 0;
   if (slot < 0 || slot >= n_slots) {
     R z;
     z.zero();
-    z.store(y, b * ldy + c);
+    z.store(y, b * ldy + c, before);
     return;
   }
   float wt[kVec][kW];
@@ -205,10 +221,10 @@ __global__ __launch_bounds__(kConvThreads) void conv_silu_step_kernel(
   for (int i = 0; i < kW - 1; ++i) {
     if (state) win[i].load(state, ((int64_t)slot * (kW - 1) + i) * channels + c); else win[i].zero();
   }
-  conv_row<kBf16, kVec, kW>(win, wt).store(y, b * ldy + c);
+  conv_row<kBf16, kVec, kW>(win, wt).store(y, b * ldy + c, before);
   if (state) {
 #pragma unroll
-    for (int i = 0; i < kW - 1; ++i) win[i + 1].store(state, ((int64_t)slot * (kW - 1) + i) * channels + c);
+    for (int i = 0; i < kW - 1; ++i) win[i + 1].store(state, ((int64_t)slot * (kW - 1) + i) * channels + c, before);
   }
 }
 
@@ -244,11 +260,8 @@ hipError_t launch_conv_width(int width, const void* x, int64_t ldx, int64_t chan
 hipError_t launch_conv_silu(const void* x, bool bf16, int64_t ldx, int64_t channels, const float* w, int width,
                             const int32_t* cu, int n_seqs, int64_t T, void* state, const int32_t* slots, int n_slots,
                             void* y, int64_t ldy, hipStream_t stream) {
-  const int64_t e = bf16 ? 2 : 4;
-  const bool vec = channels % 8 == 0 && (uintptr_t)x % 16 == 0 && ldx * e % 16 == 0 && (uintptr_t)y % 16 == 0 &&
-                   ldy * e % 16 == 0 && (uintptr_t)state % 16 == 0;
-  const auto f = bf16 ? (vec ? launch_conv_width<true, 8> : launch_conv_width<true, 1>)
-                      : (vec ? launch_conv_width<false, 8> : launch_conv_width<false, 1>);
+  const auto f = bf16 ? (channels >= 8 ? launch_conv_width<true, 8> : launch_conv_width<true, 1>)
+                      : (channels >= 4 ? launch_conv_width<false, 4> : launch_conv_width<false, 1>);
   return f(width, x, ldx, channels, w, cu, n_seqs, T, state, slots, n_slots, y, ldy, stream);
 }
 

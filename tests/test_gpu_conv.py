@@ -144,3 +144,10 @@ def test_refusals():
         with pytest.raises(nv.Nvfp4Error):
             bad()
     assert nv.conv_silu(x[:0], w).shape == (0, 64)
+
+
+@pytest.mark.parametrize("channels,dtype", [(7, BF), (9, BF), (2049, BF), (2055, BF), (3, F32), (5, F32), (1025, F32), (1027, F32)])
+def test_channels_that_end_inside_a_vector(channels, dtype):
+    """The last lane takes channels that the lane before it has too: in the same wave, or in another workgroup."""
+    _case([40, 1, 2, 0, 3, 17], channels, 4, dtype, channels, pad=1, tail=1)
+    _case([1] * 9, channels, 4, dtype, channels, step=True, pad=1, skip=(4,))
