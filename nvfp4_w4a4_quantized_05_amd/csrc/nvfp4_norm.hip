@@ -13,8 +13,8 @@
 // load and its stores.  A lane owns 16 consecutive values (one NVFP4 block, so
 // quantize_block needs no exchange between lanes).  A lane's two 16-byte loads
 // share cache lines with its neighbours' second ones, so they go through the
-// caches: 32768 x 5120 bf16 takes 242 us (5.5 TB/s) against 277 with
-// non-temporal loads and stores (fp32, where a lane has four: 467 against 842),
+// caches: 32768 x 5120 bf16 takes 237 us (5.6 TB/s) against 277 with
+// non-temporal loads and stores (fp32, where a lane has four: 431 against 842),
 // the gated norm of 32768 x 4096 144 us (5.6 TB/s) against 150 (fp32: 236
 // against 337); four or five times the values per lane took 295 us.
 #include "nvfp4_device.h"
@@ -88,15 +88,6 @@ __device__ __forceinline__ void store_one(void* p, bool bf16, int64_t at, float 
     reinterpret_cast<float*>(p)[at] = v;
 }
 
-// The 16 values but for the first `before`.
-template <bool kBf16>
-__device__ __forceinline__ void store16_from(void* base, int64_t at, const float v[16], int before) {
-  if (before == 0) return store16<kBf16>(base, at, v);
-#pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (e >= before) store_one(base, kBf16, at + e, v[e]);
-}
-
 __device__ __forceinline__ void load_weight16(const float* w, int64_t at, float v[16]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -108,12 +99,12 @@ __device__ __forceinline__ void load_weight16(const float* w, int64_t at, float 
 
 // y's destinations: values (or NULL) and NVFP4 codes with block scales (or NULL).
 __device__ __forceinline__ void store_y(const NormOut& out, int64_t row, int64_t col, int64_t cols,
-                                        const float y[16], float g, float r6, int before) {
+                                        const float y[16], float g, float r6) {
   if (out.y) {
     if (out.y_bf16)
-      store16_from<true>(out.y, row * out.ldy + col, y, before);
+      store16<true>(out.y, row * out.ldy + col, y);
     else
-      store16_from<false>(out.y, row * out.ldy + col, y, before);
+      store16<false>(out.y, row * out.ldy + col, y);
   }
   if (out.codes) {
     uint32_t w0, w1;
@@ -127,21 +118,26 @@ __device__ __forceinline__ void store_y(const NormOut& out, int64_t row, int64_t
   }
 }
 
-// One workgroup (blockDim.x threads, whole waves) per row, 16 values per lane.
+// Rows of up to 1,024 values: `lanes` (a power of two) lanes per row, a wave per
+// workgroup; wider ones: the workgroup (lanes = blockDim.x, whole waves).
 // kVec: lane l has the 16 consecutive values from 16 l; where less than 16 are
-// left, the last 16 of the row, of which it leaves the first `before` to the
-// lane before it.  Rows of less than 16: value e is column e * threads + l.
-// Odd widths at full width of the loads: 8,000 rows of 1,033 bf16 take 17 us,
-// 22 with loads of single values.
+// left, the last 16 of the row, some of which the lane before it has too: both
+// store the same bits, and since nothing is stored before the row's sum is
+// known, neither loads what the other stored, in place either.  (With t out at
+// once 32768 x 5120 takes 242 us in bf16 and 466 in fp32 instead of 237 and 431,
+// 16,000 x 704 bf16 16.8 instead of 17.7.)  Rows of less than 16: value e is
+// column e * lanes + l.
+// 8,000 rows of 1,033 bf16 take 16 us, 22 with loads of single values; 30,000 of
+// 100 take 8, 17 with a wave per row.
 template <bool kXBf16, bool kRBf16, bool kVec>
 __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const void* x, int64_t ldx, const void* residual,
                                                            int64_t ldr, float scale, const float* __restrict__ w,
-                                                           float eps, int64_t cols, void* sum, int64_t lds,
-                                                           NormOut out) {
-  const int64_t row = blockIdx.x;
-  const int threads = blockDim.x, tid = threadIdx.x;
-  const bool live = 16 * tid < cols;
-  const int col0 = min(16 * tid, (int)cols - 16), before = 16 * tid - col0;
+                                                           float eps, int64_t rows, int64_t cols, int lanes,
+                                                           void* sum, int64_t lds, NormOut out) {
+  const int tid = threadIdx.x, l = tid & (lanes <= 64 ? lanes - 1 : 1023);
+  const int64_t row = lanes <= 64 ? (int)(blockIdx.x * 64 + tid) >> __builtin_ctz(lanes) : blockIdx.x;
+  const bool live = 16 * l < cols && row < rows;
+  const int col0 = min(16 * l, (int)cols - 16), before = 16 * l - col0;
   float t[16], ss = 0.0f;
   if constexpr (kVec) {
     if (live) {
@@ -155,45 +151,51 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const void* x, int64_
 #pragma unroll
         for (int e = 0; e < 16; ++e) t[e] *= scale;
       }
-      if (sum) store16_from<kRBf16>(sum, row * lds + col0, t, before);
 #pragma unroll
       for (int e = 0; e < 16; ++e) ss = e < before ? ss : fmaf(t[e], t[e], ss);
     }
   } else {
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const int col = e * threads + tid;
-      if (col < cols) {
+      const int col = e * lanes + l;
+      if (col < cols && row < rows) {
         const float r = residual ? load_one<kRBf16>(residual, row * ldr + col) : 0.0f;
         t[e] = fmaf(scale, load_one<kXBf16>(x, row * ldx + col), r);
-        if (sum) store_one(sum, kRBf16, row * lds + col, t[e]);
         ss = fmaf(t[e], t[e], ss);
       }
     }
   }
-  __shared__ float part[16];
-  ss = wave_sum64(ss);
-  if (threads > 64) {
-    if ((tid & 63) == 0) part[tid >> 6] = ss;
-    __syncthreads();
-    ss = 0.0f;
-    for (int i = 0; i < threads / 64; ++i) ss += part[i];
+  if (lanes >= 64) {
+    __shared__ float part[16];
+    ss = wave_sum64(ss);
+    if (lanes > 64) {
+      if ((tid & 63) == 0) part[tid >> 6] = ss;
+      __syncthreads();
+      ss = 0.0f;
+      for (int i = 0; i < lanes / 64; ++i) ss += part[i];
+    }
+  } else {
+    for (int m = 1; m < lanes; m <<= 1) ss += __shfl_xor(ss, m, 64);
   }
   const float rms = 1.0f / sqrtf(ss / (float)cols + eps);
   if constexpr (kVec) {
     if (live) {
+      if (sum) store16<kRBf16>(sum, row * lds + col0, t);
       float wv[16];
       load_weight16(w, col0, wv);
 #pragma unroll
       for (int e = 0; e < 16; ++e) t[e] = t[e] * rms * wv[e];
       const float g = out.codes ? *out.gs : 1.0f;
-      store_y(out, row, col0, cols, t, g, __builtin_amdgcn_rcpf(6.0f * g), before);
+      store_y(out, row, col0, cols, t, g, __builtin_amdgcn_rcpf(6.0f * g));
     }
   } else {
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const int col = e * threads + tid;
-      if (col < cols) store_one(out.y, out.y_bf16, row * out.ldy + col, t[e] * rms * w[col]);
+      const int col = e * lanes + l;
+      if (col < cols && row < rows) {
+        if (sum) store_one(sum, kRBf16, row * lds + col, t[e]);
+        store_one(out.y, out.y_bf16, row * out.ldy + col, t[e] * rms * w[col]);
+      }
     }
   }
 }
@@ -225,16 +227,21 @@ __global__ __launch_bounds__(256) void rmsnorm_gated_kernel(const void* __restri
 #pragma unroll
   for (int e = 0; e < 16; ++e) ov[e] = ov[e] * rms * wv[e] * silu(zv[e]);
   const float g = out.codes ? *out.gs : 1.0f;
-  store_y(out, row, col, cols, ov, g, __builtin_amdgcn_rcpf(6.0f * g), 0);
+  store_y(out, row, col, cols, ov, g, __builtin_amdgcn_rcpf(6.0f * g));
 }
 
 template <bool kXBf16, bool kRBf16>
 hipError_t launch_add_typed(bool vec, const void* x, int64_t ldx, const void* residual, int64_t ldr, float scale,
                             const float* w, float eps, int64_t rows, int64_t cols, void* sum, int64_t lds,
                             const NormOut& out, hipStream_t stream) {
-  const unsigned threads = (unsigned)((cols + 16 * 64 - 1) / (16 * 64) * 64);
+  int lanes = 1;
+  while (lanes < 64 && 16 * lanes < cols) lanes *= 2;
+  if (16 * lanes < cols) lanes = (int)((cols + 16 * 64 - 1) / (16 * 64) * 64);
+  const unsigned threads = lanes <= 64 ? 64u : (unsigned)lanes;
+  const int64_t per = threads / lanes;
   const auto f = vec ? add_rmsnorm_kernel<kXBf16, kRBf16, true> : add_rmsnorm_kernel<kXBf16, kRBf16, false>;
-  f<<<(unsigned)rows, threads, 0, stream>>>(x, ldx, residual, ldr, scale, w, eps, cols, sum, lds, out);
+  f<<<(unsigned)((rows + per - 1) / per), threads, 0, stream>>>(x, ldx, residual, ldr, scale, w, eps, rows, cols, lanes,
+                                                                sum, lds, out);
   return hipGetLastError();
 }
 

@@ -195,7 +195,7 @@ def test_refusals():
             bad()
 
 
-@pytest.mark.parametrize("cols", [15, 18, 31, 1009, 1025, 1039, 5119])
+@pytest.mark.parametrize("cols", [15, 18, 31, 33, 100, 511, 1009, 1025, 1039, 5119])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_add_rmsnorm_rows_that_end_inside_a_lane(cols, dtype):
     """The last lane takes values that the lane before it has too, of which it may already have written the sum."""
