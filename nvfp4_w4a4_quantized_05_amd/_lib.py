@@ -438,7 +438,9 @@ def gdn_prefill(x: torch.Tensor, gates: torch.Tensor, cu_seqlens: torch.Tensor, 
     n_slots = n_seqs
     if state_in is not None:
         ip, n_slots = _pool(state_in, torch.float32, (n_v_heads, 128, 128), "state_in")
-    if state_out is not None:
+    if state_out is state_in:
+        op = ip
+    elif state_out is not None:
         op, n_out = _pool(state_out, torch.float32, (n_v_heads, 128, 128), "state_out")
         if ip is not None and n_out != n_slots:
             raise ValueError("state_in and state_out must have the same slots")
