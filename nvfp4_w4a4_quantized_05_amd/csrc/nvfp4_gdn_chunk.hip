@@ -419,8 +419,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
 
 // ---------------------------------------------------------------- the walk over a sequence's chunks
 //
-// One workgroup per sequence, value head and 16 state columns (columns do not
-// meet); eight waves, two per SIMD.  Waves 0-3 carry the state from chunk to
+// One workgroup per sequence, value head and kT tiles of 16 state columns
+// (columns do not meet); eight waves, two per SIMD.  Waves 0-3 carry the state from chunk to
 // chunk, waves 4-7 make the outputs beside them.
 //   State wave w holds state rows 32 w .. + 31 as two accumulators and
 // multiplies them with its own 32 columns of K for all 64 tokens; the four
@@ -433,7 +433,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
 // The output waves also bring V and the row factors to LDS.
 //   Issuing loads bounds the walk as much as the chain of steps does (about 20
 // cycles each on the path to the cache): a chunk takes 63.  Up to 128 registers
-// two workgroups share a CU, which takes 16,384 tokens in 8 sequences (32 value
+// two workgroups of one tile share a CU, which takes 16,384 tokens in 8 sequences (32 value
 // heads) from 483 to 433 us; hence offsets that a wave has in common are kept in
 // scalar registers.
 //   Measured on 32,768 tokens, 32 value heads: 680 us, 1.3 a chunk; the matrix
@@ -442,20 +442,20 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
 // Accumulator row 4 c + e of state tile t is row 32 w + 8 c + 4 t + e of S, so
 // that a lane's rows of both tiles are eight neighbours.
 constexpr int kCols = 16;
-constexpr int kParts = kD / kCols;
 constexpr int kScanThreads = 512;
 constexpr int kTStride = 40;  // bf16 per LDS row of a wave's K columns
 
+template <int kT>
 struct ScanShared {
-  floatx4_t part[4][3][64];    // K S: [token tile][its other waves][lane]
-  u32x2_t rest[3][4][64];      // V - diag(a) K S: [term][token tile][lane]
-  u32x2_t wr[5][4][64];        // W: three terms (scaled) for the state, one for o
-  u32x4_t state[4][2][64];     // S's first two terms: [32 rows][term][lane]
-  uint16_t kt[4][kC * kTStride];  // [wave]: its 32 columns of K
-  uint16_t v[kC * kCols];         // V
-  float vec[2][256];              // row factors a, b, c [64] and e^{G_C} (and as much that is not read)
-  int lost[kCols];                // a column's first token whose value is not finite
-  float decay[64][2];             // [lane][0]: e^{G_C}, NaN where the lane's column is lost
+  floatx4_t part[4][3][kT][64];  // K S: [token tile][its other waves][column tile][lane]
+  u32x2_t rest[3][4][kT][64];    // V - diag(a) K S: [term][token tile][column tile][lane]
+  u32x2_t wr[5][4][kT][64];      // W: three terms (scaled) for the state, two for o
+  u32x4_t state[4][2][kT][64];   // S's first two terms: [32 rows][term][column tile][lane]
+  uint16_t kt[4][kC * kTStride]; // [wave]: its 32 columns of K
+  uint16_t v[kT][kC * kCols];    // V
+  float vec[2][256];             // row factors a, b, c [64] and e^{G_C} (and as much that is not read)
+  int lost[kT * kCols];          // a column's first token whose value is not finite
+  float decay[kT][64][2];        // [column tile][lane][0]: e^{G_C}, NaN where the lane's column is lost
 };
 
 // One unit's rows and workspace, chunk by chunk; chunks past the end have
@@ -485,15 +485,15 @@ struct StateOperands {
   u32x4_t t[3][kB];  // [term][32 columns]
 };
 
-template <int kB>
+template <int kB, int kT>
 struct OutputOperands {
   u32x4_t q[4], p[kB];
-  u32x4_t shared;    // waves 0, 1: half a row of V, row 32 w + lane / 2; wave 2: row factors
+  u32x4_t shared[kT];  // waves 0, 1: half a row of V's tile, row 32 w + lane / 2; wave 2: row factors
 };
 
-template <int kB>
-__device__ __forceinline__ void scan_state(const ChunkSource& src, ScanShared& sh, int w, int lane,
-                                           floatx4_t (&S)[2]) {
+template <int kB, int kT>
+__device__ __forceinline__ void scan_state(const ChunkSource& src, ScanShared<kT>& sh, int w, int lane,
+                                           floatx4_t (&S)[kT][2]) {
   const int m = lane & 15, g = lane >> 4;
   const floatx4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
   typedef __attribute__((address_space(3))) shortx4_t lds_shortx4_t;
@@ -519,81 +519,94 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, ScanShared& s
     // K's columns, read back transposed below (this wave's own)
 #pragma unroll
     for (int t = 0; t < 4; ++t) *reinterpret_cast<u32x4_t*>(&sh.kt[w][(16 * ((w + t) % 4) + m) * kTStride + 8 * g]) = f.k[t];
-    u32x4_t sp[3];
+    floatx4_t own[kT];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int n = 0; n < kT; ++n) {
+      u32x4_t sp[3];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t hi, mid, lo;
+          split3(S[n][t][2 * e], S[n][t][2 * e + 1], hi, mid, lo);
+          sp[0][2 * t + e] = hi;
+          sp[1][2 * t + e] = mid;
+          sp[2][2 * t + e] = lo;
+        }
+      floatx4_t ks[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) ks[t] = mfma_bf16(f.k[t], sp[0], zero);
+#pragma unroll
+      for (int term = 1; term < 3; ++term)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) ks[t] = mfma_bf16(f.k[t], sp[term], ks[t]);
+      mfma_settle(f.k, sp);
+      sh.state[w][0][n][lane] = sp[0];
+      sh.state[w][1][n][lane] = sp[1];
+      __builtin_amdgcn_sched_barrier(0);
+      // tile (w + t) % 4 goes to its wave; this wave's own is t = 0
+#pragma unroll
+      for (int t = 1; t < 4; ++t) sh.part[(w + t) % 4][t - 1][n][lane] = ks[t];
+      own[n] = ks[0];
+    }
+    lds_barrier();
+
+    const floatx4_t fa = *reinterpret_cast<const floatx4_t*>(&sh.vec[0][16 * w + 4 * g]);
+    const floatx4_t fc = *reinterpret_cast<const floatx4_t*>(&sh.vec[0][2 * kC + 16 * w + 4 * g]);
+#pragma unroll
+    for (int n = 0; n < kT; ++n) {
+      floatx4_t kst = own[n];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const floatx4_t x = sh.part[w][i][n][lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) kst[e] += x[e];
+      }
+      // lane 4 j + c of a group of 16 reads columns 4 c .. + 3 of row 4 g + j; the lanes get them back by column
+      const u32x2_t vt = __builtin_bit_cast(
+          u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4_t*)&sh.v[n][(16 * w + 4 * g + m / 4) * kCols + 4 * (m % 4)]));
+      float r[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        r[e] = fmaf(-fa[e], kst[e], __uint_as_float(e & 1 ? vt[e / 2] & 0xFFFF0000u : vt[e / 2] << 16));
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         uint32_t hi, mid, lo;
-        split3(S[t][2 * e], S[t][2 * e + 1], hi, mid, lo);
-        sp[0][2 * t + e] = hi;
-        sp[1][2 * t + e] = mid;
-        sp[2][2 * t + e] = lo;
+        split3(r[2 * e], r[2 * e + 1], hi, mid, lo);
+        sh.rest[0][w][n][lane][e] = hi;
+        sh.rest[1][w][n][lane][e] = mid;
+        sh.rest[2][w][n][lane][e] = lo;
       }
-    floatx4_t ks[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) ks[t] = mfma_bf16(f.k[t], sp[0], zero);
-#pragma unroll
-    for (int term = 1; term < 3; ++term)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) ks[t] = mfma_bf16(f.k[t], sp[term], ks[t]);
-    mfma_settle(f.k, sp);
-    sh.state[w][0][lane] = sp[0];
-    sh.state[w][1][lane] = sp[1];
-    __builtin_amdgcn_sched_barrier(0);
-    // tile (w + t) % 4 goes to its wave; this wave's own is t = 0
-#pragma unroll
-    for (int t = 1; t < 4; ++t) sh.part[(w + t) % 4][t - 1][lane] = ks[t];
-    lds_barrier();
-
-    floatx4_t kst = ks[0];
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const floatx4_t x = sh.part[w][i][lane];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) kst[e] += x[e];
-    }
-    // lane 4 j + c of a group of 16 reads columns 4 c .. + 3 of row 4 g + j; the lanes get them back by column
-    const u32x2_t vt = __builtin_bit_cast(
-        u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4_t*)&sh.v[(16 * w + 4 * g + m / 4) * kCols + 4 * (m % 4)]));
-    const floatx4_t fa = *reinterpret_cast<const floatx4_t*>(&sh.vec[0][16 * w + 4 * g]);
-    const floatx4_t fc = *reinterpret_cast<const floatx4_t*>(&sh.vec[0][2 * kC + 16 * w + 4 * g]);
-    float r[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      r[e] = fmaf(-fa[e], kst[e], __uint_as_float(e & 1 ? vt[e / 2] & 0xFFFF0000u : vt[e / 2] << 16));
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      uint32_t hi, mid, lo;
-      split3(r[2 * e], r[2 * e + 1], hi, mid, lo);
-      sh.rest[0][w][lane][e] = hi;
-      sh.rest[1][w][lane][e] = mid;
-      sh.rest[2][w][lane][e] = lo;
     }
     fetch_k(next, fn);
     lds_barrier();
 
     // W = T (V - ..): the six products of terms i, j with i + j <= 2
-    floatx4_t wt = zero, w1 = zero;
-    {
+    floatx4_t wt[kT];
+#pragma unroll
+    for (int n = 0; n < kT; ++n) {
+      floatx4_t w0 = zero, w1 = zero;
       u32x4_t rv[3][kB];
 #pragma unroll
       for (int term = 0; term < 3; ++term)
 #pragma unroll
-        for (int sb = 0; sb < kB; ++sb) rv[term][sb] = join(sh.rest[term][2 * sb][lane], sh.rest[term][2 * sb + 1][lane]);
-      int n = 0;
+        for (int sb = 0; sb < kB; ++sb)
+          rv[term][sb] = join(sh.rest[term][2 * sb][n][lane], sh.rest[term][2 * sb + 1][n][lane]);
+      int turn = 0;
 #pragma unroll
       for (int order = 2; order >= 0; --order)
 #pragma unroll
         for (int i = 0; i <= order; ++i)
 #pragma unroll
           for (int sb = 0; sb < kB; ++sb) {  // two sums in turn: a product waits for the one before it
-            floatx4_t& acc = n++ % 2 ? w1 : wt;
+            floatx4_t& acc = turn++ % 2 ? w1 : w0;
             acc = mfma_bf16(f.t[i][sb], rv[order - i][sb], acc);
           }
       mfma_settle(f.t, rv);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) wt[n][e] = w0[e] + w1[e];
     }
-    u32x4_t kT[2][2];
+    u32x4_t kc[2][2];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -603,42 +616,46 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, ScanShared& s
           // as above: lane 4 c + e gets column 8 c + 4 t + e of four token rows
           const uint16_t* at = &sh.kt[w][(32 * sb + 16 * half + 4 * g + m / 4) * kTStride + 8 * (m % 4) + 4 * t];
           const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4_t*)at));
-          kT[t][sb][2 * half] = v[0];
-          kT[t][sb][2 * half + 1] = v[1];
+          kc[t][sb][2 * half] = v[0];
+          kc[t][sb][2 * half + 1] = v[1];
         }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) wt[e] += w1[e];
+    for (int n = 0; n < kT; ++n)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      uint32_t hi, mid, lo;
-      split3(wt[2 * e] * fc[2 * e], wt[2 * e + 1] * fc[2 * e + 1], hi, mid, lo);
-      sh.wr[0][w][lane][e] = hi;
-      sh.wr[1][w][lane][e] = mid;
-      sh.wr[2][w][lane][e] = lo;
-      const uint32_t p = pack_bf16(wt[2 * e], wt[2 * e + 1]);
-      sh.wr[3][w][lane][e] = p;
-      sh.wr[4][w][lane][e] = pack_bf16(wt[2 * e] - __uint_as_float(p << 16), wt[2 * e + 1] - __uint_as_float(p & 0xFFFF0000u));
-    }
+      for (int e = 0; e < 2; ++e) {
+        const float x = wt[n][2 * e], y = wt[n][2 * e + 1];
+        uint32_t hi, mid, lo;
+        split3(x * fc[2 * e], y * fc[2 * e + 1], hi, mid, lo);
+        sh.wr[0][w][n][lane][e] = hi;
+        sh.wr[1][w][n][lane][e] = mid;
+        sh.wr[2][w][n][lane][e] = lo;
+        const uint32_t p = pack_bf16(x, y);
+        sh.wr[3][w][n][lane][e] = p;
+        sh.wr[4][w][n][lane][e] = pack_bf16(x - __uint_as_float(p << 16), y - __uint_as_float(p & 0xFFFF0000u));
+      }
     fetch_t(next, fn);
     lds_barrier();
 
-    u32x4_t wv[3][2];
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-#pragma unroll
-      for (int sb = 0; sb < 2; ++sb) wv[i][sb] = join(sh.wr[i][2 * sb][lane], sh.wr[i][2 * sb + 1][lane]);
     // S' = e^{G_C} S + K^T (c W)
-    const float decay = sh.decay[lane][0];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int n = 0; n < kT; ++n) {
+      const float decay = sh.decay[n][lane][0];
+      u32x4_t wv[3][2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) S[t][e] *= decay;
+      for (int i = 0; i < 3; ++i)
 #pragma unroll
-      for (int term = 2; term >= 0; --term)
+        for (int sb = 0; sb < 2; ++sb) wv[i][sb] = join(sh.wr[i][2 * sb][n][lane], sh.wr[i][2 * sb + 1][n][lane]);
 #pragma unroll
-        for (int sb = 0; sb < 2; ++sb) S[t] = mfma_bf16(kT[t][sb], wv[term][sb], S[t]);
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[n][t][e] *= decay;
+#pragma unroll
+        for (int term = 2; term >= 0; --term)
+#pragma unroll
+          for (int sb = 0; sb < 2; ++sb) S[n][t] = mfma_bf16(kc[t][sb], wv[term][sb], S[n][t]);
+      }
+      mfma_settle(kc, wv);
     }
-    mfma_settle(kT, wv);
   };
 
   StateOperands<kB> f0, f1;
@@ -652,10 +669,10 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, ScanShared& s
   if (c < src.n_chunks) chunk(f0, c + 1, f1);
 }
 
-template <int kB>
-__device__ __forceinline__ void scan_output(const ChunkSource& src, ScanShared& sh, int w, int lane) {
+template <int kB, int kT>
+__device__ __forceinline__ void scan_output(const ChunkSource& src, ScanShared<kT>& sh, int w, int lane) {
   const int m = lane & 15, g = lane >> 4;
-  auto fetch = [&](int c, OutputOperands<kB>& f) {
+  auto fetch = [&](int c, OutputOperands<kB, kT>& f) {
     const __amdgpu_buffer_rsrc_t rh = src.heads(c), r = src.units(c);
 #pragma unroll
     for (int i = 0; i < 4; ++i) f.q[i] = load16b(rh, (uint32_t)(kOffQ + (4 * i + w) * kOperand + lane * 16));
@@ -664,69 +681,85 @@ __device__ __forceinline__ void scan_output(const ChunkSource& src, ScanShared& 
     if constexpr (kB == 1) {
       const __amdgpu_buffer_rsrc_t rv =
           make_rsrc(src.v + (c < src.n_chunks ? c : 0) * src.v_step, (int64_t)src.rows(c) * src.v_ld);
-      f.shared = load16b(rv, (uint32_t)(32 * w + lane / 2) * src.v_ld + (lane & 1) * 16);
+#pragma unroll
+      for (int n = 0; n < kT; ++n)
+        f.shared[n] = load16b(rv, (uint32_t)(32 * w + lane / 2) * src.v_ld + (lane & 1) * 16 + n * kCols * 2);
     } else {
-      f.shared = load16b(r, w == 2 ? (uint32_t)(kOffVec + lane * 16) : kOutside);
+      f.shared[0] = load16b(r, w == 2 ? (uint32_t)(kOffVec + lane * 16) : kOutside);
     }
   };
   // what all waves need of a chunk, between the third barrier of the one before and its own first
-  auto share = [&](int c, OutputOperands<kB>& f) {
+  auto share = [&](int c, OutputOperands<kB, kT>& f) {
     if constexpr (kB == 1) {
-      uint32_t full = 0;  // the carry of an exponent of all ones
 #pragma unroll
-      for (int e = 0; e < 4; ++e) full |= (f.shared[e] & 0x7F807F80u) + 0x00800080u;
-      if (full & 0x80008000u)
+      for (int n = 0; n < kT; ++n) {
+        u32x4_t& v = f.shared[n];
+        uint32_t full = 0;  // the carry of an exponent of all ones
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t exponent = 0x7F80u << 16 * (e % 2);
-          if ((f.shared[e / 2] & exponent) == exponent) {
-            f.shared[e / 2] &= 0xFFFFu << 16 * (1 - e % 2);
-            atomicMin(&sh.lost[8 * (lane & 1) + e], c * kC + 32 * w + lane / 2);
+        for (int e = 0; e < 4; ++e) full |= (v[e] & 0x7F807F80u) + 0x00800080u;
+        if (full & 0x80008000u)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t exponent = 0x7F80u << 16 * (e % 2);
+            if ((v[e / 2] & exponent) == exponent) {
+              v[e / 2] &= 0xFFFFu << 16 * (1 - e % 2);
+              atomicMin(&sh.lost[n * kCols + 8 * (lane & 1) + e], c * kC + 32 * w + lane / 2);
+            }
           }
-        }
-      *reinterpret_cast<u32x4_t*>(&sh.v[512 * w + 8 * lane]) = f.shared;
+        *reinterpret_cast<u32x4_t*>(&sh.v[n][512 * w + 8 * lane]) = v;
+      }
     } else
-      *reinterpret_cast<u32x4_t*>(&sh.vec[w - 2][4 * lane]) = f.shared;
+      *reinterpret_cast<u32x4_t*>(&sh.vec[w - 2][4 * lane]) = f.shared[0];
   };
-  auto chunk = [&](int c, const OutputOperands<kB>& f, OutputOperands<kB>& fn) {
+  auto chunk = [&](int c, const OutputOperands<kB, kT>& f, OutputOperands<kB, kT>& fn) {
     fetch(c + 1, fn);
     lds_barrier();
     const float b = sh.vec[0][kC + 16 * w + m];
-    floatx4_t ov = {0.0f, 0.0f, 0.0f, 0.0f};
-    u32x4_t st[2][4];
+    floatx4_t ov[kT];
 #pragma unroll
-    for (int term = 1; term >= 0; --term)
+    for (int n = 0; n < kT; ++n) {
+      ov[n] = floatx4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      u32x4_t st[2][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        st[term][i] = sh.state[i][term][lane];
-        ov = mfma_bf16(st[term][i], f.q[i], ov);
-      }
-    mfma_settle(st, f.q);
-    if (kB == 2 && w == 2) sh.decay[lane][0] = sh.lost[m] < (c + 1) * kC ? __builtin_nanf("") : sh.vec[0][3 * kC];
+      for (int term = 1; term >= 0; --term)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          st[term][i] = sh.state[i][term][n][lane];
+          ov[n] = mfma_bf16(st[term][i], f.q[i], ov[n]);
+        }
+      mfma_settle(st, f.q);
+      if (kB == 2 && w == 2)
+        sh.decay[n][lane][0] = sh.lost[n * kCols + m] < (c + 1) * kC ? __builtin_nanf("") : sh.vec[0][3 * kC];
+    }
     lds_barrier();
 #pragma unroll
-    for (int e = 0; e < 4; ++e) ov[e] *= b;
+    for (int n = 0; n < kT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ov[n][e] *= b;
     lds_barrier();
-    u32x4_t wo[2][kB];
-#pragma unroll
-    for (int i = 1; i >= 0; --i)
-#pragma unroll
-      for (int sb = 0; sb < kB; ++sb) {
-        wo[i][sb] = join(sh.wr[3 + i][2 * sb][lane], sh.wr[3 + i][2 * sb + 1][lane]);
-        ov = mfma_bf16(wo[i][sb], f.p[sb], ov);
-      }
-    mfma_settle(wo, f.p);
     const __amdgpu_buffer_rsrc_t ro = make_rsrc(src.o + c * src.o_step, (int64_t)src.rows(c) * src.o_ld);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (c * kC + 16 * w + m >= sh.lost[4 * g + e]) ov[e] = __builtin_nanf("");
-    u32x2_t out;
-    out[0] = pack_bf16(ov[0], ov[1]);
-    out[1] = pack_bf16(ov[2], ov[3]);
-    __builtin_amdgcn_raw_buffer_store_b64(out, ro, (uint32_t)(16 * w + m) * src.o_ld + 8 * g, 0, 0);
+    for (int n = 0; n < kT; ++n) {
+      u32x4_t wo[2][kB];
+#pragma unroll
+      for (int i = 1; i >= 0; --i)
+#pragma unroll
+        for (int sb = 0; sb < kB; ++sb) {
+          wo[i][sb] = join(sh.wr[3 + i][2 * sb][n][lane], sh.wr[3 + i][2 * sb + 1][n][lane]);
+          ov[n] = mfma_bf16(wo[i][sb], f.p[sb], ov[n]);
+        }
+      mfma_settle(wo, f.p);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c * kC + 16 * w + m >= sh.lost[n * kCols + 4 * g + e]) ov[n][e] = __builtin_nanf("");
+      u32x2_t out;
+      out[0] = pack_bf16(ov[n][0], ov[n][1]);
+      out[1] = pack_bf16(ov[n][2], ov[n][3]);
+      __builtin_amdgcn_raw_buffer_store_b64(out, ro, (uint32_t)(16 * w + m) * src.o_ld + 8 * g + n * kCols * 2, 0, 0);
+    }
     share(c + 1, fn);
   };
-  OutputOperands<kB> f0, f1;
+  OutputOperands<kB, kT> f0, f1;
   fetch(0, f0);
   share(0, f0);
   int c = 0;
@@ -752,23 +785,25 @@ __device__ __forceinline__ int nth_longest(const int32_t* cu, int n_seqs, int64_
   return __builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < n_seqs && rank == n));
 }
 
+template <int kT>
 __global__ __launch_bounds__(kScanThreads) void gdn_chunk_scan_kernel(
     GdnRows in, const int32_t* __restrict__ cu, int n_seqs, int64_t T, const uint8_t* ws, const uint8_t* wsh,
     const float* s_in, float* s_out, const int32_t* __restrict__ slots, int n_slots,
     uint16_t* o, int64_t ldo) {
-  __shared__ ScanShared sh;
-  // the eight column parts of a unit run on one XCD and share its L2
+  constexpr int kParts = kD / (kT * kCols);
+  __shared__ ScanShared<kT> sh;
+  // the column parts of a unit run on one XCD and share its L2
   const int unit = (int)(blockIdx.x / (8 * kParts)) * 8 + blockIdx.x % 8;
   const int part = blockIdx.x / 8 % kParts;
   if (unit >= n_seqs * in.n_v) return;
   const int s = nth_longest(cu, n_seqs, T, unit / in.n_v), h = unit % in.n_v, hk = h / (in.n_v / in.n_qk);
   const int64_t start = row_clip(cu[s], T), end = max(row_clip(cu[s + 1], T), start);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int col = part * kCols;
+  const int col = part * kT * kCols;
   const int slot = slots ? slots[s] : s;
   if (slot < 0 || slot >= n_slots) {
-    for (int64_t t = start + tid / kCols; t < end; t += kScanThreads / kCols)
-      o[t * ldo + h * kD + col + tid % kCols] = 0;
+    for (int64_t t = start + tid / (kT * kCols); t < end; t += kScanThreads / (kT * kCols))
+      o[t * ldo + h * kD + col + tid % (kT * kCols)] = 0;
     return;
   }
   ChunkSource src;
@@ -785,26 +820,30 @@ __global__ __launch_bounds__(kScanThreads) void gdn_chunk_scan_kernel(
   src.last_rows = (int)(end - start - (int64_t)(src.n_chunks - 1) * kC);
   src.v_ld = (uint32_t)in.ldx * 2;
   src.o_ld = (uint32_t)ldo * 2;
-  if (tid < kCols) sh.lost[tid] = INT_MAX;
+  if (tid < kT * kCols) sh.lost[tid] = INT_MAX;
   __syncthreads();
-  if (wave >= 6) return scan_output<2>(src, sh, wave - 4, lane);
-  if (wave >= 4) return scan_output<1>(src, sh, wave - 4, lane);
+  if (wave >= 6) return scan_output<2, kT>(src, sh, wave - 4, lane);
+  if (wave >= 4) return scan_output<1, kT>(src, sh, wave - 4, lane);
 
   const int64_t at = ((int64_t)slot * in.n_v + h) * kD * kD + (32 * wave + 8 * (lane >> 4)) * kD + col + (lane & 15);
-  floatx4_t S[2];
+  floatx4_t S[kT][2];
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) S[t][e] = s_in ? s_in[at + (4 * t + e) * kD] : 0.0f;
-  if (wave < 2)
-    scan_state<1>(src, sh, wave, lane, S);
-  else
-    scan_state<2>(src, sh, wave, lane, S);
-  if (s_out) {
+  for (int n = 0; n < kT; ++n)
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s_out[at + (4 * t + e) * kD] = S[t][e];
+      for (int e = 0; e < 4; ++e) S[n][t][e] = s_in ? s_in[at + (4 * t + e) * kD + n * kCols] : 0.0f;
+  if (wave < 2)
+    scan_state<1, kT>(src, sh, wave, lane, S);
+  else
+    scan_state<2, kT>(src, sh, wave, lane, S);
+  if (s_out) {
+#pragma unroll
+    for (int n = 0; n < kT; ++n)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s_out[at + (4 * t + e) * kD + n * kCols] = S[n][t][e];
   }
 }
 
@@ -1110,6 +1149,12 @@ int64_t chunk_places(int64_t T, int64_t n_seqs) { return T / kC + n_seqs + 1; }
 // Measured, split / whole, 32 value heads: 32,768 tokens in 48 sequences 883 /
 // 631 us, in 16 (512 units) 823 / 781 us; 16,384 in 8 (256 units) 433 / 632 us.
 constexpr int64_t kWideUnits = 512;
+// From this many on, a workgroup of the split form has two column tiles, which
+// halves the loads of a chunk's operands but leaves a CU to one workgroup.
+// Measured, one / two tiles: 27,000 tokens in 7 sequences (224 units) 703 / 623
+// us, 16,384 in 8 (256) 442 / 391, 8,191 in 12 (384) 238 / 230, 16,000 in 16 with
+// 12 value heads (192) 151 / 157, 8,192 in 4 (128) 232 / 291.
+constexpr int64_t kPairUnits = 192;
 // Below this many chunks x q/k heads, the preparation takes one workgroup per
 // value head instead of one per q/k head (which makes the group's K and Q
 // products once): 300 tokens x 4 heads 11 -> 9 us.
@@ -1135,8 +1180,11 @@ hipError_t launch_gdn_prefill(const GdnRows& in, const int32_t* cu, int n_seqs, 
   if (units >= kWideUnits)
     gdn_chunk_wide_kernel<<<(unsigned)units, kWideThreads, 0, stream>>>(
         in, cu, n_seqs, T, ws, wsh, s_in, s_out, slots, n_slots, static_cast<uint16_t*>(o), ldo);
+  else if (units >= kPairUnits)
+    gdn_chunk_scan_kernel<2><<<(unsigned)((units + 7) / 8 * 8 * (kD / (2 * kCols))), kScanThreads, 0, stream>>>(
+        in, cu, n_seqs, T, ws, wsh, s_in, s_out, slots, n_slots, static_cast<uint16_t*>(o), ldo);
   else
-    gdn_chunk_scan_kernel<<<(unsigned)((units + 7) / 8 * 8 * kParts), kScanThreads, 0, stream>>>(
+    gdn_chunk_scan_kernel<1><<<(unsigned)((units + 7) / 8 * 8 * (kD / kCols)), kScanThreads, 0, stream>>>(
         in, cu, n_seqs, T, ws, wsh, s_in, s_out, slots, n_slots, static_cast<uint16_t*>(o), ldo);
   return hipGetLastError();
 }

@@ -167,6 +167,13 @@ def test_prefill_many_sequences(lens, n_qk, n_v, gates):
     _prefill(lens, n_qk, n_v, gates=gates, seed=len(lens), pad=1, tail=3, skip=(4, 7, 23), separate=True)
 
 
+@pytest.mark.parametrize("lens,n_qk,n_v,gates,kind", [
+    ([1, 70, 0, 64, 130, 3, 63, 65] * 3, 2, 8, BF, "mixed"), ([200, 1, 0, 65] * 16, 1, 3, F32, "hold"),
+    ([129] * 6, 16, 32, F32, "reset"), ([5, 64, 192] * 9, 4, 12, BF, "scales")])   # 192 to 324 sequences x heads
+def test_prefill_some_sequences(lens, n_qk, n_v, gates, kind):
+    _prefill(lens, n_qk, n_v, gates=gates, kind=kind, seed=len(lens) + n_v, pad=1, tail=3, skip=(2,), separate=True)
+
+
 def test_prefill_many_sequences_hard_values():
     _prefill([64, 20, 70] * 22, 1, 8, kind="reset", seed=21)
     _prefill([30, 129] * 32, 2, 8, kind="scales", seed=22)
@@ -400,14 +407,14 @@ def test_refusals():
     assert nv.gdn_decode(x[:0], gates[:0], st8, **lay).shape == (0, 2 * D)
 
 
-@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("many", [0, 23, 90])
 @pytest.mark.parametrize("part,value", [("q", np.nan), ("k", np.nan), ("k", -np.inf), ("v", np.nan), ("v", np.inf),
                                         ("g", np.nan), ("beta", np.inf)])
 def test_prefill_what_is_not_finite_stays_where_it_belongs(many, part, value):
     """Bit for bit: a product with a zero of the inverse or the scores adds nothing, so what an infinity or NaN in
     one token cannot reach token by token (earlier tokens, other heads, columns, sequences) is as without it."""
     dev = need_gpu()
-    lens = [7, 150, 3] + ([1, 2] * 90 if many else [])
+    lens = [7, 150, 3] + [1, 2] * many
     n, n_qk, n_v, T = len(lens), 2, 4, sum(lens)
     cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device=dev)
     x, g, beta = _inputs(T, n_qk, n_v, 31)
