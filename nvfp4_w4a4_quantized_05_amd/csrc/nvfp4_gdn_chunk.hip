@@ -149,9 +149,9 @@ __device__ __forceinline__ void lds_barrier() {
 constexpr int kKStride = kD + 8;   // bf16 per LDS row of K
 constexpr int kXStride = kC + 4;   // floats per LDS row of A, T
 
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void gdn_chunk_prepare_kernel(GdnRows in, const int32_t* __restrict__ cu, int n_seqs,
-                                                                int64_t T, uint8_t* __restrict__ ws, uint8_t* __restrict__ wsh,
-                                                                int split) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void gdn_chunk_prepare_kernel(
+    GdnRows in, const int32_t* __restrict__ cu, int n_seqs, int64_t T, uint8_t* __restrict__ ws,
+    uint8_t* __restrict__ wsh, int split) {
   __shared__ __attribute__((aligned(16))) uint16_t kl[kC * kKStride];
   __shared__ __attribute__((aligned(16))) float X[kC * kXStride];
   // K is read only before the first head's gates; then its place takes four blocks of 16 x 16
@@ -501,7 +501,8 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, ScanShared<kT
   auto fetch_k = [&](int c, StateOperands<kB>& f) {
     const __amdgpu_buffer_rsrc_t r = src.heads(c);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) f.k[t] = load16b(r, (uint32_t)(k_place(m, g) * 16), (uint32_t)((4 * w + (w + t) % 4) * kOperand));
+    for (int t = 0; t < 4; ++t)
+      f.k[t] = load16b(r, (uint32_t)(k_place(m, g) * 16), (uint32_t)((4 * w + (w + t) % 4) * kOperand));
   };
   auto fetch_t = [&](int c, StateOperands<kB>& f) {
     const __amdgpu_buffer_rsrc_t r = src.units(c);
