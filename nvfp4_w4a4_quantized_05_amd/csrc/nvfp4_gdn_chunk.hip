@@ -18,9 +18,11 @@
 // the matrix cores.  S, T, V - ... and W are fp32 and enter as the sum of three
 // bf16 numbers (8 + 8 + 8 bits: exact), with the six largest of the nine
 // products where both sides are split: the state is as exact as an fp32 sum.
-// For O alone, whose result is bf16, S and W enter as their first two terms
-// and P is rounded to bf16 once: o is 0.0021 (2-norm, relative) off the 64-bit
-// result where rounding that to bf16 costs 0.0017.
+// For O alone, whose result is bf16, S, W and P enter as two terms each (at
+// most 2^-15 of S and 2^-16 of W and P off), with three of the four products
+// of P and W: o is the 64-bit result rounded to bf16, but where that lies this
+// close to the middle of two neighbours (0.0017 off it, 2-norm, relative, all
+// of it that rounding; 0.0021 with P in one term).
 // Decays inside a chunk are exponentials of differences of G, which is summed
 // in fp64 and kept as two floats, so that a strong decay before both tokens
 // does not cost the difference its digits.
@@ -59,7 +61,7 @@ typedef short shortx4_t __attribute__((ext_vector_type(4)));
 constexpr int kOperand = 1024;                     // bytes: 64 lanes x 8 bf16
 constexpr int kBlocks = 6;                         // (w, s) with s <= w / 2
 constexpr int kOffP = 3 * kBlocks * kOperand;      // after T's three terms
-constexpr int kOffVec = kOffP + kBlocks * kOperand;  // a, b, c [64] and e^{G_C}, fp32
+constexpr int kOffVec = kOffP + 2 * kBlocks * kOperand;  // after P's two: a, b, c [64] and e^{G_C}, fp32
 constexpr int kUnitBytes = kOffVec + 1024;
 // And for a chunk and q/k head: K, then Q, as operands of 16 tokens x 32
 // columns, [32 columns][16 tokens], so that a load is 1 KiB in a row.  K's
@@ -114,6 +116,12 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t&
   mid = __builtin_amdgcn_perm(mb, ma, 0x07060302u);
   lo = __builtin_amdgcn_perm(__float_as_uint(rb - __uint_as_float(mb)), __float_as_uint(ra - __uint_as_float(ma)),
                              0x07060302u);
+}
+
+// a as the sum of two bf16 numbers, both rounded to nearest (2^-16 of a off at most); two values packed.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16(a, b);
+  lo = pack_bf16(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
 }
 
 __device__ __forceinline__ u32x4_t join(u32x2_t a, u32x2_t b) {
@@ -291,7 +299,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
     }
     const int hw = hv % 4;
 
-    // A (fp32, to LDS) and P (bf16, out)
+    // A (fp32, to LDS) and P (two bf16 terms, out)
     const int i = 16 * w + m;
     const float alpha_i = alpha_l[hw][i], beta_i = beta_l[hw][i];
     const float bhi = i ? ghi_l[hw][max(i - 1, 0)] : 0.0f, blo = i ? glo_l[hw][max(i - 1, 0)] : 0.0f;
@@ -316,11 +324,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
         }
         *reinterpret_cast<floatx4_t*>(&X[i * kXStride + 16 * j + 4 * g]) = a;
       }
-      u32x2_t pp;
-      pp[0] = pack_bf16(p[0], p[1]);
-      pp[1] = pack_bf16(p[2], p[3]);
-      __builtin_amdgcn_raw_buffer_store_b64(pp, unit, (uint32_t)(lane * 16 + (j & 1) * 8),
-                                            kOffP + block_of(w, j / 2) * kOperand, 0);
+      u32x2_t pp[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t hi, lo;
+        split2(p[2 * e], p[2 * e + 1], hi, lo);
+        pp[0][e] = hi;
+        pp[1][e] = lo;
+      }
+#pragma unroll
+      for (int term = 0; term < 2; ++term)
+        __builtin_amdgcn_raw_buffer_store_b64(pp[term], unit, (uint32_t)(lane * 16 + (j & 1) * 8),
+                                              kOffP + (term * kBlocks + block_of(w, j / 2)) * kOperand, 0);
     }
     __builtin_amdgcn_wave_barrier();  // the diagonal block is this wave's own
 
@@ -487,7 +502,7 @@ struct StateOperands {
 
 template <int kB, int kT>
 struct OutputOperands {
-  u32x4_t q[4], p[kB];
+  u32x4_t q[4], p[2][kB];  // [32 columns], [term][32 columns]
   u32x4_t shared[kT];  // waves 0, 1: half a row of V's tile, row 32 w + lane / 2; wave 2: row factors
 };
 
@@ -630,9 +645,9 @@ __device__ __forceinline__ void scan_state(const ChunkSource& src, ScanShared<kT
         sh.wr[0][w][n][lane][e] = hi;
         sh.wr[1][w][n][lane][e] = mid;
         sh.wr[2][w][n][lane][e] = lo;
-        const uint32_t p = pack_bf16(x, y);
-        sh.wr[3][w][n][lane][e] = p;
-        sh.wr[4][w][n][lane][e] = pack_bf16(x - __uint_as_float(p << 16), y - __uint_as_float(p & 0xFFFF0000u));
+        split2(x, y, hi, lo);
+        sh.wr[3][w][n][lane][e] = hi;
+        sh.wr[4][w][n][lane][e] = lo;
       }
     fetch_t(next, fn);
     lds_barrier();
@@ -676,9 +691,12 @@ __device__ __forceinline__ void scan_output(const ChunkSource& src, ScanShared<k
   auto fetch = [&](int c, OutputOperands<kB, kT>& f) {
     const __amdgpu_buffer_rsrc_t rh = src.heads(c), r = src.units(c);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f.q[i] = load16b(rh, (uint32_t)(kOffQ + (4 * i + w) * kOperand + lane * 16));
+    for (int i = 0; i < 4; ++i) f.q[i] = load16b(rh, (uint32_t)(lane * 16), (uint32_t)(kOffQ + (4 * i + w) * kOperand));
 #pragma unroll
-    for (int sb = 0; sb < kB; ++sb) f.p[sb] = load16b(r, (uint32_t)(kOffP + block_of(w, sb) * kOperand + lane * 16));
+    for (int term = 0; term < 2; ++term)
+#pragma unroll
+      for (int sb = 0; sb < kB; ++sb)
+        f.p[term][sb] = load16b(r, (uint32_t)(lane * 16), (uint32_t)(kOffP + (term * kBlocks + block_of(w, sb)) * kOperand));
     if constexpr (kB == 1) {
       const __amdgpu_buffer_rsrc_t rv =
           make_rsrc(src.v + (c < src.n_chunks ? c : 0) * src.v_step, (int64_t)src.rows(c) * src.v_ld);
@@ -743,12 +761,15 @@ __device__ __forceinline__ void scan_output(const ChunkSource& src, ScanShared<k
     for (int n = 0; n < kT; ++n) {
       u32x4_t wo[2][kB];
 #pragma unroll
-      for (int i = 1; i >= 0; --i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int sb = 0; sb < kB; ++sb) {
-          wo[i][sb] = join(sh.wr[3 + i][2 * sb][n][lane], sh.wr[3 + i][2 * sb + 1][n][lane]);
-          ov[n] = mfma_bf16(wo[i][sb], f.p[sb], ov[n]);
-        }
+        for (int sb = 0; sb < kB; ++sb) wo[i][sb] = join(sh.wr[3 + i][2 * sb][n][lane], sh.wr[3 + i][2 * sb + 1][n][lane]);
+#pragma unroll
+      for (int order = 1; order >= 0; --order)  // terms i of P and order - i of W, the small products first
+#pragma unroll
+        for (int i = 0; i <= order; ++i)
+#pragma unroll
+          for (int sb = 0; sb < kB; ++sb) ov[n] = mfma_bf16(wo[order - i][sb], f.p[i][sb], ov[n]);
       mfma_settle(wo, f.p);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -859,10 +880,11 @@ __global__ __launch_bounds__(kScanThreads) void gdn_chunk_scan_kernel(
 constexpr int kWideWaves = 8;
 constexpr int kWideThreads = 64 * kWideWaves;
 
+constexpr int kWideUnitBytes = (kUnitBytes + kWideWaves * kOperand - 1) / (kWideWaves * kOperand) * (kWideWaves * kOperand);
+
 struct WideShared {
   uint8_t head[2][kHeadBytes];                // [chunk parity]: K and Q
-  uint8_t unit[2][4 * kBlocks * kOperand];    // T and P
-  float vec[2][256];                          // row factors a, b, c [64] and e^{G_C} (and as much that is not read)
+  uint8_t unit[2][kWideUnitBytes];            // T, P and the row factors as they lie in the workspace
   uint16_t v[kWideWaves][kC * kCols];         // [wave]: V's columns
 };
 
@@ -893,17 +915,16 @@ __global__ __launch_bounds__(kWideThreads) void gdn_chunk_wide_kernel(
     return make_rsrc(wsh + ((place + (c < n_chunks ? c : 0)) * in.n_qk + hk) * kHeadBytes, c < n_chunks ? kHeadBytes : 0);
   };
 
-  // This wave's share of what goes to LDS: an eighth of K, Q, T and P, its columns of V; the row factors come from
-  // every wave alike.  No branches: a load in one makes its use wait for every load in flight.
-  constexpr int kHeadShare = kHeadBytes / kOperand / kWideWaves, kUnitShare = 4 * kBlocks / kWideWaves;
-  u32x4_t sk[kHeadShare], st[kUnitShare], sv[2], sf;
+  // This wave's share of what goes to LDS: an eighth of K, Q, T, P and the row factors (what lies past the unit's end
+  // loads as zeros), its columns of V.  No branches: a load in one makes its use wait for every load in flight.
+  constexpr int kHeadShare = kHeadBytes / kOperand / kWideWaves, kUnitShare = kWideUnitBytes / kOperand / kWideWaves;
+  u32x4_t sk[kHeadShare], st[kUnitShare], sv[2];
   auto stage = [&](int c) {
     const __amdgpu_buffer_rsrc_t rh = heads(c), ru = units(c);
 #pragma unroll
     for (int i = 0; i < kHeadShare; ++i) sk[i] = load16b(rh, (uint32_t)((kHeadShare * w + i) * kOperand + lane * 16));
 #pragma unroll
     for (int i = 0; i < kUnitShare; ++i) st[i] = load16b(ru, (uint32_t)((kUnitShare * w + i) * kOperand + lane * 16));
-    sf = load16b(ru, (uint32_t)(kOffVec + lane * 16));
     const __amdgpu_buffer_rsrc_t rv =
         make_rsrc(reinterpret_cast<const uint16_t*>(in.x) + (start + (c < n_chunks ? (int64_t)c * kC : 0)) * in.ldx + in.v_col + h * kD + col,
                   rows(c) * v_ld);
@@ -918,7 +939,6 @@ __global__ __launch_bounds__(kWideThreads) void gdn_chunk_wide_kernel(
 #pragma unroll
     for (int i = 0; i < kUnitShare; ++i)
       *reinterpret_cast<u32x4_t*>(&sh.unit[p][(kUnitShare * w + i) * kOperand + lane * 16]) = st[i];
-    *reinterpret_cast<u32x4_t*>(&sh.vec[p][4 * lane]) = sf;
 #pragma unroll
     for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4_t*>(&sh.v[w][512 * i + 8 * lane]) = sv[i];
   };
@@ -945,7 +965,7 @@ __global__ __launch_bounds__(kWideThreads) void gdn_chunk_wide_kernel(
     const uint8_t* q_lds = k_lds + kOffQ + lane * 16;
     const uint8_t* t_lds = sh.unit[c & 1] + lane * 16;
     const uint8_t* p_lds = t_lds + kOffP;
-    const float* vec = sh.vec[c & 1];
+    const float* vec = reinterpret_cast<const float*>(sh.unit[c & 1] + kOffVec);
 
     // K S and Q S (the latter transposed: rows = state columns, lanes = tokens)
     floatx4_t ks[4] = {zero, zero, zero, zero}, qs[4] = {zero, zero, zero, zero};
@@ -1049,9 +1069,9 @@ __global__ __launch_bounds__(kWideThreads) void gdn_chunk_wide_kernel(
           wv[0][u][2 * t + e] = hi;
           wv[1][u][2 * t + e] = mid;
           wv[2][u][2 * t + e] = lo;
-          const uint32_t b = pack_bf16(x, y);
-          wo[0][u][2 * t + e] = b;
-          wo[1][u][2 * t + e] = pack_bf16(x - __uint_as_float(b << 16), y - __uint_as_float(b & 0xFFFF0000u));
+          split2(x, y, hi, lo);
+          wo[0][u][2 * t + e] = hi;
+          wo[1][u][2 * t + e] = lo;
         }
       }
     }
@@ -1065,13 +1085,19 @@ __global__ __launch_bounds__(kWideThreads) void gdn_chunk_wide_kernel(
     }
 #pragma unroll
     for (int sb = 0; sb < 2; ++sb) {
-      u32x4_t p[4];
+      u32x4_t p[4][2];  // [row tile][term]
 #pragma unroll
-      for (int t = 2 * sb; t < 4; ++t) p[t] = *reinterpret_cast<const u32x4_t*>(p_lds + block_of(t, sb) * kOperand);
+      for (int t = 2 * sb; t < 4; ++t)
 #pragma unroll
-      for (int term = 0; term < 2; ++term)
+        for (int term = 0; term < 2; ++term)
+          p[t][term] = *reinterpret_cast<const u32x4_t*>(p_lds + (term * kBlocks + block_of(t, sb)) * kOperand);
+      // terms i of P and order - i of W, the small products first
 #pragma unroll
-        for (int t = 2 * sb; t < 4; ++t) qs[t] = mfma_bf16(wo[term][sb], p[t], qs[t]);
+      for (int order = 1; order >= 0; --order)
+#pragma unroll
+        for (int i = 0; i <= order; ++i)
+#pragma unroll
+          for (int t = 2 * sb; t < 4; ++t) qs[t] = mfma_bf16(wo[order - i][sb], p[t][i], qs[t]);
       if (sb == 0)
         mfma_settle(p, wo);
       else
