@@ -121,7 +121,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_silu_kernel(
   using R = Row<kBf16, kVec>;
   const int64_t t0 = (int64_t)blockIdx.x * kRows;
   const int64_t t1 = min(t0 + kRows, T);
-  // the last sequence that starts at or before t0: no earlier one has a row in the tile
+  // the last sequence that starts at or before t0 (cut off or not): no earlier one has a row in the tile
   const int first = last_before(n_seqs, [&](int i) { return cu[i] <= t0; });
   const int64_t mine0 = ((int64_t)blockIdx.y * kConvThreads + threadIdx.x) * kVec;
   if (mine0 >= channels) return;
@@ -131,9 +131,9 @@ __global__ __launch_bounds__(kConvThreads) void conv_silu_kernel(
   load_weights<kVec, kW>(w, c, wt);
 
   for (int s = first; s < n_seqs; ++s) {
-    const int64_t start = cu[s], end = min((int64_t)cu[s + 1], T);
+    const int64_t start = row_clip(cu[s], T), end = row_clip(cu[s + 1], T);
     if (start >= t1) break;
-    if (end <= start || start < 0) continue;
+    if (end <= start) continue;
     const bool mine = start >= t0;  // this tile holds the first row
     int64_t t = mine ? start : max(t0, min(start + kW - 1, end));
     const int64_t stop = mine ? min(end, max(t1, start + kW - 1)) : min(end, t1);

@@ -77,6 +77,9 @@ __device__ __forceinline__ int last_before(int n, F before) {
   return __builtin_amdgcn_readfirstlane(first);
 }
 
+// Row numbers of packed sequences that a call may use: cut off at 0 and T.
+__device__ __forceinline__ int64_t row_clip(int32_t r, int64_t T) { return min(max((int64_t)r, (int64_t)0), T); }
+
 // Sum over the wave's 64 lanes, the same bits in every lane: each step adds
 // the same two values in either order.
 __device__ __forceinline__ float wave_sum64(float v) {

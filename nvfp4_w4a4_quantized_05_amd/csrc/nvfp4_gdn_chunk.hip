@@ -130,8 +130,6 @@ __device__ __forceinline__ u32x4_t join(u32x2_t a, u32x2_t b) {
   return r;
 }
 
-// Row numbers a call may use: cut off at 0 and T.
-__device__ __forceinline__ int64_t row_clip(int32_t r, int64_t T) { return min(max((int64_t)r, (int64_t)0), T); }
 // Workspace place of a sequence's first chunk.  cu / 64 + s leaves room for
 // one partial chunk per sequence, so places need no sum over sequences.
 __device__ __forceinline__ int64_t first_place(int64_t start, int s) { return start / kC + s; }
