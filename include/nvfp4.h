@@ -427,7 +427,8 @@ NVFP4_API nvfp4_status_t nvfp4_harmonize_fused_scales(uint8_t* scales, const flo
  * Mechanics"): per value head and token
  *     S_t = alpha_t S_{t-1} + beta_t khat_t (v_t - S_{t-1}^T khat_t)^T,
  *     o_t = S_t^T qhat_t / sqrt(128),  alpha_t = exp(g_t),
- * qhat, khat the head's q, k divided by max(|.|, 1e-6).
+ * qhat, khat the head's q, k divided by max(|.|, 1e-6), for every finite q and
+ * k (nvfp4_gdn_recurrence: while |.|^2 is finite in fp32).
  *
  *   x           device bf16 [T x ldx], one row per token (read); 16-byte
  *               aligned, ldx and the columns multiples of 8; ldx < 2^23

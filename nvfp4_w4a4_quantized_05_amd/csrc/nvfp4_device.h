@@ -80,6 +80,14 @@ __device__ __forceinline__ int last_before(int n, F before) {
 // Row numbers of packed sequences that a call may use: cut off at 0 and T.
 __device__ __forceinline__ int64_t row_clip(int32_t r, int64_t T) { return min(max((int64_t)r, (int64_t)0), T); }
 
+// What a row of 128 finite values with the squared length `sum2` (as fp32 gives
+// it, infinite on overflow) is multiplied by before it is used in place of its
+// unit vector's numerator: 2^-70 from a length of 2^52 on.  Then neither its
+// squared length (at most 2^123) nor a product of two such rows or their factors
+// overflows or becomes subnormal, and its length stays past the least one that
+// counts, 1e-6.  Exact but for values 2^-108 of the row.
+__device__ __forceinline__ float large_row_scale(float sum2) { return sum2 < 0x1p104f ? 1.0f : 0x1p-70f; }
+
 // Sum over the wave's 64 lanes, the same bits in every lane: each step adds
 // the same two values in either order.
 __device__ __forceinline__ float wave_sum64(float v) {

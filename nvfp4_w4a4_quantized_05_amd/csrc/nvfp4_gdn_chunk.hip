@@ -188,22 +188,32 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
     kf[i] = load16b(rx, live ? at + (uint32_t)in.k_col * 2 : kOutside);
     qf[i] = load16b(rx, live ? at + (uint32_t)in.q_col * 2 : kOutside);
   }
-  float k2 = 0.0f, q2 = 0.0f;
+  const auto length2 = [](const u32x4_t (&x)[4]) {  // of token 16 w + m: the four lanes that share it
+    float sum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float k0 = __uint_as_float(kf[i][e] << 16), k1 = __uint_as_float(kf[i][e] & 0xFFFF0000u);
-      const float q0 = __uint_as_float(qf[i][e] << 16), q1 = __uint_as_float(qf[i][e] & 0xFFFF0000u);
-      k2 = fmaf(k0, k0, fmaf(k1, k1, k2));
-      q2 = fmaf(q0, q0, fmaf(q1, q1, q2));
-    }
+      for (int e = 0; e < 4; ++e) {
+        const float x0 = __uint_as_float(x[i][e] << 16), x1 = __uint_as_float(x[i][e] & 0xFFFF0000u);
+        sum = fmaf(x0, x0, fmaf(x1, x1, sum));
+      }
+    sum += __shfl_xor(sum, 16, 64);
+    return sum + __shfl_xor(sum, 32, 64);
+  };
+  float k2 = length2(kf), q2 = length2(qf);
+  const float k_scale = large_row_scale(k2), q_scale = large_row_scale(q2);
+  if (__builtin_amdgcn_ballot_w64(k_scale != 1.0f || q_scale != 1.0f)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        kf[i][e] = pack_bf16(__uint_as_float(kf[i][e] << 16) * k_scale, __uint_as_float(kf[i][e] & 0xFFFF0000u) * k_scale);
+        qf[i][e] = pack_bf16(__uint_as_float(qf[i][e] << 16) * q_scale, __uint_as_float(qf[i][e] & 0xFFFF0000u) * q_scale);
+      }
+    k2 = length2(kf);
+    q2 = length2(qf);
   }
-  k2 += __shfl_xor(k2, 16, 64);
-  q2 += __shfl_xor(q2, 16, 64);
-  k2 += __shfl_xor(k2, 32, 64);
-  q2 += __shfl_xor(q2, 32, 64);
-  const bool k_bad = !(k2 <= __FLT_MAX__);
+  const bool k_bad = !(k2 <= __FLT_MAX__);  // a value that is not finite: what large_row_scale leaves cannot overflow
   uint8_t* head = wsh + (place * in.n_qk + hk) * kHeadBytes;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

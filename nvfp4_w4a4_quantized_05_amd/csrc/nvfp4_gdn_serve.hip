@@ -93,13 +93,23 @@ __global__ __launch_bounds__(256) void gdn_decode_kernel(GdnRows in, float* stat
     k[i] = load_val4<kXBf16>(in.x, k_at + r0 + 4 * i);
     q[i] = load_val4<kXBf16>(in.x, q_at + r0 + 4 * i);
   }
-  const float ka = load_val<kXBf16>(in.x, k_at + lane), kb = load_val<kXBf16>(in.x, k_at + 64 + lane);
-  const float qa = load_val<kXBf16>(in.x, q_at + lane), qb = load_val<kXBf16>(in.x, q_at + 64 + lane);
+  float ka = load_val<kXBf16>(in.x, k_at + lane), kb = load_val<kXBf16>(in.x, k_at + 64 + lane);
+  float qa = load_val<kXBf16>(in.x, q_at + lane), qb = load_val<kXBf16>(in.x, q_at + 64 + lane);
   const floatx4_t v = load_val4<kXBf16>(in.x, b * in.ldx + in.v_col + (int64_t)h * kD + col);
   const float alpha = expf(load_gate(in.gates, in.gates_bf16, b * in.ldg + in.g_col + h));
   const float beta = load_gate(in.gates, in.gates_bf16, b * in.ldg + in.beta_col + h);
-  const float rk = 1.0f / fmaxf(sqrtf(wave_sum64(fmaf(ka, ka, kb * kb))), kNormEps);
-  const float rq = 1.0f / fmaxf(sqrtf(wave_sum64(fmaf(qa, qa, qb * qb))), kNormEps);
+  float k2 = wave_sum64(fmaf(ka, ka, kb * kb)), q2 = wave_sum64(fmaf(qa, qa, qb * qb));
+  const float k_scale = large_row_scale(k2), q_scale = large_row_scale(q2);
+  if (k_scale != 1.0f || q_scale != 1.0f) {  // the same in every lane
+    ka *= k_scale, kb *= k_scale, qa *= q_scale, qb *= q_scale;
+#pragma unroll
+    for (int i = 0; i < kRows / 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) k[i][e] *= k_scale, q[i][e] *= q_scale;
+    k2 = wave_sum64(fmaf(ka, ka, kb * kb));
+    q2 = wave_sum64(fmaf(qa, qa, qb * qb));
+  }
+  const float rk = 1.0f / fmaxf(sqrtf(k2), kNormEps), rq = 1.0f / fmaxf(sqrtf(q2), kNormEps);
   const float kq = wave_sum64(fmaf(ka, qa, kb * qb)) * rk * rq;
 
   floatx4_t u = {0.0f, 0.0f, 0.0f, 0.0f}, sq = u;
