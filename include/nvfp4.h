@@ -65,7 +65,7 @@ typedef enum {
   NVFP4_ERR_ALIGN = 5,     /* a pointer is not aligned as documented           */
   NVFP4_ERR_WORKSPACE = 6, /* workspace too small                              */
   NVFP4_ERR_HIP = 7,       /* a HIP launch failed; see nvfp4_last_hip_error()  */
-  NVFP4_ERR_ALIAS = 8,     /* an output overlaps an input it must not overlap  */
+  NVFP4_ERR_ALIAS = 8,     /* an output overlaps what it must not overlap      */
   NVFP4_ERR_TOO_LARGE = 9  /* more than the allocation-free entry point's static
                               scratch (nvfp4_quantize_gemm_no_alloc)         */
 } nvfp4_status_t;
@@ -415,6 +415,10 @@ NVFP4_API nvfp4_status_t nvfp4_harmonize_fused_scales(uint8_t* scales, const flo
  *     sequence or request whose slot is outside 0 .. n_slots - 1 is skipped:
  *     its output rows are written as zeros and no state is touched (unused
  *     rows of a padded batch carry -1).  Slots of one call must be distinct.
+ *   - Nothing that a call writes may lie on anything else that it reads or
+ *     writes (NVFP4_ERR_ALIAS), except where a call allows it.  Rows are
+ *     compared column by column when their strides are the same: other columns
+ *     of the rows that hold an input are fine.
  *   - Non-finite inputs of a request give unspecified values in that
  *     request's outputs and state (of the value heads they reach), and
  *     change no other request's.
@@ -503,7 +507,7 @@ NVFP4_API nvfp4_status_t nvfp4_gdn_decode(const void* x, int32_t x_dtype, int64_
  * first in its slot; without a pool they are zeros.
  *
  *   x           device [T x ldx] of `dtype` (NVFP4_IN_F32 / _BF16), `channels`
- *               columns (read); must not overlap y (NVFP4_ERR_ALIAS)
+ *               columns (read)
  *   w           device fp32 [channels x width]
  *   width       2, 3 or 4
  *   cu_seqlens, n_seqs   as above; NULL: every row is the one new token of
@@ -536,9 +540,10 @@ NVFP4_API nvfp4_status_t nvfp4_conv_silu(const void* x, int32_t dtype, int64_t l
  *   w           device fp32 [cols];  eps > 0 and finite
  *   rows, cols  0 <= rows <= 2^22, 1 <= cols <= 16384
  *   residual_out  device out [rows x ldro] of `r_dtype`: t, or NULL.  May be
- *               residual itself (same stride)
+ *               residual or x itself (same type and stride)
  *   y           device out [rows x ldy] of `y_dtype` (NVFP4_OUT_F32 / _BF16),
- *               or NULL when codes are asked for
+ *               or NULL when codes are asked for.  May be residual or x itself
+ *               (same type and stride)
  *   y_gs, y_codes, y_scales   y as NVFP4 under the given tensor scale *y_gs
  *               (device, read), the bytes nvfp4_quantize gives for the fp32
  *               y: [rows x cols/2] (8-byte aligned) and [rows x cols/16]; or
@@ -566,7 +571,8 @@ NVFP4_API nvfp4_status_t nvfp4_add_rmsnorm(const void* x, int32_t x_dtype, int64
  *   w           device fp32 [group], the same for every group
  *   rows, cols  rows >= 0, rows * cols < 2^35; cols % group == 0
  *   group       16, 32, 64, ... or 1024
- *   y, y_dtype, ldy, y_gs, y_codes, y_scales   as for nvfp4_add_rmsnorm
+ *   y, y_dtype, ldy, y_gs, y_codes, y_scales   as for nvfp4_add_rmsnorm; y may
+ *               be o or z itself (same type and stride)
  * All pointers and row strides 16-byte aligned (codes 8, scales 1).
  */
 NVFP4_API nvfp4_status_t nvfp4_rmsnorm_gated(const void* o, int32_t o_dtype, int64_t ldo, const void* z,

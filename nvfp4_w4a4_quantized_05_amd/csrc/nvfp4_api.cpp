@@ -7,6 +7,7 @@
 
 #include <climits>
 #include <cmath>
+#include <initializer_list>
 
 #include "nvfp4_internal.h"
 
@@ -100,6 +101,43 @@ int64_t in_size(int32_t d) { return d == NVFP4_IN_BF16 ? 2 : 4; }
 bool extent_ok(int64_t rows, int64_t ld) { return ld > 0 && rows <= INT64_MAX / ld / 4; }
 bool row_aligned(const void* p, int64_t ld, int64_t esize) { return aligned(p, 16) && ld * esize % 16 == 0; }
 
+// Memory that a call reads or writes: `rows` rows of `width` bytes, `step`
+// bytes apart (step >= width); a plain array is one row, an absent one is at 0.
+struct Span {
+  uintptr_t at;
+  uint64_t rows, width, step;
+};
+Span row_span(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t esize) {
+  return {(uintptr_t)p, (uint64_t)rows, (uint64_t)(cols * esize), (uint64_t)(ld * esize)};
+}
+Span array_span(const void* p, uint64_t bytes) { return {(uintptr_t)p, 1, bytes, bytes}; }
+
+bool overlap(const Span& a, const Span& b) {
+  if (!a.at || !b.at || !a.rows || !b.rows || !a.width || !b.width) return false;
+  if (a.at >= b.at + (b.rows - 1) * b.step + b.width || b.at >= a.at + (a.rows - 1) * a.step + a.width) return false;
+  // rows of one step are apart as far as their columns are
+  if (a.rows == 1 || b.rows == 1 || a.step != b.step) return true;
+  const uint64_t d = b.at >= a.at ? (b.at - a.at) % a.step : (a.step - (a.at - b.at) % a.step) % a.step;
+  return d < a.width || d + b.width > a.step;
+}
+
+// Whether what a call writes lies on anything else of it.  It may be one of
+// `in_place` exactly, value by value.
+bool clash(std::initializer_list<Span> written, std::initializer_list<Span> read,
+           std::initializer_list<Span> in_place = {}) {
+  for (const Span* w = written.begin(); w != written.end(); ++w) {
+    for (const Span* v = written.begin(); v != w; ++v)
+      if (overlap(*w, *v)) return true;
+    for (const Span& r : read)
+      if (overlap(*w, r)) return true;
+    for (const Span& r : in_place)
+      if (overlap(*w, r) &&
+          !(w->at == r.at && w->rows == r.rows && w->width == r.width && (w->rows == 1 || w->step == r.step)))
+        return true;
+  }
+  return false;
+}
+
 // Shapes of the rows of nvfp4_gdn_prefill and nvfp4_gdn_decode.
 nvfp4_status_t gdn_rows_shape(const nvfp4::GdnRows& in, int32_t gates_dtype) {
   constexpr int64_t kD = 128, kMaxLd = (int64_t)1 << 23;
@@ -121,6 +159,23 @@ bool gdn_rows_aligned(const nvfp4::GdnRows& in, int64_t xsize) {
          aligned(in.gates, in.gates_bf16 ? 2 : 4);
 }
 
+// Whether o or the written states of a recurrence call lie on what it reads;
+// `scratch` is written too.
+bool gdn_clash(const nvfp4::GdnRows& in, int64_t xsize, int64_t rows, const Span& o, const Span& state_out,
+               const Span& state_in, const Span& scratch, const Span& cu, const Span& slots) {
+  const auto x = [&](int64_t col, int64_t heads) {
+    return row_span(static_cast<const char*>(in.x) + col * xsize, in.x ? rows : 0, heads * 128, in.ldx, xsize);
+  };
+  const int64_t gsize = in.gates_bf16 ? 2 : 4;
+  const auto gate = [&](int64_t col) {
+    return row_span(static_cast<const char*>(in.gates) + col * gsize, in.gates ? rows : 0, in.n_v, in.ldg, gsize);
+  };
+  return clash({o, scratch}, {state_in}) ||
+         clash({o, state_out, scratch},
+               {x(in.q_col, in.n_qk), x(in.k_col, in.n_qk), x(in.v_col, in.n_v), gate(in.g_col), gate(in.beta_col), cu, slots},
+               {state_in});
+}
+
 // Checks of a norm's destinations that nvfp4_add_rmsnorm and
 // nvfp4_rmsnorm_gated share; `quant`: codes are asked for.
 nvfp4_status_t norm_out_checks(const nvfp4::NormOut& out, int64_t rows, int64_t cols, bool& quant) {
@@ -132,6 +187,16 @@ nvfp4_status_t norm_out_checks(const nvfp4::NormOut& out, int64_t rows, int64_t 
   if (quant && (!aligned(out.codes, 8) || !aligned(out.gs, 4))) return NVFP4_ERR_ALIGN;
   if (out.y && !aligned(out.y, out.y_bf16 ? 2 : 4)) return NVFP4_ERR_ALIGN;
   return NVFP4_OK;
+}
+
+// Whether what a norm writes (y, codes, scales and t) lies on anything else of
+// it; a and b, its inputs, may be in the place of y or t.
+bool norm_clash(const nvfp4::NormOut& out, int64_t rows, int64_t cols, const Span& t, const Span& w, const Span& a,
+                const Span& b) {
+  const Span gs = array_span(out.gs, 4);
+  const Span codes = array_span(out.codes, (uint64_t)rows * cols / 2), scales = array_span(out.scales, (uint64_t)rows * cols / 16);
+  return clash({row_span(out.y, rows, cols, out.ldy, out.y_bf16 ? 2 : 4), t, codes, scales}, {w, gs}, {a, b}) ||
+         clash({codes, scales}, {a, b});
 }
 
 }  // namespace
@@ -410,6 +475,11 @@ nvfp4_status_t nvfp4_gdn_prefill(const void* x, int64_t ldx, int64_t q_col, int6
     if (workspace_bytes < need) return NVFP4_ERR_WORKSPACE;
     if (need > 0 && !workspace) return NVFP4_ERR_NULL;
     if (need > 0 && !aligned(workspace, 256)) return NVFP4_ERR_ALIGN;
+    const uint64_t pool = (uint64_t)n_slots * n_v_heads * 128 * 128 * 4;
+    if (gdn_clash(in, 2, T, row_span(o, T, (int64_t)n_v_heads * 128, ldo, 2), array_span(state_out, pool),
+                  array_span(state_in, pool), array_span(workspace, need), array_span(cu_seqlens, 4 * ((uint64_t)n_seqs + 1)),
+                  array_span(slots, 4 * (uint64_t)n_seqs)))
+      return NVFP4_ERR_ALIAS;
     return hip_status(nvfp4::launch_gdn_prefill(in, cu_seqlens, n_seqs, T, state_in, state_out, slots, n_slots, o,
                                                 ldo, workspace, (hipStream_t)stream));
   } catch (...) {
@@ -442,6 +512,11 @@ nvfp4_status_t nvfp4_gdn_decode(const void* x, int32_t x_dtype, int64_t ldx, int
     if (!gdn_rows_aligned(in, in_size(x_dtype)) || !row_aligned(o, ldo, o_dtype == NVFP4_OUT_BF16 ? 2 : 4) ||
         !aligned(states, 16) || !aligned(slots, 4))
       return NVFP4_ERR_ALIGN;
+    if (gdn_clash(in, in_size(x_dtype), batch,
+                  row_span(o, batch, (int64_t)n_v_heads * 128, ldo, o_dtype == NVFP4_OUT_BF16 ? 2 : 4),
+                  array_span(states, (uint64_t)n_slots * n_v_heads * 128 * 128 * 4), Span{}, Span{}, Span{},
+                  array_span(slots, 4 * (uint64_t)batch)))
+      return NVFP4_ERR_ALIAS;
     return hip_status(nvfp4::launch_gdn_decode(in, x_dtype == NVFP4_IN_BF16, batch, states, slots, n_slots, o,
                                                o_dtype == NVFP4_OUT_BF16, ldo, (hipStream_t)stream));
   } catch (...) {
@@ -465,9 +540,11 @@ nvfp4_status_t nvfp4_conv_silu(const void* x, int32_t dtype, int64_t ldx, int64_
         !aligned(slots, 4))
       return NVFP4_ERR_ALIGN;
     // neighbouring rows are read by other threads than the ones that write them
-    const uintptr_t x0 = (uintptr_t)x, x1 = x0 + (uintptr_t)(((T - 1) * ldx + channels) * e);
-    const uintptr_t y0 = (uintptr_t)y, y1 = y0 + (uintptr_t)(((T - 1) * ldy + channels) * e);
-    if (x0 < y1 && y0 < x1) return NVFP4_ERR_ALIAS;
+    if (clash({row_span(y, T, channels, ldy, e), array_span(state, (uint64_t)n_slots * (width - 1) * channels * e)},
+              {row_span(x, T, channels, ldx, e), array_span(w, (uint64_t)channels * width * 4),
+               array_span(cu_seqlens, cu_seqlens ? 4 * ((uint64_t)n_seqs + 1) : 0),
+               array_span(slots, 4 * (uint64_t)(cu_seqlens ? n_seqs : T))}))
+      return NVFP4_ERR_ALIAS;
     // without a pool every sequence starts at zeros and none is skipped
     return hip_status(nvfp4::launch_conv_silu(x, dtype == NVFP4_IN_BF16, ldx, channels, w, width, cu_seqlens,
                                               n_seqs, T, state, state ? slots : nullptr, state ? n_slots : 1, y, ldy,
@@ -502,6 +579,10 @@ nvfp4_status_t nvfp4_add_rmsnorm(const void* x, int32_t x_dtype, int64_t ldx, co
                   (residual_out && !row_aligned(residual_out, ldro, re)) ||
                   (y && !row_aligned(y, ldy, out.y_bf16 ? 2 : 4)) || !aligned(w, 16)))
       return NVFP4_ERR_ALIGN;
+    // a row is read whole before any of it is written
+    if (norm_clash(out, rows, cols, row_span(residual_out, rows, cols, ldro, re), array_span(w, cols * 4),
+                   row_span(x, rows, cols, ldx, xe), row_span(residual, rows, cols, ldr, re)))
+      return NVFP4_ERR_ALIAS;
     return hip_status(nvfp4::launch_add_rmsnorm(x, x_dtype == NVFP4_IN_BF16, ldx, residual,
                                                 r_dtype == NVFP4_IN_BF16, ldr, scale, w, eps, rows, cols,
                                                 residual_out, ldro, out, (hipStream_t)stream));
@@ -531,6 +612,10 @@ nvfp4_status_t nvfp4_rmsnorm_gated(const void* o, int32_t o_dtype, int64_t ldo, 
     if (!row_aligned(o, ldo, in_size(o_dtype)) || !row_aligned(z, ldz, in_size(z_dtype)) || !aligned(w, 16) ||
         (y && !row_aligned(y, ldy, out.y_bf16 ? 2 : 4)))
       return NVFP4_ERR_ALIGN;
+    // a lane reads its values before it writes y there
+    if (norm_clash(out, rows, cols, Span{}, array_span(w, group * 4), row_span(o, rows, cols, ldo, in_size(o_dtype)),
+                   row_span(z, rows, cols, ldz, in_size(z_dtype))))
+      return NVFP4_ERR_ALIAS;
     return hip_status(nvfp4::launch_rmsnorm_gated(o, o_dtype == NVFP4_IN_BF16, ldo, z, z_dtype == NVFP4_IN_BF16, ldz,
                                                   w, eps, rows, cols, group, out, (hipStream_t)stream));
   } catch (...) {

@@ -201,10 +201,10 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const void* x, int64_
 }
 
 // One lane per 16 values; the group's lanes (group / 16, a power of two up to 64) are consecutive
-// and add their squares with lane exchanges.
+// and add their squares with lane exchanges.  y may be in the place of o or z:
+// a lane reads no value but those it writes.
 template <bool kOBf16, bool kZBf16>
-__global__ __launch_bounds__(256) void rmsnorm_gated_kernel(const void* __restrict__ o, int64_t ldo,
-                                                            const void* __restrict__ z, int64_t ldz,
+__global__ __launch_bounds__(256) void rmsnorm_gated_kernel(const void* o, int64_t ldo, const void* z, int64_t ldz,
                                                             const float* __restrict__ w, float eps, int64_t rows,
                                                             int64_t cols, int group, NormOut out) {
   const int64_t chunks = cols / 16;
