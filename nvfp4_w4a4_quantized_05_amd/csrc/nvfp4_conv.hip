@@ -112,14 +112,19 @@ constexpr int kConvThreads = 256;
 // (5.3 TB/s) with 16 bytes a lane, 505-765 with 32.
 constexpr int kRows = 16, kAhead = 8;
 
-// Packed sequences: grid (tiles of kRows rows, channel blocks).
+// Tiles along x of a grid: a launch takes less than 2^32 threads along one
+// dimension, so those of 2^26 rows and more go on along z.
+constexpr int64_t kTilesX = (int64_t)1 << 22;
+
+// Packed sequences: grid (tiles of kRows rows, channel blocks, kTilesX tiles).
 template <bool kBf16, int kVec, int kW>
 __global__ __launch_bounds__(kConvThreads) void conv_silu_kernel(
     const void* __restrict__ x, int64_t ldx, int64_t channels, const float* __restrict__ w, const int32_t* __restrict__ cu,
     int n_seqs, int64_t T, void* state, const int32_t* __restrict__ slots, int n_slots, void* __restrict__ y,
     int64_t ldy) {
   using R = Row<kBf16, kVec>;
-  const int64_t t0 = (int64_t)blockIdx.x * kRows;
+  const int64_t t0 = (blockIdx.z * kTilesX + blockIdx.x) * kRows;
+  if (t0 >= T) return;
   const int64_t t1 = min(t0 + kRows, T);
   // the last sequence that starts at or before t0 (cut off or not): no earlier one has a row in the tile
   const int first = last_before(n_seqs, [&](int i) { return cu[i] <= t0; });
@@ -234,7 +239,8 @@ hipError_t launch_conv_typed(const void* x, int64_t ldx, int64_t channels, const
                              int64_t ldy, hipStream_t stream) {
   const unsigned blocks = (unsigned)((channels + kConvThreads * kVec - 1) / (kConvThreads * kVec));
   if (cu) {
-    const dim3 grid((unsigned)((T + kRows - 1) / kRows), blocks);
+    const int64_t tiles = (T + kRows - 1) / kRows;
+    const dim3 grid((unsigned)(tiles < kTilesX ? tiles : kTilesX), blocks, (unsigned)((tiles + kTilesX - 1) / kTilesX));
     conv_silu_kernel<kBf16, kVec, kW><<<grid, kConvThreads, 0, stream>>>(x, ldx, channels, w, cu, n_seqs, T, state,
                                                                          slots, n_slots, y, ldy);
   } else {
