@@ -538,7 +538,8 @@ NVFP4_API nvfp4_status_t nvfp4_conv_silu(const void* x, int32_t dtype, int64_t l
  *   residual    device [rows x ldr] of `r_dtype`, or NULL for zeros
  *   scale       the residual scale, finite
  *   w           device fp32 [cols];  eps > 0 and finite
- *   rows, cols  0 <= rows <= 2^22, 1 <= cols <= 16384
+ *   rows, cols  0 <= rows <= 2^22 (less than that if cols > 15360),
+ *               1 <= cols <= 16384
  *   residual_out  device out [rows x ldro] of `r_dtype`: t, or NULL.  May be
  *               residual or x itself (same type and stride)
  *   y           device out [rows x ldy] of `y_dtype` (NVFP4_OUT_F32 / _BF16),

@@ -562,6 +562,8 @@ nvfp4_status_t nvfp4_add_rmsnorm(const void* x, int32_t x_dtype, int64_t ldx, co
     if (!in_dtype_ok(x_dtype) || !in_dtype_ok(r_dtype)) return NVFP4_ERR_DTYPE;
     if (y_dtype != NVFP4_OUT_F32 && y_dtype != NVFP4_OUT_BF16) return NVFP4_ERR_DTYPE;
     if (rows < 0 || rows > (1 << 22) || cols < 1 || cols > nvfp4::kMaxNormCols) return NVFP4_ERR_SHAPE;
+    // grid size (threads below 2^32): a row of more than 15 x 1,024 columns takes 1,024
+    if (rows == (1 << 22) && cols > 15 * 1024) return NVFP4_ERR_SHAPE;
     if (!(eps > 0.0f) || !std::isfinite(eps) || !std::isfinite(scale)) return NVFP4_ERR_SHAPE;
     if (ldx < cols || !extent_ok(rows, ldx)) return NVFP4_ERR_SHAPE;
     if (residual && (ldr < cols || !extent_ok(rows, ldr))) return NVFP4_ERR_SHAPE;
