@@ -603,7 +603,7 @@ nvfp4_status_t nvfp4_rmsnorm_gated(const void* o, int32_t o_dtype, int64_t ldo, 
     if (group < 16 || group > 1024 || (group & (group - 1)) != 0) return NVFP4_ERR_SHAPE;
     if (rows < 0 || cols < 1 || cols % group != 0 || cols > INT_MAX || ldo < cols || ldz < cols)
       return NVFP4_ERR_SHAPE;
-    if (rows >= ((int64_t)1 << 35) / cols || !extent_ok(rows, ldo) || !extent_ok(rows, ldz)) return NVFP4_ERR_SHAPE;
+    if (rows > (((int64_t)1 << 35) - 1) / cols || !extent_ok(rows, ldo) || !extent_ok(rows, ldz)) return NVFP4_ERR_SHAPE;
     if (!(eps > 0.0f) || !std::isfinite(eps)) return NVFP4_ERR_SHAPE;
     if (rows == 0) return NVFP4_OK;
     if (!o || !z || !w) return NVFP4_ERR_NULL;
