@@ -363,8 +363,9 @@ def _new(shape, dtype, device, stream):
 
 def _rows(t, what):
     """(address, dtype code, rows, columns, row stride) of a 2-D bf16 or fp32
-    GPU tensor with unit column stride; the stride of one row or fewer is its
-    width."""
+    GPU tensor with unit column stride.  One row or fewer has no stride, only a
+    width: the next multiple of 8 that holds it (16 bytes), since a stride that
+    no address is made of must not be refused."""
     code = _DTYPE_CODE.get(t.dtype)
     if code is None or t.dim() != 2:
         raise ValueError(f"{what} must be 2-D bf16 or fp32, got {t.dtype} {tuple(t.shape)}")
@@ -374,7 +375,7 @@ def _rows(t, what):
         raise ValueError(f"{what} must have unit column stride")
     if not t.is_cuda:
         raise ValueError("nvfp4 calls take GPU tensors only")
-    return t.data_ptr(), code, rows, cols, ld if rows > 1 else (cols or 1)
+    return t.data_ptr(), code, rows, cols, ld if rows > 1 else max(-(-cols // 8) * 8, 8)
 
 
 def _vector(t, dtype, n, what):
