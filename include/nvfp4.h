@@ -432,7 +432,11 @@ NVFP4_API nvfp4_status_t nvfp4_harmonize_fused_scales(uint8_t* scales, const flo
  *     S_t = alpha_t S_{t-1} + beta_t khat_t (v_t - S_{t-1}^T khat_t)^T,
  *     o_t = S_t^T qhat_t / sqrt(128),  alpha_t = exp(g_t),
  * qhat, khat the head's q, k divided by max(|.|, 1e-6), for every finite q and
- * k (nvfp4_gdn_recurrence: while |.|^2 is finite in fp32).
+ * k (nvfp4_gdn_recurrence: while |.|^2 is finite in fp32).  The correction
+ * reads S_{t-1} before its decay, as that page prints the rule.  The published
+ * Gated DeltaNet decays the state first (alpha_t S_{t-1}^T khat_t in the
+ * bracket): weights trained with it give other outputs here wherever alpha_t
+ * is well below 1.  The same holds for nvfp4_gdn_decode.
  *
  *   x           device bf16 [T x ldx], one row per token (read); 16-byte
  *               aligned, ldx and the columns multiples of 8; ldx < 2^23
@@ -462,6 +466,18 @@ NVFP4_API nvfp4_status_t nvfp4_harmonize_fused_scales(uint8_t* scales, const flo
  * finite reaches what it reaches token by token: in q_t the outputs of that
  * token and head, in k_t or a gate the outputs from t on and the state, in v_t
  * the same of its column; nothing before t and no other sequence.
+ *   Precision: the states are as exact as fp32 sums token by token; o is the
+ * result rounded to bf16 once, from operands of at least 16 bits.  Which of
+ * three kernels walks the chunks depends on n_seqs * n_v_heads, and with it
+ * the order of sums: the last bits of o and of the states of one sequence may
+ * differ between calls with different numbers of sequences (the same call
+ * always gives the same bits).  The choice takes the sequences for about
+ * equally long: one long sequence with many short, empty or skipped ones
+ * beside it (n_seqs * n_v_heads >= 512) takes up to three times as long as
+ * alone.
+ *   Workspace: about 24 KB per token for 16 / 32 heads (0.8 GB for 32,768
+ * tokens), the chunks' triangular matrices and row factors of each value head
+ * and K and Q in operand order.
  */
 NVFP4_API nvfp4_status_t nvfp4_gdn_prefill(const void* x, int64_t ldx, int64_t q_col, int64_t k_col, int64_t v_col,
                                            const void* gates, int32_t gates_dtype, int64_t ldg, int64_t g_col,
@@ -518,8 +534,8 @@ NVFP4_API nvfp4_status_t nvfp4_gdn_decode(const void* x, int32_t x_dtype, int64_
  *               NULL (read, and written with the last width - 1 inputs)
  *   slots, n_slots   as above (not read without a state)
  *   y           device out [T x ldy] of `dtype`
- * Any alignment of whole elements works; 16-byte aligned pointers and
- * strides and channels % 8 == 0 take 16-byte loads.
+ * Any alignment of whole elements works; 8 bf16 or 4 fp32 channels and more
+ * are read and written 16 bytes at a time.
  */
 NVFP4_API nvfp4_status_t nvfp4_conv_silu(const void* x, int32_t dtype, int64_t ldx, int64_t channels, const float* w,
                                          int32_t width, const int32_t* cu_seqlens, int32_t n_seqs, int64_t T,
@@ -550,8 +566,8 @@ NVFP4_API nvfp4_status_t nvfp4_conv_silu(const void* x, int32_t dtype, int64_t l
  *               y: [rows x cols/2] (8-byte aligned) and [rows x cols/16]; or
  *               all three NULL.  They need cols % 16 == 0 and every pointer
  *               and row stride above 16-byte aligned
- * Without codes, any alignment of whole elements works; aligned rows of
- * cols % 16 == 0 take 16-byte loads.
+ * Without codes, any alignment of whole elements works; rows of 16 values and
+ * more are read and written 16 bytes at a time.
  */
 NVFP4_API nvfp4_status_t nvfp4_add_rmsnorm(const void* x, int32_t x_dtype, int64_t ldx, const void* residual,
                                            int32_t r_dtype, int64_t ldr, float scale, const float* w, float eps,

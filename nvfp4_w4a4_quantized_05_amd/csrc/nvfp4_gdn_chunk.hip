@@ -150,8 +150,8 @@ __device__ __forceinline__ void lds_barrier() {
 // 16 x 16 diagonal block, then blocks of 32 and of 64 are joined by
 // -X_22 A_21 X_11 with fp32 matrix products.  (Summing powers of A instead
 // would overflow for equal keys, whose inverse is harmless.)
-// Bound by what it moves: 32,768 tokens with 16 / 32 heads take 185 us for
-// 0.34 GB read and 0.69 GB written (5.5 TB/s; a plain copy of 2 GB 4.9).
+// Bound by what it moves: 32,768 tokens with 16 / 32 heads take 196-202 us for
+// 0.34 GB read and 0.79 GB written (5.6 TB/s; a plain copy of 2 GB 4.9).
 constexpr int kKStride = kD + 8;   // bf16 per LDS row of K
 constexpr int kXStride = kC + 4;   // floats per LDS row of A, T
 
@@ -455,13 +455,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void g
 // columns, lanes = tokens), so that a lane holds four neighbours of a row of o.
 // The output waves also bring V and the row factors to LDS.
 //   Issuing loads bounds the walk as much as the chain of steps does (about 20
-// cycles each on the path to the cache): a chunk takes 63.  Up to 128 registers
+// cycles each on the path to the cache): a chunk takes 66.  Up to 128 registers
 // two workgroups of one tile share a CU, which takes 16,384 tokens in 8 sequences (32 value
-// heads) from 483 to 433 us; hence offsets that a wave has in common are kept in
+// heads) from 521 to 458 us; hence offsets that a wave has in common are kept in
 // scalar registers.
-//   Measured on 32,768 tokens, 32 value heads: 680 us, 1.3 a chunk; the matrix
-// cores are busy for 24% of it, and a state wave's own chain takes 1.1 us even
-// without loads.
+//   Measured on 32,768 tokens, 32 value heads: 752-785 us in a kernel trace, 1.5
+// a chunk (the whole call, untraced, takes 920-926 us, 720 of them the walk); the
+// matrix cores are busy for 23% of it, and a state wave's own chain takes 1.1 us
+// even without loads.
 // Accumulator row 4 c + e of state tile t is row 32 w + 8 c + 4 t + e of S, so
 // that a lane's rows of both tiles are eight neighbours.
 constexpr int kCols = 16;
@@ -884,7 +885,9 @@ __global__ __launch_bounds__(kScanThreads) void gdn_chunk_scan_kernel(
 // goes through a chunk alone.  What it multiplies comes out of one product in
 // the lane order that the next one takes, so nothing is exchanged; the eight
 // waves of a workgroup (the 128 columns of one unit) share the chunk's K, Q, T
-// and P in LDS, two buffers deep, with one barrier a chunk.
+// and P in LDS, two buffers deep, with one barrier a chunk.  Measured on 32,768
+// tokens in 48 sequences, 32 value heads: 463-492 us; the matrix cores are busy
+// for 43% of it.
 constexpr int kWideWaves = 8;
 constexpr int kWideThreads = 64 * kWideWaves;
 
@@ -1180,15 +1183,20 @@ int64_t chunk_places(int64_t T, int64_t n_seqs) { return T / kC + n_seqs + 1; }
 
 // From this many sequences x value heads on, one workgroup walks a whole unit.
 // It needs two thirds of the CU time per chunk, but leaves a CU to each unit and
-// takes 5.2 us a chunk instead of 1.3, so a few long units would be left over.
-// Measured, split / whole, 32 value heads: 32,768 tokens in 48 sequences 883 /
-// 631 us, in 16 (512 units) 823 / 781 us; 16,384 in 8 (256 units) 433 / 632 us.
+// takes 5.0 us a chunk instead of 1.4, so a few long units would be left over.
+// The host does not know the lengths and takes them for about equal: one long
+// sequence among short or empty ones takes that long a chunk here as well.
+// Measured, split in two tiles / whole, 32 value heads: 32,768 tokens in 48
+// sequences 922 / 680 us, in 20 (640 units) 811 / 752, in 16 (512) 806 / 820,
+// 28,000 in 14 (448) 699 / 776, 16,384 in 8 (256) 424 / 654.
 constexpr int64_t kWideUnits = 512;
 // From this many on, a workgroup of the split form has two column tiles, which
 // halves the loads of a chunk's operands but leaves a CU to one workgroup.
-// Measured, one / two tiles: 27,000 tokens in 7 sequences (224 units) 703 / 623
-// us, 16,384 in 8 (256) 442 / 391, 8,191 in 12 (384) 238 / 230, 16,000 in 16 with
-// 12 value heads (192) 151 / 157, 8,192 in 4 (128) 232 / 291.
+// Measured, one / two tiles, 32 value heads: 8,192 tokens in 4 sequences (128
+// units) 224 / 242 us, 16,000 in 5 (160) 452 / 397, 3,000 in 6 (192) 83 / 89,
+// 16,000 in 6 442 / 394, 30,000 in 6 802 / 717, 27,000 in 7 (224) 722 / 647, 16,384
+// in 8 (256) 454 / 388, 8,191 in 12 (384) 240 / 221; 16,000 in 16 with 12 value
+// heads (192) 170 / 166, 20,000 in 48 with 4 (192) 78 / 84.
 constexpr int64_t kPairUnits = 192;
 // Below this many chunks x q/k heads, the preparation takes one workgroup per
 // value head instead of one per q/k head (which makes the group's K and Q
