@@ -73,6 +73,7 @@ typedef enum {
 typedef enum { NVFP4_IN_F32 = 0, NVFP4_IN_BF16 = 1 } nvfp4_in_t;
 typedef enum { NVFP4_OUT_F32 = 0, NVFP4_OUT_BF16 = 1 } nvfp4_out_t;
 typedef enum { NVFP4_SCALE_GIVEN = 0, NVFP4_SCALE_FROM_AMAX = 1 } nvfp4_scale_mode_t;
+typedef enum { NVFP4_KV_E4M3 = 0, NVFP4_KV_NVFP4 = 1 } nvfp4_kv_format_t;
 
 /*
  * nvfp4_quantize -- NVFP4 encode of a row-major [rows x cols] tensor
@@ -596,6 +597,158 @@ NVFP4_API nvfp4_status_t nvfp4_rmsnorm_gated(const void* o, int32_t o_dtype, int
                                              int32_t z_dtype, int64_t ldz, const float* w, float eps, int64_t rows,
                                              int64_t cols, int32_t group, void* y, int32_t y_dtype, int64_t ldy,
                                              const float* y_gs, uint8_t* y_codes, uint8_t* y_scales, void* stream);
+
+/*
+ * Serving the attention layers between their projections.  The pages name the
+ * hybrid's attention layers and their calibrated FP8 key/value cache (LIT-800,
+ * "Key takeaways"; cctest.ai, "Main findings") and leave the layer's own
+ * arithmetic open; head sizes, norms and rotation below are the usual ones and
+ * this library's assumption.  The four calls share:
+ *   - Packed sequences as in the Gated DeltaNet calls: `cu_seqlens` (DEVICE,
+ *     n_seqs + 1 non-decreasing int32 row numbers, cut off at 0 and T), or NULL:
+ *     T = n_seqs and row i is the one row of sequence i.  Rows outside every
+ *     sequence are neither read nor written.
+ *   - Positions: `kv_lens` (DEVICE int32 [n_seqs]) are the sequences' lengths
+ *     with the call's rows.  Row j of a sequence of n rows stands at position
+ *     kv_lens[i] - n + j.
+ *   - Pages: position p of sequence i lies in page page_table[i][p / page_size]
+ *     (DEVICE int32 [n_seqs x ld_table], max_pages entries a row in use), row p
+ *     % page_size of it.  A position below 0, past max_pages, or whose page is
+ *     outside 0 .. n_pages - 1 is not there: nothing is written to it, it reads
+ *     as zeros, and no row sees it.  (An unused request of a padded batch has
+ *     kv_lens 0 or pages -1.)  The host reads none of these arrays.
+ *   - The cache (nvfp4_kv_cache_t, a HOST struct of DEVICE arrays, all 16-byte
+ *     aligned), for `n_kv_heads` heads of 64, 128 or 256 dims and pages of 16,
+ *     32, ... or 1024 positions.  The tensor scales k_gs and v_gs (DEVICE, one
+ *     float each, in [2^-100, 2^100]) are the calibrated scales.
+ *       NVFP4_KV_E4M3:  k [n_pages][n_kv_heads][page_size][head_dim] and
+ *         v [n_pages][n_kv_heads][head_dim][page_size] bytes; value = E4M3 * gs,
+ *         code = E4M3 round-to-nearest-even of the exact x / gs, saturated at 448.
+ *       NVFP4_KV_NVFP4:  codes of two neighbouring dims in a byte (even dim in the
+ *         low nibble), k [..][page_size][head_dim / 2] with k_scales
+ *         [..][page_size][head_dim / 16] and v [..][head_dim / 2][page_size] with
+ *         v_scales [..][head_dim / 16][page_size]; the codes and scales that
+ *         nvfp4_quantize gives for a row's head under gs.
+ *     V is kept with its positions side by side because the second product of
+ *     the attention contracts over them: 16 of them are one load of a lane.
+ *     Values that are not finite are stored as NaN, 0x7F (in NVFP4: as the scale
+ *     of a block of zero codes that reads as NaN).
+ *   - No array that a call writes may lie on anything else that it touches
+ *     (NVFP4_ERR_ALIAS).  Two rows of one call at the same place of the cache
+ *     race for it.
+ */
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_scales; /* NVFP4_KV_NVFP4 only */
+  uint8_t* v_scales;
+  const float* k_gs;
+  const float* v_gs;
+  int32_t format;    /* nvfp4_kv_format_t */
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+} nvfp4_kv_cache_t;
+
+/*
+ * nvfp4_qk_norm_rope -- per query and key head, in one pass
+ *     y = x / sqrt(mean_head(x^2) + eps) * w,
+ * then the rotation of its first `rot` dims: pair p (a, b) becomes
+ *     (a cos - b sin, b cos + a sin)
+ * with cos = cos_sin[pos][p], sin = cos_sin[pos][rot / 2 + p], pos the row's
+ * position on the pair's axis.  fp32, rounded to bf16 once.
+ *
+ *   x           device [T x ldx] of `x_dtype` (NVFP4_IN_F32 / _BF16), q heads at
+ *               column q_col and k heads at k_col; 16-byte aligned, ldx and the
+ *               columns multiples of 8 values
+ *   T           0 <= T <= 2^25;  n_q_heads, n_kv_heads   1 .. 4096
+ *   head_dim    64, 128 or 256
+ *   q_w, k_w    device fp32 [head_dim], 16-byte aligned;  eps > 0 and finite
+ *   cos_sin     device fp32 [n_pos x rot], 16-byte aligned;  n_pos >= 1
+ *   rot         a multiple of 16, 16 <= rot <= head_dim
+ *   positions   device int32 [n_axes x T];  n_axes 1 .. 4.  A row with a
+ *               position outside 0 .. n_pos - 1 on any axis becomes zeros
+ *   pair_axis   HOST, rot / 2 bytes: the axis of each pair, below n_axes (time,
+ *               height and width of image tokens, in any arrangement); NULL with
+ *               one axis
+ *   adjacent    0: pair p is dims (p, p + rot / 2); 1: dims (2 p, 2 p + 1)
+ *   q, k        device out, bf16 [T x ldq] / [T x ldk], heads side by side;
+ *               16-byte aligned, ldq and ldk multiples of 8.  May be the columns
+ *               of x themselves (bf16, same stride)
+ */
+NVFP4_API nvfp4_status_t nvfp4_qk_norm_rope(const void* x, int32_t x_dtype, int64_t ldx, int64_t q_col, int64_t k_col,
+                                            int64_t T, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                            const float* q_w, const float* k_w, float eps, const float* cos_sin,
+                                            int32_t n_pos, int32_t rot, const int32_t* positions, int32_t n_axes,
+                                            const uint8_t* pair_axis, int32_t adjacent, void* q, int64_t ldq, void* k,
+                                            int64_t ldk, void* stream);
+
+/*
+ * nvfp4_kv_cache_write -- quantize the rows' keys and values into the cache.
+ *
+ *   cache       host struct (its arrays are written)
+ *   page_table, ld_table, max_pages, kv_lens, cu_seqlens, n_seqs, T   as above:
+ *               1 <= max_pages <= ld_table, 1 <= n_seqs <= 2^20,
+ *               (T / 16 + 2 n_seqs) * n_kv_heads * head_dim < 2^31
+ *   k, v        device [T x ldk] / [T x ldv] of `dtype` (NVFP4_IN_F32 / _BF16),
+ *               heads side by side; 16-byte aligned, strides of whole 16 bytes
+ */
+NVFP4_API nvfp4_status_t nvfp4_kv_cache_write(const nvfp4_kv_cache_t* cache, const int32_t* page_table,
+                                              int64_t ld_table, int32_t max_pages, const int32_t* kv_lens,
+                                              const int32_t* cu_seqlens, int32_t n_seqs, int64_t T, const void* k,
+                                              int64_t ldk, const void* v, int64_t ldv, int32_t dtype, void* stream);
+
+/*
+ * nvfp4_kv_cache_read -- the values at the rows' positions, E2M1 * E4M3 * gs or
+ * E4M3 * gs rounded to fp32 and, for bf16, from there: to look at a cache, to
+ * move it, or to hand it on.  Sequences of kv_lens[i] rows read all of it.
+ *
+ *   k, v        device out, [T x ldk] / [T x ldv] of `dtype` (NVFP4_OUT_F32 /
+ *               _BF16); the rest as for nvfp4_kv_cache_write
+ */
+NVFP4_API nvfp4_status_t nvfp4_kv_cache_read(const nvfp4_kv_cache_t* cache, const int32_t* page_table,
+                                             int64_t ld_table, int32_t max_pages, const int32_t* kv_lens,
+                                             const int32_t* cu_seqlens, int32_t n_seqs, int64_t T, void* k, int64_t ldk,
+                                             void* v, int64_t ldv, int32_t dtype, void* stream);
+
+/*
+ * nvfp4_attn_cached -- attention of the rows over the cache, which holds their own
+ * keys and values already (nvfp4_kv_cache_write of the same rows):
+ *     o = sum_p w_p v_p / sum_p w_p,  w_p = exp(scale q . k_p)
+ * over the positions p < kv_lens[i] that the row sees; a row that sees none gets
+ * zeros.  Query head h reads key/value head h / (n_q_heads / n_kv_heads).
+ *   Without `tree` a row sees the positions up to its own: prompts, chunks of
+ * prompts, one new token.  With it, the new rows are drafted tokens: a row sees
+ * every position before the sequence's first new row, and new row b if bit b of
+ * its mask is set (its own bit too is the caller's to set).  Bits number the first
+ * 64 new rows; those behind them are seen by none.
+ *
+ *   q           device bf16 [T x ldq], heads side by side; 16-byte aligned, ldq a
+ *               multiple of 8
+ *   T           0 <= T < 2^30;  the rest of the rows' arguments as above
+ *   n_q_heads   a multiple of n_kv_heads, at most 4096
+ *   scale       positive and finite (1 / sqrt(head_dim), as a rule)
+ *   tree        device uint64 [T], 8-byte aligned, or NULL
+ *   o           device out, bf16 [T x ldo], as q
+ *   workspace   device scratch, 256-byte aligned, of at least
+ *               nvfp4_attn_cached_workspace_size() bytes, overwritten
+ * Precision: K and V enter exactly, the weights w_p with 11 bits, sums in fp32; o
+ * is rounded to bf16 once.  A query or key that is not finite makes the rows that
+ * use it NaN, a value that is not finite its dim of the rows that see it, and
+ * nothing else.  The same call gives the same bits; which kernel runs, and with it
+ * the order of sums, goes by T * n_q_heads / (n_seqs * n_kv_heads).
+ */
+NVFP4_API nvfp4_status_t nvfp4_attn_cached(const nvfp4_kv_cache_t* cache, const int32_t* page_table, int64_t ld_table,
+                                           int32_t max_pages, const int32_t* kv_lens, const int32_t* cu_seqlens,
+                                           int32_t n_seqs, int64_t T, const void* q, int64_t ldq, int32_t n_q_heads,
+                                           float scale, const uint64_t* tree, void* o, int64_t ldo, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace nvfp4_attn_cached needs: parts of results where the work of
+ * one row is split (it does not grow with the lengths). */
+NVFP4_API size_t nvfp4_attn_cached_workspace_size(int64_t T, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
+                                                  int32_t head_dim);
 
 /* Bytes of workspace nvfp4_gemm, nvfp4_gemm_segmented and
  * nvfp4_gemm_segmented_gates need for this

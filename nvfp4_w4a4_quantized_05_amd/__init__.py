@@ -1,14 +1,16 @@
 """MI355X-native NVFP4 W4A4 linear layer: quantize, GEMM, fused-scale harmonize,
-and the Gated DeltaNet mixer between its projections.
+and the Gated DeltaNet and attention mixers between their projections.
 
 The computation lives in ``libnvfp4.so`` (hand-written HIP for gfx950 behind
 the C ABI of ``include/nvfp4.h``); this package is its thin Python binding.
 """
 from ._lib import (  # noqa: F401
     EXPORTS,
+    KvCache,
     LIB_PATH,
     Nvfp4Error,
     add_rmsnorm,
+    attn_cached,
     conv_silu,
     gemm,
     gemm_segmented,
@@ -18,7 +20,10 @@ from ._lib import (  # noqa: F401
     gdn_prefill,
     gdn_recurrence,
     harmonize_fused_scales,
+    kv_cache_read,
+    kv_cache_write,
     load,
+    qk_norm_rope,
     quantize,
     quantize_gemm,
     quantize_gemm_no_alloc,

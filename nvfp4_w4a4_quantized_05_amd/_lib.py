@@ -19,6 +19,7 @@ NVFP4_OK = 0
 IN_F32, IN_BF16 = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
 SCALE_GIVEN, SCALE_FROM_AMAX = 0, 1
+KV_FORMATS = {"fp8": 0, "nvfp4": 1}  # NVFP4_KV_E4M3, NVFP4_KV_NVFP4
 STATUS_NAMES = {0: "NVFP4_OK", 1: "NVFP4_ERR_NULL", 2: "NVFP4_ERR_SHAPE", 3: "NVFP4_ERR_DTYPE",
                 4: "NVFP4_ERR_MODE", 5: "NVFP4_ERR_ALIGN", 6: "NVFP4_ERR_WORKSPACE",
                 7: "NVFP4_ERR_HIP", 8: "NVFP4_ERR_ALIAS", 9: "NVFP4_ERR_TOO_LARGE"}
@@ -27,7 +28,8 @@ EXPORTS = ("nvfp4_quantize", "nvfp4_gemm", "nvfp4_gemm_segmented", "nvfp4_gemm_s
            "nvfp4_quantize_gemm_workspace_size", "nvfp4_quantize_gemm_no_alloc",
            "nvfp4_quantize_gemm_no_alloc_max_bytes", "nvfp4_harmonize_fused_scales",
            "nvfp4_gdn_prefill", "nvfp4_gdn_prefill_workspace_size", "nvfp4_gdn_decode", "nvfp4_conv_silu",
-           "nvfp4_add_rmsnorm", "nvfp4_rmsnorm_gated",
+           "nvfp4_add_rmsnorm", "nvfp4_rmsnorm_gated", "nvfp4_qk_norm_rope", "nvfp4_kv_cache_write",
+           "nvfp4_kv_cache_read", "nvfp4_attn_cached", "nvfp4_attn_cached_workspace_size",
            "nvfp4_gemm_workspace_size", "nvfp4_status_string", "nvfp4_last_hip_error")
 
 _lib = None
@@ -92,6 +94,16 @@ def load() -> ctypes.CDLL:
     lib.nvfp4_rmsnorm_gated.argtypes = [vp, i32, i64, vp, i32, i64, vp, f32, i64, i64, i32, vp, i32, i64, vp, vp, vp,
                                         vp]
     lib.nvfp4_rmsnorm_gated.restype = i32
+    lib.nvfp4_qk_norm_rope.argtypes = [vp, i32, i64, i64, i64, i64, i32, i32, i32, vp, vp, f32, vp, i32, i32, vp, i32,
+                                       ctypes.c_char_p, i32, vp, i64, vp, i64, vp]
+    lib.nvfp4_qk_norm_rope.restype = i32
+    for f in (lib.nvfp4_kv_cache_write, lib.nvfp4_kv_cache_read):
+        f.argtypes = [vp, vp, i64, i32, vp, vp, i32, i64, vp, i64, vp, i64, i32, vp]
+        f.restype = i32
+    lib.nvfp4_attn_cached.argtypes = [vp, vp, i64, i32, vp, vp, i32, i64, vp, i64, i32, f32, vp, vp, i64, vp, sz, vp]
+    lib.nvfp4_attn_cached.restype = i32
+    lib.nvfp4_attn_cached_workspace_size.argtypes = [i64, i32, i32, i32, i32]
+    lib.nvfp4_attn_cached_workspace_size.restype = sz
     lib.nvfp4_harmonize_fused_scales.argtypes = [vp, vp, ctypes.POINTER(i64), i32, i64, vp, vp, vp]
     lib.nvfp4_harmonize_fused_scales.restype = i32
     lib.nvfp4_gemm_workspace_size.argtypes = [i64, i64, i64, i32]
@@ -599,6 +611,231 @@ def rmsnorm_gated(o: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, *, eps
     if st:
         raise Nvfp4Error(st, "nvfp4_rmsnorm_gated")
     return out if y_gs is None else (out, codes, scales)
+
+
+class _KvCacheStruct(ctypes.Structure):  # nvfp4_kv_cache_t
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scales", "v_scales", "k_gs", "v_gs")] + \
+               [(n, ctypes.c_int32) for n in ("format", "n_pages", "page_size", "n_kv_heads", "head_dim")]
+
+
+class KvCache:
+    """A paged, quantised key/value cache of one layer (nvfp4_kv_cache_t): the
+    given uint8 tensors, which it keeps alive, and their tensor scales.
+
+    format "fp8":    k [n_pages, n_kv_heads, page_size, head_dim],
+                     v [n_pages, n_kv_heads, head_dim, page_size] (E4M3 codes)
+    format "nvfp4":  k [.., page_size, head_dim / 2], k_scales [.., page_size, head_dim / 16],
+                     v [.., head_dim / 2, page_size], v_scales [.., head_dim / 16, page_size]
+    k_gs, v_gs:      one float32 each, on the GPU
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_gs: torch.Tensor, v_gs: torch.Tensor,
+                 k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None, *, format: str):
+        if format not in KV_FORMATS:
+            raise ValueError(f"format must be one of {tuple(KV_FORMATS)}")
+        if k.dim() != 4 or v.dim() != 4:
+            raise ValueError("k and v must be 4-D")
+        fp4 = format == "nvfp4"
+        n_pages, heads, page, width = k.shape
+        dim = 2 * width if fp4 else width
+        _u8_matrix(k, (n_pages, heads, page, width), "k")
+        _u8_matrix(v, (n_pages, heads, width, page), "v")
+        if fp4 and (k_scales is None or v_scales is None):
+            raise ValueError("an nvfp4 cache needs k_scales and v_scales")
+        if not fp4 and (k_scales is not None or v_scales is not None):
+            raise ValueError("an fp8 cache has no k_scales or v_scales")
+        if fp4:
+            _u8_matrix(k_scales, (n_pages, heads, page, dim // 16), "k_scales")
+            _u8_matrix(v_scales, (n_pages, heads, dim // 16, page), "v_scales")
+        _f32_scalars(k_gs, 1, "k_gs")
+        _f32_scalars(v_gs, 1, "v_gs")
+        self._tensors = [t for t in (k, v, k_scales, v_scales, k_gs, v_gs) if t is not None]
+        _need_gpu(*self._tensors)
+        self.device = _one_device(*self._tensors)
+        self.k, self.v, self.k_scales, self.v_scales, self.k_gs, self.v_gs = k, v, k_scales, v_scales, k_gs, v_gs
+        self.format, self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = format, n_pages, page, heads, dim
+        self._struct = _KvCacheStruct(k.data_ptr(), v.data_ptr(), k_scales.data_ptr() if fp4 else None,
+                                      v_scales.data_ptr() if fp4 else None, k_gs.data_ptr(), v_gs.data_ptr(),
+                                      KV_FORMATS[format], n_pages, page, heads, dim)
+        self._ptr = ctypes.addressof(self._struct)
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, k_gs: torch.Tensor,
+              v_gs: torch.Tensor, *, format: str = "fp8") -> "KvCache":
+        """A new cache of zeros beside its tensor scales."""
+        fp4 = format == "nvfp4"
+        width = head_dim // 2 if fp4 else head_dim
+
+        def zeros(*shape):
+            return torch.zeros((n_pages, n_kv_heads, *shape), dtype=torch.uint8, device=k_gs.device)
+
+        return cls(zeros(page_size, width), zeros(width, page_size), k_gs, v_gs,
+                   zeros(page_size, head_dim // 16) if fp4 else None, zeros(head_dim // 16, page_size) if fp4 else None,
+                   format=format)
+
+
+def _one_device(*ts):
+    """Number of the GPU that all of them are on."""
+    dev = ts[0].get_device()
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("the tensors of a call must be on one GPU")
+    return dev
+
+
+def _launch_stream(dev, stream):
+    """The raw stream of a call on tensors of GPU `dev`, which must be the current one and the stream's."""
+    if dev != torch._C._cuda_getDevice() or (stream is not None and stream.device_index != dev):
+        raise ValueError("the tensors, the stream and the current device must be of one GPU")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _kv_rows(cache, page_table, kv_lens, cu_seqlens, T):
+    """(page table, its row stride, pages a row, lengths, cu_seqlens, sequences) of a call on T rows."""
+    n_seqs = kv_lens.shape[0] if kv_lens.dim() == 1 else 0
+    lp = _vector(kv_lens, torch.int32, n_seqs, "kv_lens")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != n_seqs \
+            or (page_table.stride(1) != 1 and page_table.shape[1] > 1) or not page_table.is_cuda:
+        raise ValueError("page_table must be int32 [n_seqs, pages] with unit column stride on the GPU")
+    cp = None
+    if cu_seqlens is not None:
+        cp = _vector(cu_seqlens, torch.int32, n_seqs + 1, "cu_seqlens")
+    elif T != n_seqs:
+        raise ValueError("without cu_seqlens there is one row for each sequence")
+    pages = page_table.shape[1]
+    return page_table.data_ptr(), page_table.stride(0) if n_seqs > 1 else max(pages, 1), pages, lp, cp, n_seqs
+
+
+def qk_norm_rope(x: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor, cos_sin: torch.Tensor,
+                 positions: torch.Tensor, *, q_col: int, k_col: int, n_q_heads: int, n_kv_heads: int,
+                 eps: float = 1e-6, pair_axis: bytes | None = None, adjacent: bool = False,
+                 q: torch.Tensor | None = None, k: torch.Tensor | None = None, stream=None):
+    """RMSNorm of each query and key head of x (bf16 or fp32 [T, cols], q heads
+    from column q_col, k heads from k_col) times q_weight / k_weight (float32
+    [head_dim]), then the rotation of its first cos_sin.shape[1] dims by row
+    positions[t] of cos_sin (float32 [n_pos, rot]: cosines, then sines).
+    positions: int32 [T], or [axes, T] with pair_axis, rot / 2 bytes that name
+    the axis of each pair.  Pairs are (p, p + rot / 2), or (2 p, 2 p + 1) if
+    adjacent.  Returns (q, k), bf16 [T, heads * head_dim]."""
+    xp, x_dtype, T, _, ldx = _rows(x, "x")
+    dim = q_weight.numel()
+    wq, wk = _vector(q_weight, torch.float32, dim, "q_weight"), _vector(k_weight, torch.float32, dim, "k_weight")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or not cos_sin.is_cuda:
+        raise ValueError("cos_sin must be contiguous float32 [n_pos, rot] on the GPU")
+    n_pos, rot = cos_sin.shape
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if positions.dtype != torch.int32 or positions.shape[-1] != T or positions.dim() not in (1, 2) \
+            or not positions.is_contiguous() or not positions.is_cuda:
+        raise ValueError("positions must be contiguous int32 [T] or [axes, T] on the GPU")
+    if axes > 1 and (pair_axis is None or len(pair_axis) != rot // 2):
+        raise ValueError("several axes need pair_axis, one byte for each of the rot / 2 pairs")
+    if q is None:
+        q = _new((T, n_q_heads * dim), torch.bfloat16, x.device, stream)
+    if k is None:
+        k = _new((T, n_kv_heads * dim), torch.bfloat16, x.device, stream)
+    qp, q_dtype, ldq = _out_rows(q, T, n_q_heads * dim, "q")
+    kp, k_dtype, ldk = _out_rows(k, T, n_kv_heads * dim, "k")
+    if q_dtype != OUT_BF16 or k_dtype != OUT_BF16:
+        raise ValueError("q and k must be bf16")
+    dev = _one_device(x, q_weight, k_weight, cos_sin, positions, q, k)
+    st = load().nvfp4_qk_norm_rope(xp, x_dtype, ldx, q_col, k_col, T, n_q_heads, n_kv_heads, dim, wq, wk, eps,
+                                   cos_sin.data_ptr(), n_pos, rot, positions.data_ptr(), axes,
+                                   bytes(pair_axis) if axes > 1 else None, int(adjacent), qp, ldq, kp, ldk,
+                                   _launch_stream(dev, stream))
+    if st:
+        raise Nvfp4Error(st, "nvfp4_qk_norm_rope")
+    return q, k
+
+
+def kv_cache_write(k: torch.Tensor, v: torch.Tensor, cache: KvCache, page_table: torch.Tensor, kv_lens: torch.Tensor,
+                   cu_seqlens: torch.Tensor | None = None, *, stream=None) -> None:
+    """Quantise rows of keys and values (bf16 or fp32 [T, n_kv_heads * head_dim])
+    into the cache: row j of the n rows of sequence i (cu_seqlens, or one row
+    each) goes to position kv_lens[i] - n + j, in page page_table[i, position
+    // page_size]."""
+    kp, dtype, T, cols, ldk = _rows(k, "k")
+    vp, v_dtype, v_rows, v_cols, ldv = _rows(v, "v")
+    want = cache.n_kv_heads * cache.head_dim
+    if v_dtype != dtype or v_rows != T or cols != want or v_cols != want:
+        raise ValueError(f"k and v must be [T, {want}] of one type")
+    tp, ldt, pages, lp, cp, n_seqs = _kv_rows(cache, page_table, kv_lens, cu_seqlens, T)
+    dev = _one_device(k, v, page_table, kv_lens, cu_seqlens if cp else kv_lens)
+    if dev != cache.device:
+        raise ValueError("the tensors of a call must be on one GPU")
+    st = load().nvfp4_kv_cache_write(cache._ptr, tp, ldt, pages, lp, cp, n_seqs, T, kp, ldk, vp, ldv, dtype,
+                                     _launch_stream(dev, stream))
+    if st:
+        raise Nvfp4Error(st, "nvfp4_kv_cache_write")
+
+
+def kv_cache_read(cache: KvCache, page_table: torch.Tensor, kv_lens: torch.Tensor,
+                  cu_seqlens: torch.Tensor | None = None, *, rows: int | None = None, out_dtype=torch.bfloat16,
+                  k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
+    """The values at the last n positions before kv_lens[i] of each sequence, n
+    its rows in cu_seqlens (or one).  k and v: [rows, >= n_kv_heads * head_dim],
+    bf16 or fp32, made in out_dtype where they are not given.  Returns (k, v)."""
+    cols = cache.n_kv_heads * cache.head_dim
+    if k is None or v is None:
+        if rows is None:
+            rows = k.shape[0] if k is not None else v.shape[0] if v is not None else \
+                kv_lens.shape[0] if cu_seqlens is None else None
+        if rows is None:
+            raise ValueError("rows, or k and v, must be given with cu_seqlens")
+        dtype = k.dtype if k is not None else v.dtype if v is not None else out_dtype
+        k = _new((rows, cols), dtype, kv_lens.device, stream) if k is None else k
+        v = _new((rows, cols), dtype, kv_lens.device, stream) if v is None else v
+    T = k.shape[0]
+    kp, dtype, ldk = _out_rows(k, T, cols, "k")
+    vp, v_dtype, ldv = _out_rows(v, T, cols, "v")
+    if dtype != v_dtype:
+        raise ValueError("k and v must be of one type")
+    tp, ldt, pages, lp, cp, n_seqs = _kv_rows(cache, page_table, kv_lens, cu_seqlens, T)
+    dev = _one_device(k, v, page_table, kv_lens, cu_seqlens if cp else kv_lens)
+    if dev != cache.device:
+        raise ValueError("the tensors of a call must be on one GPU")
+    st = load().nvfp4_kv_cache_read(cache._ptr, tp, ldt, pages, lp, cp, n_seqs, T, kp, ldk, vp, ldv, dtype,
+                                    _launch_stream(dev, stream))
+    if st:
+        raise Nvfp4Error(st, "nvfp4_kv_cache_read")
+    return k, v
+
+
+def attn_cached(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, kv_lens: torch.Tensor,
+                cu_seqlens: torch.Tensor | None = None, *, n_q_heads: int, scale: float | None = None,
+                tree: torch.Tensor | None = None, o: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, stream=None):
+    """Attention of the rows q (bf16 [T, n_q_heads * head_dim]) over a cache that
+    holds their keys and values already.  A row sees the positions up to its
+    own, or with tree (int64 [T], drafted tokens) every position before the
+    sequence's first new row and new row b if bit b of its mask is set.  scale
+    defaults to 1 / sqrt(head_dim).  Returns o, bf16 [T, n_q_heads * head_dim]."""
+    qp, q_dtype, T, q_cols, ldq = _rows(q, "q")
+    dim, heads = cache.head_dim, cache.n_kv_heads
+    cols = n_q_heads * dim
+    if q_dtype != IN_BF16 or q_cols < cols:
+        raise ValueError(f"q must be bf16 [T, >= {cols}]")
+    tp, ldt, pages, lp, cp, n_seqs = _kv_rows(cache, page_table, kv_lens, cu_seqlens, T)
+    mp = _vector(tree, torch.int64, T, "tree") if tree is not None else None
+    if o is None:
+        o = _new((T, cols), torch.bfloat16, q.device, stream)
+    op, o_dtype, ldo = _out_rows(o, T, cols, "o")
+    if o_dtype != OUT_BF16:
+        raise ValueError("o must be bf16")
+    lib = load()
+    need = lib.nvfp4_attn_cached_workspace_size(T, n_seqs, n_q_heads, heads, dim)
+    if workspace is None:
+        workspace = _new(need, torch.uint8, q.device, stream)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous GPU tensor")
+    dev = _one_device(q, page_table, kv_lens, cu_seqlens if cp else q, tree if mp else q, o, workspace)
+    if dev != cache.device:
+        raise ValueError("the tensors of a call must be on one GPU")
+    st = lib.nvfp4_attn_cached(cache._ptr, tp, ldt, pages, lp, cp, n_seqs, T, qp, ldq, n_q_heads,
+                               dim ** -0.5 if scale is None else scale, mp, op, ldo, workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), _launch_stream(dev, stream))
+    if st:
+        raise Nvfp4Error(st, "nvfp4_attn_cached")
+    return o
 
 
 def quantize_gemm(x: torch.Tensor, a_gs: torch.Tensor, w_codes, w_scales, w_gs, *, out_dtype=torch.float32,

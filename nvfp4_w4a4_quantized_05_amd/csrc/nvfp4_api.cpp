@@ -199,6 +199,70 @@ bool norm_clash(const nvfp4::NormOut& out, int64_t rows, int64_t cols, const Spa
          clash({codes, scales}, {a, b});
 }
 
+// Head sizes of the attention layer's calls.
+bool head_dim_ok(int64_t d) { return d == 64 || d == 128 || d == 256; }
+
+// A cache and the rows of a call on it, checked (but for alignment of what the
+// call itself adds); `empty`: no rows, nothing to do.
+nvfp4_status_t kv_checks(const nvfp4_kv_cache_t* cache, const int32_t* page_table, int64_t ld_table, int32_t max_pages,
+                         const int32_t* kv_lens, const int32_t* cu_seqlens, int32_t n_seqs, int64_t T,
+                         nvfp4::KvCache& c, nvfp4::KvRows& r, bool& empty) {
+  empty = false;
+  if (!cache) return NVFP4_ERR_NULL;
+  if (cache->format != NVFP4_KV_E4M3 && cache->format != NVFP4_KV_NVFP4) return NVFP4_ERR_MODE;
+  if (!head_dim_ok(cache->head_dim) || cache->n_kv_heads < 1 || cache->n_kv_heads > 4096 || cache->n_pages < 1)
+    return NVFP4_ERR_SHAPE;
+  const int32_t ps = cache->page_size;
+  if (ps < 16 || ps > 1024 || (ps & (ps - 1)) != 0) return NVFP4_ERR_SHAPE;
+  if (max_pages < 1 || ld_table < max_pages || n_seqs < 1 || n_seqs > (1 << 20) || T < 0 || T >= (1 << 30))
+    return NVFP4_ERR_SHAPE;
+  if (ld_table > INT64_MAX / 4 / n_seqs || (!cu_seqlens && T != n_seqs)) return NVFP4_ERR_SHAPE;
+  const bool fp4 = cache->format == NVFP4_KV_NVFP4;
+  if (T == 0) {
+    empty = true;
+    return NVFP4_OK;
+  }
+  if (!cache->k || !cache->v || !cache->k_gs || !cache->v_gs || (fp4 && (!cache->k_scales || !cache->v_scales)) ||
+      !page_table || !kv_lens)
+    return NVFP4_ERR_NULL;
+  if (!aligned(cache->k, 16) || !aligned(cache->v, 16) || (fp4 && (!aligned(cache->k_scales, 16) || !aligned(cache->v_scales, 16))) ||
+      !aligned(cache->k_gs, 4) || !aligned(cache->v_gs, 4) || !aligned(page_table, 4) || !aligned(kv_lens, 4) ||
+      !aligned(cu_seqlens, 4))
+    return NVFP4_ERR_ALIGN;
+  c = {cache->k,    cache->v, cache->k_scales, cache->v_scales, cache->k_gs, cache->v_gs, fp4, cache->n_pages,
+       __builtin_ctz((unsigned)ps), cache->n_kv_heads, cache->head_dim};
+  r = {page_table, ld_table, max_pages, kv_lens, cu_seqlens, n_seqs, T};
+  return NVFP4_OK;
+}
+
+// What those arguments span: k, v, k_scales, v_scales, k_gs, v_gs, page table, lengths, row numbers.
+struct KvSpans {
+  Span k, v, ks, vs, kg, vg, table, lens, cu;
+};
+KvSpans kv_spans(const nvfp4::KvCache& c, const nvfp4::KvRows& r) {
+  const uint64_t values = (uint64_t)c.n_pages * c.hk * c.d << c.page_shift;
+  return {array_span(c.k, c.fp4 ? values / 2 : values),
+          array_span(c.v, c.fp4 ? values / 2 : values),
+          array_span(c.fp4 ? c.k_scales : nullptr, values / 16),
+          array_span(c.fp4 ? c.v_scales : nullptr, values / 16),
+          array_span(c.k_gs, 4),
+          array_span(c.v_gs, 4),
+          row_span(r.table, r.n_seqs, r.max_pages, r.ld_table, 4),
+          array_span(r.kv_lens, 4 * (uint64_t)r.n_seqs),
+          array_span(r.cu, 4 * ((uint64_t)r.n_seqs + 1))};
+}
+
+// Shapes and places of the rows that nvfp4_kv_cache_write reads and _read writes.
+nvfp4_status_t kv_row_checks(const nvfp4::KvCache& c, const nvfp4::KvRows& r, const void* k, int64_t ldk, const void* v,
+                             int64_t ldv, int32_t dtype) {
+  const int64_t cols = (int64_t)c.hk * c.d, e = in_size(dtype);
+  if (ldk < cols || ldv < cols || !extent_ok(r.T, ldk) || !extent_ok(r.T, ldv)) return NVFP4_ERR_SHAPE;
+  if ((r.T / 16 + 2 * (int64_t)r.n_seqs) * cols >= ((int64_t)1 << 31)) return NVFP4_ERR_SHAPE;  // threads below 2^32
+  if (!k || !v) return NVFP4_ERR_NULL;
+  if (!row_aligned(k, ldk, e) || !row_aligned(v, ldv, e)) return NVFP4_ERR_ALIGN;
+  return NVFP4_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -620,6 +684,143 @@ nvfp4_status_t nvfp4_rmsnorm_gated(const void* o, int32_t o_dtype, int64_t ldo, 
       return NVFP4_ERR_ALIAS;
     return hip_status(nvfp4::launch_rmsnorm_gated(o, o_dtype == NVFP4_IN_BF16, ldo, z, z_dtype == NVFP4_IN_BF16, ldz,
                                                   w, eps, rows, cols, group, out, (hipStream_t)stream));
+  } catch (...) {
+    return NVFP4_ERR_HIP;
+  }
+}
+
+nvfp4_status_t nvfp4_qk_norm_rope(const void* x, int32_t x_dtype, int64_t ldx, int64_t q_col, int64_t k_col, int64_t T,
+                                  int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, const float* q_w,
+                                  const float* k_w, float eps, const float* cos_sin, int32_t n_pos, int32_t rot,
+                                  const int32_t* positions, int32_t n_axes, const uint8_t* pair_axis, int32_t adjacent,
+                                  void* q, int64_t ldq, void* k, int64_t ldk, void* stream) {
+  try {
+    if (!in_dtype_ok(x_dtype)) return NVFP4_ERR_DTYPE;
+    if (adjacent != 0 && adjacent != 1) return NVFP4_ERR_MODE;
+    if (!head_dim_ok(head_dim) || n_q_heads < 1 || n_q_heads > 4096 || n_kv_heads < 1 || n_kv_heads > 4096)
+      return NVFP4_ERR_SHAPE;
+    if (T < 0 || T > (1 << 25) || !(eps > 0.0f) || !std::isfinite(eps)) return NVFP4_ERR_SHAPE;
+    if (rot < 16 || rot > head_dim || rot % 16 != 0 || n_pos < 1 || n_axes < 1 || n_axes > 4) return NVFP4_ERR_SHAPE;
+    const int64_t q_cols = (int64_t)n_q_heads * head_dim, k_cols = (int64_t)n_kv_heads * head_dim;
+    if (ldx <= 0 || q_col < 0 || q_col > ldx - q_cols || k_col < 0 || k_col > ldx - k_cols || ldq < q_cols || ldk < k_cols)
+      return NVFP4_ERR_SHAPE;
+    if (!extent_ok(T, ldx) || !extent_ok(T, ldq) || !extent_ok(T, ldk)) return NVFP4_ERR_SHAPE;
+    nvfp4::QkNormRope a{x,       x_dtype == NVFP4_IN_BF16, ldx,       q_col,  k_col, T,      n_q_heads, n_kv_heads, head_dim,
+                        rot,     q_w,                      k_w,       eps,    cos_sin, n_pos, positions, n_axes,     {},
+                        adjacent == 1, static_cast<uint16_t*>(q), ldq, static_cast<uint16_t*>(k), ldk};
+    if (n_axes > 1) {
+      if (!pair_axis) return NVFP4_ERR_NULL;
+      for (int p = 0; p < rot / 2; ++p) {
+        if (pair_axis[p] >= n_axes) return NVFP4_ERR_SHAPE;
+        a.axis[p / 16] |= (uint32_t)pair_axis[p] << (p % 16 * 2);
+      }
+    }
+    if (T == 0) return NVFP4_OK;
+    if (!x || !q_w || !k_w || !cos_sin || !positions || !q || !k) return NVFP4_ERR_NULL;
+    const int64_t e = in_size(x_dtype);
+    if (!row_aligned(x, ldx, e) || ldx % 8 != 0 || q_col % 8 != 0 || k_col % 8 != 0 || !aligned(q_w, 16) ||
+        !aligned(k_w, 16) || !aligned(cos_sin, 16) || !aligned(positions, 4) || !row_aligned(q, ldq, 2) ||
+        !row_aligned(k, ldk, 2))
+      return NVFP4_ERR_ALIGN;
+    const Span xq = row_span(static_cast<const char*>(x) + q_col * e, T, q_cols, ldx, e);
+    const Span xk = row_span(static_cast<const char*>(x) + k_col * e, T, k_cols, ldx, e);
+    const Span yq = row_span(q, T, q_cols, ldq, 2), yk = row_span(k, T, k_cols, ldk, 2);
+    const Span qw = array_span(q_w, 4 * (uint64_t)head_dim), kw = array_span(k_w, 4 * (uint64_t)head_dim);
+    const Span table = array_span(cos_sin, (uint64_t)n_pos * rot * 4), pos = array_span(positions, (uint64_t)n_axes * T * 4);
+    // a head's lanes hold all of it before any of it is written; q and k of x are other waves' turns
+    if (clash({yq, yk}, {qw, kw, table, pos}) || clash({yq}, {xk}, {xq}) || clash({yk}, {xq}, {xk})) return NVFP4_ERR_ALIAS;
+    return hip_status(nvfp4::launch_qk_norm_rope(a, (hipStream_t)stream));
+  } catch (...) {
+    return NVFP4_ERR_HIP;
+  }
+}
+
+nvfp4_status_t nvfp4_kv_cache_write(const nvfp4_kv_cache_t* cache, const int32_t* page_table, int64_t ld_table,
+                                    int32_t max_pages, const int32_t* kv_lens, const int32_t* cu_seqlens,
+                                    int32_t n_seqs, int64_t T, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                    int32_t dtype, void* stream) {
+  try {
+    if (!in_dtype_ok(dtype)) return NVFP4_ERR_DTYPE;
+    nvfp4::KvCache c;
+    nvfp4::KvRows r;
+    bool empty;
+    nvfp4_status_t st = kv_checks(cache, page_table, ld_table, max_pages, kv_lens, cu_seqlens, n_seqs, T, c, r, empty);
+    if (st != NVFP4_OK || empty) return st;
+    st = kv_row_checks(c, r, k, ldk, v, ldv, dtype);
+    if (st != NVFP4_OK) return st;
+    const KvSpans s = kv_spans(c, r);
+    const int64_t cols = (int64_t)c.hk * c.d, e = in_size(dtype);
+    if (clash({s.k, s.v, s.ks, s.vs},
+              {s.kg, s.vg, s.table, s.lens, s.cu, row_span(k, T, cols, ldk, e), row_span(v, T, cols, ldv, e)}))
+      return NVFP4_ERR_ALIAS;
+    return hip_status(nvfp4::launch_kv_cache_write(c, r, k, ldk, v, ldv, dtype == NVFP4_IN_BF16, (hipStream_t)stream));
+  } catch (...) {
+    return NVFP4_ERR_HIP;
+  }
+}
+
+nvfp4_status_t nvfp4_kv_cache_read(const nvfp4_kv_cache_t* cache, const int32_t* page_table, int64_t ld_table,
+                                   int32_t max_pages, const int32_t* kv_lens, const int32_t* cu_seqlens,
+                                   int32_t n_seqs, int64_t T, void* k, int64_t ldk, void* v, int64_t ldv, int32_t dtype,
+                                   void* stream) {
+  try {
+    if (dtype != NVFP4_OUT_F32 && dtype != NVFP4_OUT_BF16) return NVFP4_ERR_DTYPE;
+    nvfp4::KvCache c;
+    nvfp4::KvRows r;
+    bool empty;
+    nvfp4_status_t st = kv_checks(cache, page_table, ld_table, max_pages, kv_lens, cu_seqlens, n_seqs, T, c, r, empty);
+    if (st != NVFP4_OK || empty) return st;
+    st = kv_row_checks(c, r, k, ldk, v, ldv, dtype);
+    if (st != NVFP4_OK) return st;
+    const KvSpans s = kv_spans(c, r);
+    const int64_t cols = (int64_t)c.hk * c.d, e = in_size(dtype);
+    if (clash({row_span(k, T, cols, ldk, e), row_span(v, T, cols, ldv, e)},
+              {s.k, s.v, s.ks, s.vs, s.kg, s.vg, s.table, s.lens, s.cu}))
+      return NVFP4_ERR_ALIAS;
+    return hip_status(nvfp4::launch_kv_cache_read(c, r, k, ldk, v, ldv, dtype == NVFP4_OUT_BF16, (hipStream_t)stream));
+  } catch (...) {
+    return NVFP4_ERR_HIP;
+  }
+}
+
+size_t nvfp4_attn_cached_workspace_size(int64_t T, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
+                                        int32_t head_dim) {
+  if (T <= 0 || T >= (1 << 30) || n_seqs < 1 || n_kv_heads < 1 || n_q_heads < 1 || n_q_heads > 4096 ||
+      n_q_heads % n_kv_heads != 0 || !head_dim_ok(head_dim))
+    return 0;
+  return nvfp4::attn_cached_workspace_bytes(T, n_seqs, n_q_heads, n_kv_heads, head_dim);
+}
+
+nvfp4_status_t nvfp4_attn_cached(const nvfp4_kv_cache_t* cache, const int32_t* page_table, int64_t ld_table,
+                                 int32_t max_pages, const int32_t* kv_lens, const int32_t* cu_seqlens, int32_t n_seqs,
+                                 int64_t T, const void* q, int64_t ldq, int32_t n_q_heads, float scale,
+                                 const uint64_t* tree, void* o, int64_t ldo, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  try {
+    nvfp4::KvCache c;
+    nvfp4::KvRows r;
+    bool empty;
+    const nvfp4_status_t st =
+        kv_checks(cache, page_table, ld_table, max_pages, kv_lens, cu_seqlens, n_seqs, T, c, r, empty);
+    if (st != NVFP4_OK) return st;
+    if (n_q_heads < 1 || n_q_heads > 4096 || n_q_heads % cache->n_kv_heads != 0) return NVFP4_ERR_SHAPE;
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return NVFP4_ERR_SHAPE;
+    const int64_t cols = (int64_t)n_q_heads * cache->head_dim;
+    if (ldq < cols || ldo < cols || !extent_ok(T, ldq) || !extent_ok(T, ldo)) return NVFP4_ERR_SHAPE;
+    if (empty) return NVFP4_OK;
+    if (!q || !o) return NVFP4_ERR_NULL;
+    if (!row_aligned(q, ldq, 2) || !row_aligned(o, ldo, 2) || !aligned(tree, 8)) return NVFP4_ERR_ALIGN;
+    const size_t need = nvfp4::attn_cached_workspace_bytes(T, n_seqs, n_q_heads, c.hk, c.d);
+    if (workspace_bytes < need) return NVFP4_ERR_WORKSPACE;
+    if (!workspace) return NVFP4_ERR_NULL;
+    if (!aligned(workspace, 256)) return NVFP4_ERR_ALIGN;
+    const KvSpans s = kv_spans(c, r);
+    if (clash({row_span(o, T, cols, ldo, 2), array_span(workspace, need)},
+              {s.k, s.v, s.ks, s.vs, s.kg, s.vg, s.table, s.lens, s.cu, row_span(q, T, cols, ldq, 2),
+               array_span(tree, 8 * (uint64_t)T)}))
+      return NVFP4_ERR_ALIAS;
+    return hip_status(nvfp4::launch_attn_cached(c, r, q, ldq, n_q_heads, scale, tree, o, ldo, workspace,
+                                                (hipStream_t)stream));
   } catch (...) {
     return NVFP4_ERR_HIP;
   }

@@ -160,4 +160,63 @@ hipError_t launch_rmsnorm_gated(const void* o, bool o_bf16, int64_t ldo, const v
                                 const float* w, float eps, int64_t rows, int64_t cols, int group,
                                 const NormOut& out, hipStream_t stream);
 
+// Norm of each query and key head, then the rotation of its first `rot` dims:
+// pair p by the angle whose cosine and sine are columns p and rot / 2 + p of
+// row pos[axis(p)] of the table.  Arguments as nvfp4_qk_norm_rope, checked.
+struct QkNormRope {
+  const void* x;
+  bool x_bf16;
+  int64_t ldx, q_col, k_col;
+  int64_t T;
+  int hq, hk, d, rot;
+  const float* q_w;
+  const float* k_w;
+  float eps;
+  const float* table;
+  int n_pos;
+  const int32_t* pos;  // [n_axes x T]
+  int n_axes;
+  uint32_t axis[8];  // two bits per pair, pair 0 in the lowest
+  bool adjacent;     // pairs (2 p, 2 p + 1) instead of (p, p + rot / 2)
+  uint16_t* q;
+  int64_t ldq;
+  uint16_t* k;
+  int64_t ldk;
+};
+hipError_t launch_qk_norm_rope(const QkNormRope& a, hipStream_t stream);
+
+// A paged, quantised key/value cache (layout: nvfp4_kv.h).
+struct KvCache {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_scales;  // NVFP4 only
+  uint8_t* v_scales;
+  const float* k_gs;
+  const float* v_gs;
+  bool fp4;
+  int n_pages, page_shift, hk, d;
+};
+
+// The rows of a call and their sequences; cu NULL: row i is sequence i's only one.
+struct KvRows {
+  const int32_t* table;
+  int64_t ld_table;
+  int max_pages;
+  const int32_t* kv_lens;
+  const int32_t* cu;
+  int n_seqs;
+  int64_t T;
+};
+
+hipError_t launch_kv_cache_write(const KvCache& c, const KvRows& r, const void* k, int64_t ldk, const void* v,
+                                 int64_t ldv, bool bf16, hipStream_t stream);
+hipError_t launch_kv_cache_read(const KvCache& c, const KvRows& r, void* k, int64_t ldk, void* v, int64_t ldv,
+                                bool bf16, hipStream_t stream);
+
+// Attention over a cache; arguments as nvfp4_attn_cached, already checked;
+// workspace of attn_cached_workspace_bytes().
+size_t attn_cached_workspace_bytes(int64_t T, int n_seqs, int hq, int hk, int d);
+hipError_t launch_attn_cached(const KvCache& c, const KvRows& r, const void* q, int64_t ldq, int hq, float scale,
+                              const uint64_t* tree, void* o, int64_t ldo, void* workspace, hipStream_t stream);
+
 }  // namespace nvfp4

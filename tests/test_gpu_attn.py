@@ -1,0 +1,276 @@
+"""nvfp4_attn_cached against the fp64 formula.
+
+Tolerance.  With u = 2^-24, a row's weights w_p (their sum 1), n keys and head
+size d: a score is a sum of d products in fp32, off by at most d u B with B =
+max_p scale sum |q_i k_pi|, its factor (scale, tensor scale, log2 e, each
+rounded) by 4 u B, the subtraction of the maximum and the exponential by 2 u
+(B + 16): weights are off by E = 2 (d + 8) u (B + 16) of themselves, and by half
+an fp16 step, 2^-11, where they enter the second product.  Their sum and the
+second product's are fp32 sums of n terms, n u each, and a few rescalings; the
+result is divided once.  So |o - O| <= (2^-11 + E + (2 n + 64) u) sum w |v|, and
+rounding to bf16 adds half a step: 2^-8 |O|.  Values of q below 2^-31 of a row's
+largest are flushed: 2^-30 B, inside E.
+  A weight that is subnormal in fp16 is off by half a step of those, 2^-25.  It is
+stored times 2^7 over the running maximum, which is some key's weight, so that is
+at most 2^-32 of the row's largest weight, itself at most 1: 2^-32 sum |v| more
+(what shows where one key has all the weight and a zero in a dim)."""
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_w4a4_quantized_05_amd as nv
+from oracle import attn_ref as A
+from tests.attn_util import Paged, i32
+from tests.gpu_util import host_f32, need_gpu
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+BF = torch.bfloat16
+
+
+def tolerance(O, mag, big, flat, d, n):
+    e = 2 * (d + 8) * U * (big[..., None] + 16)
+    return (2.0 ** -11 + e + (2 * n + 64) * U) * mag + 2.0 ** -8 * np.abs(O) + 2.0 ** -32 * flat + 2.0 ** -126
+
+
+def tree_masks(rng, n, skip_self=False):
+    """Ancestors' bits of a random tree of n tokens."""
+    seen = []
+    for i in range(n):
+        up = seen[rng.integers(max(0, i - 4), i)] if i else 0
+        seen.append((up | (0 if skip_self and i % 3 == 0 else 1 << i)) & (2 ** 64 - 1) if i < 64 else up)
+    return np.array(seen, dtype=np.uint64).astype(np.int64)
+
+
+def run(paged, rows, kv, hq, *, seed=0, tree=None, lead=0, tail=0, q_pad=0, o_pad=0, scale=None, q_edit=None, cu=True,
+        spread=1.0):
+    """Attention of sequences of rows[i] rows and length kv[i]; checks every row, and what lies around them."""
+    dev = need_gpu()
+    d, hk = paged.d, paged.hk
+    T = lead + sum(rows) + tail
+    rng = np.random.default_rng(seed)
+    q = (spread * rng.standard_normal((T, hq * d))).astype(np.float32)
+    qt = torch.full((T, hq * d + q_pad), float("nan"), dtype=BF, device=dev)
+    qt[:, :hq * d] = torch.from_numpy(q).to(dev).to(BF)
+    if q_edit:
+        q_edit(qt)
+    starts = lead + np.concatenate([[0], np.cumsum(rows)])
+    o = torch.full((T, hq * d + o_pad), 7.5, dtype=BF, device=dev)
+    cache, table = paged.to(dev)
+    masks = np.zeros(T, dtype=np.int64) if tree is None else np.concatenate(
+        [np.zeros(lead, np.int64), *tree, np.zeros(tail, np.int64)])
+    args = dict(n_q_heads=hq, scale=scale, tree=None if tree is None else torch.from_numpy(masks).to(dev), o=o)
+    cus = i32(starts, dev) if cu else None
+    nv.attn_cached(qt[:, :hq * d], cache, table, i32(kv, dev), cus, **args)
+    torch.cuda.synchronize()
+    got = host_f32(o)
+    assert np.all(got[:lead] == 7.5) and np.all(got[lead + sum(rows):] == 7.5) and np.all(got[:, hq * d:] == 7.5)
+    qh = host_f32(qt)[:, :hq * d].astype(np.float64).reshape(T, hq, d)
+    sc = float(np.float32(d ** -0.5 if scale is None else scale))
+    worst = 0.0
+    for i, (n, length) in enumerate(zip(rows, kv)):
+        have = min(max(length, 0), paged.max_pages * paged.page)
+        if n == 0:
+            continue
+        at = slice(starts[i], starts[i] + n)
+        mask = A.seen_ref(n, length, have, None if tree is None else tree[i])
+        page = paged.table[i, np.arange(have) // paged.page]
+        mask &= ((page >= 0) & (page < paged.n_pages))[None]
+        O, mag, big, flat = A.attn_ref(qh[at], paged.values("k", i, have), paged.values("v", i, have), mask, sc)
+        g = got[at, :hq * d].astype(np.float64).reshape(n, hq, d)
+        nan = np.isnan(O)
+        assert np.array_equal(np.isnan(g), nan), f"sequence {i}: NaN at {np.argwhere(np.isnan(g) != nan)[:3].tolist()}"
+        err, tol = np.abs(g - O)[~nan], tolerance(O, mag, big, flat, d, have)[~nan]
+        assert np.all(err <= tol), f"sequence {i}: worst {np.max(err / tol)} of the tolerance, " \
+                                   f"{np.count_nonzero(err > tol)} of {err.size}"
+        worst = max(worst, float(np.max(err / tol, initial=0.0)))
+    print(f"  worst {worst:.3f} of the tolerance", flush=True)
+    return o
+
+
+LENS = [0, 1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 129, 200, 257]
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("hq,hk,d,page", [(6, 1, 256, 64), (8, 2, 128, 16), (5, 5, 64, 32), (4, 2, 256, 128), (7, 1, 64, 256),
+                                          (20, 1, 128, 64), (40, 2, 64, 16), (160, 1, 64, 32)])
+def test_one_token_each(fmt, hq, hk, d, page):
+    """Decode: lengths round the tiles' and the pages' ends, a length of zero, groups of 1 to 160 heads."""
+    print(f"[attn] {fmt} one {hq}/{hk}x{d} page {page}", flush=True)
+    paged = Paged(fmt, hk, d, page, LENS, hq + d, pad_table=3)
+    run(paged, [1] * len(LENS), LENS, hq, seed=1, cu=False, q_pad=8, o_pad=16)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("hq,hk,d,page", [(6, 1, 256, 64), (8, 2, 128, 16), (3, 3, 64, 32), (20, 1, 128, 1024)])
+def test_prompts(fmt, hq, hk, d, page):
+    """Prompts from nothing and on top of a context, an empty sequence, rows in front of and behind all sequences."""
+    rows = [1, 0, 5, 64, 130, 3, 200, 17]
+    ctx = [0, 40, 0, 0, 77, 300, 64, 1]
+    kv = [a + b for a, b in zip(rows, ctx)]
+    print(f"[attn] {fmt} prompts {hq}/{hk}x{d} page {page}", flush=True)
+    run(Paged(fmt, hk, d, page, kv, d + page), rows, kv, hq, seed=2, lead=3, tail=5, q_pad=8, o_pad=8)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("hq,hk,d,page", [(6, 1, 256, 64), (8, 2, 128, 16), (2, 2, 64, 32)])
+@pytest.mark.parametrize("many", [3, 31, 70])
+def test_trees(fmt, hq, hk, d, page, many):
+    """Trees of drafted tokens, some of which do not see themselves, one that sees nothing, more than 64 rows."""
+    rows = [many, 1, max(1, many // 2), many, 2]
+    ctx = [0, 5, 100, 333, 62]
+    kv = [a + b for a, b in zip(rows, ctx)]
+    rng = np.random.default_rng(many)
+    tree = [tree_masks(rng, n, skip_self=i == 3) for i, n in enumerate(rows)]
+    tree[0][0] = 0  # no context, no draft: an empty row
+    print(f"[attn] {fmt} trees of {many} {hq}/{hk}x{d} page {page}", flush=True)
+    o = run(Paged(fmt, hk, d, page, kv, d + many), rows, kv, hq, seed=3, tree=tree, lead=1, tail=1)
+    assert np.all(host_f32(o)[1] == 0.0)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("kind", ["one", "four", "chunk"])
+def test_long_context(fmt, kind):
+    """One long sequence, split over many workgroups, beside short ones."""
+    rows = {"one": [1, 1, 1], "four": [4, 4, 4], "chunk": [50, 0, 90]}[kind]
+    kv = [9, 20011, 700] if kind != "chunk" else [50, 0, 9000]
+    print(f"[attn] {fmt} long {kind}", flush=True)
+    run(Paged(fmt, 2, 128, 64, kv, 5), rows, kv, 8, seed=4, spread=2.0)
+
+
+def test_many_sequences():
+    """More sequences than lanes, most of them short, some empty."""
+    rng = np.random.default_rng(0)
+    kv = [int(x) for x in rng.choice([0, 1, 3, 20, 65, 150], 300)]
+    rows = [int(min(x, rng.integers(0, 4))) for x in kv]
+    print("[attn] 300 sequences", flush=True)
+    run(Paged("fp8", 1, 64, 16, kv, 6), rows, kv, 2, seed=5)
+
+
+@pytest.mark.parametrize("rows,kv", [([1, 1, 1], [0, -5, 3]), ([4, 30, 6], [2, 0, -3]), ([3, 2, 70], [3, 1, 12])])
+@pytest.mark.parametrize("tree", [False, True])
+def test_lengths_below_the_rows(rows, kv, tree):
+    """Fewer positions than rows: the first rows stand before position 0 and see nothing (drafts: see by their bits)."""
+    rng = np.random.default_rng(1)
+    masks = [tree_masks(rng, n) for n in rows] if tree else None
+    print(f"[attn] rows {rows} kv {kv} tree {tree}", flush=True)
+    run(Paged("fp8", 2, 64, 16, kv, 7), rows, kv, 4, seed=6, tree=masks)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+def test_absent_pages(fmt):
+    """Page numbers outside the cache, and lengths past the table: those positions are not there."""
+    kv = [200, 100, 500, 64]
+    rows = [1, 3, 40, 2]
+    paged = Paged(fmt, 2, 128, 16, kv, 8, max_pages=12)
+    paged.table[0, 3] = -1
+    paged.table[1, 0] = paged.n_pages
+    paged.table[1, 5] = 2 ** 31 - 1
+    paged.table[2, 2:4] = -7
+    paged.table[3, :] = -1  # nothing at all: zeros
+    full = {n: paged.values(n, 0, 48) for n in "kv"}
+    assert all(np.all(np.isfinite(x)) for x in full.values())
+
+    def values(name, i, n, old=paged.values):
+        keep = paged.table.copy()
+        paged.table[:] = np.where((keep < 0) | (keep >= paged.n_pages), 0, keep)
+        try:
+            return old(name, i, n)
+        finally:
+            paged.table[:] = keep
+
+    paged.values = values
+    print(f"[attn] {fmt} absent pages", flush=True)
+    o = run(paged, rows, kv, 4, seed=7)
+    assert np.all(host_f32(o)[-2:] == 0.0)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("kind", ["prompt", "tree", "wide"])
+def test_nan_reaches_only_what_sees_it(fmt, kind):
+    """NaN in keys and values that some rows see and others do not, and in queries."""
+    rows, kv = ([20, 40], [90, 40]) if kind != "wide" else ([100, 70], [190, 70])
+    rng = np.random.default_rng(3)
+    tree = [tree_masks(rng, min(n, 64)) for n in rows] if kind == "tree" else None
+    hq, hk, d = 4, 2, 128
+    paged = Paged(fmt, hk, d, 32, kv, 9)
+    last = kv[0] - 1
+    paged.set_nan("v", 0, last - 6, 0, 37)   # seen by the last rows, or by one branch
+    paged.set_nan("v", 0, last, 1, 100)
+    paged.set_nan("k", 1, kv[1] - 3, 0, 5)
+    paged.set_nan("v", 1, 2, 1, 64)
+
+    def edit(qt):
+        qt[3, d + 7] = float("inf")
+        qt[5, 3 * d] = float("nan")
+
+    print(f"[attn] {fmt} NaN {kind}", flush=True)
+    run(paged, rows, kv, hq, seed=8, tree=tree, q_edit=edit)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("factor", [1e-30, 1e-3, 30.0, 1e30])
+def test_sizes_of_queries(fmt, factor):
+    """Queries far outside fp16: the scores are as exact, flat for tiny ones and one-hot for huge ones."""
+    kv = [130, 40]
+    print(f"[attn] {fmt} queries times {factor}", flush=True)
+
+    def edit(qt):
+        qt[:, ::7] *= 1e-6
+        qt *= factor
+
+    run(Paged(fmt, 1, 64, 16, kv, 10), [3, 2], kv, 4, seed=9, q_edit=edit, scale=0.125 / factor if factor > 1e20 else None)
+
+
+def test_rounding_to_bf16_costs_most():
+    """The whole error against fp64 stays near that of one rounding to bf16: 1.05 times its 2-norm."""
+    dev = need_gpu()
+    kv = [3000, 2100]
+    paged = Paged("fp8", 2, 128, 64, kv, 11)
+    cache, table = paged.to(dev)
+    g = torch.Generator(device=dev).manual_seed(1)
+    q = torch.randn((2, 8 * 128), generator=g, device=dev).to(BF)
+    print("[attn] rounding", flush=True)
+    o = host_f32(nv.attn_cached(q, cache, table, i32(kv, dev), n_q_heads=8)).astype(np.float64)
+    qh = host_f32(q).astype(np.float64).reshape(2, 8, 128)
+    O = np.concatenate([A.attn_ref(qh[i:i + 1], paged.values("k", i, n), paged.values("v", i, n), np.ones((1, n), bool),
+                                   128 ** -0.5)[0] for i, n in enumerate(kv)]).reshape(2, -1)
+    once = host_f32(torch.from_numpy(O).float().to(BF)).astype(np.float64)
+    ratio = np.linalg.norm(o - O) / np.linalg.norm(once - O)
+    print(f"  ratio {ratio:.4f}", flush=True)
+    assert ratio < 1.05
+
+
+def test_streams_graphs_and_repeats():
+    """The same bits on another stream, with a workspace of the caller's, and from a replayed graph whose lengths change."""
+    dev = need_gpu()
+    kv, rows, hq, hk, d = [700, 64, 1300], [4, 4, 4], 8, 2, 128
+    paged = Paged("fp8", hk, d, 64, kv, 12)
+    cache, table = paged.to(dev)
+    cu = i32([0, 4, 8, 12], dev)
+    lens = i32(kv, dev)
+    q = torch.randn((12, hq * d), device=dev).to(BF)
+    print("[attn] streams and graphs", flush=True)
+    want = nv.attn_cached(q, cache, table, lens, cu, n_q_heads=hq)
+    assert torch.equal(want, nv.attn_cached(q, cache, table, lens, cu, n_q_heads=hq))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = nv.attn_cached(q, cache, table, lens, cu, n_q_heads=hq, stream=side)
+    side.synchronize()
+    assert torch.equal(want, got)
+    need = nv.load().nvfp4_attn_cached_workspace_size(12, 3, hq, hk, d)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=dev)  # NaN everywhere
+    o = torch.zeros_like(want)
+    with torch.cuda.stream(side):
+        nv.attn_cached(q, cache, table, lens, cu, n_q_heads=hq, o=o, workspace=ws)
+    side.synchronize()
+    assert torch.equal(want, o)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        nv.attn_cached(q, cache, table, lens, cu, n_q_heads=hq, o=o, workspace=ws)
+    for new in (kv, [5, 4, 1299], [0, 64, 100], kv):
+        lens.copy_(i32(new, dev))
+        o.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, nv.attn_cached(q, cache, table, lens, cu, n_q_heads=hq))
