@@ -104,17 +104,27 @@ struct SeqWork {
   __device__ __forceinline__ int64_t total() const { return before(tiles); }
 };
 
-__device__ __forceinline__ int64_t cache_rows(const Attn& a) { return (int64_t)a.r.max_pages << a.c.page_shift; }
+// Values that are the same in every lane, told to the compiler: they then live
+// in scalar registers, and branches on them are branches of the wave.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
+}
+
+// Positions that the page table has room for, and that fit the kernels' ints.
+__device__ __forceinline__ int cache_rows(const Attn& a) {
+  return (int)min((int64_t)a.r.max_pages << a.c.page_shift, (int64_t)INT32_MAX - 127);
+}
 
 __device__ __forceinline__ SeqWork seq_work(const Attn& a, int i) {
   SeqWork w;
   w.rows = seq_rows(a.r, i);
-  const int64_t most = cache_rows(a);
+  const int most = cache_rows(a);
   if (a.tree) {
-    w.first = min(max((int64_t)w.rows.kv, (int64_t)1), max(most, (int64_t)1)) + kStep - 1;
+    w.first = min(max(w.rows.kv, 1), most) + kStep - 1;
     w.slope = 0;
   } else {
-    w.first = min(max((int64_t)w.rows.kv - w.rows.n, (int64_t)0), most) + a.tokens + kStep - 1;
+    w.first = min(max((int64_t)w.rows.kv - w.rows.n, (int64_t)0), (int64_t)most) + a.tokens + kStep - 1;
     w.slope = a.tokens;
   }
   w.tiles = (w.rows.n + a.tokens - 1) / a.tokens;
@@ -122,17 +132,17 @@ __device__ __forceinline__ SeqWork seq_work(const Attn& a, int i) {
   return w;
 }
 
-// All sequences' steps, and with `find` the sequence that holds step `pos`
-// (pos < total) and the steps before it.  Every lane of the wave gets the same.
+// All sequences' steps; every lane of the wave gets the sum.
 __device__ __forceinline__ int64_t total_steps(const Attn& a) {
   const int lane = threadIdx.x & 63;
   int64_t sum = 0;
   for (int i = lane; i < a.r.n_seqs; i += 64) sum += seq_work(a, i).total();
 #pragma unroll
   for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m, 64);
-  return sum;
+  return uniform(sum);
 }
 
+// The sequence that holds step `pos` (below the total), and the steps before it.
 __device__ __forceinline__ int find_seq(const Attn& a, int64_t pos, int64_t& before) {
   const int lane = threadIdx.x & 63;
   before = 0;
@@ -142,33 +152,43 @@ __device__ __forceinline__ int find_seq(const Attn& a, int64_t pos, int64_t& bef
     const uint64_t past = __builtin_amdgcn_ballot_w64(upto > pos);
     if (past) {
       const int at = __builtin_ctzll(past);
-      before = __shfl(upto - mine, at, 64);
-      return __builtin_amdgcn_readfirstlane(i0 + at);
+      before = uniform(__shfl(upto - mine, at, 64));
+      return uniform(i0 + at);
     }
-    before = __shfl(upto, 63, 64);
+    before = uniform(__shfl(upto, 63, 64));
   }
-  return -1;
+  return 0;
 }
 
 // A unit of work: one tile of one sequence's rows and one (head, part).
 struct Unit {
   int seq;
   SeqWork w;
-  int tile, minor;
-  int64_t start, steps;  // its place among all steps
+  int tile, minor, steps;
+  int64_t start;  // its first step among all
 };
+
+__device__ __forceinline__ void take_seq(const Attn& a, Unit& u, int seq) {
+  u.seq = seq;
+  u.w = seq_work(a, seq);
+  u.w.rows.row0 = uniform(u.w.rows.row0);
+  u.w.rows.n = uniform(u.w.rows.n);
+  u.w.rows.kv = uniform(u.w.rows.kv);
+  u.w.first = uniform(u.w.first);
+  u.w.tiles = uniform(u.w.tiles);
+}
 
 __device__ __forceinline__ Unit unit_at(const Attn& a, int64_t pos) {
   Unit u;
   int64_t before;
-  u.seq = find_seq(a, pos, before);
-  u.w = seq_work(a, u.seq);
+  const int seq = find_seq(a, pos, before);
+  take_seq(a, u, seq);
   const int64_t x = pos - before;
   u.tile = u.w.tiles == 1 ? 0 : last_before(u.w.tiles, [&](int r) { return u.w.before(r) <= x; });
-  u.steps = u.w.steps(u.tile);
-  const int64_t y = x - u.w.before(u.tile);
-  u.minor = (int)(y / u.steps);
-  u.start = pos - y % u.steps;
+  u.steps = uniform((int)u.w.steps(u.tile));
+  const int64_t y = uniform(x - u.w.before(u.tile));
+  u.minor = uniform((int)(y / u.steps));
+  u.start = pos - (y - (int64_t)u.minor * u.steps);
   return u;
 }
 
@@ -179,10 +199,10 @@ __device__ __forceinline__ void next_unit(const Attn& a, Unit& u) {
   u.minor = 0;
   if (++u.tile == u.w.tiles) {
     u.tile = 0;
-    do u.w = seq_work(a, ++u.seq);
+    do take_seq(a, u, u.seq + 1);
     while (u.w.tiles == 0 && u.seq + 1 < a.r.n_seqs);
   }
-  u.steps = u.w.steps(u.tile);
+  u.steps = uniform((int)u.w.steps(u.tile));
 }
 
 // Row `rho` of a unit's tile: its token and query head, or token -1.
@@ -198,9 +218,25 @@ __device__ __forceinline__ RowOf row_of(const Attn& a, const Unit& u, int rows, 
 }
 
 // Positions that a row of token j sees at the most: [0, limit).
-__device__ __forceinline__ int64_t row_limit(const Attn& a, const SeqRows& s, int64_t most, int token) {
+__device__ __forceinline__ int row_limit(const Attn& a, const SeqRows& s, int token) {
   const int64_t end = a.tree ? (int64_t)s.kv : min((int64_t)s.kv, (int64_t)s.kv - s.n + token + 1);
-  return max(min(end, most), (int64_t)0);
+  return (int)max(min(end, (int64_t)cache_rows(a)), (int64_t)0);
+}
+
+// What a wave with rows row0 .. row0 + count - 1 of the tile has to do.
+struct Reach {
+  int all;    // every row of it sees the positions below
+  int steps;  // steps up to the last position that one of them sees
+};
+__device__ __forceinline__ Reach reach_of(const Attn& a, const Unit& u, int rows, int row0, int count) {
+  const int wide = a.parts == 1 ? a.group : rows;
+  const SeqRows& s = u.w.rows;
+  const int first = u.tile * a.tokens, last = min(first + a.tokens, s.n) - 1;
+  const int t0 = first + row0 / wide, t1 = min(first + (row0 + count - 1) / wide, last);
+  Reach r;
+  r.all = a.tree ? (int)min((int64_t)s.kv - s.n, (int64_t)cache_rows(a)) : row_limit(a, s, t0);
+  r.steps = t0 > t1 ? 0 : (row_limit(a, s, t1) + kStep - 1) / kStep;
+  return r;
 }
 
 __device__ __forceinline__ float max_over_g(float v) {  // over lanes n, n + 16, n + 32, n + 48
@@ -268,255 +304,55 @@ __device__ __forceinline__ void half8s_of_pairs(uint32_t lo, uint32_t hi, const 
   odd = __builtin_bit_cast(half8_t, o);
 }
 
-// kSplit: the workgroup's four waves have the same 16 kNT rows and every fourth
-// step each, and are joined through LDS; else 16 kNT rows each and every step.
-template <bool kFp4, int kD, int kNT, bool kSplit>
-struct Kernel {
-  static constexpr int kWaveRows = 16 * kNT, kRows = kSplit ? kWaveRows : 4 * kWaveRows;
+// Pages of a step's keys: of the lane's K rows' block of 16 and of its own block g.
+struct Pages {
+  int k, v;
+};
+__device__ __forceinline__ Pages pages_of(const Attn& a, int seq, int step) {
+  const int lane = threadIdx.x & 63;
+  const int64_t key0 = (int64_t)step * kStep;
+  return {page_of(a.r, a.c, seq, key0 + 16 * ((lane & 15) >> 2)), page_of(a.r, a.c, seq, key0 + 16 * (lane >> 4))};
+}
+__device__ __forceinline__ bool all_there(const Pages& p) { return __builtin_amdgcn_ballot_w64((p.k | p.v) < 0) == 0; }
+
+// Sizes of a format's operands, and a wave's rows and results.
+template <bool kFp4, int kD, int kNT>
+struct Rows {
+  static constexpr int kWaveRows = 16 * kNT;
   // K: a lane has kVals values of a row per load, dims 4 kVals c + kVals g and on
   static constexpr int kBytes = kFp4 && kD == 64 ? 8 : 16, kVals = kFp4 ? 2 * kBytes : kBytes;
   static constexpr int kLoads = kD / (4 * kVals), kFrags = kD / 32, kPerLoad = kVals / 8;
   // V: kTiles operands of 16 dims; NVFP4's come in pairs, dims d and d + 1
   static constexpr int kTiles = kD / 16, kVLoads = kFp4 ? kTiles / 2 : kTiles;
+  typedef floatx4_t Scores[kNT][4];
 
-  struct Wave {
-    half8_t q[kNT][kFrags];
-    floatx4_t o[kNT][kTiles];
-    float m[kNT], l[kNT], c1[kNT];  // running maximum, the lane's part of the sum, factor of the scores (log2)
-    int64_t limit[kNT];             // positions the row may see
-    uint64_t seen[kNT];             // tree: its mask
-  };
+  half8_t q[kNT][kFrags];
+  floatx4_t o[kNT][kTiles];
+  float m[kNT], l[kNT], c1[kNT];  // running maximum, the lane's part of the sum, factor of the scores (log2)
+  float fate[kNT];                // 1, or NaN
+  int limit[kNT];                 // positions the row may see
+  uint64_t seen[kNT];             // tree: its mask
 
-  // Pages of a step's keys: of the lane's K rows' block of 16 and of its own block g.
-  struct Pages {
-    int k, v;
-  };
-  static __device__ __forceinline__ Pages pages_of(const Attn& a, int seq, int64_t key0) {
-    const int lane = threadIdx.x & 63;
-    return {page_of(a.r, a.c, seq, key0 + 16 * ((lane & 15) >> 2)), page_of(a.r, a.c, seq, key0 + 16 * (lane >> 4))};
-  }
-
-  // Bits of the lane's 16 keys from position `key` on that row nt sees.
-  static __device__ __forceinline__ uint32_t seen_bits(const Attn& a, const Wave& w, int nt, const SeqRows& s,
-                                                       int64_t key, bool has_page) {
-    const auto below = [&](int64_t end) {
-      const int n = (int)min(max(end - key, (int64_t)0), (int64_t)16);
-      return (1u << n) - 1u;
-    };
-    uint32_t bits = below(w.limit[nt]);
-    if (a.tree) {
-      const int64_t ctx = (int64_t)s.kv - s.n, b = key - ctx;
-      const uint64_t drafts = b >= 0 ? (b < 64 ? w.seen[nt] >> b : 0) : (b > -16 ? w.seen[nt] << -b : 0);
-      bits &= below(ctx) | (uint32_t)drafts;
-    }
-    return has_page ? bits : 0u;
-  }
-
-  // One step: keys key0 .. key0 + 63.  kMasked: some row does not see all of them.
-  template <bool kMasked>
-  static __device__ __forceinline__ void step(const Attn& a, Wave& w, const Unit& u, int64_t key0, Pages pg) {
-    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-    const int head = u.minor / a.parts, ps = 1 << a.c.page_shift;
-    const int krow = (int)(key0 + 16 * (n >> 2) + (n & 3)) & (ps - 1), vrow = (int)(key0 + 16 * g) & (ps - 1);
-    const int64_t kunit = (int64_t)max(pg.k, 0) * a.c.hk + head, vunit = (int64_t)max(pg.v, 0) * a.c.hk + head;
-
-    // ---- scores
-    floatx4_t s[kNT][4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) s[nt][t] = floatx4_t{0, 0, 0, 0};
-      const int64_t row = kunit * ps + krow + 4 * t;
-      const uint8_t* at = a.c.k + row * code_bytes<kFp4>(kD) + kBytes * g;
-#pragma unroll
-      for (int c = 0; c < kLoads; ++c) {
-        uint32_t x[4];
-        if constexpr (kBytes == 16) {
-          const u32x4_t v = *reinterpret_cast<const u32x4_t*>(at + 64 * c);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = v[i];
-        } else {
-          const u32x2_t v = *reinterpret_cast<const u32x2_t*>(at + 32 * c);
-          x[0] = v[0];
-          x[1] = v[1];
-        }
-        half2_t sc = {0, 0};
-        if constexpr (kFp4) {
-          const uint8_t* from = a.c.k_scales + row * (kD / 16) + (4 * kVals * c + kVals * g) / 16;
-          const uint32_t b = kVals == 32 ? *reinterpret_cast<const uint16_t*>(from) : *from;
-          sc = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)b, 1.0f, false);
-        }
-#pragma unroll
-        for (int f = 0; f < kPerLoad; ++f) {
-          half8_t k8;
-          if constexpr (kFp4) {
-            const half2_t s2 = {sc[f / 2], sc[f / 2]};
-            k8 = half8_of_e2m1(x[f], s2);
-          } else {
-            k8 = half8_of_e4m3(x[2 * f], x[2 * f + 1]);
-          }
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) s[nt][t] = mfma(k8, w.q[nt][kPerLoad * c + f], s[nt][t]);
-        }
-      }
-    }
-
-    // ---- softmax: the lane has row n's scores of keys key0 + 16 g + 4 t + i
-    half8_t p[kNT][2];
-    uint32_t bits[kNT];
-    const int64_t key = key0 + 16 * g;
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-      if constexpr (kMasked) bits[nt] = seen_bits(a, w, nt, u.w.rows, key, pg.v >= 0);
-      float top = -INFINITY;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        if constexpr (kMasked) s[nt][e / 4][e % 4] = bits[nt] >> e & 1 ? s[nt][e / 4][e % 4] : -INFINITY;
-        top = fmaxf(top, s[nt][e / 4][e % 4]);
-      }
-      top *= w.c1[nt];
-      if (__builtin_amdgcn_ballot_w64(top > w.m[nt] + kLag)) {
-        const float now = fmaxf(w.m[nt], max_over_g(top)), f = __builtin_amdgcn_exp2f(w.m[nt] - now);
-        w.m[nt] = now;
-        w.l[nt] *= f;
-#pragma unroll
-        for (int d = 0; d < kTiles; ++d) w.o[nt][d] *= f;
-      }
-      const float off = kLift - w.m[nt];
-      half2_t h[8];
-      float sum = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 16; e += 2) {
-        float x = __builtin_amdgcn_exp2f(fmaf(s[nt][e / 4][e % 4], w.c1[nt], off));
-        float y = __builtin_amdgcn_exp2f(fmaf(s[nt][e / 4][e % 4 + 1], w.c1[nt], off));
-        if constexpr (kMasked) {
-          x = bits[nt] >> e & 1 ? x : 0.0f;
-          y = bits[nt] >> (e + 1) & 1 ? y : 0.0f;
-        }
-        sum += x + y;
-        h[e / 2] = two_fp16(x, y);
-      }
-      w.l[nt] += sum;
-      p[nt][0] = __builtin_bit_cast(half8_t, *(const half2_t(*)[4])h);
-      p[nt][1] = __builtin_bit_cast(half8_t, *(const half2_t(*)[4])(h + 4));
-    }
-
-    // ---- result
-    uint32_t keep[4];  // bytes of the lane's 16 keys that exist
-    bool nan = false;
-    if constexpr (kMasked) {
-      const int64_t end = min((int64_t)u.w.rows.kv, cache_rows(a));
-      const int have = pg.v >= 0 ? (int)min(max(end - key, (int64_t)0), (int64_t)16) : 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int b = min(max(have - 4 * i, 0), 4);
-        keep[i] = b == 4 ? ~0u : (1u << (8 * b)) - 1u;
-      }
-    }
-    const auto load = [&](const uint8_t* from) {
-      u32x4_t x = *reinterpret_cast<const u32x4_t*>(from);
-      if constexpr (kMasked) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] &= keep[i];
-      }
-      return x;
-    };
-    u32x4_t codes[kVLoads], scales[kFp4 ? kVLoads : 1];
-#pragma unroll
-    for (int d = 0; d < kVLoads; ++d) {
-      codes[d] = load(a.c.v + (vunit * code_bytes<kFp4>(kD) + 16 * d + n) * ps + vrow);
-      if constexpr (kFp4) scales[d] = load(a.c.v_scales + (vunit * (kD / 16) + 2 * d + (n >> 3)) * ps + vrow);
-      if constexpr (kMasked) {
-        const u32x4_t x = kFp4 ? scales[kFp4 ? d : 0] : codes[d];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) nan = nan || (((x[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u);
-      }
-    }
-    const auto operand = [&](int d, int h, half8_t& v0, half8_t& v1) {  // of keys 8 h .. 8 h + 7
-      if constexpr (kFp4) {
-        half2_t sc[4];
-        sc[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)scales[d][2 * h], 1.0f, false);
-        sc[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)scales[d][2 * h], 1.0f, true);
-        sc[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)scales[d][2 * h + 1], 1.0f, false);
-        sc[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)scales[d][2 * h + 1], 1.0f, true);
-        half8s_of_pairs(codes[d][2 * h], codes[d][2 * h + 1], sc, v0, v1);
-      } else {
-        v0 = half8_of_e4m3(codes[d][2 * h], codes[d][2 * h + 1]);
-      }
-    };
-    if (kMasked && __builtin_amdgcn_ballot_w64(nan)) {
-      for (int nt = 0; nt < kNT; ++nt) {
-        half8_t see[2];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) see[e / 8][e % 8] = bits[nt] >> e & 1 ? (_Float16)1 : (_Float16)0;
-#pragma unroll
-        for (int d = 0; d < kVLoads; ++d) {
-          floatx4_t found[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            half8_t v[2], bad[2];
-            operand(d, h, v[0], v[1]);
-#pragma unroll
-            for (int x = 0; x < (kFp4 ? 2 : 1); ++x) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const bool is = !(v[x][e] == v[x][e]);
-                bad[x][e] = is ? (_Float16)1 : (_Float16)0;
-                v[x][e] = is ? (_Float16)0 : v[x][e];
-              }
-              found[x] = mfma(bad[x], see[h], found[x]);
-              const int at = kFp4 ? 2 * d + x : d;
-              w.o[nt][at] = mfma(v[x], p[nt][h], w.o[nt][at]);
-            }
-          }
-#pragma unroll
-          for (int x = 0; x < (kFp4 ? 2 : 1); ++x)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (found[x][i] > 0.0f) w.o[nt][kFp4 ? 2 * d + x : d][i] = __builtin_nanf("");
-        }
-      }
-      return;
-    }
-#pragma unroll
-    for (int d = 0; d < kVLoads; ++d) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        half8_t v0, v1;
-        operand(d, h, v0, v1);
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-          if constexpr (kFp4) {
-            w.o[nt][2 * d] = mfma(v0, p[nt][h], w.o[nt][2 * d]);
-            w.o[nt][2 * d + 1] = mfma(v1, p[nt][h], w.o[nt][2 * d + 1]);
-          } else {
-            w.o[nt][d] = mfma(v0, p[nt][h], w.o[nt][d]);
-          }
-        }
-      }
-    }
-  }
-
-  static __device__ __forceinline__ void load_q(const Attn& a, Wave& w, const Unit& u, int row0) {
+  __device__ __forceinline__ void load_q(const Attn& a, const Unit& u, int rows, int row0) {
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const float k_gs = *a.c.k_gs;
-    const int64_t most = cache_rows(a);
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
-      const RowOf r = row_of(a, u, kRows, row0 + 16 * nt + n);
+      const RowOf r = row_of(a, u, rows, row0 + 16 * nt + n);
       const bool real = r.token >= 0;
       const int64_t row = u.w.rows.row0 + (real ? r.token : 0);
-      const uint16_t* from = a.q + row * a.ldq + (int64_t)(real ? r.head : 0) * kD;
+      const uint16_t* from = a.q + row * a.ldq + (int64_t)(real ? r.head : 0) * kD + kVals * g;
       u32x4_t x[kFrags];
       uint32_t top = 0;
 #pragma unroll
       for (int f = 0; f < kFrags; ++f) {
         x[f] = u32x4_t{0, 0, 0, 0};
-        if (real)
-          x[f] = *reinterpret_cast<const u32x4_t*>(from + 4 * kVals * (f / kPerLoad) + kVals * g + 8 * (f % kPerLoad));
+        if (real) x[f] = *reinterpret_cast<const u32x4_t*>(from + 4 * kVals * (f / kPerLoad) + 8 * (f % kPerLoad));
+      }
+#pragma unroll
+      for (int f = 0; f < kFrags; ++f)
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = max(top, max(x[f][i] & 0x7FFFu, x[f][i] >> 16 & 0x7FFFu));
-      }
       top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
       top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
       const int exponent = max((int)(top >> 7), 1) - 127, shift = 14 - exponent;  // of the row's largest value
@@ -528,147 +364,588 @@ struct Kernel {
         for (int i = 0; i < 4; ++i)
           h[i] = two_fp16(ldexpf(finite ? __uint_as_float(x[f][i] << 16) : 0.0f, shift),
                           ldexpf(finite ? __uint_as_float(x[f][i] & 0xFFFF0000u) : 0.0f, shift));
-        w.q[nt][f] = __builtin_bit_cast(half8_t, h);
+        q[nt][f] = __builtin_bit_cast(half8_t, h);
       }
-      // what is not finite in q makes every score of the row NaN
-      w.c1[nt] = finite ? ldexpf(a.scale * k_gs, -shift) : __builtin_nanf("");
-      w.m[nt] = kNoMax;
-      w.l[nt] = 0.0f;
-      w.limit[nt] = real ? row_limit(a, u.w.rows, most, r.token) : 0;
-      w.seen[nt] = a.tree && real ? a.tree[row] : 0;
+      c1[nt] = ldexpf(a.scale * k_gs, -shift);
+      fate[nt] = finite ? 1.0f : __builtin_nanf("");  // what is not finite in q makes the row NaN if it sees anything
+      m[nt] = kNoMax;
+      l[nt] = 0.0f;
+      limit[nt] = real ? row_limit(a, u.w.rows, r.token) : 0;
+      seen[nt] = a.tree && real ? a.tree[row] : 0;
 #pragma unroll
-      for (int d = 0; d < kTiles; ++d) w.o[nt][d] = floatx4_t{0, 0, 0, 0};
+      for (int d = 0; d < kTiles; ++d) o[nt][d] = floatx4_t{0, 0, 0, 0};
     }
   }
 
-  // The eight values of row n that lane (n, g) has of tiles 2 x and 2 x + 1:
-  // two runs of four dims, at dims d0 and d1.
-  static __device__ __forceinline__ void runs_of(int x, int g, int& d0, int& d1) {
-    d0 = kFp4 ? 32 * x + 8 * g : 32 * x + 4 * g;
-    d1 = kFp4 ? d0 + 4 : d0 + 16;
-  }
-  static __device__ __forceinline__ void in_order(const floatx4_t& a, const floatx4_t& b, floatx4_t r[2]) {
-    if constexpr (kFp4) {
-      r[0] = floatx4_t{a[0], b[0], a[1], b[1]};
-      r[1] = floatx4_t{a[2], b[2], a[3], b[3]};
-    } else {
-      r[0] = a;
-      r[1] = b;
+  // Bits of the lane's 16 keys from position `key` on that row n of tile nt sees.
+  __device__ __forceinline__ uint32_t seen_bits(const Attn& a, int nt, const SeqRows& s, int key, bool has_page) const {
+    const auto below = [&](int64_t end) { return (1u << (int)min(max(end - key, (int64_t)0), (int64_t)16)) - 1u; };
+    uint32_t bits = below(limit[nt]);
+    if (a.tree) {
+      const int64_t ctx = (int64_t)s.kv - s.n, b = key - ctx;
+      const uint64_t drafts = b >= 0 ? (b < 64 ? seen[nt] >> b : 0) : (b > -16 ? seen[nt] << -b : 0);
+      bits &= below(ctx) | (uint32_t)drafts;
     }
+    return has_page ? bits : 0u;
   }
 
-  // Row rho's pair x of tiles, with its maximum m and sum l: to the output if
-  // the unit is whole (slot < 0), else to the workspace.
-  static __device__ __forceinline__ void emit(const Attn& a, const Unit& u, int rho, int x, const floatx4_t& t0,
-                                              const floatx4_t& t1, float m, float l, int64_t slot) {
-    const int g = (threadIdx.x & 63) >> 4;
-    const RowOf r = row_of(a, u, kRows, rho);
-    if (r.token < 0) return;
-    int d[2];
-    runs_of(x, g, d[0], d[1]);
-    floatx4_t v[2];
-    in_order(t0, t1, v);
-    if (slot < 0) {
-      const float f = l == 0.0f ? 0.0f : *a.c.v_gs / l;  // a row that sees nothing is zeros
-      uint16_t* to = a.o + (u.w.rows.row0 + r.token) * a.ldo + (int64_t)r.head * kD;
+  // The running maximum after scores s; what it moves by is taken out of the sum and the result.
+  __device__ __forceinline__ void raise_max(const Scores& s) {
+    float top[kNT];
+    bool lags = false;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        u32x2_t b;
-        b[0] = pack_bf16(v[i][0] * f, v[i][1] * f);
-        b[1] = pack_bf16(v[i][2] * f, v[i][3] * f);
-        *reinterpret_cast<u32x2_t*>(to + d[i]) = b;
-      }
-      return;
+    for (int nt = 0; nt < kNT; ++nt) {
+      top[nt] = fmaxf(s[nt][0][0], s[nt][0][1]);
+#pragma unroll
+      for (int e = 2; e < 16; ++e) top[nt] = fmaxf(top[nt], s[nt][e / 4][e % 4]);
+      top[nt] *= c1[nt];
+      lags = lags || top[nt] > m[nt] + kLag;
     }
-    float* part = a.part + slot * (kRows * (kD + 2));
-#pragma unroll
-    for (int i = 0; i < 2; ++i) *reinterpret_cast<floatx4_t*>(part + rho * kD + d[i]) = v[i];
-    if (x == 0 && g == 0) {
-      part[kRows * kD + 2 * rho] = m;
-      part[kRows * kD + 2 * rho + 1] = l;
-    }
-  }
-
-  // Steps [k0, k1) of unit u.
-  static __device__ __forceinline__ void run_unit(const Attn& a, const Unit& u, int64_t k0, int64_t k1, int64_t slot,
-                                                  floatx4_t* lds) {
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = lane & 15;
-    const int row0 = kSplit ? 0 : wave * kWaveRows;
-    Wave w;
-    load_q(a, w, u, row0);
-    // the wave's first and last token, and from them the steps it has
-    const int wide = a.parts == 1 ? a.group : kRows;
-    const SeqRows& s = u.w.rows;
-    const int64_t most = cache_rows(a);
-    const int t0 = u.tile * a.tokens + row0 / wide;
-    const int t1 = min(min(u.tile * a.tokens + (row0 + kWaveRows - 1) / wide, (u.tile + 1) * a.tokens - 1), s.n - 1);
-    const int64_t reach = t0 > t1 ? 0 : row_limit(a, s, most, t1);
-    const int64_t all = a.tree ? min((int64_t)s.kv - s.n, most) : row_limit(a, s, most, t0);  // every row sees these
-    const int64_t end = min(k1, (reach + kStep - 1) / kStep), by = kSplit ? 4 : 1;
-    int64_t k = k0 + (kSplit ? wave : 0);
-    Pages next = k < end ? pages_of(a, u.seq, k * kStep) : Pages{-1, -1};
-    for (; k < end; k += by) {
-      const Pages pg = next;
-      if (k + by < end) next = pages_of(a, u.seq, (k + by) * kStep);
-      if ((k + 1) * kStep <= all && __builtin_amdgcn_ballot_w64(pg.k < 0 || pg.v < 0) == 0)
-        step<false>(a, w, u, k * kStep, pg);
-      else
-        step<true>(a, w, u, k * kStep, pg);
-    }
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) w.l[nt] = sum_over_g(w.l[nt]);
-    if constexpr (!kSplit) {
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-        for (int x = 0; x < kTiles / 2; ++x)
-          emit(a, u, row0 + 16 * nt + n, x, w.o[nt][2 * x], w.o[nt][2 * x + 1], w.m[nt], w.l[nt], slot);
-    } else {
-      // four waves' results of the same rows: four pairs of tiles at a time, each wave adds up one pair
-      float* ml = reinterpret_cast<float*>(lds + 4 * 8 * 64);  // [wave][nt][16][2]
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-        if (lane < 16) {
-          ml[((wave * kNT + nt) * 16 + n) * 2] = w.m[nt];
-          ml[((wave * kNT + nt) * 16 + n) * 2 + 1] = w.l[nt];
-        }
-      __syncthreads();
+    if (__builtin_amdgcn_ballot_w64(lags)) {
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
-        float m = kNoMax, l = 0.0f;
+        const float now = fmaxf(m[nt], max_over_g(top[nt])), f = __builtin_amdgcn_exp2f(m[nt] - now);
+        m[nt] = now;
+        l[nt] *= f;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) m = fmaxf(m, ml[((v * kNT + nt) * 16 + n) * 2]);
+        for (int d = 0; d < kTiles; ++d) o[nt][d] *= f;
+      }
+    }
+  }
+
+  // Scores of keys key .. key + 15 that their row does not see become -inf.
+  __device__ __forceinline__ void hide(const Attn& a, const SeqRows& sr, int key, bool has_page, Scores& s) const {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float* at = ml + ((v * kNT + nt) * 16 + n) * 2;
-          l += at[1] * __builtin_amdgcn_exp2f(at[0] - m);
+    for (int nt = 0; nt < kNT; ++nt) {
+      const uint32_t bits = seen_bits(a, nt, sr, key, has_page);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[nt][e / 4][e % 4] = bits >> e & 1 ? s[nt][e / 4][e % 4] : -INFINITY;
+    }
+  }
+
+  // Part x of `parts` of the rows' weights of the lane's 16 keys, under the running maximum.
+  __device__ __forceinline__ void weights(int x, int parts, const Scores& s, half8_t p[kNT][2]) {
+#pragma unroll
+    for (int i = 8 * kNT * x / parts; i < 8 * kNT * (x + 1) / parts; ++i) {
+      const int nt = i / 8, e = i % 8 * 2;
+      const float off = kLift - m[nt];
+      const float v = __builtin_amdgcn_exp2f(fmaf(s[nt][e / 4][e % 4], c1[nt], off));
+      const float y = __builtin_amdgcn_exp2f(fmaf(s[nt][e / 4][e % 4 + 1], c1[nt], off));
+      l[nt] += v + y;
+      const half2_t h = two_fp16(v, y);
+      p[nt][e / 8][e % 8] = h[0];
+      p[nt][e / 8][e % 8 + 1] = h[1];
+    }
+  }
+
+  // Operand h of V's tile d (keys 8 h .. 8 h + 7 of the lane's) times the weights.
+  __device__ __forceinline__ void add_value(int d, int h, const half8_t& v, const half8_t p[kNT][2]) {
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) o[nt][d] = mfma(v, p[nt][h], o[nt][d]);
+  }
+  // Results of tile d that see a NaN of V become NaN; v: the tile's operands of keys 8 h .. as they were stored.
+  __device__ __forceinline__ void spread_nan(int d, const half8_t v[2], const uint32_t bits[kNT]) {
+    half8_t bad[2];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) bad[e / 8][e % 8] = v[e / 8][e % 8] == v[e / 8][e % 8] ? (_Float16)0 : (_Float16)1;
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      floatx4_t found = {0, 0, 0, 0};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        half8_t see;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) see[e] = bits[nt] >> (8 * h + e) & 1 ? (_Float16)1 : (_Float16)0;
+        found = mfma(bad[h], see, found);
+      }
+      floatx4_t more;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) more[i] = found[i] > 0.0f ? __builtin_nanf("") : 0.0f;
+      o[nt][d] += more;
+    }
+  }
+
+  // The sums of the rows over all lanes; NaN where the row is.
+  __device__ __forceinline__ void finish_sums() {
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      const float sum = sum_over_g(l[nt]);
+      l[nt] = sum == 0.0f ? 0.0f : sum * fate[nt];
+    }
+  }
+};
+
+// Where a row's results go: to the output if its unit is whole (slot < 0), else to the workspace.
+template <bool kFp4, int kD>
+struct Sink {
+  uint16_t* to;
+  float* part;
+  float f;
+  // Row rho (of `rows`), its maximum m and sum l.
+  __device__ __forceinline__ Sink(const Attn& a, const Unit& u, int rows, int rho, float m, float l, int slot) {
+    const int g = (threadIdx.x & 63) >> 4;
+    const RowOf r = row_of(a, u, rows, rho);
+    to = nullptr;
+    part = nullptr;
+    if (r.token < 0) return;
+    if (slot < 0) {
+      f = l == 0.0f ? 0.0f : *a.c.v_gs / l;  // a row that sees nothing is zeros
+      to = a.o + (u.w.rows.row0 + r.token) * a.ldo + (int64_t)r.head * kD;
+    } else {
+      float* base = a.part + (int64_t)slot * (rows * (kD + 2));
+      part = base + rho * kD;
+      if (g == 0) {
+        base[rows * kD + 2 * rho] = m;
+        base[rows * kD + 2 * rho + 1] = l;
+      }
+    }
+  }
+  // Tiles 2 x and 2 x + 1: the lane's eight values are two runs of four dims.
+  __device__ __forceinline__ void put(int x, const floatx4_t& t0, const floatx4_t& t1) const {
+    const int g = (threadIdx.x & 63) >> 4, d0 = kFp4 ? 32 * x + 8 * g : 32 * x + 4 * g, d1 = kFp4 ? d0 + 4 : d0 + 16;
+    const floatx4_t v0 = kFp4 ? floatx4_t{t0[0], t1[0], t0[1], t1[1]} : t0;
+    const floatx4_t v1 = kFp4 ? floatx4_t{t0[2], t1[2], t0[3], t1[3]} : t1;
+    if (to) {
+      u32x2_t b;
+      b[0] = pack_bf16(v0[0] * f, v0[1] * f);
+      b[1] = pack_bf16(v0[2] * f, v0[3] * f);
+      *reinterpret_cast<u32x2_t*>(to + d0) = b;
+      b[0] = pack_bf16(v1[0] * f, v1[1] * f);
+      b[1] = pack_bf16(v1[2] * f, v1[3] * f);
+      *reinterpret_cast<u32x2_t*>(to + d1) = b;
+    } else if (part) {
+      *reinterpret_cast<floatx4_t*>(part + d0) = v0;
+      *reinterpret_cast<floatx4_t*>(part + d1) = v1;
+    }
+  }
+};
+
+// Codes of a lane: of `kN` loads of K rows or V lines, with NVFP4's scales.
+template <bool kFp4, int kN>
+struct RawK {
+  u32x4_t x[kN];
+  uint32_t sc[kFp4 ? kN : 1];
+};
+template <bool kFp4, int kN>
+struct RawV {
+  u32x4_t x[kN], sc[kFp4 ? kN : 1];
+};
+
+// How many of a lane's 16 keys of a step are there.
+__device__ __forceinline__ int keys_there(const Attn& a, const SeqRows& s, int step, int page) {
+  const int exist = min(s.kv, cache_rows(a)), key = step * kStep + 16 * ((threadIdx.x & 63) >> 4);
+  return page < 0 ? 0 : min(max(exist - key, 0), 16);
+}
+
+template <bool kFp4, int kD>
+struct Codes {
+  using R = Rows<kFp4, kD, 1>;
+
+  // The lane's part of the row of K's tile t.
+  static __device__ __forceinline__ void load_k(const Attn& a, int head, int step, int page, int t,
+                                                RawK<kFp4, R::kLoads>& r) {
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4, ps = 1 << a.c.page_shift;
+    const int krow = (step * kStep + 16 * (n >> 2) + (n & 3)) & (ps - 1);
+    const int64_t row = ((int64_t)max(page, 0) * a.c.hk + head) * ps + krow + 4 * t;
+    const uint8_t* at = a.c.k + row * code_bytes<kFp4>(kD) + R::kBytes * g;
+#pragma unroll
+    for (int c = 0; c < R::kLoads; ++c) {
+      if constexpr (R::kBytes == 16) {
+        r.x[c] = *reinterpret_cast<const u32x4_t*>(at + 64 * c);
+      } else {
+        const u32x2_t v = *reinterpret_cast<const u32x2_t*>(at + 32 * c);
+        r.x[c][0] = v[0];
+        r.x[c][1] = v[1];
+      }
+      if constexpr (kFp4) {
+        const uint8_t* from = a.c.k_scales + row * (kD / 16) + (4 * R::kVals * c + R::kVals * g) / 16;
+        r.sc[c] = R::kVals == 32 ? *reinterpret_cast<const uint16_t*>(from) : *from;
+      }
+    }
+  }
+  // Operand f of them.
+  static __device__ __forceinline__ half8_t key(const RawK<kFp4, R::kLoads>& r, int f) {
+    const int c = f / R::kPerLoad, i = f % R::kPerLoad;
+    if constexpr (kFp4) {
+      const half2_t sc = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)r.sc[c], 1.0f, false);
+      const half2_t s2 = {sc[i / 2], sc[i / 2]};
+      return half8_of_e2m1(r.x[c][i], s2);
+    } else {
+      return half8_of_e4m3(r.x[c][2 * i], r.x[c][2 * i + 1]);
+    }
+  }
+
+  // V's loads first, first + by, ...
+  template <int kN>
+  static __device__ __forceinline__ void load_v(const Attn& a, int head, int step, int page, int first, int by,
+                                                RawV<kFp4, kN>& r) {
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4, ps = 1 << a.c.page_shift;
+    const int vrow = (step * kStep + 16 * g) & (ps - 1);
+    const int64_t unit = (int64_t)max(page, 0) * a.c.hk + head;
+    const uint8_t* at = a.c.v + (unit * code_bytes<kFp4>(kD) + 16 * first + n) * ps + vrow;
+    const uint8_t* sc = kFp4 ? a.c.v_scales + (unit * (kD / 16) + 2 * first + (n >> 3)) * ps + vrow : nullptr;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      r.x[i] = *reinterpret_cast<const u32x4_t*>(at + 16 * by * i * ps);
+      if constexpr (kFp4) r.sc[i] = *reinterpret_cast<const u32x4_t*>(sc + 2 * by * i * ps);
+    }
+  }
+  // Codes (scales) behind the first `keep` of the lane's 16 keys, and NaN among the others, become zeros; whether
+  // there was such a NaN in any lane.
+  template <int kN>
+  static __device__ __forceinline__ bool clear_v(RawV<kFp4, kN>& r, int keep) {
+    uint32_t bad = 0;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      u32x4_t& x = kFp4 ? r.sc[kFp4 ? i : 0] : r.x[i];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const int b = min(max(keep - 4 * w, 0), 4);
+        x[w] &= b == 4 ? ~0u : (1u << (8 * b)) - 1u;
+        const uint32_t nan = ((x[w] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // top bit of a NaN byte
+        bad |= nan;
+        x[w] &= ~((nan >> 7) * 0xFFu);
+      }
+    }
+    return __builtin_amdgcn_ballot_w64(bad != 0) != 0;
+  }
+  // What clear_v took out of the steps k, k + by, ... before `end`: the results that see it become NaN.  The codes
+  // are read once more, of the steps that not every row sees all of (`all`: positions that every row sees).
+  template <int kNT>
+  static __device__ __forceinline__ void spread_nan(const Attn& a, const Unit& u, Rows<kFp4, kD, kNT>& w, int head, int k,
+                                                 int end, int by, int all) {
+    for (; k < end; k += by) {
+      const Pages pg = pages_of(a, u.seq, k);
+      if ((k + 1) * kStep <= all && all_there(pg)) continue;
+      const int keep = keys_there(a, u.w.rows, k, pg.v), key = k * kStep + 16 * ((threadIdx.x & 63) >> 4);
+      uint32_t bits[kNT];
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) bits[nt] = w.seen_bits(a, nt, u.w.rows, key, pg.v >= 0) & ((1u << keep) - 1u);
+#pragma unroll
+      for (int d = 0; d < R::kVLoads; ++d) {
+        RawV<kFp4, 1> r;
+        half8_t v[2][2];
+        load_v(a, head, k, pg.v, d, 0, r);
+        u32x4_t& x = kFp4 ? r.sc[0] : r.x[0];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // keys that are not there may hold anything
+          const int b = min(max(keep - 4 * i, 0), 4);
+          x[i] &= b == 4 ? ~0u : (1u << (8 * b)) - 1u;
         }
-        const float f = __builtin_amdgcn_exp2f(w.m[nt] - m);
-        constexpr int kPairs = kTiles / 2, kAtOnce = kPairs < 4 ? kPairs : 4;
+        value(r, 0, 0, v[0][0], v[1][0]);
+        value(r, 0, 1, v[0][1], v[1][1]);
+        w.spread_nan(kFp4 ? 2 * d : d, v[0], bits);
+        if constexpr (kFp4) w.spread_nan(2 * d + 1, v[1], bits);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  // Operand h (keys 8 h .. 8 h + 7 of the lane's) of load i: v0, and in NVFP4 v1 of the next dim.
+  template <int kN>
+  static __device__ __forceinline__ void value(const RawV<kFp4, kN>& r, int i, int h, half8_t& v0, half8_t& v1) {
+    if constexpr (kFp4) {
+      half2_t sc[4];
+      sc[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)r.sc[i][2 * h], 1.0f, false);
+      sc[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)r.sc[i][2 * h], 1.0f, true);
+      sc[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)r.sc[i][2 * h + 1], 1.0f, false);
+      sc[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)r.sc[i][2 * h + 1], 1.0f, true);
+      half8s_of_pairs(r.x[i][2 * h], r.x[i][2 * h + 1], sc, v0, v1);
+    } else {
+      v0 = half8_of_e4m3(r.x[i][2 * h], r.x[i][2 * h + 1]);
+    }
+  }
+};
+
+// Few rows per sequence (decode): the workgroup's four waves have the same 16
+// kNT rows and every fourth step each, straight from memory to the matrix
+// instructions; their results are joined through LDS.
+template <bool kFp4, int kD, int kNT>
+struct Few {
+  using R = Rows<kFp4, kD, kNT>;
+  using C = Codes<kFp4, kD>;
+  static constexpr int kRows = R::kWaveRows;
+  struct Lds {
+    floatx4_t sums[4 * 8 * 64];
+    float ml[4][kNT][16][2];
+  };
+  struct Keys {
+    RawK<kFp4, R::kLoads> t[4];
+  };
+  static __device__ __forceinline__ void load_keys(const Attn& a, int head, int step, const Pages& pg, Keys& k) {
 #pragma unroll
-        for (int x0 = 0; x0 < kPairs; x0 += kAtOnce) {
+    for (int t = 0; t < 4; ++t) C::load_k(a, head, step, pg.k, t, k.t[t]);
+  }
+
+  // Step `step`, whose keys are in k; those of `after` (its pages pg2) are asked for.  `whole`: every row sees all of it.
+  // Returns whether NaN was taken out of its values.
+  static __device__ __forceinline__ bool run_step(const Attn& a, const Unit& u, int head, R& w, Keys& k, int step,
+                                                  const Pages& pg, bool whole, int after, const Pages& pg2) {
+    const int g = (threadIdx.x & 63) >> 4;
+    RawV<kFp4, R::kVLoads> rv;
+    C::load_v(a, head, step, pg.v, 0, 1, rv);
+    typename R::Scores s;
 #pragma unroll
-          for (int i = 0; i < 2 * kAtOnce; ++i) lds[(wave * 8 + i) * 64 + lane] = w.o[nt][2 * x0 + i] * f;
-          __syncthreads();
-          if (wave < kAtOnce) {
-            floatx4_t t[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    for (int t = 0; t < 4; ++t) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
+      for (int f = 0; f < R::kFrags; ++f) {
+        const half8_t k8 = C::key(k.t[t], f);
 #pragma unroll
-              for (int i = 0; i < 2; ++i) t[i] += lds[(v * 8 + 2 * wave + i) * 64 + lane];
-            emit(a, u, 16 * nt + n, x0 + wave, t[0], t[1], m, l, slot);
-          }
-          __syncthreads();
+        for (int nt = 0; nt < kNT; ++nt) s[nt][t] = mfma(k8, w.q[nt][f], f == 0 ? floatx4_t{0, 0, 0, 0} : s[nt][t]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    load_keys(a, head, after, pg2, k);
+    half8_t p[kNT][2];
+    if (!whole) w.hide(a, u.w.rows, step * kStep + 16 * g, pg.v >= 0, s);
+    w.raise_max(s);
+    w.weights(0, 1, s, p);
+    bool nan = false;
+    if (!whole) nan = C::clear_v(rv, keys_there(a, u.w.rows, step, pg.v));
+#pragma unroll
+    for (int d = 0; d < R::kVLoads; ++d) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        half8_t v0, v1;
+        C::value(rv, d, h, v0, v1);
+        w.add_value(kFp4 ? 2 * d : d, h, v0, p);
+        if constexpr (kFp4) w.add_value(2 * d + 1, h, v1, p);
+      }
+      if (d % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+    }
+    return nan;
+  }
+
+  static __device__ __forceinline__ void run_unit(const Attn& a, const Unit& u, int k0, int k1, int slot, Lds& lds) {
+    const int wave = uniform((int)threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15;
+    const int head = u.minor / a.parts;
+    R w;
+    w.load_q(a, u, kRows, 0);
+    const Reach reach = reach_of(a, u, kRows, 0, kRows);
+    const int end = min(k1, reach.steps);
+    int k = k0 + wave;
+    bool nan = false;
+    if (k < end) {
+      Keys keys;
+      Pages pg = pages_of(a, u.seq, k), pg2 = pages_of(a, u.seq, min(k + 4, end - 1));
+      load_keys(a, head, k, pg, keys);
+      for (; k < end; k += 4) {
+        const Pages pg3 = pages_of(a, u.seq, min(k + 8, end - 1));
+        nan |= run_step(a, u, head, w, keys, k, pg, (k + 1) * kStep <= reach.all && all_there(pg), min(k + 4, end - 1), pg2);
+        pg = pg2;
+        pg2 = pg3;
+      }
+    }
+    if (nan) C::spread_nan(a, u, w, head, k0 + wave, end, 4, reach.all);
+    w.finish_sums();
+    // four waves' results of the same rows: four pairs of tiles at a time, each wave adds up one pair
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      if (lane < 16) {
+        lds.ml[wave][nt][n][0] = w.m[nt];
+        lds.ml[wave][nt][n][1] = w.l[nt];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      float m = kNoMax, l = 0.0f;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) m = fmaxf(m, lds.ml[v][nt][n][0]);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) l += lds.ml[v][nt][n][1] * __builtin_amdgcn_exp2f(lds.ml[v][nt][n][0] - m);
+      const float f = __builtin_amdgcn_exp2f(w.m[nt] - m);
+      const Sink<kFp4, kD> sink(a, u, kRows, 16 * nt + n, m, l, slot);
+      constexpr int kPairs = R::kTiles / 2, kAtOnce = kPairs < 4 ? kPairs : 4;
+#pragma unroll
+      for (int x0 = 0; x0 < kPairs; x0 += kAtOnce) {
+#pragma unroll
+        for (int i = 0; i < 2 * kAtOnce; ++i) lds.sums[(wave * 8 + i) * 64 + lane] = w.o[nt][2 * x0 + i] * f;
+        __syncthreads();
+        if (wave < kAtOnce) {
+          floatx4_t t[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) t[i] += lds.sums[(v * 8 + 2 * wave + i) * 64 + lane];
+          sink.put(x0 + wave, t[0], t[1]);
         }
+        __syncthreads();
       }
     }
   }
 };
 
-template <bool kFp4, int kD, int kNT, bool kSplit>
-__global__ __launch_bounds__(256) void attn_kernel(Attn a) {
-  using K = Kernel<kFp4, kD, kNT, kSplit>;
-  __shared__ floatx4_t lds[kSplit ? 4 * 8 * 64 + 4 * kNT * 16 / 2 : 1];
+// Many rows per sequence (prompts, large trees): the waves have 16 kNT rows each
+// and share every step's keys, which the workgroup makes fp16 once, in LDS, in
+// the order of the matrix instructions' operands (a lane's 16 bytes side by
+// side: no bank conflicts, constant offsets).  In registers each wave would
+// convert all of them itself, as many vector instructions as the softmax has.
+// Wave t converts K's tile t and every fourth load of V.
+//
+// One barrier a step.  In step j the scores of step j + 1 are multiplied while
+// step j's softmax is evaluated (neither waits for the other), then P V of step j;
+// codes of K's step j + 2 and V's step j + 1 are asked for at its beginning and
+// converted at its end, into the halves of the buffers that step j - 1 was the last
+// to read.
+template <bool kFp4, int kD, int kNT>
+struct Many {
+  using R = Rows<kFp4, kD, kNT>;
+  using C = Codes<kFp4, kD>;
+  static constexpr int kRows = 4 * R::kWaveRows;
+  static constexpr int kMine = R::kVLoads < 4 ? 1 : R::kVLoads / 4;  // V loads of a wave
+  struct Lds {
+    u32x4_t k[2][4 * R::kFrags * 64], v[2][2 * R::kTiles * 64];  // operands of a step, 1 KiB each
+    int nan[4];
+  };
+  struct State {
+    RawK<kFp4, R::kLoads> rk;
+    RawV<kFp4, kMine> rv;
+    Pages p0, p1, p2;  // of steps k, k + 1, k + 2
+    bool nan;          // whether this wave took NaN out of values
+    typename R::Scores s;
+  };
+
+  static __device__ __forceinline__ void store_k(const RawK<kFp4, R::kLoads>& r, int f, u32x4_t* to) {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    to[(wave * R::kFrags + f) * 64 + lane] = __builtin_bit_cast(u32x4_t, C::key(r, f));
+  }
+  static __device__ __forceinline__ bool has_v() { return R::kVLoads >= 4 || (int)(threadIdx.x >> 6) < R::kVLoads; }
+  static __device__ __forceinline__ void load_v(const Attn& a, int head, int step, int page, RawV<kFp4, kMine>& r) {
+    if (has_v()) C::load_v(a, head, step, page, threadIdx.x >> 6, 4, r);
+  }
+  static __device__ __forceinline__ void store_v(const RawV<kFp4, kMine>& r, int i, int h, u32x4_t* to) {
+    const int d = (threadIdx.x >> 6) + 4 * i, lane = threadIdx.x & 63;
+    if (!has_v()) return;
+    half8_t v0, v1;
+    C::value(r, i, h, v0, v1);
+    to[((kFp4 ? 2 * d : d) * 2 + h) * 64 + lane] = __builtin_bit_cast(u32x4_t, v0);
+    if constexpr (kFp4) to[((2 * d + 1) * 2 + h) * 64 + lane] = __builtin_bit_cast(u32x4_t, v1);
+  }
+
+  // Step k of the unit, its scores in st.s.  `mine`: what this wave has; `everyone`: positions that all rows of
+  // the workgroup see.  The parts between the scheduling barriers hold matrix and vector instructions that do not
+  // wait for each other, and the LDS reads of the next part; without the barriers the compiler asks for all
+  // of a step's operands at once, more than there are registers.
+  static __device__ __forceinline__ void run_step(const Attn& a, const Unit& u, int head, R& w, State& st, Lds& lds,
+                                                  int k, int k0, int end, const Reach& mine, int everyone) {
+    const int lane = threadIdx.x & 63, g = lane >> 4, b = (k - k0) & 1;
+    const int k1 = min(k + 1, end - 1), k2 = min(k + 2, end - 1);
+    C::load_k(a, head, k2, st.p2.k, threadIdx.x >> 6, st.rk);
+    load_v(a, head, k1, st.p1.v, st.rv);
+    const Pages p3 = pages_of(a, u.seq, min(k + 3, end - 1));
+    {
+      const half8_t* kf = reinterpret_cast<const half8_t*>(lds.k[b ^ 1]) + lane;
+      const half8_t* vf = reinterpret_cast<const half8_t*>(lds.v[b]) + lane;
+      half8_t p[kNT][2];
+      typename R::Scores next;
+      constexpr int kPart = R::kFrags < 4 ? R::kFrags : 4, kParts = 4 * R::kFrags / kPart;  // operands at a time
+      half8_t f[2][kPart];
+#pragma unroll
+      for (int i = 0; i < kPart; ++i) f[0][i] = kf[i * 64];
+      if ((k + 1) * kStep > mine.all || !all_there(st.p0)) w.hide(a, u.w.rows, k * kStep + 16 * g, st.p0.v >= 0, st.s);
+      w.raise_max(st.s);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int x = 0; x < kParts; ++x) {
+        if (x + 1 < kParts) {
+#pragma unroll
+          for (int i = 0; i < kPart; ++i) f[(x + 1) & 1][i] = kf[((x + 1) * kPart + i) * 64];
+        }
+#pragma unroll
+        for (int i = 0; i < kPart; ++i) {
+          const int t = (x * kPart + i) / R::kFrags, q = (x * kPart + i) % R::kFrags;
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt)
+            next[nt][t] = mfma(f[x & 1][i], w.q[nt][q], q == 0 ? floatx4_t{0, 0, 0, 0} : next[nt][t]);
+        }
+        w.weights(x, kParts, st.s, p);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      half8_t v[2][4];  // two tiles of dims at a time
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[0][i] = vf[i * 64];
+#pragma unroll
+      for (int x = 0; x < R::kTiles / 2; ++x) {
+        if (x + 1 < R::kTiles / 2) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[(x + 1) & 1][i] = vf[(4 * (x + 1) + i) * 64];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w.add_value(2 * x + i / 2, i % 2, v[x & 1][i], p);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) st.s[nt][t] = next[nt][t];
+    }
+    // values that some row of the workgroup does not see
+    if (has_v() && ((k1 + 1) * kStep > everyone || !all_there(st.p1)))
+      st.nan |= C::clear_v(st.rv, keys_there(a, u.w.rows, k1, st.p1.v));
+#pragma unroll
+    for (int f = 0; f < R::kFrags; ++f) store_k(st.rk, f, lds.k[b]);
+#pragma unroll
+    for (int i = 0; i < 2 * kMine; ++i) store_v(st.rv, i / 2, i % 2, lds.v[b ^ 1]);
+    __syncthreads();
+    st.p0 = st.p1;
+    st.p1 = st.p2;
+    st.p2 = p3;
+  }
+
+  static __device__ __forceinline__ void run_unit(const Attn& a, const Unit& u, int k0, int k1, int slot, Lds& lds) {
+    const int wave = uniform((int)threadIdx.x >> 6), n = threadIdx.x & 15;
+    const int row0 = wave * R::kWaveRows, head = u.minor / a.parts;
+    R w;
+    w.load_q(a, u, kRows, row0);
+    const Reach mine = reach_of(a, u, kRows, row0, R::kWaveRows), whole = reach_of(a, u, kRows, 0, kRows);
+    const int end = min(k1, whole.steps);
+    if (k0 < end) {
+      State st;
+      st.p0 = pages_of(a, u.seq, k0);
+      st.p1 = pages_of(a, u.seq, min(k0 + 1, end - 1));
+      st.p2 = pages_of(a, u.seq, min(k0 + 2, end - 1));
+      C::load_k(a, head, k0, st.p0.k, wave, st.rk);
+      load_v(a, head, k0, st.p0.v, st.rv);
+#pragma unroll
+      for (int f = 0; f < R::kFrags; ++f) store_k(st.rk, f, lds.k[0]);
+      st.nan = has_v() && ((k0 + 1) * kStep > whole.all || !all_there(st.p0)) &&
+               C::clear_v(st.rv, keys_there(a, u.w.rows, k0, st.p0.v));
+#pragma unroll
+      for (int i = 0; i < 2 * kMine; ++i) store_v(st.rv, i / 2, i % 2, lds.v[0]);
+      C::load_k(a, head, min(k0 + 1, end - 1), st.p1.k, wave, st.rk);
+#pragma unroll
+      for (int f = 0; f < R::kFrags; ++f) store_k(st.rk, f, lds.k[1]);
+      __syncthreads();
+      const half8_t* kf = reinterpret_cast<const half8_t*>(lds.k[0]) + (threadIdx.x & 63);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int f = 0; f < R::kFrags; ++f)
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt)
+            st.s[nt][t] = mfma(kf[(t * R::kFrags + f) * 64], w.q[nt][f], f == 0 ? floatx4_t{0, 0, 0, 0} : st.s[nt][t]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      __syncthreads();
+      for (int k = k0; k < end; ++k) run_step(a, u, head, w, st, lds, k, k0, end, mine, whole.all);
+      if ((threadIdx.x & 63) == 0) lds.nan[wave] = st.nan;
+      __syncthreads();
+      if (lds.nan[0] | lds.nan[1] | lds.nan[2] | lds.nan[3]) C::spread_nan(a, u, w, head, k0, end, 1, whole.all);
+      __syncthreads();
+    }
+    w.finish_sums();
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      const Sink<kFp4, kD> sink(a, u, kRows, row0 + 16 * nt + n, w.m[nt], w.l[nt], slot);
+#pragma unroll
+      for (int x = 0; x < R::kTiles / 2; ++x) sink.put(x, w.o[nt][2 * x], w.o[nt][2 * x + 1]);
+    }
+  }
+};
+
+// The workgroup's range of steps, unit by unit: run(unit, first step, step behind the last, slot of its part or -1).
+template <class Run>
+__device__ __forceinline__ void run_range(const Attn& a, Run run) {
   // neighbouring ranges on one XCD (workgroups go round the eight in turn): they share keys
   const int w = (int)(blockIdx.x & 7) * (a.ranges / 8) + (int)(blockIdx.x >> 3);
   const int64_t total = total_steps(a);
@@ -678,14 +955,25 @@ __global__ __launch_bounds__(256) void attn_kernel(Attn a) {
   if (pos >= end) return;
   Unit u = unit_at(a, pos);
   while (true) {
-    const int64_t k0 = pos - u.start, k1 = min(u.steps, end - u.start);
+    const int k0 = (int)(pos - u.start), k1 = (int)min((int64_t)u.steps, end - u.start);
     // a unit that is cut: its part behind the cut at the range's beginning, or before the one at its end
-    const int64_t slot = k0 > 0 ? 2 * (int64_t)w : k1 < u.steps ? 2 * (int64_t)w + 1 : -1;
-    K::run_unit(a, u, k0, k1, slot, lds);
+    run(u, k0, k1, k0 > 0 ? 2 * w : k1 < u.steps ? 2 * w + 1 : -1);
     pos = u.start + k1;
     if (pos >= end) return;
     next_unit(a, u);
   }
+}
+
+template <bool kFp4, int kD, int kNT>
+__global__ __launch_bounds__(256) void attn_few_kernel(Attn a) {
+  __shared__ typename Few<kFp4, kD, kNT>::Lds lds;
+  run_range(a, [&](const Unit& u, int k0, int k1, int slot) { Few<kFp4, kD, kNT>::run_unit(a, u, k0, k1, slot, lds); });
+}
+
+template <bool kFp4, int kD, int kNT>
+__global__ __launch_bounds__(256) void attn_many_kernel(Attn a) {
+  __shared__ typename Many<kFp4, kD, kNT>::Lds lds;
+  run_range(a, [&](const Unit& u, int k0, int k1, int slot) { Many<kFp4, kD, kNT>::run_unit(a, u, k0, k1, slot, lds); });
 }
 
 // The first range that begins inside a unit joins the unit's parts: the end of
@@ -761,13 +1049,13 @@ Plan plan_of(int64_t T, int n_seqs, int group, int d) {
   const int64_t rows = (T * group + n_seqs - 1) / n_seqs;
   if (rows <= 16) return {1, true, 16, 512, 4};
   if (rows <= 32) return {2, true, 32, 512, 4};
-  return {2, false, 128, 512, 4};
+  return {2, false, 128, 256, 4};
 }
 
 template <bool kFp4, int kD>
 void launch_typed(const Plan& p, const Attn& a, hipStream_t stream) {
-  const auto f = p.nt == 1 ? attn_kernel<kFp4, kD, 1, true>
-                           : p.split ? attn_kernel<kFp4, kD, 2, true> : attn_kernel<kFp4, kD, 2, false>;
+  const auto f = p.nt == 1 ? attn_few_kernel<kFp4, kD, 1>
+                           : p.split ? attn_few_kernel<kFp4, kD, 2> : attn_many_kernel<kFp4, kD, 2>;
   f<<<(unsigned)p.ranges, 256, 0, stream>>>(a);
   attn_join_kernel<kD><<<dim3((unsigned)p.ranges - 1, 16), 256, 0, stream>>>(a, p.rows);
 }
