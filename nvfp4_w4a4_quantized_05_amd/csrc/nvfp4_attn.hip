@@ -57,6 +57,7 @@ struct Attn {
   float* part;      // [2 x ranges][rows x (d + 2)]
   int ranges;       // workgroups
   int least;        // steps of a range, at least
+  int start;        // what beginning and ending a unit takes, in steps
   int tokens, parts;  // tokens per tile of rows; tiles that a token's heads take
 };
 
@@ -90,7 +91,8 @@ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, in
 // A sequence's share of the work.  Its tiles of rows (`tokens` tokens each) take
 // (first + r tokens) / 64 steps per head, r the tile: with first = context +
 // tokens + 63 that is what the tile's last token sees, rounded up (for the last
-// tile that may be a step more than there is).
+// tile that may be a step more than there is).  Beginning and ending a unit takes as long as some
+// steps; they are counted behind its own, so that a range of many short units is no longer than others.
 struct SeqWork {
   SeqRows rows;
   int64_t first;
@@ -127,6 +129,7 @@ __device__ __forceinline__ SeqWork seq_work(const Attn& a, int i) {
     w.first = min(max((int64_t)w.rows.kv - w.rows.n, (int64_t)0), (int64_t)most) + a.tokens + kStep - 1;
     w.slope = a.tokens;
   }
+  w.first += a.start * kStep;
   w.tiles = (w.rows.n + a.tokens - 1) / a.tokens;
   w.minor = a.c.hk * a.parts;
   return w;
@@ -245,11 +248,6 @@ __device__ __forceinline__ float max_over_g(float v) {  // over lanes n, n + 16,
   const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
-__device__ __forceinline__ float sum_over_g(float v) {
-  v += __shfl_xor(v, 32, 64);
-  return v + __shfl_xor(v, 16, 64);
-}
-
 __device__ __forceinline__ floatx4_t mfma(const half8_t& a, const half8_t& b, const floatx4_t& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
@@ -304,19 +302,31 @@ __device__ __forceinline__ void half8s_of_pairs(uint32_t lo, uint32_t hi, const 
   odd = __builtin_bit_cast(half8_t, o);
 }
 
-// Pages of a step's keys: of the lane's K rows' block of 16 and of its own block g.
+// Pages of a step's keys: of the lane's K rows' block of 16 and of its own block g; -1 where there is none.
 struct Pages {
   int k, v;
 };
-__device__ __forceinline__ Pages pages_of(const Attn& a, int seq, int step) {
-  const int lane = threadIdx.x & 63;
-  const int64_t key0 = (int64_t)step * kStep;
-  return {page_of(a.r, a.c, seq, key0 + 16 * ((lane & 15) >> 2)), page_of(a.r, a.c, seq, key0 + 16 * (lane >> 4))};
+// They are asked for a step or more before they are needed: entries_of only loads (from within the table always),
+// pages_of says what was found, once it has arrived.
+__device__ __forceinline__ Pages entries_of(const Attn& a, int seq, int step) {
+  const int lane = threadIdx.x & 63, last = a.r.max_pages - 1, shift = a.c.page_shift - 4;
+  const int* row = a.r.table + (int64_t)seq * a.r.ld_table;
+  const int k = (4 * step + ((lane & 15) >> 2)) >> shift, v = (4 * step + (lane >> 4)) >> shift;
+  return {row[min(k, last)], row[min(v, last)]};
+}
+__device__ __forceinline__ Pages pages_of(const Attn& a, int step, const Pages& e) {
+  const int lane = threadIdx.x & 63, shift = a.c.page_shift - 4;
+  const int k = (4 * step + ((lane & 15) >> 2)) >> shift, v = (4 * step + (lane >> 4)) >> shift;
+  return {k < a.r.max_pages && (unsigned)e.k < (unsigned)a.c.n_pages ? e.k : -1,
+          v < a.r.max_pages && (unsigned)e.v < (unsigned)a.c.n_pages ? e.v : -1};
+}
+__device__ __forceinline__ Pages pages_now(const Attn& a, int seq, int step) {
+  return pages_of(a, step, entries_of(a, seq, step));
 }
 __device__ __forceinline__ bool all_there(const Pages& p) { return __builtin_amdgcn_ballot_w64((p.k | p.v) < 0) == 0; }
 
 // Sizes of a format's operands, and a wave's rows and results.
-template <bool kFp4, int kD, int kNT>
+template <bool kFp4, int kD, int kNT, bool kPin>
 struct Rows {
   static constexpr int kWaveRows = 16 * kNT;
   // K: a lane has kVals values of a row per load, dims 4 kVals c + kVals g and on
@@ -328,7 +338,9 @@ struct Rows {
 
   half8_t q[kNT][kFrags];
   floatx4_t o[kNT][kTiles];
-  float m[kNT], l[kNT], c1[kNT];  // running maximum, the lane's part of the sum, factor of the scores (log2)
+  // The sum of a row's weights is one more result, with ones for V: no vector additions, no exchange between lanes.
+  floatx4_t sum[kNT];
+  float m[kNT], c1[kNT];          // running maximum, factor of the scores (log2)
   float fate[kNT];                // 1, or NaN
   int limit[kNT];                 // positions the row may see
   uint64_t seen[kNT];             // tree: its mask
@@ -365,11 +377,14 @@ struct Rows {
           h[i] = two_fp16(ldexpf(finite ? __uint_as_float(x[f][i] << 16) : 0.0f, shift),
                           ldexpf(finite ? __uint_as_float(x[f][i] & 0xFFFF0000u) : 0.0f, shift));
         q[nt][f] = __builtin_bit_cast(half8_t, h);
+        // to an accumulation register, where matrix instructions can read it, and for good: left to itself the
+        // compiler keeps its parts apart and puts them together again in every step
+        if constexpr (kPin) asm volatile("" : "+a"(q[nt][f]));
       }
       c1[nt] = ldexpf(a.scale * k_gs, -shift);
       fate[nt] = finite ? 1.0f : __builtin_nanf("");  // what is not finite in q makes the row NaN if it sees anything
       m[nt] = kNoMax;
-      l[nt] = 0.0f;
+      sum[nt] = floatx4_t{0, 0, 0, 0};
       limit[nt] = real ? row_limit(a, u.w.rows, r.token) : 0;
       seen[nt] = a.tree && real ? a.tree[row] : 0;
 #pragma unroll
@@ -406,7 +421,7 @@ struct Rows {
       for (int nt = 0; nt < kNT; ++nt) {
         const float now = fmaxf(m[nt], max_over_g(top[nt])), f = __builtin_amdgcn_exp2f(m[nt] - now);
         m[nt] = now;
-        l[nt] *= f;
+        sum[nt] *= f;
 #pragma unroll
         for (int d = 0; d < kTiles; ++d) o[nt][d] *= f;
       }
@@ -431,13 +446,19 @@ struct Rows {
       const float off = kLift - m[nt];
       const float v = __builtin_amdgcn_exp2f(fmaf(s[nt][e / 4][e % 4], c1[nt], off));
       const float y = __builtin_amdgcn_exp2f(fmaf(s[nt][e / 4][e % 4 + 1], c1[nt], off));
-      l[nt] += v + y;
       const half2_t h = two_fp16(v, y);
       p[nt][e / 8][e % 8] = h[0];
       p[nt][e / 8][e % 8 + 1] = h[1];
     }
   }
 
+  __device__ __forceinline__ void add_sums(const half8_t p[kNT][2]) {
+    const half8_t one = {1, 1, 1, 1, 1, 1, 1, 1};
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) sum[nt] = mfma(one, p[nt][h], sum[nt]);
+  }
   // Operand h of V's tile d (keys 8 h .. 8 h + 7 of the lane's) times the weights.
   __device__ __forceinline__ void add_value(int d, int h, const half8_t& v, const half8_t p[kNT][2]) {
 #pragma unroll
@@ -465,14 +486,8 @@ struct Rows {
     }
   }
 
-  // The sums of the rows over all lanes; NaN where the row is.
-  __device__ __forceinline__ void finish_sums() {
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-      const float sum = sum_over_g(l[nt]);
-      l[nt] = sum == 0.0f ? 0.0f : sum * fate[nt];
-    }
-  }
+  // The sum of row n's weights; NaN where the row is.
+  __device__ __forceinline__ float total(int nt) const { return sum[nt][0] == 0.0f ? 0.0f : sum[nt][0] * fate[nt]; }
 };
 
 // Where a row's results go: to the output if its unit is whole (slot < 0), else to the workspace.
@@ -539,7 +554,7 @@ __device__ __forceinline__ int keys_there(const Attn& a, const SeqRows& s, int s
 
 template <bool kFp4, int kD>
 struct Codes {
-  using R = Rows<kFp4, kD, 1>;
+  using R = Rows<kFp4, kD, 1, false>;
 
   // The lane's part of the row of K's tile t.
   static __device__ __forceinline__ void load_k(const Attn& a, int head, int step, int page, int t,
@@ -611,11 +626,11 @@ struct Codes {
   }
   // What clear_v took out of the steps k, k + by, ... before `end`: the results that see it become NaN.  The codes
   // are read once more, of the steps that not every row sees all of (`all`: positions that every row sees).
-  template <int kNT>
-  static __device__ __forceinline__ void spread_nan(const Attn& a, const Unit& u, Rows<kFp4, kD, kNT>& w, int head, int k,
+  template <int kNT, bool kPin>
+  static __device__ __forceinline__ void spread_nan(const Attn& a, const Unit& u, Rows<kFp4, kD, kNT, kPin>& w, int head, int k,
                                                  int end, int by, int all) {
     for (; k < end; k += by) {
-      const Pages pg = pages_of(a, u.seq, k);
+      const Pages pg = pages_now(a, u.seq, k);
       if ((k + 1) * kStep <= all && all_there(pg)) continue;
       const int keep = keys_there(a, u.w.rows, k, pg.v), key = k * kStep + 16 * ((threadIdx.x & 63) >> 4);
       uint32_t bits[kNT];
@@ -661,7 +676,7 @@ struct Codes {
 // instructions; their results are joined through LDS.
 template <bool kFp4, int kD, int kNT>
 struct Few {
-  using R = Rows<kFp4, kD, kNT>;
+  using R = Rows<kFp4, kD, kNT, false>;
   using C = Codes<kFp4, kD>;
   static constexpr int kRows = R::kWaveRows;
   struct Lds {
@@ -699,6 +714,7 @@ struct Few {
     if (!whole) w.hide(a, u.w.rows, step * kStep + 16 * g, pg.v >= 0, s);
     w.raise_max(s);
     w.weights(0, 1, s, p);
+    w.add_sums(p);
     bool nan = false;
     if (!whole) nan = C::clear_v(rv, keys_there(a, u.w.rows, step, pg.v));
 #pragma unroll
@@ -719,30 +735,31 @@ struct Few {
     const int wave = uniform((int)threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15;
     const int head = u.minor / a.parts;
     R w;
-    w.load_q(a, u, kRows, 0);
     const Reach reach = reach_of(a, u, kRows, 0, kRows);
     const int end = min(k1, reach.steps);
     int k = k0 + wave;
+    const int last = max(end - 1, k0);
+    const Pages e0 = entries_of(a, u.seq, min(k, last)), e1 = entries_of(a, u.seq, min(k + 4, last));
+    w.load_q(a, u, kRows, 0);
     bool nan = false;
     if (k < end) {
       Keys keys;
-      Pages pg = pages_of(a, u.seq, k), pg2 = pages_of(a, u.seq, min(k + 4, end - 1));
+      Pages pg = pages_of(a, k, e0), pg2 = pages_of(a, min(k + 4, end - 1), e1);
       load_keys(a, head, k, pg, keys);
       for (; k < end; k += 4) {
-        const Pages pg3 = pages_of(a, u.seq, min(k + 8, end - 1));
+        const Pages e = entries_of(a, u.seq, min(k + 8, end - 1));
         nan |= run_step(a, u, head, w, keys, k, pg, (k + 1) * kStep <= reach.all && all_there(pg), min(k + 4, end - 1), pg2);
         pg = pg2;
-        pg2 = pg3;
+        pg2 = pages_of(a, min(k + 8, end - 1), e);
       }
     }
     if (nan) C::spread_nan(a, u, w, head, k0 + wave, end, 4, reach.all);
-    w.finish_sums();
     // four waves' results of the same rows: four pairs of tiles at a time, each wave adds up one pair
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
       if (lane < 16) {
         lds.ml[wave][nt][n][0] = w.m[nt];
-        lds.ml[wave][nt][n][1] = w.l[nt];
+        lds.ml[wave][nt][n][1] = w.total(nt);
       }
     }
     __syncthreads();
@@ -789,7 +806,7 @@ struct Few {
 // to read.
 template <bool kFp4, int kD, int kNT>
 struct Many {
-  using R = Rows<kFp4, kD, kNT>;
+  using R = Rows<kFp4, kD, kNT, true>;
   using C = Codes<kFp4, kD>;
   static constexpr int kRows = 4 * R::kWaveRows;
   static constexpr int kMine = R::kVLoads < 4 ? 1 : R::kVLoads / 4;  // V loads of a wave
@@ -802,7 +819,6 @@ struct Many {
     RawV<kFp4, kMine> rv;
     Pages p0, p1, p2;  // of steps k, k + 1, k + 2
     bool nan;          // whether this wave took NaN out of values
-    typename R::Scores s;
   };
 
   static __device__ __forceinline__ void store_k(const RawK<kFp4, R::kLoads>& r, int f, u32x4_t* to) {
@@ -822,28 +838,28 @@ struct Many {
     if constexpr (kFp4) to[((2 * d + 1) * 2 + h) * 64 + lane] = __builtin_bit_cast(u32x4_t, v1);
   }
 
-  // Step k of the unit, its scores in st.s.  `mine`: what this wave has; `everyone`: positions that all rows of
+  // Step k of the unit (the b-th, modulo 2), its scores in `now`; the next step's go to `next`.  `mine`: what this wave has; `everyone`: positions that all rows of
   // the workgroup see.  The parts between the scheduling barriers hold matrix and vector instructions that do not
   // wait for each other, and the LDS reads of the next part; without the barriers the compiler asks for all
   // of a step's operands at once, more than there are registers.
   static __device__ __forceinline__ void run_step(const Attn& a, const Unit& u, int head, R& w, State& st, Lds& lds,
-                                                  int k, int k0, int end, const Reach& mine, int everyone) {
-    const int lane = threadIdx.x & 63, g = lane >> 4, b = (k - k0) & 1;
+                                                  int k, int end, const Reach& mine, int everyone, const int b,
+                                                  typename R::Scores& now, typename R::Scores& next) {
+    const int lane = threadIdx.x & 63, g = lane >> 4;
     const int k1 = min(k + 1, end - 1), k2 = min(k + 2, end - 1);
     C::load_k(a, head, k2, st.p2.k, threadIdx.x >> 6, st.rk);
     load_v(a, head, k1, st.p1.v, st.rv);
-    const Pages p3 = pages_of(a, u.seq, min(k + 3, end - 1));
+    const Pages e3 = entries_of(a, u.seq, min(k + 3, end - 1));
     {
       const half8_t* kf = reinterpret_cast<const half8_t*>(lds.k[b ^ 1]) + lane;
       const half8_t* vf = reinterpret_cast<const half8_t*>(lds.v[b]) + lane;
       half8_t p[kNT][2];
-      typename R::Scores next;
       constexpr int kPart = R::kFrags < 4 ? R::kFrags : 4, kParts = 4 * R::kFrags / kPart;  // operands at a time
       half8_t f[2][kPart];
 #pragma unroll
       for (int i = 0; i < kPart; ++i) f[0][i] = kf[i * 64];
-      if ((k + 1) * kStep > mine.all || !all_there(st.p0)) w.hide(a, u.w.rows, k * kStep + 16 * g, st.p0.v >= 0, st.s);
-      w.raise_max(st.s);
+      if ((k + 1) * kStep > mine.all || !all_there(st.p0)) w.hide(a, u.w.rows, k * kStep + 16 * g, st.p0.v >= 0, now);
+      w.raise_max(now);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int x = 0; x < kParts; ++x) {
@@ -858,9 +874,10 @@ struct Many {
           for (int nt = 0; nt < kNT; ++nt)
             next[nt][t] = mfma(f[x & 1][i], w.q[nt][q], q == 0 ? floatx4_t{0, 0, 0, 0} : next[nt][t]);
         }
-        w.weights(x, kParts, st.s, p);
+        w.weights(x, kParts, now, p);
         __builtin_amdgcn_sched_barrier(0);
       }
+      w.add_sums(p);
       half8_t v[2][4];  // two tiles of dims at a time
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[0][i] = vf[i * 64];
@@ -874,10 +891,6 @@ struct Many {
         for (int i = 0; i < 4; ++i) w.add_value(2 * x + i / 2, i % 2, v[x & 1][i], p);
         __builtin_amdgcn_sched_barrier(0);
       }
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) st.s[nt][t] = next[nt][t];
     }
     // values that some row of the workgroup does not see
     if (has_v() && ((k1 + 1) * kStep > everyone || !all_there(st.p1)))
@@ -889,54 +902,64 @@ struct Many {
     __syncthreads();
     st.p0 = st.p1;
     st.p1 = st.p2;
-    st.p2 = p3;
+    st.p2 = pages_of(a, min(k + 3, end - 1), e3);
   }
 
   static __device__ __forceinline__ void run_unit(const Attn& a, const Unit& u, int k0, int k1, int slot, Lds& lds) {
     const int wave = uniform((int)threadIdx.x >> 6), n = threadIdx.x & 15;
     const int row0 = wave * R::kWaveRows, head = u.minor / a.parts;
     R w;
-    w.load_q(a, u, kRows, row0);
     const Reach mine = reach_of(a, u, kRows, row0, R::kWaveRows), whole = reach_of(a, u, kRows, 0, kRows);
     const int end = min(k1, whole.steps);
+    // the page numbers are on their way while q is
+    const int last = max(end - 1, k0);
+    const Pages e0 = entries_of(a, u.seq, k0), e1 = entries_of(a, u.seq, min(k0 + 1, last)),
+                e2 = entries_of(a, u.seq, min(k0 + 2, last));
+    w.load_q(a, u, kRows, row0);
     if (k0 < end) {
       State st;
-      st.p0 = pages_of(a, u.seq, k0);
-      st.p1 = pages_of(a, u.seq, min(k0 + 1, end - 1));
-      st.p2 = pages_of(a, u.seq, min(k0 + 2, end - 1));
+      st.p0 = pages_of(a, k0, e0);
+      st.p1 = pages_of(a, min(k0 + 1, end - 1), e1);
+      st.p2 = pages_of(a, min(k0 + 2, end - 1), e2);
+      RawK<kFp4, R::kLoads> rk1;
       C::load_k(a, head, k0, st.p0.k, wave, st.rk);
       load_v(a, head, k0, st.p0.v, st.rv);
+      C::load_k(a, head, min(k0 + 1, end - 1), st.p1.k, wave, rk1);
 #pragma unroll
       for (int f = 0; f < R::kFrags; ++f) store_k(st.rk, f, lds.k[0]);
       st.nan = has_v() && ((k0 + 1) * kStep > whole.all || !all_there(st.p0)) &&
                C::clear_v(st.rv, keys_there(a, u.w.rows, k0, st.p0.v));
 #pragma unroll
       for (int i = 0; i < 2 * kMine; ++i) store_v(st.rv, i / 2, i % 2, lds.v[0]);
-      C::load_k(a, head, min(k0 + 1, end - 1), st.p1.k, wave, st.rk);
 #pragma unroll
-      for (int f = 0; f < R::kFrags; ++f) store_k(st.rk, f, lds.k[1]);
+      for (int f = 0; f < R::kFrags; ++f) store_k(rk1, f, lds.k[1]);
       __syncthreads();
       const half8_t* kf = reinterpret_cast<const half8_t*>(lds.k[0]) + (threadIdx.x & 63);
+      typename R::Scores s0, s1;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
 #pragma unroll
         for (int f = 0; f < R::kFrags; ++f)
 #pragma unroll
           for (int nt = 0; nt < kNT; ++nt)
-            st.s[nt][t] = mfma(kf[(t * R::kFrags + f) * 64], w.q[nt][f], f == 0 ? floatx4_t{0, 0, 0, 0} : st.s[nt][t]);
+            s0[nt][t] = mfma(kf[(t * R::kFrags + f) * 64], w.q[nt][f], f == 0 ? floatx4_t{0, 0, 0, 0} : s0[nt][t]);
         __builtin_amdgcn_sched_barrier(0);
       }
       __syncthreads();
-      for (int k = k0; k < end; ++k) run_step(a, u, head, w, st, lds, k, k0, end, mine, whole.all);
+      for (int k = k0;;) {
+        run_step(a, u, head, w, st, lds, k, end, mine, whole.all, 0, s0, s1);
+        if (++k >= end) break;
+        run_step(a, u, head, w, st, lds, k, end, mine, whole.all, 1, s1, s0);
+        if (++k >= end) break;
+      }
       if ((threadIdx.x & 63) == 0) lds.nan[wave] = st.nan;
       __syncthreads();
       if (lds.nan[0] | lds.nan[1] | lds.nan[2] | lds.nan[3]) C::spread_nan(a, u, w, head, k0, end, 1, whole.all);
       __syncthreads();
     }
-    w.finish_sums();
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
-      const Sink<kFp4, kD> sink(a, u, kRows, row0 + 16 * nt + n, w.m[nt], w.l[nt], slot);
+      const Sink<kFp4, kD> sink(a, u, kRows, row0 + 16 * nt + n, w.m[nt], w.total(nt), slot);
 #pragma unroll
       for (int x = 0; x < R::kTiles / 2; ++x) sink.put(x, w.o[nt][2 * x], w.o[nt][2 * x + 1]);
     }
@@ -1042,14 +1065,14 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Attn a, int rows) {
 struct Plan {
   int nt;
   bool split;
-  int rows, ranges, least;
+  int rows, ranges, least, start;
 };
 
 Plan plan_of(int64_t T, int n_seqs, int group, int d) {
   const int64_t rows = (T * group + n_seqs - 1) / n_seqs;
-  if (rows <= 16) return {1, true, 16, 512, 4};
-  if (rows <= 32) return {2, true, 32, 512, 4};
-  return {2, false, 128, 256, 4};
+  if (rows <= 16) return {1, true, 16, 512, 4, 4};
+  if (rows <= 32) return {2, true, 32, 512, 4, 4};
+  return {2, false, 128, 256, 4, 4};
 }
 
 template <bool kFp4, int kD>
@@ -1072,7 +1095,7 @@ hipError_t launch_attn_cached(const KvCache& c, const KvRows& r, const void* q, 
   const int group = hq / c.hk;
   const Plan p = plan_of(r.T, r.n_seqs, group, c.d);
   const Attn a{c,      r,       static_cast<const uint16_t*>(q), ldq, group, scale * 1.44269504088896340736f, tree,
-               static_cast<uint16_t*>(o), ldo, static_cast<float*>(workspace), p.ranges, p.least,
+               static_cast<uint16_t*>(o), ldo, static_cast<float*>(workspace), p.ranges, p.least, p.start,
                group <= p.rows ? p.rows / group : 1, group <= p.rows ? 1 : (group + p.rows - 1) / p.rows};
   if (c.fp4)
     c.d == 64 ? launch_typed<true, 64>(p, a, stream)
