@@ -135,22 +135,30 @@ __device__ __forceinline__ SeqWork seq_work(const Attn& a, int i) {
   return w;
 }
 
-// All sequences' steps; every lane of the wave gets the sum.
-__device__ __forceinline__ int64_t total_steps(const Attn& a) {
+// How the steps of all sequences are cut into ranges.
+struct Cut {
+  int64_t total, each;  // steps in all; steps of a range
+  int64_t mine;         // the lane's sequence's (of the first 64)
+};
+__device__ __forceinline__ Cut cut_of(const Attn& a) {
   const int lane = threadIdx.x & 63;
-  int64_t sum = 0;
-  for (int i = lane; i < a.r.n_seqs; i += 64) sum += seq_work(a, i).total();
+  Cut c;
+  c.mine = lane < a.r.n_seqs ? seq_work(a, lane).total() : 0;
+  int64_t sum = c.mine;
+  for (int i = lane + 64; i < a.r.n_seqs; i += 64) sum += seq_work(a, i).total();
 #pragma unroll
   for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m, 64);
-  return uniform(sum);
+  c.total = uniform(sum);
+  c.each = max((c.total + a.ranges - 1) / a.ranges, (int64_t)a.least);
+  return c;
 }
 
 // The sequence that holds step `pos` (below the total), and the steps before it.
-__device__ __forceinline__ int find_seq(const Attn& a, int64_t pos, int64_t& before) {
+__device__ __forceinline__ int find_seq(const Attn& a, const Cut& c, int64_t pos, int64_t& before) {
   const int lane = threadIdx.x & 63;
   before = 0;
   for (int i0 = 0; i0 < a.r.n_seqs; i0 += 64) {
-    const int64_t mine = i0 + lane < a.r.n_seqs ? seq_work(a, i0 + lane).total() : 0;
+    const int64_t mine = i0 == 0 ? c.mine : i0 + lane < a.r.n_seqs ? seq_work(a, i0 + lane).total() : 0;
     const int64_t upto = before + scan64(mine);
     const uint64_t past = __builtin_amdgcn_ballot_w64(upto > pos);
     if (past) {
@@ -181,10 +189,10 @@ __device__ __forceinline__ void take_seq(const Attn& a, Unit& u, int seq) {
   u.w.tiles = uniform(u.w.tiles);
 }
 
-__device__ __forceinline__ Unit unit_at(const Attn& a, int64_t pos) {
+__device__ __forceinline__ Unit unit_at(const Attn& a, const Cut& c, int64_t pos) {
   Unit u;
   int64_t before;
-  const int seq = find_seq(a, pos, before);
+  const int seq = find_seq(a, c, pos, before);
   take_seq(a, u, seq);
   const int64_t x = pos - before;
   u.tile = u.w.tiles == 1 ? 0 : last_before(u.w.tiles, [&](int r) { return u.w.before(r) <= x; });
@@ -971,12 +979,11 @@ template <class Run>
 __device__ __forceinline__ void run_range(const Attn& a, Run run) {
   // neighbouring ranges on one XCD (workgroups go round the eight in turn): they share keys
   const int w = (int)(blockIdx.x & 7) * (a.ranges / 8) + (int)(blockIdx.x >> 3);
-  const int64_t total = total_steps(a);
-  const int64_t each = max((total + a.ranges - 1) / a.ranges, (int64_t)a.least);
-  int64_t pos = w * each;
-  const int64_t end = min(pos + each, total);
+  const Cut c = cut_of(a);
+  int64_t pos = w * c.each;
+  const int64_t end = min(pos + c.each, c.total);
   if (pos >= end) return;
-  Unit u = unit_at(a, pos);
+  Unit u = unit_at(a, c, pos);
   while (true) {
     const int k0 = (int)(pos - u.start), k1 = (int)min((int64_t)u.steps, end - u.start);
     // a unit that is cut: its part behind the cut at the range's beginning, or before the one at its end
@@ -999,62 +1006,86 @@ __global__ __launch_bounds__(256) void attn_many_kernel(Attn a) {
   run_range(a, [&](const Unit& u, int k0, int k1, int slot) { Many<kFp4, kD, kNT>::run_unit(a, u, k0, k1, slot, lds); });
 }
 
-// The first range that begins inside a unit joins the unit's parts: the end of
-// the range before, its own, and those behind it up to the unit's end.  One
-// row at a time; kD / 4 lanes share a row's values, the workgroup's 1024 / kD
-// such groups its parts.
+// A unit that is cut `cuts` times has cuts + 1 parts: the end of one range, whole
+// ranges, and the beginning of the last.  Its rows are joined by the workgroups
+// of its cuts (blockIdx.x + 1 is the range that begins there; blockIdx.y shares
+// the rows out further).  kD / 4 lanes share a row's values.  With few parts each
+// such group of lanes joins a row of its own, else the groups share a row's parts.
+// (With one workgroup per row and cut, most of which found nothing to do, joining took as long as
+// the attention itself: 10.6 us of 24 for one request, 33 of 130 for 16 trees.)
 template <int kD>
 __global__ __launch_bounds__(256) void attn_join_kernel(Attn a, int rows) {
-  constexpr int kLanes = kD / 4, kGroups = 256 / kLanes;
+  constexpr int kLanes = kD / 4, kGroups = 256 / kLanes, kFewParts = 16;
   const int w = blockIdx.x + 1;
-  const int64_t total = total_steps(a);
-  const int64_t each = max((total + a.ranges - 1) / a.ranges, (int64_t)a.least);
-  const int64_t pos = w * each;
-  if (pos >= total) return;
-  const Unit u = unit_at(a, pos);
-  if (u.start == pos || u.start < pos - each) return;  // no cut here, or one before it in the same unit
-  const int last = (int)((u.start + u.steps - 1) / each);  // the range of its last step
-  const int n_parts = last - w + 2;
+  const Cut c = cut_of(a);
+  const int64_t pos = w * c.each;
+  if (pos >= c.total) return;
+  const Unit u = unit_at(a, c, pos);
+  if (u.start == pos) return;  // between two units
+  const int first = (int)(u.start / c.each) + 1, cuts = (int)((u.start + u.steps - 1) / c.each) - first + 1;
+  const int share = (w - first) * gridDim.y + blockIdx.y, shares = cuts * gridDim.y;
   const int lane = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
   const int64_t size = (int64_t)rows * (kD + 2);
-  const auto part = [&](int i) { return a.part + (i == 0 ? 2 * (int64_t)(w - 1) + 1 : 2 * (int64_t)(w + i - 1)) * size; };
-  __shared__ float tops[4], ls[kGroups];
+  const float* parts = a.part + (2 * (int64_t)first - 1) * size;  // of the range before: slot 2 (first - 1) + 1
+  const auto part = [&](int i) { return parts + (i == 0 ? 0 : 2 * i - 1) * size; };
+  const float v_gs = *a.c.v_gs;
+  const auto put = [&](const RowOf& r, const floatx4_t& o, float l) {
+    const float f = l == 0.0f ? 0.0f : v_gs / l;  // a row that sees nothing is zeros
+    u32x2_t b;
+    b[0] = pack_bf16(o[0] * f, o[1] * f);
+    b[1] = pack_bf16(o[2] * f, o[3] * f);
+    *reinterpret_cast<u32x2_t*>(a.o + (u.w.rows.row0 + r.token) * a.ldo + (int64_t)r.head * kD + 4 * lane) = b;
+  };
+  // Parts first, first + by, ... of row rho, under their own maximum.
+  const auto join = [&](int rho, int from, int by, float& m, float& l, floatx4_t& o) {
+    m = kNoMax;
+    l = 0.0f;
+    o = floatx4_t{0, 0, 0, 0};
+#pragma unroll 4
+    for (int i = from; i <= cuts; i += by) m = fmaxf(m, part(i)[rows * kD + 2 * rho]);
+#pragma unroll 4
+    for (int i = from; i <= cuts; i += by) {
+      const float* p = part(i);
+      const float f = __builtin_amdgcn_exp2f(p[rows * kD + 2 * rho] - m);
+      l += p[rows * kD + 2 * rho + 1] * f;
+      o += *reinterpret_cast<const floatx4_t*>(p + rho * kD + 4 * lane) * f;
+    }
+  };
+  float m, l;
+  floatx4_t o;
+  if (cuts < kFewParts) {
+    for (int rho = share * kGroups + grp; rho < rows; rho += shares * kGroups) {
+      const RowOf r = row_of(a, u, rows, rho);
+      if (r.token < 0) continue;
+      join(rho, 0, 1, m, l, o);
+      put(r, o, l);
+    }
+    return;
+  }
+  __shared__ float ml[2][kGroups];
   __shared__ floatx4_t sums[256];
-  for (int rho = blockIdx.y; rho < rows; rho += gridDim.y) {
+  for (int rho = share; rho < rows; rho += shares) {
     const RowOf r = row_of(a, u, rows, rho);
     if (r.token < 0) continue;
-    // the maximum, and the sum under it, over all parts
-    float m = kNoMax;
-    for (int i = threadIdx.x; i < n_parts; i += 256) m = fmaxf(m, part(i)[(int64_t)rows * kD + 2 * rho]);
-#pragma unroll
-    for (int b = 32; b > 0; b >>= 1) m = fmaxf(m, __shfl_xor(m, b, 64));
-    if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-    floatx4_t o = {0, 0, 0, 0};
-    float l = 0.0f;
-#pragma unroll 4
-    for (int i = grp; i < n_parts; i += kGroups) {
-      const float* p = part(i);
-      const float f = __builtin_amdgcn_exp2f(p[(int64_t)rows * kD + 2 * rho] - m);
-      l += p[(int64_t)rows * kD + 2 * rho + 1] * f;
-      o += *reinterpret_cast<const floatx4_t*>(p + (int64_t)rho * kD + 4 * lane) * f;
-    }
+    join(rho, grp, kGroups, m, l, o);
     sums[threadIdx.x] = o;
-    if (lane == 0) ls[grp] = l;
+    if (lane == 0) {
+      ml[0][grp] = m;
+      ml[1][grp] = l;
+    }
     __syncthreads();
     if (grp == 0) {
-      float sum = ls[0];
 #pragma unroll
-      for (int i = 1; i < kGroups; ++i) {
-        o += sums[i * kLanes + lane];
-        sum += ls[i];
+      for (int i = 1; i < kGroups; ++i) m = fmaxf(m, ml[0][i]);
+      l = 0.0f;
+      o = floatx4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) {
+        const float f = __builtin_amdgcn_exp2f(ml[0][i] - m);
+        l += ml[1][i] * f;
+        o += sums[i * kLanes + lane] * f;
       }
-      const float f = sum == 0.0f ? 0.0f : *a.c.v_gs / sum;
-      u32x2_t b;
-      b[0] = pack_bf16(o[0] * f, o[1] * f);
-      b[1] = pack_bf16(o[2] * f, o[3] * f);
-      *reinterpret_cast<u32x2_t*>(a.o + (u.w.rows.row0 + r.token) * a.ldo + (int64_t)r.head * kD + 4 * lane) = b;
+      put(r, o, l);
     }
     __syncthreads();
   }
@@ -1070,9 +1101,9 @@ struct Plan {
 
 Plan plan_of(int64_t T, int n_seqs, int group, int d) {
   const int64_t rows = (T * group + n_seqs - 1) / n_seqs;
-  if (rows <= 16) return {1, true, 16, 512, 4, 4};
-  if (rows <= 32) return {2, true, 32, 512, 4, 4};
-  return {2, false, 128, 256, 4, 4};
+  if (rows <= 16) return {1, true, 16, 256, 4, 4};
+  if (rows <= 32) return {2, true, 32, 256, 4, 4};
+  return {2, false, 128, 256, 4, 8};
 }
 
 template <bool kFp4, int kD>
@@ -1080,7 +1111,7 @@ void launch_typed(const Plan& p, const Attn& a, hipStream_t stream) {
   const auto f = p.nt == 1 ? attn_few_kernel<kFp4, kD, 1>
                            : p.split ? attn_few_kernel<kFp4, kD, 2> : attn_many_kernel<kFp4, kD, 2>;
   f<<<(unsigned)p.ranges, 256, 0, stream>>>(a);
-  attn_join_kernel<kD><<<dim3((unsigned)p.ranges - 1, 16), 256, 0, stream>>>(a, p.rows);
+  attn_join_kernel<kD><<<dim3((unsigned)p.ranges - 1, p.split ? 1 : 8), 256, 0, stream>>>(a, p.rows);
 }
 
 }  // namespace
