@@ -412,22 +412,23 @@ struct Rows {
     return has_page ? bits : 0u;
   }
 
-  // The running maximum after scores s; what it moves by is taken out of the sum and the result.
-  __device__ __forceinline__ void raise_max(const Scores& s) {
-    float top[kNT];
+  // Part x of `parts` of the largest of each row's scores that the lane has.
+  __device__ __forceinline__ void tops(int x, int parts, const Scores& s, float top[kNT]) const {
+#pragma unroll
+    for (int i = 16 * kNT * x / parts; i < 16 * kNT * (x + 1) / parts; ++i) {
+      const int nt = i / 16, e = i % 16;
+      top[nt] = e == 0 ? s[nt][0][0] : fmaxf(top[nt], s[nt][e / 4][e % 4]);
+    }
+  }
+  // The running maximum after scores with the given tops; what it moves by is taken out of the sum and the result.
+  __device__ __forceinline__ void raise_max(const float top[kNT]) {
     bool lags = false;
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-      top[nt] = fmaxf(s[nt][0][0], s[nt][0][1]);
-#pragma unroll
-      for (int e = 2; e < 16; ++e) top[nt] = fmaxf(top[nt], s[nt][e / 4][e % 4]);
-      top[nt] *= c1[nt];
-      lags = lags || top[nt] > m[nt] + kLag;
-    }
+    for (int nt = 0; nt < kNT; ++nt) lags = lags || top[nt] * c1[nt] > m[nt] + kLag;
     if (__builtin_amdgcn_ballot_w64(lags)) {
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
-        const float now = fmaxf(m[nt], max_over_g(top[nt])), f = __builtin_amdgcn_exp2f(m[nt] - now);
+        const float now = fmaxf(m[nt], max_over_g(top[nt] * c1[nt])), f = __builtin_amdgcn_exp2f(m[nt] - now);
         m[nt] = now;
         sum[nt] *= f;
 #pragma unroll
@@ -720,7 +721,9 @@ struct Few {
     load_keys(a, head, after, pg2, k);
     half8_t p[kNT][2];
     if (!whole) w.hide(a, u.w.rows, step * kStep + 16 * g, pg.v >= 0, s);
-    w.raise_max(s);
+    float top[kNT];
+    w.tops(0, 1, s, top);
+    w.raise_max(top);
     w.weights(0, 1, s, p);
     w.add_sums(p);
     bool nan = false;
@@ -846,71 +849,84 @@ struct Many {
     if constexpr (kFp4) to[((2 * d + 1) * 2 + h) * 64 + lane] = __builtin_bit_cast(u32x4_t, v1);
   }
 
-  // Step k of the unit (the b-th, modulo 2), its scores in `now`; the next step's go to `next`.  `mine`: what this wave has; `everyone`: positions that all rows of
-  // the workgroup see.  The parts between the scheduling barriers hold matrix and vector instructions that do not
-  // wait for each other, and the LDS reads of the next part; without the barriers the compiler asks for all
-  // of a step's operands at once, more than there are registers.
+  // A step's scores and the largest of each row's.
+  struct Found {
+    typename R::Scores s;
+    float top[kNT];
+  };
+
+  // Step k of the unit (the b-th, modulo 2), whose scores are in `now`; the next step's go to `next`.  `mine`: what
+  // this wave has; `everyone`: positions that all rows of the workgroup see.  The parts between the scheduling barriers
+  // hold matrix and vector instructions that do not wait for each other, and the LDS reads of the next part;
+  // without the barriers the compiler asks for all of a step's operands at once, more than there are registers.
   static __device__ __forceinline__ void run_step(const Attn& a, const Unit& u, int head, R& w, State& st, Lds& lds,
                                                   int k, int end, const Reach& mine, int everyone, const int b,
-                                                  typename R::Scores& now, typename R::Scores& next) {
-    const int lane = threadIdx.x & 63, g = lane >> 4;
-    const int k1 = min(k + 1, end - 1), k2 = min(k + 2, end - 1);
-    C::load_k(a, head, k2, st.p2.k, threadIdx.x >> 6, st.rk);
-    load_v(a, head, k1, st.p1.v, st.rv);
-    const Pages e3 = entries_of(a, u.seq, min(k + 3, end - 1));
-    {
-      const half8_t* kf = reinterpret_cast<const half8_t*>(lds.k[b ^ 1]) + lane;
-      const half8_t* vf = reinterpret_cast<const half8_t*>(lds.v[b]) + lane;
-      half8_t p[kNT][2];
-      constexpr int kPart = R::kFrags < 4 ? R::kFrags : 4, kParts = 4 * R::kFrags / kPart;  // operands at a time
-      half8_t f[2][kPart];
+                                                  Found& now, Found& next) {
+    const int lane = threadIdx.x & 63, g = lane >> 4, wave = threadIdx.x >> 6;
+    const int k1 = min(k + 1, end - 1), k2 = min(k + 2, end - 1), k3 = min(k + 3, end - 1);
+    const half8_t* kf = reinterpret_cast<const half8_t*>(lds.k[b ^ 1]) + lane;
+    const half8_t* vf = reinterpret_cast<const half8_t*>(lds.v[b]) + lane;
+    constexpr int kPart = R::kFrags < 4 ? R::kFrags : 4, kParts = 4 * R::kFrags / kPart;  // K's operands at a time
+    half8_t p[kNT][2], f[2][kPart];
 #pragma unroll
-      for (int i = 0; i < kPart; ++i) f[0][i] = kf[i * 64];
-      if ((k + 1) * kStep > mine.all || !all_there(st.p0)) w.hide(a, u.w.rows, k * kStep + 16 * g, st.p0.v >= 0, now);
-      w.raise_max(now);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int x = 0; x < kParts; ++x) {
-        if (x + 1 < kParts) {
-#pragma unroll
-          for (int i = 0; i < kPart; ++i) f[(x + 1) & 1][i] = kf[((x + 1) * kPart + i) * 64];
-        }
-#pragma unroll
-        for (int i = 0; i < kPart; ++i) {
-          const int t = (x * kPart + i) / R::kFrags, q = (x * kPart + i) % R::kFrags;
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
-            next[nt][t] = mfma(f[x & 1][i], w.q[nt][q], q == 0 ? floatx4_t{0, 0, 0, 0} : next[nt][t]);
-        }
-        w.weights(x, kParts, now, p);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      w.add_sums(p);
-      half8_t v[2][4];  // two tiles of dims at a time
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[0][i] = vf[i * 64];
-#pragma unroll
-      for (int x = 0; x < R::kTiles / 2; ++x) {
-        if (x + 1 < R::kTiles / 2) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[(x + 1) & 1][i] = vf[(4 * (x + 1) + i) * 64];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w.add_value(2 * x + i / 2, i % 2, v[x & 1][i], p);
-        __builtin_amdgcn_sched_barrier(0);
-      }
+    for (int i = 0; i < kPart; ++i) f[0][i] = kf[i * 64];
+    if ((k + 1) * kStep > mine.all || !all_there(st.p0)) {
+      w.hide(a, u.w.rows, k * kStep + 16 * g, st.p0.v >= 0, now.s);
+      w.tops(0, 1, now.s, now.top);
     }
+    w.raise_max(now.top);
+    Pages e3;
+#pragma unroll
+    for (int x = 0; x < kParts; ++x) {
+      if (x == 0) {
+        C::load_k(a, head, k2, st.p2.k, wave, st.rk);
+        load_v(a, head, k1, st.p1.v, st.rv);
+        e3 = entries_of(a, u.seq, k3);
+      }
+      if (x + 1 < kParts) {
+#pragma unroll
+        for (int i = 0; i < kPart; ++i) f[(x + 1) & 1][i] = kf[((x + 1) * kPart + i) * 64];
+      }
+#pragma unroll
+      for (int i = 0; i < kPart; ++i) {
+        const int t = (x * kPart + i) / R::kFrags, q = (x * kPart + i) % R::kFrags;
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+          next.s[nt][t] = mfma(f[x & 1][i], w.q[nt][q], q == 0 ? floatx4_t{0, 0, 0, 0} : next.s[nt][t]);
+      }
+      w.weights(x, kParts, now.s, p);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    half8_t v[2][4];  // V's operands of two tiles of dims at a time
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[0][i] = vf[i * 64];
+    w.add_sums(p);
     // values that some row of the workgroup does not see
     if (has_v() && ((k1 + 1) * kStep > everyone || !all_there(st.p1)))
       st.nan |= C::clear_v(st.rv, keys_there(a, u.w.rows, k1, st.p1.v));
+    constexpr int kPairs = R::kTiles / 2, kStores = R::kFrags + 2 * kMine;
 #pragma unroll
-    for (int f = 0; f < R::kFrags; ++f) store_k(st.rk, f, lds.k[b]);
+    for (int x = 0; x < kPairs; ++x) {
+      if (x + 1 < kPairs) {
 #pragma unroll
-    for (int i = 0; i < 2 * kMine; ++i) store_v(st.rv, i / 2, i % 2, lds.v[b ^ 1]);
+        for (int i = 0; i < 4; ++i) v[(x + 1) & 1][i] = vf[(4 * (x + 1) + i) * 64];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w.add_value(2 * x + i / 2, i % 2, v[x & 1][i], p);
+      w.tops(x, kPairs, next.s, next.top);
+#pragma unroll
+      for (int i = kStores * x / kPairs; i < kStores * (x + 1) / kPairs; ++i) {
+        if (i < R::kFrags)
+          store_k(st.rk, i, lds.k[b]);
+        else
+          store_v(st.rv, (i - R::kFrags) / 2, (i - R::kFrags) % 2, lds.v[b ^ 1]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
     __syncthreads();
     st.p0 = st.p1;
     st.p1 = st.p2;
-    st.p2 = pages_of(a, min(k + 3, end - 1), e3);
+    st.p2 = pages_of(a, k3, e3);
   }
 
   static __device__ __forceinline__ void run_unit(const Attn& a, const Unit& u, int k0, int k1, int slot, Lds& lds) {
@@ -943,16 +959,17 @@ struct Many {
       for (int f = 0; f < R::kFrags; ++f) store_k(rk1, f, lds.k[1]);
       __syncthreads();
       const half8_t* kf = reinterpret_cast<const half8_t*>(lds.k[0]) + (threadIdx.x & 63);
-      typename R::Scores s0, s1;
+      Found s0, s1;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
 #pragma unroll
         for (int f = 0; f < R::kFrags; ++f)
 #pragma unroll
           for (int nt = 0; nt < kNT; ++nt)
-            s0[nt][t] = mfma(kf[(t * R::kFrags + f) * 64], w.q[nt][f], f == 0 ? floatx4_t{0, 0, 0, 0} : s0[nt][t]);
+            s0.s[nt][t] = mfma(kf[(t * R::kFrags + f) * 64], w.q[nt][f], f == 0 ? floatx4_t{0, 0, 0, 0} : s0.s[nt][t]);
         __builtin_amdgcn_sched_barrier(0);
       }
+      w.tops(0, 1, s0.s, s0.top);
       __syncthreads();
       for (int k = k0;;) {
         run_step(a, u, head, w, st, lds, k, end, mine, whole.all, 0, s0, s1);
