@@ -28,7 +28,7 @@
 //    step's second product is done with those as zeros and a third product of
 //    what is seen and what is NaN says where the result is NaN.
 //
-// Work: the steps of all (sequence, tile of rows, head) are laid end to end and
+// Work: the keys of all (sequence, tile of rows, head) are laid end to end and
 // cut into equal ranges, one per workgroup, so that one long sequence among
 // short ones, or one request alone, still fills the GPU.  Every workgroup finds
 // its place from the lengths by itself.  A unit cut by a range's end leaves its
@@ -40,6 +40,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kStep = 64;      // keys per step
+constexpr int kRanges = 256;   // workgroups, one for each CU
 constexpr float kLag = 8.0f;   // log2: how far the running maximum may lag behind
 constexpr float kLift = 7.0f;  // log2: P is stored times 2^7
 constexpr float kNoMax = -0x1p100f;
@@ -54,10 +55,9 @@ struct Attn {
   const uint64_t* tree;
   uint16_t* o;
   int64_t ldo;
-  float* part;      // [2 x ranges][rows x (d + 2)]
-  int ranges;       // workgroups
-  int least;        // steps of a range, at least
-  int start;        // what beginning and ending a unit takes, in steps
+  float* part;      // [2 kRanges][rows x (d + 2)]
+  int least;        // keys of a range, at least
+  int start;        // what beginning and ending a unit takes, in keys
   int tokens, parts;  // tokens per tile of rows; tiles that a token's heads take
 };
 
@@ -71,38 +71,28 @@ __device__ __forceinline__ int64_t scan64(int64_t v) {  // inclusive, over the w
   return v;
 }
 
-// sum over r < n of (a r + b) / m, rounded down, for a, b >= 0.
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
-  int64_t sum = 0;
-  while (n > 0) {
-    sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const int64_t top = a * n + b;
-    n = top / m;
-    b = top % m;
-    const int64_t t = m;
-    m = a;
-    a = t;
-  }
-  return sum;
+// a / b for 0 <= a < 2^62, b > 0 and quotients below 2^52: the quotient of the doubles is off by one at most.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  int64_t q = (int64_t)((double)a / (double)b);
+  const int64_t r = a - q * b;
+  return r < 0 ? q - 1 : r >= b ? q + 1 : q;
 }
 
-// A sequence's share of the work.  Its tiles of rows (`tokens` tokens each) take
-// (first + r tokens) / 64 steps per head, r the tile: with first = context +
-// tokens + 63 that is what the tile's last token sees, rounded up (for the last
-// tile that may be a step more than there is).  Beginning and ending a unit takes as long as some
-// steps; they are counted behind its own, so that a range of many short units is no longer than others.
+// A sequence's share of the work, counted in keys.  Its tiles of rows (`tokens`
+// tokens each) count first + r slope keys per head, r the tile: what the tile's
+// last token sees (or somewhat more in the last tile), and what beginning and
+// ending a unit takes, so that a range of many short units is no longer than others.
+// Step k of a unit belongs to the range that holds its key 64 k.
 struct SeqWork {
   SeqRows rows;
   int64_t first;
   int slope;
   int tiles;
-  int minor;  // heads x parts, which share a tile's number of steps
-  __device__ __forceinline__ int64_t before(int64_t r) const {  // steps of the tiles before r
-    return minor * (r == 1 || slope == 0 ? r * (first / kStep) : floor_sum(r, kStep, slope, first));
+  int minor;  // heads x parts, which share a tile's count
+  __device__ __forceinline__ int64_t before(int64_t r) const {  // keys of the tiles before r
+    return minor * (r * first + r * (r - 1) / 2 * slope);
   }
-  __device__ __forceinline__ int64_t steps(int64_t r) const { return (first + r * slope) / kStep; }
+  __device__ __forceinline__ int64_t keys(int64_t r) const { return first + r * slope; }
   __device__ __forceinline__ int64_t total() const { return before(tiles); }
 };
 
@@ -123,21 +113,20 @@ __device__ __forceinline__ SeqWork seq_work(const Attn& a, int i) {
   w.rows = seq_rows(a.r, i);
   const int most = cache_rows(a);
   if (a.tree) {
-    w.first = min(max(w.rows.kv, 1), most) + kStep - 1;
+    w.first = min(max(w.rows.kv, 1), most) + a.start;
     w.slope = 0;
   } else {
-    w.first = min(max((int64_t)w.rows.kv - w.rows.n, (int64_t)0), (int64_t)most) + a.tokens + kStep - 1;
+    w.first = min(max((int64_t)w.rows.kv - w.rows.n, (int64_t)0), (int64_t)most) + a.tokens + a.start;
     w.slope = a.tokens;
   }
-  w.first += a.start * kStep;
   w.tiles = (w.rows.n + a.tokens - 1) / a.tokens;
   w.minor = a.c.hk * a.parts;
   return w;
 }
 
-// How the steps of all sequences are cut into ranges.
+// How the keys of all sequences are cut into ranges.
 struct Cut {
-  int64_t total, each;  // steps in all; steps of a range
+  int64_t total, each;  // keys in all; keys of a range
   int64_t mine;         // the lane's sequence's (of the first 64)
 };
 __device__ __forceinline__ Cut cut_of(const Attn& a) {
@@ -149,11 +138,11 @@ __device__ __forceinline__ Cut cut_of(const Attn& a) {
 #pragma unroll
   for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m, 64);
   c.total = uniform(sum);
-  c.each = max((c.total + a.ranges - 1) / a.ranges, (int64_t)a.least);
+  c.each = max((c.total + kRanges - 1) / kRanges, (int64_t)a.least);
   return c;
 }
 
-// The sequence that holds step `pos` (below the total), and the steps before it.
+// The sequence that holds key `pos` (below the total), and the keys before it.
 __device__ __forceinline__ int find_seq(const Attn& a, const Cut& c, int64_t pos, int64_t& before) {
   const int lane = threadIdx.x & 63;
   before = 0;
@@ -175,8 +164,8 @@ __device__ __forceinline__ int find_seq(const Attn& a, const Cut& c, int64_t pos
 struct Unit {
   int seq;
   SeqWork w;
-  int tile, minor, steps;
-  int64_t start;  // its first step among all
+  int tile, minor;
+  int64_t start, keys;  // its place among all keys
 };
 
 __device__ __forceinline__ void take_seq(const Attn& a, Unit& u, int seq) {
@@ -196,16 +185,16 @@ __device__ __forceinline__ Unit unit_at(const Attn& a, const Cut& c, int64_t pos
   take_seq(a, u, seq);
   const int64_t x = pos - before;
   u.tile = u.w.tiles == 1 ? 0 : last_before(u.w.tiles, [&](int r) { return u.w.before(r) <= x; });
-  u.steps = uniform((int)u.w.steps(u.tile));
+  u.keys = uniform(u.w.keys(u.tile));
   const int64_t y = uniform(x - u.w.before(u.tile));
-  u.minor = uniform((int)(y / u.steps));
-  u.start = pos - (y - (int64_t)u.minor * u.steps);
+  u.minor = uniform((int)quotient(y, u.keys));
+  u.start = pos - (y - (int64_t)u.minor * u.keys);
   return u;
 }
 
 // The unit behind u (there is one).
 __device__ __forceinline__ void next_unit(const Attn& a, Unit& u) {
-  u.start += u.steps;
+  u.start += u.keys;
   if (++u.minor < u.w.minor) return;
   u.minor = 0;
   if (++u.tile == u.w.tiles) {
@@ -213,7 +202,7 @@ __device__ __forceinline__ void next_unit(const Attn& a, Unit& u) {
     do take_seq(a, u, u.seq + 1);
     while (u.w.tiles == 0 && u.seq + 1 < a.r.n_seqs);
   }
-  u.steps = uniform((int)u.w.steps(u.tile));
+  u.keys = uniform(u.w.keys(u.tile));
 }
 
 // Row `rho` of a unit's tile: its token and query head, or token -1.
@@ -991,21 +980,22 @@ struct Many {
   }
 };
 
-// The workgroup's range of steps, unit by unit: run(unit, first step, step behind the last, slot of its part or -1).
+// The workgroup's range, unit by unit: run(unit, first step, step behind the last, slot of its part or -1).
 template <class Run>
 __device__ __forceinline__ void run_range(const Attn& a, Run run) {
   // neighbouring ranges on one XCD (workgroups go round the eight in turn): they share keys
-  const int w = (int)(blockIdx.x & 7) * (a.ranges / 8) + (int)(blockIdx.x >> 3);
+  const int w = (int)(blockIdx.x & 7) * (kRanges / 8) + (int)(blockIdx.x >> 3);
   const Cut c = cut_of(a);
   int64_t pos = w * c.each;
   const int64_t end = min(pos + c.each, c.total);
   if (pos >= end) return;
   Unit u = unit_at(a, c, pos);
   while (true) {
-    const int k0 = (int)(pos - u.start), k1 = (int)min((int64_t)u.steps, end - u.start);
+    const int64_t from = pos - u.start, to = min(u.keys, end - u.start);
     // a unit that is cut: its part behind the cut at the range's beginning, or before the one at its end
-    run(u, k0, k1, k0 > 0 ? 2 * w : k1 < u.steps ? 2 * w + 1 : -1);
-    pos = u.start + k1;
+    const int slot = from > 0 ? 2 * w : to < u.keys ? 2 * w + 1 : -1;
+    run(u, (int)((from + kStep - 1) / kStep), (int)((to + kStep - 1) / kStep), slot);
+    pos = u.start + to;
     if (pos >= end) return;
     next_unit(a, u);
   }
@@ -1039,7 +1029,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Attn a, int rows) {
   if (pos >= c.total) return;
   const Unit u = unit_at(a, c, pos);
   if (u.start == pos) return;  // between two units
-  const int first = (int)(u.start / c.each) + 1, cuts = (int)((u.start + u.steps - 1) / c.each) - first + 1;
+  const int first = (int)quotient(u.start, c.each) + 1, cuts = (int)quotient(u.start + u.keys - 1, c.each) - first + 1;
   const int share = (w - first) * gridDim.y + blockIdx.y, shares = cuts * gridDim.y;
   const int lane = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
   const int64_t size = (int64_t)rows * (kD + 2);
@@ -1113,29 +1103,29 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Attn a, int rows) {
 struct Plan {
   int nt;
   bool split;
-  int rows, ranges, least, start;
+  int rows, least, start;
 };
 
 Plan plan_of(int64_t T, int n_seqs, int group, int d) {
   const int64_t rows = (T * group + n_seqs - 1) / n_seqs;
-  if (rows <= 16) return {1, true, 16, 256, 4, 4};
-  if (rows <= 32) return {2, true, 32, 256, 4, 4};
-  return {2, false, 128, 256, 4, 8};
+  if (rows <= 16) return {1, true, 16, 256, 256};
+  if (rows <= 32) return {2, true, 32, 256, 256};
+  return {2, false, 128, 256, 512};
 }
 
 template <bool kFp4, int kD>
 void launch_typed(const Plan& p, const Attn& a, hipStream_t stream) {
   const auto f = p.nt == 1 ? attn_few_kernel<kFp4, kD, 1>
                            : p.split ? attn_few_kernel<kFp4, kD, 2> : attn_many_kernel<kFp4, kD, 2>;
-  f<<<(unsigned)p.ranges, 256, 0, stream>>>(a);
-  attn_join_kernel<kD><<<dim3((unsigned)p.ranges - 1, p.split ? 1 : 8), 256, 0, stream>>>(a, p.rows);
+  f<<<kRanges, 256, 0, stream>>>(a);
+  attn_join_kernel<kD><<<dim3(kRanges - 1, p.split ? 1 : 8), 256, 0, stream>>>(a, p.rows);
 }
 
 }  // namespace
 
 size_t attn_cached_workspace_bytes(int64_t T, int n_seqs, int hq, int hk, int d) {
   const Plan p = plan_of(T, n_seqs, hq / hk, d);
-  return (size_t)2 * p.ranges * p.rows * (d + 2) * sizeof(float);
+  return (size_t)2 * kRanges * p.rows * (d + 2) * sizeof(float);
 }
 
 hipError_t launch_attn_cached(const KvCache& c, const KvRows& r, const void* q, int64_t ldq, int hq, float scale,
@@ -1143,7 +1133,7 @@ hipError_t launch_attn_cached(const KvCache& c, const KvRows& r, const void* q, 
   const int group = hq / c.hk;
   const Plan p = plan_of(r.T, r.n_seqs, group, c.d);
   const Attn a{c,      r,       static_cast<const uint16_t*>(q), ldq, group, scale * 1.44269504088896340736f, tree,
-               static_cast<uint16_t*>(o), ldo, static_cast<float*>(workspace), p.ranges, p.least, p.start,
+               static_cast<uint16_t*>(o), ldo, static_cast<float*>(workspace), p.least, p.start,
                group <= p.rows ? p.rows / group : 1, group <= p.rows ? 1 : (group + p.rows - 1) / p.rows};
   if (c.fp4)
     c.d == 64 ? launch_typed<true, 64>(p, a, stream)
