@@ -1,0 +1,150 @@
+// Attention over the cache for few rows per sequence (nvfp4_attn.h): decode, small trees.
+#include "nvfp4_attn_rows.h"
+
+namespace nvfp4 {
+namespace {
+
+// Few rows per sequence (decode): the workgroup's four waves have the same 16
+// kNT rows and every fourth step each, straight from memory to the matrix
+// instructions; their results are joined through LDS.
+template <bool kFp4, int kD, int kNT>
+struct Few {
+  using R = Rows<kFp4, kD, kNT>;
+  using C = Codes<kFp4, kD>;
+  static constexpr int kRows = R::kWaveRows;
+  struct Lds {
+    floatx4_t sums[4 * 8 * 64];
+    float ml[4][kNT][16][2];
+  };
+  struct Keys {
+    RawK<kFp4, R::kLoads> t[4];
+  };
+  static __device__ __forceinline__ void load_keys(const Attn& a, int head, int step, const Pages& pg, Keys& k) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) C::load_k(a, head, step, pg.k, t, k.t[t]);
+  }
+
+  // Step `step`, whose keys are in k; those of `after` (its pages pg2) are asked for.  `whole`: every row sees all of it.
+  // Returns whether NaN was taken out of its values.
+  static __device__ __forceinline__ bool run_step(const Attn& a, const Unit& u, int head, R& w, Keys& k, int step,
+                                                  const Pages& pg, bool whole, int after, const Pages& pg2) {
+    const int g = (threadIdx.x & 63) >> 4;
+    RawV<kFp4, R::kVLoads> rv;
+    C::load_v(a, head, step, pg.v, 0, 1, rv);
+    typename R::Scores s;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int f = 0; f < R::kFrags; ++f) {
+        const half8_t k8 = C::key(k.t[t], f);
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) s[nt][t] = mfma(k8, w.q[nt][f], f == 0 ? floatx4_t{0, 0, 0, 0} : s[nt][t]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    load_keys(a, head, after, pg2, k);
+    half8_t p[kNT][2];
+    if (!whole) w.hide(a, u.w.rows, step * kStep + 16 * g, pg.v >= 0, s);
+    float top[kNT];
+    w.tops(0, 1, s, top);
+    w.raise_max(top);
+    w.weights(0, 1, s, p);
+    w.add_sums(p);
+    bool nan = false;
+    if (!whole) nan = C::clear_v(rv, keys_there(a, u.w.rows, step * kStep + 16 * g, pg.v));
+#pragma unroll
+    for (int d = 0; d < R::kVLoads; ++d) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        half8_t v0, v1;
+        C::value(rv, d, h, v0, v1);
+        w.add_value(kFp4 ? 2 * d : d, h, v0, p);
+        if constexpr (kFp4) w.add_value(2 * d + 1, h, v1, p);
+      }
+      if (d % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+    }
+    return nan;
+  }
+
+  static __device__ __forceinline__ void run_unit(const Attn& a, const Unit& u, int k0, int k1, int slot, Lds& lds) {
+    const int wave = uniform((int)threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15;
+    const int head = u.minor / a.parts;
+    R w;
+    const Reach reach = reach_of(a, u, kRows, 0, kRows);
+    const int end = min(k1, reach.steps);
+    int k = k0 + wave;
+    const int last = max(end - 1, k0);
+    const Pages e0 = entries_of(a, u.seq, min(k, last)), e1 = entries_of(a, u.seq, min(k + 4, last));
+    w.load_q(a, u, kRows, 0);
+    bool nan = false;
+    if (k < end) {
+      Keys keys;
+      Pages pg = pages_of(a, k, e0), pg2 = pages_of(a, min(k + 4, end - 1), e1);
+      load_keys(a, head, k, pg, keys);
+      for (; k < end; k += 4) {
+        const Pages e = entries_of(a, u.seq, min(k + 8, end - 1));
+        nan |= run_step(a, u, head, w, keys, k, pg, (k + 1) * kStep <= reach.all && all_there(pg), min(k + 4, end - 1), pg2);
+        pg = pg2;
+        pg2 = pages_of(a, min(k + 8, end - 1), e);
+      }
+    }
+    if (nan) C::spread_nan(a, u, w, head, k0 + wave, end, 4, reach.all);
+    // four waves' results of the same rows: four pairs of tiles at a time, each wave adds up one pair
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      if (lane < 16) {
+        lds.ml[wave][nt][n][0] = w.m[nt];
+        lds.ml[wave][nt][n][1] = w.total(nt);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      float m = kNoMax, l = 0.0f;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) m = fmaxf(m, lds.ml[v][nt][n][0]);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) l += lds.ml[v][nt][n][1] * __builtin_amdgcn_exp2f(lds.ml[v][nt][n][0] - m);
+      const float f = __builtin_amdgcn_exp2f(w.m[nt] - m);
+      const Sink<kFp4, kD> sink(a, u, kRows, 16 * nt + n, m, l, slot);
+      constexpr int kPairs = R::kTiles / 2, kAtOnce = kPairs < 4 ? kPairs : 4;
+#pragma unroll
+      for (int x0 = 0; x0 < kPairs; x0 += kAtOnce) {
+#pragma unroll
+        for (int i = 0; i < 2 * kAtOnce; ++i) lds.sums[(wave * 8 + i) * 64 + lane] = w.o[nt][2 * x0 + i] * f;
+        __syncthreads();
+        if (wave < kAtOnce) {
+          floatx4_t t[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) t[i] += lds.sums[(v * 8 + 2 * wave + i) * 64 + lane];
+          sink.put(x0 + wave, t[0], t[1]);
+        }
+        __syncthreads();
+      }
+    }
+  }
+};
+
+template <bool kFp4, int kD, int kNT>
+__global__ __launch_bounds__(256) void attn_few_kernel(Attn a) {
+  __shared__ typename Few<kFp4, kD, kNT>::Lds lds;
+  run_range(a, [&](const Unit& u, int k0, int k1, int slot) { Few<kFp4, kD, kNT>::run_unit(a, u, k0, k1, slot, lds); });
+}
+
+template <bool kFp4, int kD>
+void launch_typed(const Attn& a, int nt, hipStream_t stream) {
+  (nt == 1 ? attn_few_kernel<kFp4, kD, 1> : attn_few_kernel<kFp4, kD, 2>)<<<kRanges, 256, 0, stream>>>(a);
+}
+
+}  // namespace
+
+void launch_attn_few(const Attn& a, int nt, hipStream_t stream) {
+  const int d = a.c.d;
+  const auto f = a.c.fp4 ? (d == 64 ? launch_typed<true, 64> : d == 128 ? launch_typed<true, 128> : launch_typed<true, 256>)
+                         : (d == 64 ? launch_typed<false, 64> : d == 128 ? launch_typed<false, 128> : launch_typed<false, 256>);
+  f(a, nt, stream);
+}
+
+}  // namespace nvfp4
