@@ -50,9 +50,10 @@ struct Attn {
   const uint64_t* tree;
   uint16_t* o;
   int64_t ldo;
-  float* part;      // [2 kRanges][rows x (d + 2)]
+  float* part;      // [2 ranges][rows x (d + 2)]
   int least;        // keys of a range, at least
   int start;        // what beginning and ending a unit takes, in keys
+  int ranges;       // workgroups, a multiple of 8
   int tokens, parts;  // tokens per tile of rows; tiles that a token's heads take
 };
 
@@ -63,7 +64,7 @@ void launch_attn_many(const Attn& a, hipStream_t stream);
 namespace {
 
 constexpr int kStep = 64;      // keys per step
-constexpr int kRanges = 256;   // workgroups, one for each CU
+constexpr int kCus = 256;
 constexpr float kLag = 8.0f;   // log2: how far the running maximum may lag behind
 constexpr float kLift = 7.0f;  // log2: P is stored times 2^7
 constexpr float kNoMax = -0x1p100f;
@@ -145,7 +146,7 @@ __device__ __forceinline__ Cut cut_of(const Attn& a) {
 #pragma unroll
   for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m, 64);
   c.total = uniform(sum);
-  c.each = max((c.total + kRanges - 1) / kRanges, (int64_t)a.least);
+  c.each = max((c.total + a.ranges - 1) / a.ranges, (int64_t)a.least);
   return c;
 }
 
@@ -326,7 +327,7 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t x) { return ((x & 0x7F7F7
 template <class Run>
 __device__ __forceinline__ void run_range(const Attn& a, Run run) {
   // neighbouring ranges on one XCD (workgroups go round the eight in turn): they share keys
-  const int w = (int)(blockIdx.x & 7) * (kRanges / 8) + (int)(blockIdx.x >> 3);
+  const int w = (int)(blockIdx.x & 7) * (a.ranges / 8) + (int)(blockIdx.x >> 3);
   const Cut c = cut_of(a);
   int64_t pos = w * c.each;
   const int64_t end = min(pos + c.each, c.total);

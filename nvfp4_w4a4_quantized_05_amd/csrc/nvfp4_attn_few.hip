@@ -128,14 +128,14 @@ struct Few {
 };
 
 template <bool kFp4, int kD, int kNT>
-__global__ __launch_bounds__(256) void attn_few_kernel(Attn a) {
+__global__ __launch_bounds__(256, kD < 256 ? 2 : 1) void attn_few_kernel(Attn a) {
   __shared__ typename Few<kFp4, kD, kNT>::Lds lds;
   run_range(a, [&](const Unit& u, int k0, int k1, int slot) { Few<kFp4, kD, kNT>::run_unit(a, u, k0, k1, slot, lds); });
 }
 
 template <bool kFp4, int kD>
 void launch_typed(const Attn& a, int nt, hipStream_t stream) {
-  (nt == 1 ? attn_few_kernel<kFp4, kD, 1> : attn_few_kernel<kFp4, kD, 2>)<<<kRanges, 256, 0, stream>>>(a);
+  (nt == 1 ? attn_few_kernel<kFp4, kD, 1> : attn_few_kernel<kFp4, kD, 2>)<<<a.ranges, 256, 0, stream>>>(a);
 }
 
 }  // namespace

@@ -141,7 +141,7 @@ struct Many {
     const Pages e0 = entries_of(a, u.seq, k0), e1 = entries_of(a, u.seq, min(k0 + 1, last)),
                 e2 = entries_of(a, u.seq, min(k0 + 2, last));
     w.load_q(a, u, kRows, row0);
-    w.pin_q();
+    if constexpr (kD != 128) w.pin_q();
     if (k0 < end) {
       State st;
       st.p0 = pages_of(a, k0, e0);
@@ -194,7 +194,7 @@ struct Many {
 };
 
 template <bool kFp4, int kD, int kNT>
-__global__ __launch_bounds__(256) void attn_many_kernel(Attn a) {
+__global__ __launch_bounds__(256, kD == 128 ? 2 : 1) void attn_many_kernel(Attn a) {
   __shared__ typename Many<kFp4, kD, kNT>::Lds lds;
   run_range(a, [&](const Unit& u, int k0, int k1, int slot) { Many<kFp4, kD, kNT>::run_unit(a, u, k0, k1, slot, lds); });
 }
@@ -205,7 +205,7 @@ void launch_attn_many(const Attn& a, hipStream_t stream) {
   const int d = a.c.d;
   const auto f = a.c.fp4 ? (d == 64 ? attn_many_kernel<true, 64, 2> : d == 128 ? attn_many_kernel<true, 128, 2> : attn_many_kernel<true, 256, 2>)
                          : (d == 64 ? attn_many_kernel<false, 64, 2> : d == 128 ? attn_many_kernel<false, 128, 2> : attn_many_kernel<false, 256, 2>);
-  f<<<kRanges, 256, 0, stream>>>(a);
+  f<<<a.ranges, 256, 0, stream>>>(a);
 }
 
 }  // namespace nvfp4
