@@ -135,26 +135,33 @@ __device__ __forceinline__ Place place_of(const KvRows& r, int b) {
   return p;
 }
 
+// The place that workgroup x takes.  Workgroups go round the eight XCDs in turn; eight neighbouring places go to one of
+// them, since up to eight (a page of 128 rows) share lines of V, which one L2 then puts together.
+__device__ __forceinline__ int place_index() {
+  const int x = blockIdx.x, base = x & ~63;
+  return base + 64 <= (int)gridDim.x ? base + (x & 7) * 8 + (x >> 3 & 7) : x;
+}
+
 // Threads: kD, thread (j, l) = (t / (kD / 16), t % (kD / 16)): position j of
 // the block, dims 16 l .. 16 l + 15.  blockIdx: block, head, K or V.
 template <bool kFp4, bool kBf16, int kD>
 __global__ __launch_bounds__(kD) void kv_write_kernel(KvCache c, KvRows r, const void* k, int64_t ldk, const void* v,
                                                       int64_t ldv) {
   constexpr int kL = kD / 16;
-  const Place p = place_of(r, blockIdx.x);
+  const Place p = place_of(r, place_index());
   if (p.lo >= p.hi) return;
-  const int page = page_of(r, c, p.seq, p.pos0);
-  if (page < 0) return;  // before position 0 too
   const int h = blockIdx.y, t = threadIdx.x, j = t / kL, l = t % kL;
+  const bool is_v = blockIdx.z, live = p.pos0 + j >= p.lo && p.pos0 + j < p.hi;
+  float x[16];
+  if (live) load16<kBf16>(is_v ? v : k, (p.row0 + j) * (is_v ? ldv : ldk) + h * kD + 16 * l, x);
+  const int page = page_of(r, c, p.seq, p.pos0);  // while the row is on its way
+  if (page < 0) return;  // before position 0 too
   const int ps = 1 << c.page_shift, row = (int)p.pos0 & (ps - 1);
   const int64_t unit = (int64_t)page * c.hk + h;  // (page, head)
-  const bool is_v = blockIdx.z, live = p.pos0 + j >= p.lo && p.pos0 + j < p.hi;
   const float g = is_v ? *c.v_gs : *c.k_gs;
   u32x4_t w = {0, 0, 0, 0};
   uint32_t scale = 0;
   if (live) {
-    float x[16];
-    load16<kBf16>(is_v ? v : k, (p.row0 + j) * (is_v ? ldv : ldk) + h * kD + 16 * l, x);
     if constexpr (kFp4) {
       uint32_t w0, w1;
       scale = quantize_block(x, g, __builtin_amdgcn_rcpf(6.0f * g), w0, w1);
@@ -234,7 +241,7 @@ __device__ __forceinline__ void decode16(const u32x4_t& w, uint32_t scale, float
 template <bool kFp4, bool kBf16, int kD>
 __global__ __launch_bounds__(kD) void kv_read_kernel(KvCache c, KvRows r, void* k, int64_t ldk, void* v, int64_t ldv) {
   constexpr int kL = kD / 16, kCodes = code_bytes<kFp4>(kD), kLines = kCodes + (kFp4 ? kL : 0), kPer = kCodes / kL;
-  const Place p = place_of(r, blockIdx.x);
+  const Place p = place_of(r, place_index());
   if (p.lo >= p.hi) return;
   const int page = page_of(r, c, p.seq, p.pos0);
   const int h = blockIdx.y, t = threadIdx.x, j = t / kL, l = t % kL;
