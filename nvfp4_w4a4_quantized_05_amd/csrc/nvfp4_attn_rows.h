@@ -93,7 +93,9 @@ struct Rows {
                           ldexpf(finite ? __uint_as_float(x[f][i] & 0xFFFF0000u) : 0.0f, shift));
         q[nt][f] = __builtin_bit_cast(half8_t, h);
       }
-      c1[nt] = ldexpf(a.scale * k_gs, -shift);
+      // Kept normal and below 2^64: under the one all scores are 0 to any precision (but -inf times it is -inf still),
+      // over the other any two that differ at all are further apart than weights can be (and none reaches kNoMax).
+      c1[nt] = fminf(fmaxf(ldexpf(a.scale * k_gs, -shift), 0x1p-126f), 0x1p64f);
       fate[nt] = finite ? 1.0f : __builtin_nanf("");  // what is not finite in q makes the row NaN if it sees anything
       m[nt] = kNoMax;
       sum[nt] = floatx4_t{0, 0, 0, 0};

@@ -5,10 +5,13 @@ size d: a score is a sum of d products in fp32, off by at most d u B with B =
 max_p scale sum |q_i k_pi|, its factor (scale, tensor scale, log2 e, each
 rounded) by 4 u B, the subtraction of the maximum and the exponential by 2 u
 (B + 16): weights are off by E = 2 (d + 8) u (B + 16) of themselves, and by half
-an fp16 step, 2^-11, where they enter the second product.  Their sum and the
-second product's are fp32 sums of n terms, n u each, and a few rescalings; the
-result is divided once.  So |o - O| <= (2^-11 + E + (2 n + 64) u) sum w |v|, and
-rounding to bf16 adds half a step: 2^-8 |O|.  Values of q below 2^-31 of a row's
+an fp16 step, at most 2^-11, since the second product and their own sum take them
+in fp16.  With w (1 + e_p), |e_p| <= e = 2^-11, in both, o = O + sum w e_p (v_p - O)
+/ sum w (1 + e_p): off by at most e / (1 - e) (sum w |v| + |O|), where 2^-11 / (1 -
+2^-11) < 1.001 2^-11.  The two sums are fp32 sums of n terms, n u each, and a few
+rescalings; the result is divided once.  So |o - O| <= 1.001 2^-11 (sum w |v| +
+|O|) + (E + (2 n + 64) u) sum w |v|, and rounding to bf16 adds half a step: 2^-8
+|O|.  Values of q below 2^-31 of a row's
 largest are flushed: 2^-30 B, inside E.
   A weight that is subnormal in fp16 is off by half a step of those, 2^-25.  It is
 stored times 2^7 over the running maximum, which is some key's weight, so that is
@@ -30,7 +33,8 @@ BF = torch.bfloat16
 
 def tolerance(O, mag, big, flat, d, n):
     e = 2 * (d + 8) * U * (big[..., None] + 16)
-    return (2.0 ** -11 + e + (2 * n + 64) * U) * mag + 2.0 ** -8 * np.abs(O) + 2.0 ** -32 * flat + 2.0 ** -126
+    fp16 = 1.001 * 2.0 ** -11 * (mag + np.abs(O))
+    return fp16 + (e + (2 * n + 64) * U) * mag + 2.0 ** -8 * np.abs(O) + 2.0 ** -32 * flat + 2.0 ** -126
 
 
 def tree_masks(rng, n, skip_self=False):
@@ -220,6 +224,83 @@ def test_sizes_of_queries(fmt, factor):
         qt *= factor
 
     run(Paged(fmt, 1, 64, 16, kv, 10), [3, 2], kv, 4, seed=9, q_edit=edit, scale=0.125 / factor if factor > 1e20 else None)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("rows", [[1, 1], [3, 9], [70, 40]])
+def test_queries_of_zeros_and_ends_of_bf16(fmt, rows):
+    """Rows of zeros (all keys weigh the same), of bf16's smallest and largest values, with a small tensor scale."""
+    kv = [130, 77]
+    print(f"[attn] {fmt} zeros {rows}", flush=True)
+
+    def edit(qt):
+        qt[:, :64] = 0
+        qt[:, 64:128] = 2.0 ** -133   # bf16's smallest subnormal
+        qt[:, 128:192] = torch.sign(qt[:, 128:192].float()).to(BF) * 3.3e38
+
+    paged = Paged(fmt, 1, 64, 16, kv, 13, k_gs=1e-6)
+    paged.gs["k"] = np.float32(1e-6)
+    run(paged, rows, kv, 4, seed=10, q_edit=edit)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("rows", [1, 5, 90])
+def test_places_past_32_bits(fmt, rows):
+    """Pages whose keys and values lie behind 4 GiB give the bits that the same pages give at the beginning."""
+    dev = need_gpu()
+    hk, d, page, hq, n = 4, 256, 64, 8, 400
+    w = d if fmt == "fp8" else d // 2
+    n_pages = 2 ** 32 // (hk * page * w) + 40
+    need = -(-n // page)
+    print(f"[attn] {fmt} {n_pages} pages", flush=True)
+    scales = {}
+    if fmt == "nvfp4":
+        scales = {"k_scales": torch.empty((n_pages, hk, page, d // 16), dtype=torch.uint8, device=dev),
+                  "v_scales": torch.empty((n_pages, hk, d // 16, page), dtype=torch.uint8, device=dev)}
+    gs = torch.full((2,), 0.01, device=dev)
+    cache = nv.KvCache(torch.empty((n_pages, hk, page, w), dtype=torch.uint8, device=dev),
+                       torch.empty((n_pages, hk, w, page), dtype=torch.uint8, device=dev), gs[:1], gs[1:], format=fmt, **scales)
+    far = torch.arange(n_pages - need, n_pages, dtype=torch.int32, device=dev)[None].contiguous()
+    near = torch.arange(need, dtype=torch.int32, device=dev).flip(0)[None].contiguous()
+    g = torch.Generator(device=dev).manual_seed(3)
+    k = torch.randn((n, hk * d), generator=g, device=dev).to(BF)
+    v = torch.randn((n, hk * d), generator=g, device=dev).to(BF)
+    q = torch.randn((rows, hq * d), generator=g, device=dev).to(BF)
+    lens, cu, cu_n = i32([n], dev), i32([0, rows], dev), i32([0, n], dev)
+    got = []
+    for table in (far, near):
+        nv.kv_cache_write(k, v, cache, table, lens, cu_n)
+        back = nv.kv_cache_read(cache, table, lens, cu_n, rows=n)
+        got.append((nv.attn_cached(q, cache, table, lens, cu, n_q_heads=hq), *back))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert not torch.equal(got[0][1], torch.zeros_like(got[0][1])) and bool(torch.isfinite(got[0][0].float()).all())
+    at = torch.arange(n, device=dev)
+    assert torch.equal(cache.k[far[0, at // page].long(), :, at % page], cache.k[near[0, at // page].long(), :, at % page])
+
+
+def test_two_calls_at_once_and_shared_pages():
+    """Calls on two streams, on sequences that share the pages of a common beginning, give what each gives alone."""
+    dev = need_gpu()
+    hk, d, hq, page = 2, 128, 8, 64
+    kv = [5000, 4200]
+    paged = Paged("nvfp4", hk, d, page, kv, 14)
+    cache, table = paged.to(dev)
+    table = table.contiguous()
+    table[1, :50] = table[0, :50]
+    g = torch.Generator(device=dev).manual_seed(4)
+    print("[attn] two streams", flush=True)
+    calls = []
+    for rows in (1, 60):
+        q = torch.randn((2 * rows, hq * d), generator=g, device=dev).to(BF)
+        calls.append((q, cache, table, i32(kv, dev), i32([0, rows, 2 * rows], dev)))
+    alone = [nv.attn_cached(*c, n_q_heads=hq) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(3):
+        both = [nv.attn_cached(*c, n_q_heads=hq, stream=s) for c, s in zip(calls, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(alone, both))
 
 
 def test_rounding_to_bf16_costs_most():
