@@ -13,7 +13,7 @@ struct Few {
   using C = Codes<kFp4, kD>;
   static constexpr int kRows = R::kWaveRows;
   struct Lds {
-    floatx4_t sums[4 * 8 * 64];
+    floatx4_t sums[4 * R::kTiles * 64];
     float ml[4][kNT][16][2];
   };
   struct Keys {
@@ -89,7 +89,7 @@ struct Few {
       }
     }
     if (nan) C::spread_nan(a, u, w, head, k0 + wave, end, 4, reach.all);
-    // four waves' results of the same rows: four pairs of tiles at a time, each wave adds up one pair
+    // four waves' results of the same rows; each wave adds up every fourth pair of tiles
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
       if (lane < 16) {
@@ -107,22 +107,22 @@ struct Few {
       for (int v = 0; v < 4; ++v) l += lds.ml[v][nt][n][1] * __builtin_amdgcn_exp2f(lds.ml[v][nt][n][0] - m);
       const float f = __builtin_amdgcn_exp2f(w.m[nt] - m);
       const Sink<kFp4, kD> sink(a, u, kRows, 16 * nt + n, m, l, slot);
-      constexpr int kPairs = R::kTiles / 2, kAtOnce = kPairs < 4 ? kPairs : 4;
+      constexpr int kPairs = R::kTiles / 2;
 #pragma unroll
-      for (int x0 = 0; x0 < kPairs; x0 += kAtOnce) {
+      for (int i = 0; i < R::kTiles; ++i) lds.sums[(wave * R::kTiles + i) * 64 + lane] = w.o[nt][i] * f;
+      __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 2 * kAtOnce; ++i) lds.sums[(wave * 8 + i) * 64 + lane] = w.o[nt][2 * x0 + i] * f;
-        __syncthreads();
-        if (wave < kAtOnce) {
-          floatx4_t t[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+      for (int x0 = 0; x0 < kPairs; x0 += 4) {
+        const int x = x0 + wave;
+        if (x >= kPairs) break;
+        floatx4_t t[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
+        for (int v = 0; v < 4; ++v)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) t[i] += lds.sums[(v * 8 + 2 * wave + i) * 64 + lane];
-          sink.put(x0 + wave, t[0], t[1]);
-        }
-        __syncthreads();
+          for (int i = 0; i < 2; ++i) t[i] += lds.sums[(v * R::kTiles + 2 * x + i) * 64 + lane];
+        sink.put(x, t[0], t[1]);
       }
+      __syncthreads();
     }
   }
 };
