@@ -53,12 +53,12 @@ struct Attn {
   float* part;      // [2 ranges][rows x (d + 2)]
   int least;        // keys of a range, at least
   int start;        // what beginning and ending a unit takes, in keys
-  int ranges;       // workgroups, a multiple of 8
+  int ranges;       // of workgroups, or (solo) of waves; a multiple of 32
   int tokens, parts;  // tokens per tile of rows; tiles that a token's heads take
 };
 
 // The kernels for few and for many rows per sequence (16 nt and 128 rows of a tile).
-void launch_attn_few(const Attn& a, int nt, hipStream_t stream);
+void launch_attn_few(const Attn& a, int nt, bool solo, hipStream_t stream);
 void launch_attn_many(const Attn& a, hipStream_t stream);
 
 namespace {
@@ -323,11 +323,12 @@ __device__ __forceinline__ uint32_t kept_bytes(int keep, int w) {
 // Top bit of every byte that is a NaN code.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t x) { return ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
-// The workgroup's range, unit by unit: run(unit, first step, step behind the last, slot of its part or -1).
+// Neighbouring ranges go to one XCD (workgroups go round the eight in turn): they share keys.
+__device__ __forceinline__ int xcd_order(int block, int blocks) { return (block & 7) * (blocks / 8) + (block >> 3); }
+
+// Range w, unit by unit: run(unit, first step, step behind the last, slot of its part or -1).
 template <class Run>
-__device__ __forceinline__ void run_range(const Attn& a, Run run) {
-  // neighbouring ranges on one XCD (workgroups go round the eight in turn): they share keys
-  const int w = (int)(blockIdx.x & 7) * (a.ranges / 8) + (int)(blockIdx.x >> 3);
+__device__ __forceinline__ void run_range(const Attn& a, int w, Run run) {
   const Cut c = cut_of(a);
   int64_t pos = w * c.each;
   const int64_t end = min(pos + c.each, c.total);

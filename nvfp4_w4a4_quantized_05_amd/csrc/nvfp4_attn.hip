@@ -93,38 +93,45 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Attn a, int rows) {
 // key/value head, which the host knows, so that no kernel waits for lengths.
 struct Plan {
   int nt;
-  bool split;
+  bool split, solo;
   int rows, least, start, ranges;
 };
 
-Plan plan_of(int64_t T, int n_seqs, int group, int d) {
+Plan plan_of(int64_t T, int n_seqs, int hk, int group, int d) {
   // Two workgroups on a CU where their registers allow it, so that one multiplies while the other waits or evaluates
   // its softmax.  One -> two, us: seven chunks of 1100 rows behind 6000, d 128, 2360 -> 2045 (NVFP4), 2228 -> 1990 (E4M3);
   // d 64, 2015 -> 1473, 1621 -> 1259; 64 tokens behind 8200, d 128, 84.0 -> 74.3, 108.1 -> 103.5; trees of 5, d 128,
   // 55 -> 42; two tokens behind 131072, E4M3, d 128, 105.2 -> 106.6, the only one that lost.
   const int ranges = d < 256 ? 2 * kCus : kCus;
   const int64_t rows = (T * group + n_seqs - 1) / n_seqs;
-  if (rows <= 16) return {1, true, 16, 256, 256, ranges};
-  if (rows <= 32) return {2, true, 32, 256, 256, ranges};
-  return {2, false, 128, 256, 512, ranges};
+  if (rows <= 32) {
+    const int nt = rows <= 16 ? 1 : 2;
+    // A range for every wave, where there are units enough (a quarter as many with 32 rows, whose sums are joined for
+    // longer).  Workgroups -> waves, us, E4M3, d 256, 4 heads: 64 tokens behind 1000, 53.0 -> 38.0, behind 3000, 100 -> 89,
+    // behind 100, 29.2 -> 30.5, behind 8200, 195 -> 195; 600 behind 200, 141 -> 102; trees of 5, 16 of them behind 4100,
+    // 80 -> 57, behind 500, 39 -> 49.  Fewer lose: 16 tokens behind 1000, 24.0 -> 28.8, one behind 1000, 19.3 -> 26.1.
+    const bool solo = (int64_t)n_seqs * hk * (nt == 1 ? 1 : 4) >= ranges;
+    return {nt, true, solo, 16 * nt, 256, solo ? 192 : 256, solo ? 4 * ranges : ranges};
+  }
+  return {2, false, false, 128, 256, 512, ranges};
 }
 
 }  // namespace
 
 size_t attn_cached_workspace_bytes(int64_t T, int n_seqs, int hq, int hk, int d) {
-  const Plan p = plan_of(T, n_seqs, hq / hk, d);
+  const Plan p = plan_of(T, n_seqs, hk, hq / hk, d);
   return (size_t)2 * p.ranges * p.rows * (d + 2) * sizeof(float);
 }
 
 hipError_t launch_attn_cached(const KvCache& c, const KvRows& r, const void* q, int64_t ldq, int hq, float scale,
                               const uint64_t* tree, void* o, int64_t ldo, void* workspace, hipStream_t stream) {
   const int group = hq / c.hk;
-  const Plan p = plan_of(r.T, r.n_seqs, group, c.d);
+  const Plan p = plan_of(r.T, r.n_seqs, c.hk, group, c.d);
   const Attn a{c,      r,       static_cast<const uint16_t*>(q), ldq, group, scale * 1.44269504088896340736f, tree,
                static_cast<uint16_t*>(o), ldo, static_cast<float*>(workspace), p.least, p.start, p.ranges,
                group <= p.rows ? p.rows / group : 1, group <= p.rows ? 1 : (group + p.rows - 1) / p.rows};
   if (p.split)
-    launch_attn_few(a, p.nt, stream);
+    launch_attn_few(a, p.nt, p.solo, stream);
   else
     launch_attn_many(a, stream);
   const auto join = c.d == 64 ? attn_join_kernel<64> : c.d == 128 ? attn_join_kernel<128> : attn_join_kernel<256>;

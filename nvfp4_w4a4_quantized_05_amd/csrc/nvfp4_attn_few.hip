@@ -7,13 +7,19 @@ namespace {
 // Few rows per sequence (decode): the workgroup's four waves have the same 16
 // kNT rows and every fourth step each, straight from memory to the matrix
 // instructions; their results are joined through LDS.
-template <bool kFp4, int kD, int kNT>
+//
+// Where there are units enough, every wave has a range of its own instead (solo):
+// a unit takes as long to begin and to end (6 us, waiting for lengths, page
+// numbers, queries and the first keys, one after the other) as 200 keys take, and
+// so four of them are begun at once.
+template <bool kFp4, int kD, int kNT, bool kSolo>
 struct Few {
+  static constexpr int kBy = kSolo ? 1 : 4;  // steps from a wave's step to its next
   using R = Rows<kFp4, kD, kNT>;
   using C = Codes<kFp4, kD>;
   static constexpr int kRows = R::kWaveRows;
   struct Lds {
-    floatx4_t sums[4 * R::kTiles * 64];
+    floatx4_t sums[kSolo ? 1 : 4 * R::kTiles * 64];
     float ml[4][kNT][16][2];
   };
   struct Keys {
@@ -67,28 +73,37 @@ struct Few {
   }
 
   static __device__ __forceinline__ void run_unit(const Attn& a, const Unit& u, int k0, int k1, int slot, Lds& lds) {
-    const int wave = uniform((int)threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15;
+    const int wave = kSolo ? 0 : uniform((int)threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15;
     const int head = u.minor / a.parts;
     R w;
     const Reach reach = reach_of(a, u, kRows, 0, kRows);
     const int end = min(k1, reach.steps);
     int k = k0 + wave;
     const int last = max(end - 1, k0);
-    const Pages e0 = entries_of(a, u.seq, min(k, last)), e1 = entries_of(a, u.seq, min(k + 4, last));
+    const Pages e0 = entries_of(a, u.seq, min(k, last)), e1 = entries_of(a, u.seq, min(k + kBy, last));
     w.load_q(a, u, kRows, 0);
     bool nan = false;
     if (k < end) {
       Keys keys;
-      Pages pg = pages_of(a, k, e0), pg2 = pages_of(a, min(k + 4, end - 1), e1);
+      Pages pg = pages_of(a, k, e0), pg2 = pages_of(a, min(k + kBy, end - 1), e1);
       load_keys(a, head, k, pg, keys);
-      for (; k < end; k += 4) {
-        const Pages e = entries_of(a, u.seq, min(k + 8, end - 1));
-        nan |= run_step(a, u, head, w, keys, k, pg, (k + 1) * kStep <= reach.all && all_there(pg), min(k + 4, end - 1), pg2);
+      for (; k < end; k += kBy) {
+        const Pages e = entries_of(a, u.seq, min(k + 2 * kBy, end - 1));
+        nan |= run_step(a, u, head, w, keys, k, pg, (k + 1) * kStep <= reach.all && all_there(pg), min(k + kBy, end - 1), pg2);
         pg = pg2;
-        pg2 = pages_of(a, min(k + 8, end - 1), e);
+        pg2 = pages_of(a, min(k + 2 * kBy, end - 1), e);
       }
     }
-    if (nan) C::spread_nan(a, u, w, head, k0 + wave, end, 4, reach.all);
+    if (nan) C::spread_nan(a, u, w, head, k0 + wave, end, kBy, reach.all);
+    if constexpr (kSolo) {
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        const Sink<kFp4, kD> sink(a, u, kRows, 16 * nt + n, w.m[nt], w.total(nt), slot);
+#pragma unroll
+        for (int x = 0; x < R::kTiles / 2; ++x) sink.put(x, w.o[nt][2 * x], w.o[nt][2 * x + 1]);
+      }
+      return;
+    }
     // four waves' results of the same rows; each wave adds up every fourth pair of tiles
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
@@ -127,24 +142,30 @@ struct Few {
   }
 };
 
-template <bool kFp4, int kD, int kNT>
+template <bool kFp4, int kD, int kNT, bool kSolo>
 __global__ __launch_bounds__(256, kD < 256 ? 2 : 1) void attn_few_kernel(Attn a) {
-  __shared__ typename Few<kFp4, kD, kNT>::Lds lds;
-  run_range(a, [&](const Unit& u, int k0, int k1, int slot) { Few<kFp4, kD, kNT>::run_unit(a, u, k0, k1, slot, lds); });
+  using F = Few<kFp4, kD, kNT, kSolo>;
+  __shared__ typename F::Lds lds;
+  const int block = xcd_order(blockIdx.x, gridDim.x);
+  run_range(a, kSolo ? 4 * block + uniform((int)threadIdx.x >> 6) : block,
+            [&](const Unit& u, int k0, int k1, int slot) { F::run_unit(a, u, k0, k1, slot, lds); });
 }
 
 template <bool kFp4, int kD>
-void launch_typed(const Attn& a, int nt, hipStream_t stream) {
-  (nt == 1 ? attn_few_kernel<kFp4, kD, 1> : attn_few_kernel<kFp4, kD, 2>)<<<a.ranges, 256, 0, stream>>>(a);
+void launch_typed(const Attn& a, int nt, bool solo, hipStream_t stream) {
+  if (solo)
+    (nt == 1 ? attn_few_kernel<kFp4, kD, 1, true> : attn_few_kernel<kFp4, kD, 2, true>)<<<a.ranges / 4, 256, 0, stream>>>(a);
+  else
+    (nt == 1 ? attn_few_kernel<kFp4, kD, 1, false> : attn_few_kernel<kFp4, kD, 2, false>)<<<a.ranges, 256, 0, stream>>>(a);
 }
 
 }  // namespace
 
-void launch_attn_few(const Attn& a, int nt, hipStream_t stream) {
+void launch_attn_few(const Attn& a, int nt, bool solo, hipStream_t stream) {
   const int d = a.c.d;
   const auto f = a.c.fp4 ? (d == 64 ? launch_typed<true, 64> : d == 128 ? launch_typed<true, 128> : launch_typed<true, 256>)
                          : (d == 64 ? launch_typed<false, 64> : d == 128 ? launch_typed<false, 128> : launch_typed<false, 256>);
-  f(a, nt, stream);
+  f(a, nt, solo, stream);
 }
 
 }  // namespace nvfp4

@@ -196,7 +196,7 @@ struct Many {
 template <bool kFp4, int kD, int kNT>
 __global__ __launch_bounds__(256, kD == 128 ? 2 : 1) void attn_many_kernel(Attn a) {
   __shared__ typename Many<kFp4, kD, kNT>::Lds lds;
-  run_range(a, [&](const Unit& u, int k0, int k1, int slot) { Many<kFp4, kD, kNT>::run_unit(a, u, k0, k1, slot, lds); });
+  run_range(a, xcd_order(blockIdx.x, a.ranges), [&](const Unit& u, int k0, int k1, int slot) { Many<kFp4, kD, kNT>::run_unit(a, u, k0, k1, slot, lds); });
 }
 
 }  // namespace

@@ -151,6 +151,25 @@ def test_many_sequences():
     run(Paged("fp8", 1, 64, 16, kv, 6), rows, kv, 2, seed=5)
 
 
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("hq,hk,d,page", [(16, 8, 256, 64), (32, 8, 128, 16), (8, 8, 64, 32)])
+@pytest.mark.parametrize("kind", ["one", "rows", "tree"])
+def test_batches_of_short_sequences(fmt, hq, hk, d, page, kind):
+    """So many sequences that every wave has a range of its own; some are empty, one is cut over many waves."""
+    kv = [LENS[i % len(LENS)] for i in range(72)]
+    kv[40] = 3000
+    n = {"one": 1, "rows": 20 * hk // hq, "tree": 5}[kind]
+    rows = [1] * 72 if kind == "one" else [min(k, n) if i % 9 else 0 for i, k in enumerate(kv)]
+    rng = np.random.default_rng(8)
+    tree = [tree_masks(rng, x) for x in rows] if kind == "tree" else None
+    print(f"[attn] {fmt} 72 sequences {kind} {hq}/{hk}x{d}", flush=True)
+    paged = Paged(fmt, hk, d, page, kv, d + 1)
+    paged.set_nan("v", 40, 2999, 3, 5)
+    paged.set_nan("v", 40, 1500, 1, 9)
+    paged.set_nan("k", 41, 0, 2, 3)
+    run(paged, rows, kv, hq, seed=11, tree=tree, cu=kind != "one")
+
+
 @pytest.mark.parametrize("rows,kv", [([1, 1, 1], [0, -5, 3]), ([4, 30, 6], [2, 0, -3]), ([3, 2, 70], [3, 1, 12])])
 @pytest.mark.parametrize("tree", [False, True])
 def test_lengths_below_the_rows(rows, kv, tree):
