@@ -46,5 +46,5 @@ def test_distances_around_matrix_instructions(listing):
 
 def test_scratch_memory(listing):
     sizes = [int(x) for x in re.findall(r"\.private_segment_fixed_size:\s+(\d+)", listing)]
-    assert len(sizes) == 6 or len(sizes) == 12
+    assert sizes and len(sizes) % 6 == 0  # three head sizes, two formats
     assert max(sizes) <= 128
