@@ -616,7 +616,8 @@ NVFP4_API nvfp4_status_t nvfp4_rmsnorm_gated(const void* o, int32_t o_dtype, int
  *     % page_size of it.  A position below 0, past max_pages, or whose page is
  *     outside 0 .. n_pages - 1 is not there: nothing is written to it, it reads
  *     as zeros, and no row sees it.  (An unused request of a padded batch has
- *     kv_lens 0 or pages -1.)  The host reads none of these arrays.
+ *     kv_lens 0 or pages -1.)  Attention stops at position 2^31 - 128.  The host
+ *     reads none of these arrays.
  *   - The cache (nvfp4_kv_cache_t, a HOST struct of DEVICE arrays, all 16-byte
  *     aligned), for `n_kv_heads` heads of 64, 128 or 256 dims and pages of 16,
  *     32, ... or 1024 positions.  The tensor scales k_gs and v_gs (DEVICE, one
