@@ -135,37 +135,49 @@ __device__ __forceinline__ SeqWork seq_work(const Attn& a, int i) {
 // How the keys of all sequences are cut into ranges.
 struct Cut {
   int64_t total, each;  // keys in all; keys of a range
-  int64_t mine;         // the lane's sequence's (of the first 64)
+  int64_t mine;         // of the lane's share of the sequences, `chunk` neighbours
+  int chunk;
 };
 __device__ __forceinline__ Cut cut_of(const Attn& a) {
   const int lane = threadIdx.x & 63;
   Cut c;
-  c.mine = lane < a.r.n_seqs ? seq_work(a, lane).total() : 0;
+  c.chunk = (a.r.n_seqs + 63) / 64;
+  c.mine = lane * c.chunk < a.r.n_seqs ? seq_work(a, lane * c.chunk).total() : 0;
+  if (c.chunk > 1) {
+#pragma unroll 4
+    for (int i = lane * c.chunk + 1; i < min((lane + 1) * c.chunk, a.r.n_seqs); ++i) c.mine += seq_work(a, i).total();
+  }
   int64_t sum = c.mine;
-  for (int i = lane + 64; i < a.r.n_seqs; i += 64) sum += seq_work(a, i).total();
+  if (a.r.n_seqs > 1) {
 #pragma unroll
-  for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m, 64);
+    for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m, 64);
+  }
   c.total = uniform(sum);
   c.each = max((c.total + a.ranges - 1) / a.ranges, (int64_t)a.least);
   return c;
 }
 
+// The first lane whose keys, in order behind `before`, go past `pos`, and the keys before it; -1 where none does.
+__device__ __forceinline__ int find_lane(int64_t mine, int64_t pos, int64_t& before) {
+  const int64_t upto = before + scan64(mine);
+  const uint64_t past = __builtin_amdgcn_ballot_w64(upto > pos);
+  const int at = past ? __builtin_ctzll(past) : 63;
+  before = uniform(__shfl(past ? upto - mine : upto, at, 64));
+  return past ? uniform(at) : -1;
+}
+
 // The sequence that holds key `pos` (below the total), and the keys before it.
 __device__ __forceinline__ int find_seq(const Attn& a, const Cut& c, int64_t pos, int64_t& before) {
-  const int lane = threadIdx.x & 63;
   before = 0;
-  for (int i0 = 0; i0 < a.r.n_seqs; i0 += 64) {
-    const int64_t mine = i0 == 0 ? c.mine : i0 + lane < a.r.n_seqs ? seq_work(a, i0 + lane).total() : 0;
-    const int64_t upto = before + scan64(mine);
-    const uint64_t past = __builtin_amdgcn_ballot_w64(upto > pos);
-    if (past) {
-      const int at = __builtin_ctzll(past);
-      before = uniform(__shfl(upto - mine, at, 64));
-      return uniform(i0 + at);
-    }
-    before = uniform(__shfl(upto, 63, 64));
+  if (a.r.n_seqs == 1) return 0;
+  const int first = max(find_lane(c.mine, pos, before), 0) * c.chunk, end = min(first + c.chunk, a.r.n_seqs);
+  if (c.chunk == 1) return first;
+  for (int i0 = first; i0 < end; i0 += 64) {
+    const int i = i0 + (threadIdx.x & 63);
+    const int at = find_lane(i < end ? seq_work(a, i).total() : 0, pos, before);
+    if (at >= 0) return i0 + at;
   }
-  return 0;
+  return end - 1;
 }
 
 // A unit of work: one tile of one sequence's rows and one (head, part).

@@ -151,6 +151,22 @@ def test_many_sequences():
     run(Paged("fp8", 1, 64, 16, kv, 6), rows, kv, 2, seed=5)
 
 
+@pytest.mark.parametrize("n", [65, 129, 4500])
+@pytest.mark.parametrize("kind", ["one", "rows"])
+def test_places_of_many_sequences(n, kind):
+    """More sequences than a wave has lanes, and than lanes' shares of 64: runs of empty ones, a long one in the middle."""
+    rng = np.random.default_rng(n)
+    kv = [int(x) for x in rng.choice([0, 1, 3, 20, 70], n)]
+    kv[n // 3:n // 3 + n // 5] = [0] * (n // 5)
+    kv[n // 2] = 2000
+    rows = [1] * n if kind == "one" else [int(min(x, rng.integers(0, 3))) for x in kv]
+    if kind == "rows":
+        rows[n // 2 + 1] = kv[n // 2 + 1] = 150
+        rows[0] = rows[-1] = 0
+    print(f"[attn] {n} sequences {kind}", flush=True)
+    run(Paged("fp8", 1, 64, 16, kv, 15), rows, kv, 2, seed=12, cu=kind != "one")
+
+
 @pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
 @pytest.mark.parametrize("hq,hk,d,page", [(16, 8, 256, 64), (32, 8, 128, 16), (8, 8, 64, 32)])
 @pytest.mark.parametrize("kind", ["one", "rows", "tree"])
