@@ -40,6 +40,16 @@
 
 namespace nvfp4 {
 
+// The unit that a range's beginning cuts, for the joining of its parts.
+struct Joint {
+  int64_t row0;  // of its sequence
+  int n;         // its sequence's rows
+  int tile, minor;
+  int first;     // the first range that begins within it
+  int cuts;      // ranges that do; 0: this one begins between two units, or not at all
+  int unused;
+};
+
 struct Attn {
   KvCache c;
   KvRows r;
@@ -51,6 +61,7 @@ struct Attn {
   uint16_t* o;
   int64_t ldo;
   float* part;      // [2 ranges][rows x (d + 2)]
+  Joint* joints;    // [ranges]
   int least;        // keys of a range, at least
   int start;        // what beginning and ending a unit takes, in keys
   int ranges;       // of workgroups, or (solo) of waves; a multiple of 32
@@ -229,12 +240,15 @@ __device__ __forceinline__ void next_unit(const Attn& a, Unit& u) {
 struct RowOf {
   int token, head;
 };
-__device__ __forceinline__ RowOf row_of(const Attn& a, const Unit& u, int rows, int rho) {
+__device__ __forceinline__ RowOf row_of(const Attn& a, int tile, int minor, int n, int rows, int rho) {
   const int wide = a.parts == 1 ? a.group : rows;
-  const int h = (u.minor % a.parts) * rows + rho % wide;
-  const int token = u.tile * a.tokens + rho / wide;
-  const bool real = rho < a.tokens * wide && h < a.group && token < u.w.rows.n;
-  return {real ? token : -1, (u.minor / a.parts) * a.group + h};
+  const int h = (minor % a.parts) * rows + rho % wide;
+  const int token = tile * a.tokens + rho / wide;
+  const bool real = rho < a.tokens * wide && h < a.group && token < n;
+  return {real ? token : -1, (minor / a.parts) * a.group + h};
+}
+__device__ __forceinline__ RowOf row_of(const Attn& a, const Unit& u, int rows, int rho) {
+  return row_of(a, u.tile, u.minor, u.w.rows.n, rows, rho);
 }
 
 // Positions that a row of token j sees at the most: [0, limit).
@@ -344,8 +358,17 @@ __device__ __forceinline__ void run_range(const Attn& a, int w, Run run) {
   const Cut c = cut_of(a);
   int64_t pos = w * c.each;
   const int64_t end = min(pos + c.each, c.total);
-  if (pos >= end) return;
+  const bool one = (threadIdx.x & 63) == 0;
+  if (pos >= end) {
+    if (one) a.joints[w].cuts = 0;
+    return;
+  }
   Unit u = unit_at(a, c, pos);
+  if (one) {
+    const int first = (int)quotient(u.start, c.each) + 1;
+    const int cuts = u.start == pos ? 0 : (int)quotient(u.start + u.keys - 1, c.each) - first + 1;
+    a.joints[w] = {u.w.rows.row0, u.w.rows.n, u.tile, u.minor, first, cuts, 0};
+  }
   while (true) {
     const int64_t from = pos - u.start, to = min(u.keys, end - u.start);
     // a unit that is cut: its part behind the cut at the range's beginning, or before the one at its end

@@ -6,21 +6,19 @@ namespace {
 
 // A unit that is cut `cuts` times has cuts + 1 parts: the end of one range, whole
 // ranges, and the beginning of the last.  Its rows are joined by the workgroups
-// of its cuts (blockIdx.x + 1 is the range that begins there; blockIdx.y shares
+// of its cuts (blockIdx.x + 1 is the range that begins there and has said so; blockIdx.y shares
 // the rows out further).  kD / 4 lanes share a row's values.  With few parts each
 // such group of lanes joins a row of its own, else the groups share a row's parts.
 // (With one workgroup per row and cut, most of which found nothing to do, joining took as long as
-// the attention itself: 10.6 us of 24 for one request, 33 of 130 for 16 trees.)
+// the attention itself: 10.6 us of 24 for one request, 33 of 130 for 16 trees.  Finding the cut units
+// from the lengths once more, as the attention does, 8 us of 92 for 600 tokens behind 200.)
 template <int kD>
 __global__ __launch_bounds__(256) void attn_join_kernel(Attn a, int rows) {
   constexpr int kLanes = kD / 4, kGroups = 256 / kLanes, kFewParts = 16;
   const int w = blockIdx.x + 1;
-  const Cut c = cut_of(a);
-  const int64_t pos = w * c.each;
-  if (pos >= c.total) return;
-  const Unit u = unit_at(a, c, pos);
-  if (u.start == pos) return;  // between two units
-  const int first = (int)quotient(u.start, c.each) + 1, cuts = (int)quotient(u.start + u.keys - 1, c.each) - first + 1;
+  const Joint u = a.joints[w];
+  if (u.cuts == 0) return;
+  const int first = u.first, cuts = u.cuts;
   const int share = (w - first) * gridDim.y + blockIdx.y, shares = cuts * gridDim.y;
   const int lane = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
   const int64_t size = (int64_t)rows * (kD + 2);
@@ -32,7 +30,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Attn a, int rows) {
     u32x2_t b;
     b[0] = pack_bf16(o[0] * f, o[1] * f);
     b[1] = pack_bf16(o[2] * f, o[3] * f);
-    *reinterpret_cast<u32x2_t*>(a.o + (u.w.rows.row0 + r.token) * a.ldo + (int64_t)r.head * kD + 4 * lane) = b;
+    *reinterpret_cast<u32x2_t*>(a.o + (u.row0 + r.token) * a.ldo + (int64_t)r.head * kD + 4 * lane) = b;
   };
   // Parts first, first + by, ... of row rho, under their own maximum.
   const auto join = [&](int rho, int from, int by, float& m, float& l, floatx4_t& o) {
@@ -53,7 +51,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Attn a, int rows) {
   floatx4_t o;
   if (cuts < kFewParts) {
     for (int rho = share * kGroups + grp; rho < rows; rho += shares * kGroups) {
-      const RowOf r = row_of(a, u, rows, rho);
+      const RowOf r = row_of(a, u.tile, u.minor, u.n, rows, rho);
       if (r.token < 0) continue;
       join(rho, 0, 1, m, l, o);
       put(r, o, l);
@@ -63,7 +61,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Attn a, int rows) {
   __shared__ float ml[2][kGroups];
   __shared__ floatx4_t sums[256];
   for (int rho = share; rho < rows; rho += shares) {
-    const RowOf r = row_of(a, u, rows, rho);
+    const RowOf r = row_of(a, u.tile, u.minor, u.n, rows, rho);
     if (r.token < 0) continue;
     join(rho, grp, kGroups, m, l, o);
     sums[threadIdx.x] = o;
@@ -109,18 +107,21 @@ Plan plan_of(int64_t T, int n_seqs, int hk, int group, int d) {
     // A range for every wave, where there are units enough (a quarter as many with 32 rows, whose sums are joined for
     // longer).  Workgroups -> waves, us, E4M3, d 256, 4 heads: 64 tokens behind 1000, 53.0 -> 38.0, behind 3000, 100 -> 89,
     // behind 100, 29.2 -> 30.5, behind 8200, 195 -> 195; 600 behind 200, 141 -> 102; trees of 5, 16 of them behind 4100,
-    // 80 -> 57, behind 500, 39 -> 49.  Fewer lose: 16 tokens behind 1000, 24.0 -> 28.8, one behind 1000, 19.3 -> 26.1.
+    // 80 -> 57, behind 500, 39 -> 49 (before the search for a place and the joining got shorter: 600 behind 200 now 84).
+    // Fewer lose: 16 tokens behind 1000, 24.0 -> 28.8, one behind 1000, 19.3 -> 26.1.
     const bool solo = (int64_t)n_seqs * hk * (nt == 1 ? 1 : 4) >= ranges;
     return {nt, true, solo, 16 * nt, 256, solo ? 192 : 256, solo ? 4 * ranges : ranges};
   }
   return {2, false, false, 128, 256, 512, ranges};
 }
 
+size_t part_bytes(const Plan& p, int d) { return (size_t)2 * p.ranges * p.rows * (d + 2) * sizeof(float); }
+
 }  // namespace
 
 size_t attn_cached_workspace_bytes(int64_t T, int n_seqs, int hq, int hk, int d) {
   const Plan p = plan_of(T, n_seqs, hk, hq / hk, d);
-  return (size_t)2 * p.ranges * p.rows * (d + 2) * sizeof(float);
+  return part_bytes(p, d) + p.ranges * sizeof(Joint);
 }
 
 hipError_t launch_attn_cached(const KvCache& c, const KvRows& r, const void* q, int64_t ldq, int hq, float scale,
@@ -128,14 +129,15 @@ hipError_t launch_attn_cached(const KvCache& c, const KvRows& r, const void* q, 
   const int group = hq / c.hk;
   const Plan p = plan_of(r.T, r.n_seqs, c.hk, group, c.d);
   const Attn a{c,      r,       static_cast<const uint16_t*>(q), ldq, group, scale * 1.44269504088896340736f, tree,
-               static_cast<uint16_t*>(o), ldo, static_cast<float*>(workspace), p.least, p.start, p.ranges,
+               static_cast<uint16_t*>(o), ldo, static_cast<float*>(workspace),
+               reinterpret_cast<Joint*>(static_cast<char*>(workspace) + part_bytes(p, c.d)), p.least, p.start, p.ranges,
                group <= p.rows ? p.rows / group : 1, group <= p.rows ? 1 : (group + p.rows - 1) / p.rows};
   if (p.split)
     launch_attn_few(a, p.nt, p.solo, stream);
   else
     launch_attn_many(a, stream);
   const auto join = c.d == 64 ? attn_join_kernel<64> : c.d == 128 ? attn_join_kernel<128> : attn_join_kernel<256>;
-  join<<<dim3(p.ranges - 1, p.split ? 1 : 8), 256, 0, stream>>>(a, p.rows);
+  join<<<dim3(p.ranges - 1, p.split ? 2 * p.nt : 8), 256, 0, stream>>>(a, p.rows);
   return hipGetLastError();
 }
 
