@@ -24,16 +24,16 @@
 //    2^8 behind, its largest value is 2^15, and values are normal down to
 //    2^-21 of the row's maximum, below that off by 2^-32 of it.
 //  * What is not finite in V reaches only the rows that see it: where a step
-//    hides keys from some rows, a lane looks for NaN codes, and if there are any the
-//    step's second product is done with those as zeros and a third product of
-//    what is seen and what is NaN says where the result is NaN.
+//    hides keys from some rows, NaN codes are taken as zeros, and if there were
+//    any, the unit's steps of that kind are read once more behind the last one and a
+//    product of what is seen and what is NaN says which results are NaN.
 //
 // Work: the keys of all (sequence, tile of rows, head) are laid end to end and
-// cut into equal ranges, one per workgroup, so that one long sequence among
-// short ones, or one request alone, still fills the GPU.  Every workgroup finds
-// its place from the lengths by itself.  A unit cut by a range's end leaves its
-// maximum, sum and unscaled result in the workspace, and a second kernel joins
-// them, in order.
+// cut into equal ranges, one per workgroup (or per wave, for many short
+// sequences), so that one long sequence among short ones, or one request alone,
+// still fills the GPU.  Every range finds its place from the lengths by itself.  A
+// unit cut by a range's end leaves its maximum, sum and unscaled result in the
+// workspace, and a second kernel joins them, in order.
 #pragma once
 
 #include "nvfp4_kv.h"

@@ -151,6 +151,24 @@ def test_many_sequences():
     run(Paged("fp8", 1, 64, 16, kv, 6), rows, kv, 2, seed=5)
 
 
+@pytest.mark.parametrize("hq,hk", [(4096, 1), (4096, 4096), (2050, 2)])
+def test_most_heads(hq, hk):
+    """The largest numbers of heads: one key/value head for all, and one for each."""
+    kv = [70, 5]
+    print(f"[attn] {hq}/{hk} heads", flush=True)
+    run(Paged("fp8", hk, 64, 16, kv, 16), [1, 2], kv, hq, seed=13)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+def test_one_draft_each(fmt):
+    """A tree mask without row numbers: one draft per request, which sees itself or not."""
+    kv = [1, 1, 40, 200, 0, 65]
+    tree = [np.array([m], dtype=np.int64) for m in (1, 0, 1, 0, 1, -1)]
+    print(f"[attn] {fmt} one draft each", flush=True)
+    o = run(Paged(fmt, 2, 128, 32, kv, 17), [1] * 6, kv, 8, seed=14, tree=tree, cu=False)
+    assert np.all(host_f32(o)[[1, 4]] == 0.0)
+
+
 @pytest.mark.parametrize("n", [65, 129, 4500])
 @pytest.mark.parametrize("kind", ["one", "rows"])
 def test_places_of_many_sequences(n, kind):
