@@ -1,0 +1,114 @@
+"""The attention layer's kernels built for the host (calls.cpp), and calls of them on guarded arrays."""
+import ctypes
+import os
+import re
+import shutil
+import subprocess
+
+import numpy as np
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+ROOT = os.path.dirname(os.path.dirname(HERE))
+CSRC = os.path.join(ROOT, "nvfp4_w4a4_quantized_05_amd", "csrc")
+SOURCES = ("nvfp4_attn.hip", "nvfp4_attn_few.hip", "nvfp4_attn_many.hip", "nvfp4_rope.hip")
+
+# kernel<<<grid, block, 0, stream>>>(  ->  host_launch(kernel, grid, block,
+_LAUNCH = re.compile(r"(\w+(?:<[^<>()\n]*>)?|(?<=  )\([^;\n]*\))<<<(.+?), (\w[\w.]*|\d+), 0, stream>>>\(")
+
+
+def clang():
+    """A clang++ that builds for this machine, or None: the vector types of the sources are clang's."""
+    for c in ("/opt/rocm/llvm/bin/clang++", shutil.which("clang++")):
+        if c and os.path.exists(c):
+            return c
+    return None
+
+
+def build(out_dir):
+    """Compile the kernels' sources for the host; returns the library."""
+    for name in os.listdir(CSRC):
+        with open(os.path.join(CSRC, name)) as f:
+            text = f.read()
+        if name in SOURCES:
+            text, n = _LAUNCH.subn(r"host_launch(\1, \2, \3, ", text)
+            assert n and "<<<" not in text, f"{name}: a launch that is written otherwise"
+        with open(os.path.join(out_dir, name), "w") as f:
+            f.write(re.sub(r'asm volatile\("" : "\+a".*', ";", text))  # a hint about registers
+    lib = os.path.join(out_dir, "libhost.so")
+    cmd = [clang(), "-x", "c++", "-std=c++17", "-O1", "-march=native", "-ffp-contract=off", "-shared", "-fPIC", "-w", "-I", HERE,
+           "-I", os.path.join(ROOT, "include"), "-I", str(out_dir), os.path.join(HERE, "calls.cpp"), "-o", lib]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr[-3000:]
+    lib = ctypes.CDLL(lib)
+    vp, i32, i64, f32, u64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_uint64
+    lib.host_alloc.argtypes, lib.host_alloc.restype = [u64, i32], vp
+    lib.host_attn_workspace.argtypes, lib.host_attn_workspace.restype = [i64, i32, i32, i32, i32], u64
+    lib.host_attn_plan.argtypes, lib.host_attn_plan.restype = [i64, i32, i32, i32, i32, vp], None
+    lib.host_attn.argtypes = [vp] * 6 + [i32] * 5 + [vp, i64, i32, vp, vp, i32, i64, vp, i64, i32, f32, vp, vp, i64, vp]
+    lib.host_attn.restype = u64
+    return lib
+
+
+class Arrays:
+    """Copies of arrays between unmapped pages, at their end or at their beginning; freed with the object's library only."""
+
+    def __init__(self, lib, at_end):
+        self.lib, self.at_end, self.made = lib, at_end, []
+
+    def put(self, a, name):
+        """Address of a copy of `a`, which is then that memory."""
+        a = np.ascontiguousarray(a)
+        p = self.lib.host_alloc(a.nbytes, int(self.at_end))
+        view = np.ctypeslib.as_array((ctypes.c_uint8 * a.nbytes).from_address(p)).view(a.dtype).reshape(a.shape)
+        view[...] = a
+        self.made.append((p, a.nbytes, name))
+        return p, view
+
+    def owner(self, address):
+        """What array an address lies next to."""
+        return min(self.made, key=lambda m: max(m[0] - address, address - m[0] - m[1]))[2]
+
+
+def bf16(x):
+    """fp32 values as bf16 bits, round to nearest even (finite values)."""
+    b = np.ascontiguousarray(x, dtype=np.float32).view(np.uint32)
+    return ((b + 0x7FFF + (b >> 16 & 1)) >> 16).astype(np.uint16)
+
+
+def f32(b):
+    """bf16 bits as fp32."""
+    return (b.astype(np.uint32) << 16).view(np.float32)
+
+
+def plan(lib, T, n_seqs, hk, group, d):
+    out = (ctypes.c_int32 * 3)()
+    lib.host_attn_plan(T, n_seqs, hk, group, d, out)
+    return tuple(out)
+
+
+def attn(lib, paged, rows, kv, hq, q, *, tree=None, scale=None, cu=True, lead=0, tail=0, at_end=True, max_pages=None):
+    """The call on a tests.attn_util.Paged cache and bf16 bits q [T, hq * d].  Returns o as fp32; rows outside the sequences 7.5."""
+    d, hk, T = paged.d, paged.hk, lead + sum(rows) + tail
+    mem = Arrays(lib, at_end)
+
+    def put(a, name):
+        return mem.put(a, name)[0]
+
+    fp4 = paged.fmt == "nvfp4"
+    k, v = put(paged.codes["k"], "k"), put(np.swapaxes(paged.codes["v"], 2, 3), "v")
+    ks = put(paged.scales["k"], "k_scales") if fp4 else None
+    vs = put(np.swapaxes(paged.scales["v"], 2, 3), "v_scales") if fp4 else None
+    gs = [put(np.array([paged.gs[n]], dtype=np.float32), n + "_gs") for n in "kv"]
+    most = paged.max_pages if max_pages is None else max_pages
+    table = put(paged.table[:, :most], "page_table")
+    lens = put(np.array(kv, dtype=np.int32), "kv_lens")
+    starts = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32) + np.int32(lead)
+    cus = put(starts, "cu_seqlens") if cu else None
+    masks = None if tree is None else put(np.concatenate([np.zeros(lead, np.int64), *tree, np.zeros(tail, np.int64)]), "tree")
+    o, out = mem.put(np.full((T, hq * d), 0x40F0, dtype=np.uint16), "o")
+    need = lib.host_attn_workspace(T, len(rows), hq, hk, d)
+    ws = put(np.full(need // 4, np.nan, dtype=np.float32), "workspace")
+    at = lib.host_attn(k, v, ks, vs, *gs, int(fp4), paged.n_pages, paged.page.bit_length() - 1, hk, d, table, most, most, lens,
+                       cus, len(rows), T, put(q, "q"), hq * d, hq, d ** -0.5 if scale is None else scale, masks, o, hq * d, ws)
+    assert at == 0, f"an access out of bounds, next to {mem.owner(at)}"
+    return f32(out), starts
