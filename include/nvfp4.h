@@ -737,7 +737,7 @@ NVFP4_API nvfp4_status_t nvfp4_kv_cache_read(const nvfp4_kv_cache_t* cache, cons
  * Precision: K and V enter exactly, the weights w_p with 11 bits, sums in fp32; o
  * is rounded to bf16 once.  A query or key that is not finite makes the rows that
  * use it NaN, a value that is not finite its dim of the rows that see it, and
- * nothing else.  The same call gives the same bits; which kernel runs, and with it
+ * nothing else: finite scores may be of any size.  The same call gives the same bits; which kernel runs, and with it
  * the order of sums, goes by T * n_q_heads / (n_seqs * n_kv_heads).
  */
 NVFP4_API nvfp4_status_t nvfp4_attn_cached(const nvfp4_kv_cache_t* cache, const int32_t* page_table, int64_t ld_table,

@@ -60,7 +60,7 @@ struct Attn {
   const uint64_t* tree;
   uint16_t* o;
   int64_t ldo;
-  float* part;      // [2 ranges][rows x (d + 2)]
+  float* part;      // [2 ranges][rows x (d + kPartMore)]
   Joint* joints;    // [ranges]
   int least;        // keys of a range, at least
   int start;        // what beginning and ending a unit takes, in keys
@@ -78,7 +78,8 @@ constexpr int kStep = 64;      // keys per step
 constexpr int kCus = 256;
 constexpr float kLag = 8.0f;   // log2: how far the running maximum may lag behind
 constexpr float kLift = 7.0f;  // log2: P is stored times 2^7
-constexpr float kNoMax = -0x1p100f;
+constexpr float kFar = 4096.0f;  // log2: from here on weights are formed from differences of scores
+constexpr int kPartMore = 3;    // of a row's part, beside its values: maximum, sum, factor of the scores
 
 __device__ __forceinline__ int64_t scan64(int64_t v) {  // inclusive, over the wave
   const int lane = threadIdx.x & 63;
@@ -271,6 +272,11 @@ __device__ __forceinline__ Reach reach_of(const Attn& a, const Unit& u, int rows
   r.all = a.tree ? (int)min((int64_t)s.kv - s.n, (int64_t)cache_rows(a)) : row_limit(a, s, t0);
   r.steps = t0 > t1 ? 0 : (row_limit(a, s, t1) + kStep - 1) / kStep;
   return r;
+}
+
+// What weights under the maximum `from` are multiplied by to be under `to`; c1: the factor of the scores.
+__device__ __forceinline__ float rescale(float from, float to, float c1) {
+  return from == to ? 1.0f : __builtin_amdgcn_exp2f((from - to) * c1);
 }
 
 __device__ __forceinline__ half2_t two_fp16(float a, float b) {  // round to nearest even

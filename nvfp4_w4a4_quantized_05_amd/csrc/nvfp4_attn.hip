@@ -21,7 +21,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Attn a, int rows) {
   const int first = u.first, cuts = u.cuts;
   const int share = (w - first) * gridDim.y + blockIdx.y, shares = cuts * gridDim.y;
   const int lane = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
-  const int64_t size = (int64_t)rows * (kD + 2);
+  const int64_t size = (int64_t)rows * (kD + kPartMore);
   const float* parts = a.part + (2 * (int64_t)first - 1) * size;  // of the range before: slot 2 (first - 1) + 1
   const auto part = [&](int i) { return parts + (i == 0 ? 0 : 2 * i - 1) * size; };
   const float v_gs = *a.c.v_gs;
@@ -34,16 +34,17 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Attn a, int rows) {
   };
   // Parts first, first + by, ... of row rho, under their own maximum.
   const auto join = [&](int rho, int from, int by, float& m, float& l, floatx4_t& o) {
-    m = kNoMax;
+    m = -INFINITY;
     l = 0.0f;
     o = floatx4_t{0, 0, 0, 0};
+    const int more = rows * kD + kPartMore * rho;
 #pragma unroll 4
-    for (int i = from; i <= cuts; i += by) m = fmaxf(m, part(i)[rows * kD + 2 * rho]);
+    for (int i = from; i <= cuts; i += by) m = fmaxf(m, part(i)[more]);
 #pragma unroll 4
     for (int i = from; i <= cuts; i += by) {
       const float* p = part(i);
-      const float f = __builtin_amdgcn_exp2f(p[rows * kD + 2 * rho] - m);
-      l += p[rows * kD + 2 * rho + 1] * f;
+      const float f = rescale(p[more], m, p[more + 2]);
+      l += p[more + 1] * f;
       o += *reinterpret_cast<const floatx4_t*>(p + rho * kD + 4 * lane) * f;
     }
   };
@@ -73,11 +74,12 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Attn a, int rows) {
     if (grp == 0) {
 #pragma unroll
       for (int i = 1; i < kGroups; ++i) m = fmaxf(m, ml[0][i]);
+      const float c1 = part(0)[rows * kD + kPartMore * rho + 2];
       l = 0.0f;
       o = floatx4_t{0, 0, 0, 0};
 #pragma unroll
       for (int i = 0; i < kGroups; ++i) {
-        const float f = __builtin_amdgcn_exp2f(ml[0][i] - m);
+        const float f = rescale(ml[0][i], m, c1);
         l += ml[1][i] * f;
         o += sums[i * kLanes + lane] * f;
       }
@@ -115,7 +117,7 @@ Plan plan_of(int64_t T, int n_seqs, int hk, int group, int d) {
   return {2, false, false, 128, 256, 512, ranges};
 }
 
-size_t part_bytes(const Plan& p, int d) { return (size_t)2 * p.ranges * p.rows * (d + 2) * sizeof(float); }
+size_t part_bytes(const Plan& p, int d) { return (size_t)2 * p.ranges * p.rows * (d + kPartMore) * sizeof(float); }
 
 }  // namespace
 

@@ -56,7 +56,7 @@ struct Few {
     if (!whole) w.hide(a, u.w.rows, step * kStep + 16 * g, pg.v >= 0, s);
     float top[kNT];
     w.tops(0, 1, s, top);
-    w.raise_max(top);
+    w.raise_max(top, s);
     w.weights(0, 1, s, p);
     w.add_sums(p);
     bool nan = false;
@@ -101,7 +101,7 @@ struct Few {
     if constexpr (kSolo) {
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
-        const Sink<kFp4, kD> sink(a, u, kRows, 16 * nt + n, w.m[nt], w.total(nt), slot);
+        const Sink<kFp4, kD> sink(a, u, kRows, 16 * nt + n, w.m[nt], w.total(nt), w.c1[nt], slot);
 #pragma unroll
         for (int x = 0; x < R::kTiles / 2; ++x) sink.put(x, w.o[nt][2 * x], w.o[nt][2 * x + 1]);
       }
@@ -118,13 +118,13 @@ struct Few {
     __syncthreads();
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
-      float m = kNoMax, l = 0.0f;
+      float m = -INFINITY, l = 0.0f;
 #pragma unroll
       for (int v = 0; v < 4; ++v) m = fmaxf(m, lds.ml[v][nt][n][0]);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) l += lds.ml[v][nt][n][1] * __builtin_amdgcn_exp2f(lds.ml[v][nt][n][0] - m);
-      const float f = __builtin_amdgcn_exp2f(w.m[nt] - m);
-      const Sink<kFp4, kD> sink(a, u, kRows, 16 * nt + n, m, l, slot);
+      for (int v = 0; v < 4; ++v) l += lds.ml[v][nt][n][1] * rescale(lds.ml[v][nt][n][0], m, w.c1[nt]);
+      const float f = rescale(w.m[nt], m, w.c1[nt]);
+      const Sink<kFp4, kD> sink(a, u, kRows, 16 * nt + n, m, l, w.c1[nt], slot);
       constexpr int kPairs = R::kTiles / 2;
 #pragma unroll
       for (int i = 0; i < R::kTiles; ++i) lds.sums[(wave * R::kTiles + i) * 64 + lane] = w.o[nt][i] * f;

@@ -81,7 +81,7 @@ struct Many {
       w.hide(a, u.w.rows, k * kStep + 16 * g, st.p0.v >= 0, now.s);
       w.tops(0, 1, now.s, now.top);
     }
-    w.raise_max(now.top);
+    w.raise_max(now.top, now.s);
     Pages e3;
 #pragma unroll
     for (int x = 0; x < kParts; ++x) {
@@ -192,7 +192,7 @@ struct Many {
     }
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
-      const Sink<kFp4, kD> sink(a, u, kRows, row0 + 16 * nt + n, w.m[nt], w.total(nt), slot);
+      const Sink<kFp4, kD> sink(a, u, kRows, row0 + 16 * nt + n, w.m[nt], w.total(nt), w.c1[nt], slot);
 #pragma unroll
       for (int x = 0; x < R::kTiles / 2; ++x) sink.put(x, w.o[nt][2 * x], w.o[nt][2 * x + 1]);
     }

@@ -55,7 +55,12 @@ struct Rows {
   floatx4_t o[kNT][kTiles];
   // The sum of a row's weights is one more result, with ones for V: no vector additions, no exchange between lanes.
   floatx4_t sum[kNT];
-  float m[kNT], c1[kNT];          // running maximum, factor of the scores (log2)
+  // The running maximum is kept in the scores' own units, -inf before the first; c1 makes powers of two of them.
+  // A weight is 2^(s c1 + off).  Where |m c1| passes kFar in a row of the wave, the rounding of off (2^-24 of it) would
+  // reach a fp16 weight's own, and from 2^28 on more than fp16 holds (NaN, or no weight at all): the wave then takes m
+  // off the scores first, exactly as far as weights go (`far`; 16 kNT subtractions more a step).
+  float m[kNT], c1[kNT], off[kNT];
+  bool far;
   float fate[kNT];                // 1, or NaN
   int limit[kNT];                 // positions the row may see
   uint64_t seen[kNT];             // tree: its mask
@@ -94,16 +99,18 @@ struct Rows {
         q[nt][f] = __builtin_bit_cast(half8_t, h);
       }
       // Kept normal and below 2^64: under the one all scores are 0 to any precision (but -inf times it is -inf still),
-      // over the other any two that differ at all are further apart than weights can be (and none reaches kNoMax).
+      // over the other any two that differ at all are further apart than weights can be.
       c1[nt] = fminf(fmaxf(ldexpf(a.scale * k_gs, -shift), 0x1p-126f), 0x1p64f);
       fate[nt] = finite ? 1.0f : __builtin_nanf("");  // what is not finite in q makes the row NaN if it sees anything
-      m[nt] = kNoMax;
+      m[nt] = -INFINITY;
+      off[nt] = kLift;
       sum[nt] = floatx4_t{0, 0, 0, 0};
       limit[nt] = real ? row_limit(a, u.w.rows, r.token) : 0;
       seen[nt] = a.tree && real ? a.tree[row] : 0;
 #pragma unroll
       for (int d = 0; d < kTiles; ++d) o[nt][d] = floatx4_t{0, 0, 0, 0};
     }
+    far = false;
   }
 
   // Part x of `parts` of the largest of each row's scores that the lane has.
@@ -115,18 +122,32 @@ struct Rows {
     }
   }
   // The running maximum after scores with the given tops; what it moves by is taken out of the sum and the result.
-  __device__ __forceinline__ void raise_max(const float top[kNT]) {
+  __device__ __forceinline__ void raise_max(const float top[kNT], Scores& s) {
     bool lags = false;
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) lags = lags || top[nt] * c1[nt] > m[nt] + kLag;
+    for (int nt = 0; nt < kNT; ++nt) lags = lags || (top[nt] - m[nt]) * c1[nt] > kLag;
     if (__builtin_amdgcn_ballot_w64(lags)) {
+      bool past = false;
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
-        const float now = fmaxf(m[nt], max_over_g(top[nt] * c1[nt])), f = __builtin_amdgcn_exp2f(m[nt] - now);
+        const float now = fmaxf(m[nt], max_over_g(top[nt])), f = rescale(m[nt], now, c1[nt]);
         m[nt] = now;
         sum[nt] *= f;
 #pragma unroll
         for (int d = 0; d < kTiles; ++d) o[nt][d] *= f;
+        const float at = now == -INFINITY ? 0.0f : now * c1[nt];
+        off[nt] = kLift - at;
+        past = past || fabsf(at) > kFar;
+      }
+      far = __builtin_amdgcn_ballot_w64(past) != 0;
+    }
+    if (far) {
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        const float base = fmaxf(m[nt], -0x1p100f);  // before the first: -inf less it is -inf still
+        off[nt] = kLift;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[nt][e / 4][e % 4] -= base;
       }
     }
   }
@@ -155,9 +176,8 @@ struct Rows {
 #pragma unroll
     for (int i = 8 * kNT * x / parts; i < 8 * kNT * (x + 1) / parts; ++i) {
       const int nt = i / 8, e = i % 8 * 2;
-      const float off = kLift - m[nt];
-      const float v = __builtin_amdgcn_exp2f(fmaf(s[nt][e / 4][e % 4], c1[nt], off));
-      const float y = __builtin_amdgcn_exp2f(fmaf(s[nt][e / 4][e % 4 + 1], c1[nt], off));
+      const float v = __builtin_amdgcn_exp2f(fmaf(s[nt][e / 4][e % 4], c1[nt], off[nt]));
+      const float y = __builtin_amdgcn_exp2f(fmaf(s[nt][e / 4][e % 4 + 1], c1[nt], off[nt]));
       const half2_t h = two_fp16(v, y);
       p[nt][e / 8][e % 8] = h[0];
       p[nt][e / 8][e % 8 + 1] = h[1];
@@ -208,8 +228,8 @@ struct Sink {
   uint16_t* to;
   float* part;
   float f;
-  // Row rho (of `rows`), its maximum m and sum l.
-  __device__ __forceinline__ Sink(const Attn& a, const Unit& u, int rows, int rho, float m, float l, int slot) {
+  // Row rho (of `rows`), its maximum m, sum l and factor of the scores c1.
+  __device__ __forceinline__ Sink(const Attn& a, const Unit& u, int rows, int rho, float m, float l, float c1, int slot) {
     const int g = (threadIdx.x & 63) >> 4;
     const RowOf r = row_of(a, u, rows, rho);
     to = nullptr;
@@ -219,11 +239,13 @@ struct Sink {
       f = l == 0.0f ? 0.0f : *a.c.v_gs / l;  // a row that sees nothing is zeros
       to = a.o + (u.w.rows.row0 + r.token) * a.ldo + (int64_t)r.head * kD;
     } else {
-      float* base = a.part + (int64_t)slot * (rows * (kD + 2));
+      float* base = a.part + (int64_t)slot * (rows * (kD + kPartMore));
       part = base + rho * kD;
       if (g == 0) {
-        base[rows * kD + 2 * rho] = m;
-        base[rows * kD + 2 * rho + 1] = l;
+        float* more = base + rows * kD + kPartMore * rho;
+        more[0] = m;
+        more[1] = l;
+        more[2] = c1;
       }
     }
   }

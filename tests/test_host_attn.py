@@ -71,3 +71,82 @@ def test_bounds_and_values(lib, fmt, form, at_end):
     paged = Paged(fmt, hk, d, page, kv, 3)
     paged.set_nan("v", 0, kv[0] - 1, 0, 5)
     run(lib, paged, rows, kv, hq, form, lead=2, tail=3, at_end=at_end)
+
+
+def check_one_hot(got, q, paged, kv, rows, starts, hq, scale):
+    """Rows whose largest score is ahead of the others by more than scores can be off by, and 40 beside: the other
+    weights are below e^-40 in all, so o is that key's value, times and divided by its weight: three fp32 roundings and
+    one to bf16.  (A row has one key that is ahead in nearly all of the random rows; how many is asserted.)"""
+    d, checked, seen = paged.d, 0, 0
+    for i, (n, length) in enumerate(zip(rows, kv)):
+        k, v = paged.values("k", i, length), paged.values("v", i, length)
+        for j in range(n):
+            for h in range(hq):
+                keys = k[:length - n + j + 1, h // (hq // paged.hk)]
+                x = q[starts[i] + j].reshape(hq, d)[h]
+                s = keys @ x * scale
+                big = np.max(np.abs(keys) @ np.abs(x)) * scale
+                order = np.argsort(s)
+                seen += 1
+                if len(s) > 1 and s[order[-1]] - s[order[-2]] < 4 * (d + 8) * 2.0 ** -24 * big + 40:
+                    continue
+                checked += 1
+                want = v[order[-1], h // (hq // paged.hk)]
+                g = got[starts[i] + j].reshape(hq, d)[h]
+                tol = (2.0 ** -8 + 2.0 ** -22) * np.abs(want) + 2.0 ** -50 * np.abs(v).max()
+                assert np.all(np.abs(g - want) <= tol), (i, j, h, s[order[-1]], np.abs(g - want).max())
+    assert checked > 0.9 * seen, (checked, seen)
+
+
+# maxima of about 1e8 to 1e26 in scores, positive and (few keys) negative
+FACTORS = [1e8, 3e8, 1e9, 1e10, 3e10, 1e13, 1e17, 1e25]
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("form,heads,rows,ctx", [("16 rows", (4, 2, 64, 16), [1, 2], [129, 2]), ("32 rows", (4, 1, 64, 32), [5, 6], [600, 1]),
+                                                 ("128 rows", (4, 1, 64, 16), [20, 30], [60, 0])])
+@pytest.mark.parametrize("factor", FACTORS)
+def test_finite_queries_of_any_size(lib, fmt, form, heads, rows, ctx, factor):
+    """One-hot softmaxes: scores up to 1e27 in both directions give the value of the largest."""
+    hq, hk, d, page = heads
+    kv = [a + b for a, b in zip(rows, ctx)]
+    paged = Paged(fmt, hk, d, page, kv, 21)
+    q = H.bf16(factor * np.random.default_rng(5).standard_normal((sum(rows), hq * d)).astype(np.float32))
+    got, starts = H.attn(lib, paged, rows, kv, hq, q)
+    check_one_hot(got, H.f32(q).astype(np.float64), paged, kv, rows, starts, hq, float(np.float32(d ** -0.5)))
+
+
+def common_part(hk, d, page, kv, group, n_rows, seed):
+    """Scores of about 10,450 that differ by up to 39, every sum of which is exact in fp32: dim 0 gives each key
+    4080 * 256, dim 1 a product of whole numbers up to 255 * 15.  (cache, queries [n_rows, hq * d], scale)."""
+    paged = Paged("fp8", hk, d, page, kv, seed)
+    rng = np.random.default_rng(seed)
+    live = paged.codes["k"] != 0x7F
+    for dim, values in ((0, np.array([256.0])), (1, np.arange(1.0, 16.0))):
+        codes = A.e4m3_codes(rng.choice(values, paged.codes["k"].shape[:3]), 1.0)
+        paged.codes["k"][..., dim] = np.where(live[..., dim], codes, 0x7F)
+    q = np.zeros((n_rows, hk * group, d), np.float32)
+    q[..., 0], q[..., 1] = 4080.0, rng.integers(1, 256, q.shape[:2])
+    return paged, q.reshape(n_rows, -1), float(np.float32(0.01 / paged.gs["k"]))
+
+
+def check_common_part(got, q, paged, rows, kv, starts, hq, scale):
+    """As tests/test_gpu_attn.py's bound, with scores that are exact: their factor's error counts for their distance from
+    the maximum only (39 of them; 8 for the sum's d)."""
+    for i, (n, length) in enumerate(zip(rows, kv)):
+        mask = A.seen_ref(n, length, length)
+        x = q[starts[i]:starts[i] + n].astype(np.float64).reshape(n, hq, paged.d)
+        O, mag, _, flat = A.attn_ref(x, paged.values("k", i, length), paged.values("v", i, length), mask, scale)
+        err = np.abs(got[starts[i]:starts[i] + n].astype(np.float64).reshape(O.shape) - O)
+        assert np.all(err <= tolerance(O, mag, np.full((n, hq), 39.0), flat, 8, length))
+
+
+@pytest.mark.parametrize("heads,rows,ctx", [((4, 2, 64, 16), [1, 2], [700, 2]), ((4, 1, 128, 32), [5, 6], [600, 1]),
+                                            ((4, 1, 64, 16), [30, 30], [400, 0])])
+def test_large_scores_that_differ_little(lib, heads, rows, ctx):
+    """Weights of scores far from zero go by their differences, in every part of a cut row."""
+    hq, hk, d, page = heads
+    kv = [a + b for a, b in zip(rows, ctx)]
+    paged, q, scale = common_part(hk, d, page, kv, hq // hk, sum(rows), 22)
+    got, starts = H.attn(lib, paged, rows, kv, hq, H.bf16(q), scale=scale)
+    check_common_part(got, q, paged, rows, kv, starts, hq, scale)
