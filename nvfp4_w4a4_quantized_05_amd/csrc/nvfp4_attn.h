@@ -133,7 +133,7 @@ __device__ __forceinline__ SeqWork seq_work(const Attn& a, int i) {
   w.rows = seq_rows(a.r, i);
   const int most = cache_rows(a);
   if (a.tree) {
-    w.first = min(max(w.rows.kv, 1), most) + a.start;
+    w.first = (int64_t)min(max(w.rows.kv, 1), most) + a.start;
     w.slope = 0;
   } else {
     w.first = min(max((int64_t)w.rows.kv - w.rows.n, (int64_t)0), (int64_t)most) + a.tokens + a.start;

@@ -119,6 +119,14 @@ Plan plan_of(int64_t T, int n_seqs, int hk, int group, int d) {
 
 size_t part_bytes(const Plan& p, int d) { return (size_t)2 * p.ranges * p.rows * (d + kPartMore) * sizeof(float); }
 
+Attn attn_of(const Plan& p, const KvCache& c, const KvRows& r, const void* q, int64_t ldq, int group, float scale,
+             const uint64_t* tree, void* o, int64_t ldo, void* workspace) {
+  return {c,      r,       static_cast<const uint16_t*>(q), ldq, group, scale * 1.44269504088896340736f, tree,
+          static_cast<uint16_t*>(o), ldo, static_cast<float*>(workspace),
+          reinterpret_cast<Joint*>(static_cast<char*>(workspace) + part_bytes(p, c.d)), p.least, p.start, p.ranges,
+          group <= p.rows ? p.rows / group : 1, group <= p.rows ? 1 : (group + p.rows - 1) / p.rows};
+}
+
 }  // namespace
 
 size_t attn_cached_workspace_bytes(int64_t T, int n_seqs, int hq, int hk, int d) {
@@ -130,10 +138,7 @@ hipError_t launch_attn_cached(const KvCache& c, const KvRows& r, const void* q, 
                               const uint64_t* tree, void* o, int64_t ldo, void* workspace, hipStream_t stream) {
   const int group = hq / c.hk;
   const Plan p = plan_of(r.T, r.n_seqs, c.hk, group, c.d);
-  const Attn a{c,      r,       static_cast<const uint16_t*>(q), ldq, group, scale * 1.44269504088896340736f, tree,
-               static_cast<uint16_t*>(o), ldo, static_cast<float*>(workspace),
-               reinterpret_cast<Joint*>(static_cast<char*>(workspace) + part_bytes(p, c.d)), p.least, p.start, p.ranges,
-               group <= p.rows ? p.rows / group : 1, group <= p.rows ? 1 : (group + p.rows - 1) / p.rows};
+  const Attn a = attn_of(p, c, r, q, ldq, group, scale, tree, o, ldo, workspace);
   if (p.split)
     launch_attn_few(a, p.nt, p.solo, stream);
   else

@@ -35,8 +35,9 @@ def build(out_dir):
         with open(os.path.join(out_dir, name), "w") as f:
             f.write(re.sub(r'asm volatile\("" : "\+a".*', ";", text))  # a hint about registers
     lib = os.path.join(out_dir, "libhost.so")
-    cmd = [clang(), "-x", "c++", "-std=c++17", "-O1", "-march=native", "-ffp-contract=off", "-shared", "-fPIC", "-w", "-I", HERE,
-           "-I", os.path.join(ROOT, "include"), "-I", str(out_dir), os.path.join(HERE, "calls.cpp"), "-o", lib]
+    # -fwrapv: whole numbers that overflow do so as the GPU's would
+    cmd = [clang(), "-x", "c++", "-std=c++17", "-O1", "-march=native", "-ffp-contract=off", "-fwrapv", "-shared", "-fPIC", "-w",
+           "-I", HERE, "-I", os.path.join(ROOT, "include"), "-I", str(out_dir), os.path.join(HERE, "calls.cpp"), "-o", lib]
     res = subprocess.run(cmd, capture_output=True, text=True)
     assert res.returncode == 0, res.stderr[-3000:]
     lib = ctypes.CDLL(lib)
@@ -46,6 +47,7 @@ def build(out_dir):
     lib.host_attn_plan.argtypes, lib.host_attn_plan.restype = [i64, i32, i32, i32, i32, vp], None
     lib.host_attn.argtypes = [vp] * 6 + [i32] * 5 + [vp, i64, i32, vp, vp, i32, i64, vp, i64, i32, f32, vp, vp, i64, vp]
     lib.host_attn.restype = u64
+    lib.host_attn_pieces.argtypes, lib.host_attn_pieces.restype = [i32] * 4 + [vp, vp, i32, i64, i32, i32, vp, i32], i32
     return lib
 
 
@@ -84,6 +86,16 @@ def plan(lib, T, n_seqs, hk, group, d):
     out = (ctypes.c_int32 * 3)()
     lib.host_attn_plan(T, n_seqs, hk, group, d, out)
     return tuple(out)
+
+
+def pieces(lib, rows, kv, hq, hk, d, page, max_pages, tree):
+    """[n, 8]: range, sequence, tile, minor, first step, step behind the last, slot and the unit's steps of all work."""
+    lens, cu = np.array(kv, dtype=np.int32), np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    out = np.zeros((1 << 16, 8), dtype=np.int64)
+    n = lib.host_attn_pieces(page.bit_length() - 1, hk, d, max_pages, lens.ctypes.data, cu.ctypes.data, len(rows), int(cu[-1]), hq,
+                             int(tree), out.ctypes.data, len(out))
+    assert n <= len(out)
+    return out[:n]
 
 
 def attn(lib, paged, rows, kv, hq, q, *, tree=None, scale=None, cu=True, lead=0, tail=0, at_end=True, max_pages=None):

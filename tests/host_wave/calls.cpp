@@ -153,6 +153,21 @@ uint64_t guarded(F f) {
 
 }  // namespace host
 
+// What the ranges of a call would do, without doing it: a workgroup of one wave per range.
+namespace nvfp4 {
+struct Piece {
+  int64_t range, seq, tile, minor, k0, k1, slot, steps;  // steps: of the unit's rows, from its first key
+};
+static void pieces_kernel(Attn a, int rows, Piece* out, int most, int* n) {
+  run_range(a, blockIdx.x, [&](const Unit& u, int k0, int k1, int slot) {
+    if (threadIdx.x == 0) {
+      if (*n < most) out[*n] = {(int64_t)blockIdx.x, u.seq, u.tile, u.minor, k0, k1, slot, reach_of(a, u, rows, 0, rows).steps};
+      ++*n;
+    }
+  });
+}
+}  // namespace nvfp4
+
 extern "C" {
 
 // `bytes` between unmapped pages, at the beginning of the mapped ones or (at_end) at their end.
@@ -183,6 +198,21 @@ uint64_t host_attn(uint8_t* k, uint8_t* v, uint8_t* ks, uint8_t* vs, const float
   const nvfp4::KvCache c{k, v, ks, vs, k_gs, v_gs, fp4 != 0, n_pages, page_shift, hk, d};
   const nvfp4::KvRows r{table, ld_table, max_pages, lens, cu, n_seqs, T};
   return host::guarded([&] { nvfp4::launch_attn_cached(c, r, q, ldq, hq, scale, tree, o, ldo, workspace, nullptr); });
+}
+
+// Pieces of work [most][8] of a call (their number is returned): rows and lengths as for host_attn, no cache.
+int host_attn_pieces(int page_shift, int hk, int d, int max_pages, const int32_t* lens, const int32_t* cu, int n_seqs,
+                     int64_t T, int hq, int tree, int64_t* out, int most) {
+  const nvfp4::KvCache c{nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, false, 1, page_shift, hk, d};
+  const nvfp4::KvRows r{nullptr, max_pages, max_pages, lens, cu, n_seqs, T};
+  const nvfp4::Plan p = nvfp4::plan_of(T, n_seqs, hk, hq / hk, d);
+  uint64_t mask = 0;  // whether there is one is all that places depend on
+  void* ws = calloc(1, nvfp4::attn_cached_workspace_bytes(T, n_seqs, hq, hk, d));
+  const nvfp4::Attn a = nvfp4::attn_of(p, c, r, nullptr, 0, hq / hk, 1.0f, tree ? &mask : nullptr, nullptr, 0, ws);
+  int n = 0;
+  host_launch(nvfp4::pieces_kernel, dim3(p.ranges), dim3(64), a, p.rows, reinterpret_cast<nvfp4::Piece*>(out), most, &n);
+  free(ws);
+  return n;
 }
 
 }  // extern "C"

@@ -150,3 +150,32 @@ def test_large_scores_that_differ_little(lib, heads, rows, ctx):
     paged, q, scale = common_part(hk, d, page, kv, hq // hk, sum(rows), 22)
     got, starts = H.attn(lib, paged, rows, kv, hq, H.bf16(q), scale=scale)
     check_common_part(got, q, paged, rows, kv, starts, hq, scale)
+
+
+TOP = 2 ** 31 - 1
+LENGTHS = [([1, 1, 1], [5, 70, 1000]), ([3, 3, 3], [TOP, 100, 3]), ([5, 2], [TOP - 200, TOP]), ([40, 1, 90], [90, TOP, 4000]),
+           ([100, 60], [TOP - 128, 60]), ([2, 0, 3], [-5, TOP, 0]), ([1] * 70, [TOP] * 35 + [64] * 35)]
+
+
+@pytest.mark.parametrize("rows,kv", LENGTHS)
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("hq,hk", [(1, 1), (6, 2)])
+def test_ranges_take_every_step_once(lib, rows, kv, tree, hq, hk):
+    """Each unit's steps are in one range or in neighbouring ones, none twice, none left out, for lengths up to int32's
+    last; whole units have no slot, cut ones those of their cuts."""
+    d, page, max_pages = 64, 1024, 1 << 21
+    tile_rows = H.plan(lib, sum(rows), len(rows), hk, hq // hk, d)[0]
+    tokens = tile_rows // (hq // hk)
+    got = {}
+    for r, seq, tile, minor, k0, k1, slot, steps in H.pieces(lib, rows, kv, hq, hk, d, page, max_pages, tree).tolist():
+        got.setdefault((seq, tile, minor), []).append((r, k0, k1, slot, steps))
+    units = {(i, t, h) for i, n in enumerate(rows) for t in range(-(-n // tokens)) for h in range(hk)}
+    assert set(got) == units
+    for (seq, tile, _), parts in got.items():
+        last = kv[seq] if tree else min(kv[seq], kv[seq] - rows[seq] + min((tile + 1) * tokens, rows[seq]))
+        steps = -(-max(0, min(last, TOP - 127)) // 64)
+        assert {p[4] for p in parts} == {steps}
+        assert [p[0] for p in parts] == list(range(parts[0][0], parts[0][0] + len(parts)))
+        assert parts[0][1] == 0 and parts[-1][2] >= steps and all(a[2] == b[1] for a, b in zip(parts, parts[1:]))
+        slots = [-1] if len(parts) == 1 else [2 * parts[0][0] + 1] + [2 * p[0] for p in parts[1:]]
+        assert [p[3] for p in parts] == slots
