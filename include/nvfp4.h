@@ -658,7 +658,8 @@ typedef struct {
  * then the rotation of its first `rot` dims: pair p (a, b) becomes
  *     (a cos - b sin, b cos + a sin)
  * with cos = cos_sin[pos][p], sin = cos_sin[pos][rot / 2 + p], pos the row's
- * position on the pair's axis.  fp32, rounded to bf16 once.
+ * position on the pair's axis.  fp32, rounded to bf16 once; finite values may be
+ * of any size.
  *
  *   x           device [T x ldx] of `x_dtype` (NVFP4_IN_F32 / _BF16), q heads at
  *               column q_col and k heads at k_col; 16-byte aligned, ldx and the

@@ -98,14 +98,27 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRope a, int wav
     const bool is_q = h < a.hq;
     const int64_t from = t * a.ldx + (is_q ? a.q_col + (int64_t)h * a.d : a.k_col + (int64_t)(h - a.hq) * a.d);
     uint16_t* to = is_q ? a.q + t * a.ldq + (int64_t)h * a.d : a.k + t * a.ldk + (int64_t)(h - a.hq) * a.d;
-    float v[16], ss = 0.0f;
+    float v[16], eps = a.eps;
     load8<kBf16>(a.x, from + at0, v);
     load8<kBf16>(a.x, from + at1, v + 8);
+    const auto sum_squares = [&] {
+      float s = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) ss = fmaf(v[e], v[e], ss);
+      for (int e = 0; e < 16; ++e) s = fmaf(v[e], v[e], s);
 #pragma unroll
-    for (int m = 1; m < kLanes; m <<= 1) ss += __shfl_xor(ss, m, 64);
-    const float rms = 1.0f / sqrtf(ss / (float)a.d + a.eps);
+      for (int m = 1; m < kLanes; m <<= 1) s += __shfl_xor(s, m, 64);
+      return s;
+    };
+    float ss = sum_squares();
+    // Heads of finite values may have squares past fp32 (from 1.1e18 on, if all 256 are): they, and eps, are made smaller first.
+    if (__builtin_amdgcn_ballot_w64(!(ss < 0x1p104f))) {
+      const float by = large_row_scale(ss);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] *= by;
+      eps = eps * by * by;
+      ss = sum_squares();
+    }
+    const float rms = 1.0f / sqrtf(ss / (float)a.d + eps);
 #pragma unroll
     for (int e = 0; e < 16; ++e) v[e] = v[e] * rms * (is_q ? qw[e] : kw[e]);
     if (turns) {

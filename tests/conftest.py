@@ -21,6 +21,15 @@ def golden_dir():
 
 
 @pytest.fixture(scope="session")
+def host_lib(tmp_path_factory):
+    """The attention layer's kernels built for the host (skipped without clang)."""
+    from tests import host_wave
+    if host_wave.clang() is None:
+        pytest.skip("clang not available")
+    return host_wave.build(str(tmp_path_factory.mktemp("host")))
+
+
+@pytest.fixture(scope="session")
 def gemm_kernels_asm(tmp_path_factory):
     """{kernel symbol: [instruction text]} of nvfp4_gemm.hip compiled for
     gfx950 with the library's flags (skipped without hipcc)."""

@@ -48,6 +48,8 @@ def build(out_dir):
     lib.host_attn.argtypes = [vp] * 6 + [i32] * 5 + [vp, i64, i32, vp, vp, i32, i64, vp, i64, i32, f32, vp, vp, i64, vp]
     lib.host_attn.restype = u64
     lib.host_attn_pieces.argtypes, lib.host_attn_pieces.restype = [i32] * 4 + [vp, vp, i32, i64, i32, i32, vp, i32], i32
+    lib.host_rope.argtypes = [vp, i32, i64, i64, i64, i64, i32, i32, i32, i32, vp, vp, f32, vp, i32, vp, i32, vp, i32, vp, vp]
+    lib.host_rope.restype = u64
     return lib
 
 
@@ -124,3 +126,18 @@ def attn(lib, paged, rows, kv, hq, q, *, tree=None, scale=None, cu=True, lead=0,
                        cus, len(rows), T, put(q, "q"), hq * d, hq, d ** -0.5 if scale is None else scale, masks, o, hq * d, ws)
     assert at == 0, f"an access out of bounds, next to {mem.owner(at)}"
     return f32(out), starts
+
+
+def rope(lib, x, q_w, k_w, table, pos, *, q_col, k_col, hq, hk, eps, pair_axis=None, adjacent=False, at_end=True):
+    """The call on x (fp32, or bf16 bits) [T, cols]; pos [axes, T].  Returns q and k as fp32."""
+    mem, d, T = Arrays(lib, at_end), len(q_w), x.shape[0]
+    axis = np.zeros(8, dtype=np.uint32)
+    for p, n in enumerate(pair_axis or ()):
+        axis[p // 16] |= np.uint32(n << p % 16 * 2)
+    q, qv = mem.put(np.zeros((T, hq * d), np.uint16), "q")
+    k, kv = mem.put(np.zeros((T, hk * d), np.uint16), "k")
+    at = lib.host_rope(mem.put(x, "x")[0], int(x.dtype == np.uint16), x.shape[1], q_col, k_col, T, hq, hk, d, table.shape[1],
+                       mem.put(q_w, "q_w")[0], mem.put(k_w, "k_w")[0], eps, mem.put(table, "cos_sin")[0], table.shape[0],
+                       mem.put(pos.astype(np.int32), "positions")[0], pos.shape[0], mem.put(axis, "axes")[0], int(adjacent), q, k)
+    assert at == 0, f"an access out of bounds, next to {mem.owner(at)}"
+    return f32(qv), f32(kv)

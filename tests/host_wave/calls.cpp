@@ -200,6 +200,15 @@ uint64_t host_attn(uint8_t* k, uint8_t* v, uint8_t* ks, uint8_t* vs, const float
   return host::guarded([&] { nvfp4::launch_attn_cached(c, r, q, ldq, hq, scale, tree, o, ldo, workspace, nullptr); });
 }
 
+uint64_t host_rope(const void* x, int bf16, int64_t ldx, int64_t q_col, int64_t k_col, int64_t T, int hq, int hk, int d,
+                   int rot, const float* q_w, const float* k_w, float eps, const float* table, int n_pos, const int32_t* pos,
+                   int n_axes, const uint32_t* axis, int adjacent, uint16_t* q, uint16_t* k) {
+  nvfp4::QkNormRope a{x,   bf16 != 0, ldx,   q_col, k_col,  T,  hq,           hk, d,          rot, q_w, k_w,
+                      eps, table,     n_pos, pos,   n_axes, {}, adjacent != 0, q,  (int64_t)hq * d, k, (int64_t)hk * d};
+  memcpy(a.axis, axis, sizeof a.axis);
+  return host::guarded([&] { nvfp4::launch_qk_norm_rope(a, nullptr); });
+}
+
 // Pieces of work [most][8] of a call (their number is returned): rows and lengths as for host_attn, no cache.
 int host_attn_pieces(int page_shift, int hk, int d, int max_pages, const int32_t* lens, const int32_t* cu, int n_seqs,
                      int64_t T, int hq, int tree, int64_t* out, int most) {

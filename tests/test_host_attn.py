@@ -17,10 +17,8 @@ FORMS = {"16 rows": (16, False), "32 rows": (32, False), "16 rows a wave": (16, 
 
 
 @pytest.fixture(scope="module")
-def lib(tmp_path_factory):
-    if H.clang() is None:
-        pytest.skip("clang not available")
-    return H.build(str(tmp_path_factory.mktemp("host")))
+def lib(host_lib):
+    return host_lib
 
 
 def run(lib, paged, rows, kv, hq, form, *, seed=0, tree=None, scale=None, spread=1.0, cu=True, lead=0, tail=0, at_end=True,
