@@ -717,8 +717,10 @@ def qk_norm_rope(x: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor
     positions: int32 [T], or [axes, T] with pair_axis, rot / 2 bytes that name
     the axis of each pair.  Pairs are (p, p + rot / 2), or (2 p, 2 p + 1) if
     adjacent.  Returns (q, k), bf16 [T, heads * head_dim]."""
-    xp, x_dtype, T, _, ldx = _rows(x, "x")
+    xp, x_dtype, T, cols, ldx = _rows(x, "x")
     dim = q_weight.numel()
+    if min(q_col, k_col) < 0 or max(q_col + n_q_heads * dim, k_col + n_kv_heads * dim) > cols:
+        raise ValueError(f"the heads must lie in the {cols} columns of x")
     wq, wk = _vector(q_weight, torch.float32, dim, "q_weight"), _vector(k_weight, torch.float32, dim, "k_weight")
     if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or not cos_sin.is_cuda:
         raise ValueError("cos_sin must be contiguous float32 [n_pos, rot] on the GPU")
