@@ -56,7 +56,8 @@ struct Attn {
   const uint16_t* q;
   int64_t ldq;
   int group;        // query heads per key/value head
-  float scale;      // times log2(e)
+  float scale;      // of the scores, times log2(e): scale * 2^power, scale in [0.7, 1.5), as the product with the
+  int power;        // tensor scale may be no fp32 number where the scores themselves are
   const uint64_t* tree;
   uint16_t* o;
   int64_t ldo;

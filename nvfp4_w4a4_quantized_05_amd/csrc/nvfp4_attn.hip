@@ -1,6 +1,8 @@
 // Attention over the cache (nvfp4_attn.h): the layout of a call, and the joining of parts.
 #include "nvfp4_attn.h"
 
+#include <cmath>
+
 namespace nvfp4 {
 namespace {
 
@@ -121,7 +123,9 @@ size_t part_bytes(const Plan& p, int d) { return (size_t)2 * p.ranges * p.rows *
 
 Attn attn_of(const Plan& p, const KvCache& c, const KvRows& r, const void* q, int64_t ldq, int group, float scale,
              const uint64_t* tree, void* o, int64_t ldo, void* workspace) {
-  return {c,      r,       static_cast<const uint16_t*>(q), ldq, group, scale * 1.44269504088896340736f, tree,
+  int power;
+  const float mantissa = std::frexp(scale, &power) * 1.44269504088896340736f;
+  return {c,      r,       static_cast<const uint16_t*>(q), ldq, group, mantissa, power, tree,
           static_cast<uint16_t*>(o), ldo, static_cast<float*>(workspace),
           reinterpret_cast<Joint*>(static_cast<char*>(workspace) + part_bytes(p, c.d)), p.least, p.start, p.ranges,
           group <= p.rows ? p.rows / group : 1, group <= p.rows ? 1 : (group + p.rows - 1) / p.rows};

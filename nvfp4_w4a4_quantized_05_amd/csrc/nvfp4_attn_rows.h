@@ -100,7 +100,7 @@ struct Rows {
       }
       // Kept normal and below 2^64: under the one all scores are 0 to any precision (but -inf times it is -inf still),
       // over the other any two that differ at all are further apart than weights can be.
-      c1[nt] = fminf(fmaxf(ldexpf(a.scale * k_gs, -shift), 0x1p-126f), 0x1p64f);
+      c1[nt] = fminf(fmaxf(ldexpf(a.scale * k_gs, a.power - shift), 0x1p-126f), 0x1p64f);
       fate[nt] = finite ? 1.0f : __builtin_nanf("");  // what is not finite in q makes the row NaN if it sees anything
       m[nt] = -INFINITY;
       off[nt] = kLift;

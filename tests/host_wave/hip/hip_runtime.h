@@ -211,14 +211,3 @@ inline uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel) {
 #define __builtin_amdgcn_cvt_pk_fp8_f32(a, b, old, high) (abort(), 0)
 #define __builtin_amdgcn_perm host::perm
 #define __builtin_amdgcn_sched_barrier(x)
-#define __builtin_amdgcn_frexp_mantf host_frexp_mant
-#define __builtin_amdgcn_frexp_expf host_frexp_exp
-inline float host_frexp_mant(float v) {
-  int e;
-  return frexpf(v, &e);
-}
-inline int host_frexp_exp(float v) {
-  int e;
-  frexpf(v, &e);
-  return e;
-}

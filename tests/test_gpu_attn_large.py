@@ -7,7 +7,8 @@ import torch
 import nvfp4_w4a4_quantized_05_amd as nv
 from tests.attn_util import Paged, i32
 from tests.gpu_util import host_f32, need_gpu
-from tests.test_host_attn import FACTORS, check_common_part, check_one_hot, common_part
+from tests.test_gpu_attn import run
+from tests.test_host_attn import FACTORS, FACTORS_OF_SCORES, check_common_part, check_one_hot, common_part
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +49,12 @@ def test_large_scores_that_differ_little(shape):
     paged, q, scale = common_part(hk, d, page, kv, hq // hk, sum(rows), 22)
     got, starts = call(paged, torch.from_numpy(q).to(need_gpu()).bfloat16(), rows, kv, hq, scale)
     check_common_part(got, q, paged, rows, kv, starts, hq, scale)
+
+
+@pytest.mark.parametrize("shape", range(len(SHAPES)))
+@pytest.mark.parametrize("scale,k_gs,spread", FACTORS_OF_SCORES)
+def test_factors_whose_product_is_no_fp32_number(shape, scale, k_gs, spread):
+    (hq, hk, d, page), rows, ctx = SHAPES[shape]
+    kv = [a + b for a, b in zip(rows, ctx)]
+    print(f"[attn] shape {shape} scale {scale} {k_gs}", flush=True)
+    run(Paged("fp8", hk, d, page, kv, 23, k_gs=k_gs), rows, kv, hq, scale=scale, spread=spread)

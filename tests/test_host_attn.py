@@ -177,3 +177,15 @@ def test_ranges_take_every_step_once(lib, rows, kv, tree, hq, hk):
         assert parts[0][1] == 0 and parts[-1][2] >= steps and all(a[2] == b[1] for a, b in zip(parts, parts[1:]))
         slots = [-1] if len(parts) == 1 else [2 * parts[0][0] + 1] + [2 * p[0] for p in parts[1:]]
         assert [p[3] for p in parts] == slots
+
+
+# scale, tensor scale of the keys, size of the queries: scores of ordinary size whose factors' product is not
+FACTORS_OF_SCORES = [(3.2e38, 1e-30, 1e-9), (1e30, 1e9, 3e-40), (1e-12, 2.0 ** -100, 6e37)]
+
+
+@pytest.mark.parametrize("form", list(CASES))
+@pytest.mark.parametrize("scale,k_gs,spread", FACTORS_OF_SCORES)
+def test_factors_whose_product_is_no_fp32_number(lib, form, scale, k_gs, spread):
+    (hq, hk, d, page), rows, ctx = CASES[form]
+    kv = [a + b for a, b in zip(rows, ctx)]
+    run(lib, Paged("fp8", hk, d, page, kv, 23, k_gs=k_gs), rows, kv, hq, form, scale=scale, spread=spread)
