@@ -57,6 +57,8 @@ CASES = {
     "16 rows": ((6, 1, 256, 64), [1, 2, 0, 1], [300, 0, 40, 15]),
     "32 rows": ((4, 2, 128, 16), [12, 9, 0, 17], [900, 5, 0, 63]),
     "128 rows": ((6, 2, 64, 32), [40, 0, 130, 3], [70, 0, 5, 1000]),
+    "16 rows a wave": ((8, 8, 64, 16), [1, 2, 0, 1] * 16, [700, 0, 40, 15] + [17, 5, 0, 64] * 15),
+    "32 rows a wave": ((24, 8, 64, 32), [7, 13, 0, 9] * 4, [600, 0, 40, 15] + [17, 5, 0, 64] * 3),
 }
 
 
@@ -189,3 +191,13 @@ def test_factors_whose_product_is_no_fp32_number(lib, form, scale, k_gs, spread)
     (hq, hk, d, page), rows, ctx = CASES[form]
     kv = [a + b for a, b in zip(rows, ctx)]
     run(lib, Paged("fp8", hk, d, page, kv, 23, k_gs=k_gs), rows, kv, hq, form, scale=scale, spread=spread)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("at_end", [True, False])
+@pytest.mark.parametrize("hq,hk,d,page,form", [(160, 1, 64, 32, "128 rows"), (40, 1, 128, 16, "128 rows"), (20, 1, 256, 64, "32 rows"),
+                                               (7, 1, 64, 256, "16 rows"), (300, 1, 64, 16, "128 rows")])
+def test_many_heads_of_one_key_value_head(lib, fmt, at_end, hq, hk, d, page, form):
+    """Groups of heads that fill no tile, or take several; tiles whose last waves have no row."""
+    kv = [0, 1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 129, 200, 257]
+    run(lib, Paged(fmt, hk, d, page, kv, hq + d), [1] * len(kv), kv, hq, form, cu=False, at_end=at_end)
