@@ -10,7 +10,7 @@ import numpy as np
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(os.path.dirname(HERE))
 CSRC = os.path.join(ROOT, "nvfp4_w4a4_quantized_05_amd", "csrc")
-SOURCES = ("nvfp4_attn.hip", "nvfp4_attn_few.hip", "nvfp4_attn_many.hip", "nvfp4_rope.hip")
+SOURCES = ("nvfp4_attn.hip", "nvfp4_attn_few.hip", "nvfp4_attn_many.hip", "nvfp4_kv_cache.hip", "nvfp4_rope.hip")
 
 # kernel<<<grid, block, 0, stream>>>(  ->  host_launch(kernel, grid, block,
 _LAUNCH = re.compile(r"(\w+(?:<[^<>()\n]*>)?|(?<=  )\([^;\n]*\))<<<(.+?), (\w[\w.]*|\d+), 0, stream>>>\(")
@@ -48,6 +48,8 @@ def build(out_dir):
     lib.host_attn.argtypes = [vp] * 6 + [i32] * 5 + [vp, i64, i32, vp, vp, i32, i64, vp, i64, i32, f32, vp, vp, i64, vp]
     lib.host_attn.restype = u64
     lib.host_attn_pieces.argtypes, lib.host_attn_pieces.restype = [i32] * 4 + [vp, vp, i32, i64, i32, i32, vp, i32], i32
+    lib.host_kv.argtypes = [i32] + [vp] * 6 + [i32] * 5 + [vp, i64, i32, vp, vp, i32, i64, vp, vp, i64, i32]
+    lib.host_kv.restype = u64
     lib.host_rope.argtypes = [vp, i32, i64, i64, i64, i64, i32, i32, i32, i32, vp, vp, f32, vp, i32, vp, i32, vp, i32, vp, vp]
     lib.host_rope.restype = u64
     return lib
@@ -100,7 +102,39 @@ def pieces(lib, rows, kv, hq, hk, d, page, max_pages, tree):
     return out[:n]
 
 
-def attn(lib, paged, rows, kv, hq, q, *, tree=None, scale=None, cu=True, lead=0, tail=0, at_end=True, max_pages=None):
+def _cache(mem, paged):
+    """The arguments for a Paged cache and, by name, its arrays as the call will leave them."""
+    fp4, args, left = paged.fmt == "nvfp4", [], {}
+    for a, turned in (("codes", False), ("codes", True), ("scales", False), ("scales", True)):
+        name = "kv"[turned]
+        x = getattr(paged, a)[name]
+        p, left[name, a] = mem.put(np.swapaxes(x, 2, 3) if turned else x, f"{name} {a}") if a == "codes" or fp4 else (None, x)
+        args.append(p)
+    args += [mem.put(np.array([paged.gs[n]], dtype=np.float32), n + "_gs")[0] for n in "kv"]
+    args += [int(fp4), paged.n_pages, paged.page.bit_length() - 1, paged.hk, paged.d]
+    table = mem.put(paged.table[:, :paged.max_pages], "page_table")[0]
+    return args + [table, paged.max_pages, paged.max_pages], left
+
+
+def _sequences(mem, rows, kv, cu, lead):
+    lens = mem.put(np.array(kv, dtype=np.int32), "kv_lens")[0]
+    starts = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32) + np.int32(lead)
+    return [lens, mem.put(starts, "cu_seqlens")[0] if cu else None, len(rows)], starts
+
+
+def kv_rows(lib, paged, rows, kv, k, v, *, write, cu=True, lead=0, at_end=True):
+    """kv_cache_write of rows k and v [T, hk * d] (fp32, or bf16 bits), or _read in place of them.  Returns (k, v, the cache's
+    arrays by (name, "codes" or "scales"), row-major)."""
+    mem = Arrays(lib, at_end)
+    cache, left = _cache(mem, paged)
+    seqs, _ = _sequences(mem, rows, kv, cu, lead)
+    (kp, k), (vp, v) = mem.put(k, "k rows"), mem.put(v, "v rows")
+    at = lib.host_kv(int(write), *cache, *seqs, k.shape[0], kp, vp, k.shape[1], int(k.dtype == np.uint16))
+    assert at == 0, f"an access out of bounds, next to {mem.owner(at)}"
+    return k, v, {n: np.swapaxes(x, 2, 3) if n[0] == "v" and x.size else x for n, x in left.items()}
+
+
+def attn(lib, paged, rows, kv, hq, q, *, tree=None, scale=None, cu=True, lead=0, tail=0, at_end=True):
     """The call on a tests.attn_util.Paged cache and bf16 bits q [T, hq * d].  Returns o as fp32; rows outside the sequences 7.5."""
     d, hk, T = paged.d, paged.hk, lead + sum(rows) + tail
     mem = Arrays(lib, at_end)
@@ -108,22 +142,13 @@ def attn(lib, paged, rows, kv, hq, q, *, tree=None, scale=None, cu=True, lead=0,
     def put(a, name):
         return mem.put(a, name)[0]
 
-    fp4 = paged.fmt == "nvfp4"
-    k, v = put(paged.codes["k"], "k"), put(np.swapaxes(paged.codes["v"], 2, 3), "v")
-    ks = put(paged.scales["k"], "k_scales") if fp4 else None
-    vs = put(np.swapaxes(paged.scales["v"], 2, 3), "v_scales") if fp4 else None
-    gs = [put(np.array([paged.gs[n]], dtype=np.float32), n + "_gs") for n in "kv"]
-    most = paged.max_pages if max_pages is None else max_pages
-    table = put(paged.table[:, :most], "page_table")
-    lens = put(np.array(kv, dtype=np.int32), "kv_lens")
-    starts = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32) + np.int32(lead)
-    cus = put(starts, "cu_seqlens") if cu else None
+    cache, _ = _cache(mem, paged)
+    seqs, starts = _sequences(mem, rows, kv, cu, lead)
     masks = None if tree is None else put(np.concatenate([np.zeros(lead, np.int64), *tree, np.zeros(tail, np.int64)]), "tree")
     o, out = mem.put(np.full((T, hq * d), 0x40F0, dtype=np.uint16), "o")
     need = lib.host_attn_workspace(T, len(rows), hq, hk, d)
     ws = put(np.full(need // 4, np.nan, dtype=np.float32), "workspace")
-    at = lib.host_attn(k, v, ks, vs, *gs, int(fp4), paged.n_pages, paged.page.bit_length() - 1, hk, d, table, most, most, lens,
-                       cus, len(rows), T, put(q, "q"), hq * d, hq, d ** -0.5 if scale is None else scale, masks, o, hq * d, ws)
+    at = lib.host_attn(*cache, *seqs, T, put(q, "q"), hq * d, hq, d ** -0.5 if scale is None else scale, masks, o, hq * d, ws)
     assert at == 0, f"an access out of bounds, next to {mem.owner(at)}"
     return f32(out), starts
 

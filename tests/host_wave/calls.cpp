@@ -11,6 +11,7 @@
 #include "nvfp4_attn.hip"
 #include "nvfp4_attn_few.hip"
 #include "nvfp4_attn_many.hip"
+#include "nvfp4_kv_cache.hip"
 #include "nvfp4_rope.hip"
 
 threadIdx_t threadIdx;
@@ -198,6 +199,19 @@ uint64_t host_attn(uint8_t* k, uint8_t* v, uint8_t* ks, uint8_t* vs, const float
   const nvfp4::KvCache c{k, v, ks, vs, k_gs, v_gs, fp4 != 0, n_pages, page_shift, hk, d};
   const nvfp4::KvRows r{table, ld_table, max_pages, lens, cu, n_seqs, T};
   return host::guarded([&] { nvfp4::launch_attn_cached(c, r, q, ldq, hq, scale, tree, o, ldo, workspace, nullptr); });
+}
+
+uint64_t host_kv(int write, uint8_t* k, uint8_t* v, uint8_t* ks, uint8_t* vs, const float* k_gs, const float* v_gs, int fp4,
+                 int n_pages, int page_shift, int hk, int d, const int32_t* table, int64_t ld_table, int max_pages,
+                 const int32_t* lens, const int32_t* cu, int n_seqs, int64_t T, void* rk, void* rv, int64_t ld, int bf16) {
+  const nvfp4::KvCache c{k, v, ks, vs, k_gs, v_gs, fp4 != 0, n_pages, page_shift, hk, d};
+  const nvfp4::KvRows r{table, ld_table, max_pages, lens, cu, n_seqs, T};
+  return host::guarded([&] {
+    if (write)
+      nvfp4::launch_kv_cache_write(c, r, rk, ld, rv, ld, bf16 != 0, nullptr);
+    else
+      nvfp4::launch_kv_cache_read(c, r, rk, ld, rv, ld, bf16 != 0, nullptr);
+  });
 }
 
 uint64_t host_rope(const void* x, int bf16, int64_t ldx, int64_t q_col, int64_t k_col, int64_t T, int hq, int hk, int d,

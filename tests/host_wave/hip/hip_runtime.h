@@ -93,6 +93,17 @@ inline float e2m1(uint32_t c) {
   constexpr float v[8] = {0, 0.5f, 1, 1.5f, 2, 3, 4, 6};
   return c & 8 ? -v[c & 7] : v[c & 7];
 }
+// The code of the nearest of n values, ties to the even code (values past the last: the last, or `past`).
+template <class F>
+uint32_t nearest(float v, uint32_t n, F of, uint32_t sign) {
+  const float a = fabsf(v);
+  uint32_t c = 0;
+  while (c + 1 < n && of(c + 1) <= a) ++c;
+  if (c + 1 < n && (a - of(c) > of(c + 1) - a || (a - of(c) == of(c + 1) - a && c % 2))) ++c;
+  return c | (signbit(v) ? sign : 0);
+}
+inline uint32_t to_e4m3(float v) { return fabsf(v) <= 464.0f ? nearest(v, 127, e4m3, 128) : 127; }
+inline uint32_t to_e2m1(float v) { return nearest(v, 8, e2m1, 8); }
 
 }  // namespace host
 
@@ -190,6 +201,22 @@ inline h2 two_fp4(uint32_t w, float scale, int byte) {
   const uint32_t b = w >> (8 * byte);
   return h2{(_Float16)(e2m1(b & 15) * scale), (_Float16)(e2m1(b >> 4 & 15) * scale)};
 }
+inline f2 two_f32_fp8(int w, bool high) {
+  const uint32_t b = (uint32_t)w >> (high ? 16 : 0);
+  return f2{e4m3(b & 255), e4m3(b >> 8 & 255)};
+}
+inline f2 two_f32_fp4(uint32_t w, float scale, int byte) {
+  const uint32_t b = w >> (8 * byte);
+  return f2{e2m1(b & 15) * scale, e2m1(b >> 4 & 15) * scale};
+}
+inline int two_to_fp8(float a, float b, int old, bool high) {
+  const uint32_t v = to_e4m3(a) | to_e4m3(b) << 8;
+  return (int)(high ? ((uint32_t)old & 0xFFFFu) | v << 16 : ((uint32_t)old & 0xFFFF0000u) | v);
+}
+inline uint32_t two_to_fp4(uint32_t old, float a, float b, float scale, int byte) {
+  const uint32_t v = to_e2m1(a / scale) | to_e2m1(b / scale) << 4;
+  return (old & ~(255u << (8 * byte))) | v << (8 * byte);
+}
 inline uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel) {
   const uint64_t all = (uint64_t)hi << 32 | lo;
   uint32_t r = 0;
@@ -208,6 +235,9 @@ inline uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel) {
 #define __builtin_amdgcn_cvt_scalef32_pk_f16_fp8 host::two_fp8
 #define __builtin_amdgcn_cvt_scalef32_pk_f16_fp4 host::two_fp4
 #define __builtin_amdgcn_cvt_f32_fp8(w, byte) host::e4m3((uint32_t)(w) >> (8 * (byte)) & 255)
-#define __builtin_amdgcn_cvt_pk_fp8_f32(a, b, old, high) (abort(), 0)
+#define __builtin_amdgcn_cvt_pk_fp8_f32 host::two_to_fp8
+#define __builtin_amdgcn_cvt_pk_f32_fp8 host::two_f32_fp8
+#define __builtin_amdgcn_cvt_scalef32_pk_f32_fp4 host::two_f32_fp4
+#define __builtin_amdgcn_cvt_scalef32_pk_fp4_f32 host::two_to_fp4
 #define __builtin_amdgcn_perm host::perm
 #define __builtin_amdgcn_sched_barrier(x)
