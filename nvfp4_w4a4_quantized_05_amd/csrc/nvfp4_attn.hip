@@ -109,10 +109,10 @@ Plan plan_of(int64_t T, int n_seqs, int hk, int group, int d) {
   if (rows <= 32) {
     const int nt = rows <= 16 ? 1 : 2;
     // A range for every wave, where there are units enough (a quarter as many with 32 rows, whose sums are joined for
-    // longer).  Workgroups -> waves, us, E4M3, d 256, 4 heads: 64 tokens behind 1000, 53.0 -> 38.0, behind 3000, 100 -> 89,
-    // behind 100, 29.2 -> 30.5, behind 8200, 195 -> 195; 600 behind 200, 141 -> 102; trees of 5, 16 of them behind 4100,
-    // 80 -> 57, behind 500, 39 -> 49 (before the search for a place and the joining got shorter: 600 behind 200 now 84).
-    // Fewer lose: 16 tokens behind 1000, 24.0 -> 28.8, one behind 1000, 19.3 -> 26.1.
+    // longer).  Workgroups -> waves, us, E4M3, 24/4 heads of 256: 64 tokens behind 100, 27.8 -> 28.0, behind 1000,
+    // 51.3 -> 35.6, behind 3000, 101.5 -> 85.9, behind 8200, 196.0 -> 194.7; 600 behind 200, 131 -> 85; 16 trees of 5
+    // (32 rows) behind 4100, 73.5 -> 54.1.  Behind 500 these lose, 31.7 -> 43.5, but the host does not know the lengths.
+    // Fewer units lose, or gain little: 16 tokens behind 1000, 23.5 -> 28.4, one, 18.1 -> 24.9, 32, 34.8 -> 32.9.
     const bool solo = (int64_t)n_seqs * hk * (nt == 1 ? 1 : 4) >= ranges;
     return {nt, true, solo, 16 * nt, 256, solo ? 192 : 256, solo ? 4 * ranges : ranges};
   }

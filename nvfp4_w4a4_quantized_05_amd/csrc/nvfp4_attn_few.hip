@@ -8,8 +8,8 @@ namespace {
 // kNT rows and every fourth step each, straight from memory to the matrix
 // instructions; their results are joined through LDS.  A step's V is asked for
 // at its beginning and the next step's K behind its scores.  Bound by HBM where there
-// are keys enough: 64 tokens behind up to 16K, E4M3, 24/4 heads of 256, 180 us for
-// 1.03 GB (5.7 TB/s); two behind 131072, NVFP4, 32/8 heads of 128, 61 us (5.1 TB/s).
+// are keys enough: 64 tokens behind up to 16K, E4M3, 24/4 heads of 256, 184 us for
+// 1.03 GB (5.6 TB/s); two behind 131072, NVFP4, 32/8 heads of 128, 61 us (5.1 TB/s).
 //
 // Where there are units enough, every wave has a range of its own instead (solo):
 // a unit takes as long to begin and to end (6 us, waiting for lengths, page

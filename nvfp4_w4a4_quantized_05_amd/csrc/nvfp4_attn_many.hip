@@ -11,10 +11,12 @@ namespace {
 // convert all of them itself, as many vector instructions as the softmax has.
 // Wave t converts K's tile t and every fourth load of V.
 //
-// Bound by instruction issue and by the waits of a lone wave on each SIMD: a prompt
-// of 32768, E4M3, 24/4 heads of 256, takes 13.4 ms, 985 TFLOP/s of the 1530 of a
-// library product; matrix instructions are busy for 41% of the cycles.  Heads of 128 (two
-// waves a SIMD): 7 NVFP4 chunks of 1100 rows behind 6000, 32/8 heads, 2.05 ms, 965 TFLOP/s.
+// Bound by LDS, by instruction issue and by the waits of a lone wave on each SIMD: a
+// prompt of 32768, E4M3, 24/4 heads of 256, takes 13.4 ms, 985 TFLOP/s of the 1530 of a
+// library product.  Matrix instructions are busy for 42% of the cycles.  Each wave reads
+// a whole step's operands for its 32 rows: at 128 B a clock the 16-byte accesses of 64 lanes
+// take 52% of the cycles.  Heads of 128 (two waves a SIMD): 7 NVFP4 chunks of 1100 rows
+// behind 6000, 32/8 heads, 2.05 ms, 965 TFLOP/s, 45% and 53%.
 // 32x32x16 instructions took 10% fewer cycles at a lower clock, 14.25 ms.
 //
 // One barrier a step.  In step j the scores of step j + 1 are multiplied while

@@ -11,9 +11,10 @@
 // or 16 bytes a thread.  V is turned over in LDS, so that where all 16 positions
 // are the call's, 16 bytes go out at once; at the ends of a sequence's rows, and
 // for single tokens, only the bytes of its own positions are written.
-// Measured, 32768 rows of 4 heads of 256, bf16, NVFP4: write 47 us (172 MB at 3.7
-// TB/s; the exact rounding takes half of that in vector instructions), read 32 us
-// (5.3 TB/s, a large copy's rate).
+// Measured, 32768 rows of 4 heads of 256, bf16: write NVFP4 47 us (172 MB at 3.7
+// TB/s; the exact rounding keeps vector instructions busy for 64% of the cycles, LDS
+// 27%), E4M3 56 us (201 MB at 3.6 TB/s; 50%, LDS 44%: the byte stores that turn v over
+// meet in one bank); read NVFP4 32 us (5.3 TB/s, a large copy's rate).
 #include "nvfp4_kv.h"
 #include "nvfp4_quant_block.h"
 

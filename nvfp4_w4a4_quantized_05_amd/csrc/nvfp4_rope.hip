@@ -11,7 +11,7 @@
 // eight pairs 8 l .. 8 l + 7: no exchange but the sum of squares over the
 // head's d / 16 lanes.  A wave takes heads of one token, so its cosines and
 // sines are loaded once for all of them.  Measured: 32768 tokens of 28 heads of
-// 256 in bf16 182 us, 0.95 GB at 5.2 TB/s, a large copy's rate (5.3); 4099 tokens of
+// 256 in bf16 184 us, 0.95 GB at 5.2 TB/s, a large copy's rate (5.3); 4099 tokens of
 // 40 heads of 128 from fp32 33 us, 3.9 TB/s; 64 tokens 3.8 us.
 #include "nvfp4_device.h"
 #include "nvfp4_internal.h"
