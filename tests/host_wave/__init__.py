@@ -43,6 +43,7 @@ def build(out_dir):
     lib = ctypes.CDLL(lib)
     vp, i32, i64, f32, u64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_uint64
     lib.host_alloc.argtypes, lib.host_alloc.restype = [u64, i32], vp
+    lib.host_free.argtypes, lib.host_free.restype = [vp, u64], None
     lib.host_attn_workspace.argtypes, lib.host_attn_workspace.restype = [i64, i32, i32, i32, i32], u64
     lib.host_attn_plan.argtypes, lib.host_attn_plan.restype = [i64, i32, i32, i32, i32, vp], None
     lib.host_attn.argtypes = [vp] * 6 + [i32] * 5 + [vp, i64, i32, vp, vp, i32, i64, vp, i64, i32, f32, vp, vp, i64, vp]
@@ -56,7 +57,7 @@ def build(out_dir):
 
 
 class Arrays:
-    """Copies of arrays between unmapped pages, at their end or at their beginning; freed with the object's library only."""
+    """Copies of arrays between unmapped pages, at their end or at their beginning, until the object is closed."""
 
     def __init__(self, lib, at_end):
         self.lib, self.at_end, self.made = lib, at_end, []
@@ -69,6 +70,18 @@ class Arrays:
         view[...] = a
         self.made.append((p, a.nbytes, name))
         return p, view
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *_):
+        for p, nbytes, _ in self.made:
+            self.lib.host_free(p, nbytes)
+        self.made = []
+
+    def checked(self, at):
+        """A call's answer: 0, or the address of an access out of bounds."""
+        assert at == 0, f"an access out of bounds, next to {self.owner(at)}"
 
     def owner(self, address):
         """What array an address lies next to."""
@@ -125,44 +138,40 @@ def _sequences(mem, rows, kv, cu, lead):
 def kv_rows(lib, paged, rows, kv, k, v, *, write, cu=True, lead=0, at_end=True):
     """kv_cache_write of rows k and v [T, hk * d] (fp32, or bf16 bits), or _read in place of them.  Returns (k, v, the cache's
     arrays by (name, "codes" or "scales"), row-major)."""
-    mem = Arrays(lib, at_end)
-    cache, left = _cache(mem, paged)
-    seqs, _ = _sequences(mem, rows, kv, cu, lead)
-    (kp, k), (vp, v) = mem.put(k, "k rows"), mem.put(v, "v rows")
-    at = lib.host_kv(int(write), *cache, *seqs, k.shape[0], kp, vp, k.shape[1], int(k.dtype == np.uint16))
-    assert at == 0, f"an access out of bounds, next to {mem.owner(at)}"
-    return k, v, {n: np.swapaxes(x, 2, 3) if n[0] == "v" and x.size else x for n, x in left.items()}
+    with Arrays(lib, at_end) as mem:
+        cache, left = _cache(mem, paged)
+        seqs, _ = _sequences(mem, rows, kv, cu, lead)
+        (kp, k), (vp, v) = mem.put(k, "k rows"), mem.put(v, "v rows")
+        mem.checked(lib.host_kv(int(write), *cache, *seqs, k.shape[0], kp, vp, k.shape[1], int(k.dtype == np.uint16)))
+        return k.copy(), v.copy(), {n: (np.swapaxes(x, 2, 3) if n[0] == "v" and x.size else x).copy() for n, x in left.items()}
 
 
 def attn(lib, paged, rows, kv, hq, q, *, tree=None, scale=None, cu=True, lead=0, tail=0, at_end=True):
     """The call on a tests.attn_util.Paged cache and bf16 bits q [T, hq * d].  Returns o as fp32; rows outside the sequences 7.5."""
     d, hk, T = paged.d, paged.hk, lead + sum(rows) + tail
-    mem = Arrays(lib, at_end)
-
-    def put(a, name):
-        return mem.put(a, name)[0]
-
-    cache, _ = _cache(mem, paged)
-    seqs, starts = _sequences(mem, rows, kv, cu, lead)
-    masks = None if tree is None else put(np.concatenate([np.zeros(lead, np.int64), *tree, np.zeros(tail, np.int64)]), "tree")
-    o, out = mem.put(np.full((T, hq * d), 0x40F0, dtype=np.uint16), "o")
-    need = lib.host_attn_workspace(T, len(rows), hq, hk, d)
-    ws = put(np.full(need // 4, np.nan, dtype=np.float32), "workspace")
-    at = lib.host_attn(*cache, *seqs, T, put(q, "q"), hq * d, hq, d ** -0.5 if scale is None else scale, masks, o, hq * d, ws)
-    assert at == 0, f"an access out of bounds, next to {mem.owner(at)}"
-    return f32(out), starts
+    with Arrays(lib, at_end) as mem:
+        cache, _ = _cache(mem, paged)
+        seqs, starts = _sequences(mem, rows, kv, cu, lead)
+        masks = None if tree is None else mem.put(np.concatenate([np.zeros(lead, np.int64), *tree, np.zeros(tail, np.int64)]), "tree")[0]
+        o, out = mem.put(np.full((T, hq * d), 0x40F0, dtype=np.uint16), "o")
+        need = lib.host_attn_workspace(T, len(rows), hq, hk, d)
+        ws = mem.put(np.full(need // 4, np.nan, dtype=np.float32), "workspace")[0]
+        mem.checked(lib.host_attn(*cache, *seqs, T, mem.put(q, "q")[0], hq * d, hq, d ** -0.5 if scale is None else scale, masks, o,
+                                  hq * d, ws))
+        return f32(out), starts
 
 
 def rope(lib, x, q_w, k_w, table, pos, *, q_col, k_col, hq, hk, eps, pair_axis=None, adjacent=False, at_end=True):
     """The call on x (fp32, or bf16 bits) [T, cols]; pos [axes, T].  Returns q and k as fp32."""
-    mem, d, T = Arrays(lib, at_end), len(q_w), x.shape[0]
+    d, T = len(q_w), x.shape[0]
     axis = np.zeros(8, dtype=np.uint32)
     for p, n in enumerate(pair_axis or ()):
         axis[p // 16] |= np.uint32(n << p % 16 * 2)
-    q, qv = mem.put(np.zeros((T, hq * d), np.uint16), "q")
-    k, kv = mem.put(np.zeros((T, hk * d), np.uint16), "k")
-    at = lib.host_rope(mem.put(x, "x")[0], int(x.dtype == np.uint16), x.shape[1], q_col, k_col, T, hq, hk, d, table.shape[1],
-                       mem.put(q_w, "q_w")[0], mem.put(k_w, "k_w")[0], eps, mem.put(table, "cos_sin")[0], table.shape[0],
-                       mem.put(pos.astype(np.int32), "positions")[0], pos.shape[0], mem.put(axis, "axes")[0], int(adjacent), q, k)
-    assert at == 0, f"an access out of bounds, next to {mem.owner(at)}"
-    return f32(qv), f32(kv)
+    with Arrays(lib, at_end) as mem:
+        q, qv = mem.put(np.zeros((T, hq * d), np.uint16), "q")
+        k, kv = mem.put(np.zeros((T, hk * d), np.uint16), "k")
+        mem.checked(lib.host_rope(mem.put(x, "x")[0], int(x.dtype == np.uint16), x.shape[1], q_col, k_col, T, hq, hk, d, table.shape[1],
+                                  mem.put(q_w, "q_w")[0], mem.put(k_w, "k_w")[0], eps, mem.put(table, "cos_sin")[0], table.shape[0],
+                                  mem.put(pos.astype(np.int32), "positions")[0], pos.shape[0], mem.put(axis, "axes")[0],
+                                  int(adjacent), q, k))
+        return f32(qv), f32(kv)

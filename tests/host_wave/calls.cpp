@@ -180,6 +180,11 @@ void* host_alloc(uint64_t bytes, int at_end) {
   return p + page + (at_end ? room - bytes : 0);
 }
 
+void host_free(void* p, uint64_t bytes) {
+  const uint64_t page = 4096, at = reinterpret_cast<uint64_t>(p) / page * page;
+  munmap(reinterpret_cast<void*>(at - page), (bytes + page - 1) / page * page + 2 * page);
+}
+
 uint64_t host_attn_workspace(int64_t T, int n_seqs, int hq, int hk, int d) {
   return nvfp4::attn_cached_workspace_bytes(T, n_seqs, hq, hk, d);
 }
