@@ -738,9 +738,10 @@ NVFP4_API nvfp4_status_t nvfp4_kv_cache_read(const nvfp4_kv_cache_t* cache, cons
  * Precision: K and V enter exactly, the weights w_p with 11 bits, sums in fp32; o
  * is rounded to bf16 once.  A query or key that is not finite makes the rows that
  * use it NaN, a value that is not finite its dim of the rows that see it, and
- * nothing else: finite scores may be of any size.  The same call gives the same bits; which kernel runs, and with it
- * the order of sums, goes by T * n_q_heads / (n_seqs * n_kv_heads), an average: a
- * prompt's chunk among many single tokens may run faster as a call of its own.
+ * nothing else: finite scores may be of any size.  The same call gives the same
+ * bits; which kernel runs, and with it the order of sums, goes by
+ * T * n_q_heads / (n_seqs * n_kv_heads), an average: a prompt's chunk among many
+ * single tokens may run faster as a call of its own.
  */
 NVFP4_API nvfp4_status_t nvfp4_attn_cached(const nvfp4_kv_cache_t* cache, const int32_t* page_table, int64_t ld_table,
                                            int32_t max_pages, const int32_t* kv_lens, const int32_t* cu_seqlens,
